@@ -84,7 +84,8 @@ enum {
     PSTAT_ERR_ALIGN = -5,       /* a pointer lacks the alignment stated for it */
     PSTAT_ERR_WORKSPACE = -6,   /* workspace NULL or smaller than required */
     PSTAT_ERR_CUDA = -7,        /* a CUDA runtime call or launch failed */
-    PSTAT_ERR_UNSUPPORTED = -8  /* the current device is not sm_103 (GB300) */
+    PSTAT_ERR_UNSUPPORTED = -8, /* the current device is not sm_103 (GB300) */
+    PSTAT_ERR_PARAM = -9        /* a numeric parameter lies outside its range */
 };
 
 /* Bits OR-ed into *dev_error by the kernels. */
@@ -92,6 +93,8 @@ enum {
 #define PSTAT_DEV_EMPTY_ROW 0x2 /* every logit of a row is -inf: softmax undefined */
 #define PSTAT_DEV_TIMEOUT 0x4   /* a bounded wait on an asynchronous copy gave up */
 #define PSTAT_DEV_RANGE 0x8     /* lm_head backward: a value exceeds the fp16 range (65504) */
+#define PSTAT_DEV_BAD_PARAM 0x10 /* a row's temperature, top_p, min_p or uniform is out of range */
+#define PSTAT_DEV_NONFINITE 0x20 /* the gradient norm is infinite or NaN */
 
 #define PSTAT_MAX_SHARDS 64
 #define PSTAT_CHUNK_BF16 4096 /* chunk length in elements for bf16 logits */
@@ -364,6 +367,141 @@ PSTAT_API int pstat_lmhead_backward(const void* hidden, const void* W, int64_t T
                           const int64_t* labels, int64_t ignore_index, const float* weights,
                           const float* rowstats, float* dhidden, float* dW, void* workspace,
                           size_t ws_bytes, int* dev_error, pstat_stream_t stream);
+
+/*
+ * Tempered, truncated distributions: drawing a token from a row, and the
+ * policy statistics of a given label under the distribution that draws come
+ * from (the ratio pi/mu of an RL step compares two policies under one
+ * distribution, so its trainer side needs the rollout's temperature and
+ * truncation).
+ *
+ * Row z[0..V), temperature t, M = max z, x_v = (z_v - M)/t, e_v = e^(x_v).
+ * Tokens are ordered by (logit descending, index ascending); -inf logits are
+ * masked and never kept.  Each filter keeps a prefix of that order:
+ *   top_k  the first top_k tokens (top_k <= 0 or >= V: all);
+ *   top_p  the shortest prefix whose mass reaches top_p times the mass that
+ *          top_k left (top_p = 1: all);
+ *   min_p  the tokens with e_v >= min_p (min_p = 0: all).
+ * The kept set is the shortest of the three.  Its last token is the cut
+ * (tau, i): v is kept when z_v > tau, or z_v == tau and v <= i.  With no
+ * filter the cut is (-inf, V - 1).
+ * Which tokens are kept and drawn is decided as in exact arithmetic (fixed-
+ * point weights of about 46 bits, integer sums), ties by the lowest index.
+ * The results of a row depend on its own values and settings only: they are
+ * bit-identical in any batch.
+ * A row with a NaN or +inf logit, or without a finite one, has no
+ * distribution: PSTAT_DEV_EMPTY_ROW, NaN outputs, token and cut index -1.
+ */
+
+#define PSTAT_FILTER_MAX_V (1 << 20) /* largest vocabulary of these entry points */
+#define PSTAT_FILTER_MAX_T (1 << 24) /* most rows of one call */
+
+/* Settings of a call: one value for every row, or a device array [T] that
+ * replaces it where the pointer is not NULL.  A row whose array value is out of
+ * range gets PSTAT_DEV_BAD_PARAM, NaN outputs, token and cut index -1; a value
+ * of the struct itself out of range is PSTAT_ERR_PARAM. */
+typedef struct {
+    float temperature;         /* in [2^-20, 2^20]; sampling also takes 0: the first maximum */
+    float top_p;               /* in (0, 1] */
+    float min_p;               /* in [0, 1] */
+    int64_t top_k;
+    const float* temperatures; /* device [T] or NULL */
+    const int32_t* top_ks;
+    const float* top_ps;
+    const float* min_ps;
+} pstat_filters;
+
+/*
+ * Workspace bytes of pstat_sample and pstat_filtered_forward on T rows of V
+ * logits (V <= PSTAT_FILTER_MAX_V, T <= PSTAT_FILTER_MAX_T).
+ */
+PSTAT_API int pstat_filter_workspace_size(int64_t T, int64_t V, pstat_dtype dt, size_t* bytes);
+
+/*
+ * Draws one token per row: the first v in index order whose kept mass
+ * sum_{w <= v, kept} e_w exceeds uniform times the whole kept mass.
+ *   uniform      [T] float in [0, 1).
+ *   out_token    [T] int64.
+ *   out_logprob  [T] float: x_v - ln sum_{kept} e (0 at temperature 0).
+ *   Logits, dev_error and stream as pstat_forward; workspace 16-byte aligned,
+ *   at least pstat_filter_workspace_size(...) bytes.
+ */
+PSTAT_API int pstat_sample(const void* logits, pstat_dtype dt, int64_t T, int64_t V, int64_t ld,
+                           const float* uniform, const pstat_filters* filters, int64_t* out_token,
+                           float* out_logprob, void* workspace, size_t ws_bytes, int* dev_error,
+                           pstat_stream_t stream);
+
+/*
+ * Policy statistics of labels under the tempered, truncated distribution.
+ *   labels         [T] int64 (NULL: every row ignored).
+ *   out_logprob    [T] float: x_y - ln S, S the kept mass; -inf where y is not
+ *                  kept, +0 where it is ignore_index.
+ *   out_entropy    [T] float: ln S - (1/S) sum_{kept} e x.
+ *   out_rowstats   [T, 2] float (M, ln S).
+ *   out_cut_logit  [T] float and out_cut_index [T] int64: the cut.
+ *   All outputs are required.  Labels outside [0, V): PSTAT_DEV_BAD_LABEL,
+ *   logprob and entropy NaN.  Workspace as pstat_sample.
+ */
+PSTAT_API int pstat_filtered_forward(const void* logits, pstat_dtype dt, int64_t T, int64_t V,
+                                     int64_t ld, const int64_t* labels, int64_t ignore_index,
+                                     const pstat_filters* filters, float* out_logprob,
+                                     float* out_entropy, float* out_rowstats,
+                                     float* out_cut_logit, int64_t* out_cut_index,
+                                     void* workspace, size_t ws_bytes, int* dev_error,
+                                     pstat_stream_t stream);
+
+/*
+ * Weighted backward of that logprob:
+ *   dlogits_v = (w/t) (1[v = y] - kept_v e_v / S),
+ * an all +0.0 row where y is ignored, w = 0 or y is not kept.  The kept set is
+ * held fixed, as the truncation is piecewise constant in the logits.
+ *   rowstats, cut_logit, cut_index  from pstat_filtered_forward on the same
+ *                  logits and settings.
+ *   temperature    for every row, or `temperatures` [T] where not NULL.
+ *   weights, out_dlogits, out_dt, ld_out as pstat_backward.
+ */
+PSTAT_API int pstat_filtered_backward(const void* logits, pstat_dtype dt, int64_t T, int64_t V,
+                                      int64_t ld, const int64_t* labels, int64_t ignore_index,
+                                      const float* weights, const float* rowstats,
+                                      const float* cut_logit, const int64_t* cut_index,
+                                      float temperature, const float* temperatures,
+                                      void* out_dlogits, pstat_dtype out_dt, int64_t ld_out,
+                                      int* dev_error, pstat_stream_t stream);
+
+/*
+ * The global L2 norm of a list of gradients, and clipping by it.
+ *   norm = sqrt(sum over all elements of all tensors of g^2)
+ *   out  = g * min(1, max_norm / norm)
+ * The list is a HOST array; each entry names `n` contiguous elements on the
+ * device.  Tensors may differ in type and size, be empty, and start at any
+ * element; at most PSTAT_GRAD_MAX_ELEMENTS each.  Squares are summed without
+ * overflow or underflow, in an order fixed by the sizes: the same list gives
+ * the same bits.  An empty list has norm 0.
+ */
+#define PSTAT_GRAD_MAX_ELEMENTS ((int64_t)1 << 40)
+typedef struct {
+    const void* data;
+    void* out; /* clipping: where the scaled tensor goes, same type; may equal data */
+    int64_t n;
+    pstat_dtype dtype;
+} pstat_tensor;
+
+PSTAT_API int pstat_grad_workspace_size(const pstat_tensor* tensors, int64_t n_tensors,
+                                        size_t* bytes);
+
+/* out_norm: device float.  An infinite or NaN norm sets PSTAT_DEV_NONFINITE.
+ * Workspace 8-byte aligned, at least pstat_grad_workspace_size(...) bytes. */
+PSTAT_API int pstat_grad_norm(const pstat_tensor* tensors, int64_t n_tensors, float* out_norm,
+                              void* workspace, size_t ws_bytes, int* dev_error,
+                              pstat_stream_t stream);
+
+/* The norm before clipping goes to out_norm.  max_norm >= 0.  When the norm is
+ * infinite or NaN the tensors are passed on unscaled (and the bit is set), so
+ * that the caller can drop the step.  An `out` may not overlap another
+ * tensor of the list. */
+PSTAT_API int pstat_clip_grad_norm(const pstat_tensor* tensors, int64_t n_tensors, float max_norm,
+                                   float* out_norm, void* workspace, size_t ws_bytes,
+                                   int* dev_error, pstat_stream_t stream);
 
 /*
  * Self-test of the bounded waits.  Every kernel of this library waits on its

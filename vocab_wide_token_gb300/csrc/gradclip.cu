@@ -1,0 +1,335 @@
+// gradclip.cu -- the global L2 norm of a list of gradient tensors and their
+// scaling by min(1, max_norm / norm).
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace pstat {
+namespace {
+
+constexpr int kGnThreads = 256;
+constexpr int kGnUnroll = 4;                // 16-byte vectors in flight per thread
+constexpr int64_t kUnitBytes = (int64_t)kGnThreads * kGnUnroll * 16;  // 16 KiB of one tensor
+constexpr int kMaxBlocks = 1024;            // partial sums
+constexpr int kBatch = 800;                 // tensors of one launch (they travel as its arguments)
+
+struct GradTensor {
+    const void* in;
+    void* out;
+    int64_t n;
+    uint32_t first_unit;
+    uint32_t bf16;
+};
+template <int N>
+struct GradBatch {
+    int count;
+    uint32_t units;
+    GradTensor t[N];
+};
+
+__device__ __forceinline__ float elem(const void* p, int64_t i, bool bf16) {
+    return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16)
+                : static_cast<const float*>(p)[i];
+}
+
+// Sum of squares of up to 8 floats, as a double.  In fp32 it is used where no
+// square can have overflowed or lost its low bits (the sum is in [2^-60, 2^120];
+// then squares below 2^-126 are below 2^-66 of it); elsewhere in fp64.
+template <int N>
+__device__ __forceinline__ double squares(const float (&x)[N]) {
+    float s = 0.f, any = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        s = fmaf(x[i], x[i], s);
+        any = fmaxf(any, fabsf(x[i]));
+    }
+    if (s > 8.6736174e-19f && s < 1.3292280e36f) return (double)s;
+    if (s == 0.f && any == 0.f) return 0.0;
+    double d = 0.0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) d = fma((double)x[i], (double)x[i], d);
+    return d;
+}
+
+__device__ __forceinline__ double vector_squares(const uint4& q, bool bf16) {
+    if (bf16) {
+        const float x[8] = {bf2_lo(q.x), bf2_hi(q.x), bf2_lo(q.y), bf2_hi(q.y),
+                            bf2_lo(q.z), bf2_hi(q.z), bf2_lo(q.w), bf2_hi(q.w)};
+        return squares(x);
+    }
+    const float x[4] = {__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z),
+                        __uint_as_float(q.w)};
+    return squares(x);
+}
+
+// Fixed-order sum of one double per thread; the result is valid in thread 0.
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double warp[kGnThreads / 32];
+#pragma unroll
+    for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+    if ((threadIdx.x & 31) == 0) warp[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double s = 0.0;
+    for (int w = 0; w < kGnThreads / 32; ++w) s += warp[w];
+    __syncthreads();
+    return s;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kGnThreads)
+    square_sums_kernel(const __grid_constant__ GradBatch<N> g, double* __restrict__ partial) {
+    const uint32_t u0 = (uint32_t)((uint64_t)g.units * blockIdx.x / gridDim.x);
+    const uint32_t u1 = (uint32_t)((uint64_t)g.units * (blockIdx.x + 1) / gridDim.x);
+    double sum = 0.0;
+    int i = 0;
+    for (uint32_t u = u0; u < u1; ++u) {
+        while (i + 1 < g.count && g.t[i + 1].first_unit <= u) ++i;
+        const GradTensor& t = g.t[i];
+        const bool bf16 = t.bf16;
+        const int64_t per = kUnitBytes / (bf16 ? 2 : 4);
+        const int64_t e0 = (int64_t)(u - t.first_unit) * per;
+        const int64_t e1 = min(t.n, e0 + per);
+        const int vec = bf16 ? 8 : 4;
+        int64_t done = e0;
+        if ((reinterpret_cast<uintptr_t>(t.in) & 15u) == 0) {
+            const int nv = (int)((e1 - e0) / vec);
+            const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(t.in) + e0 * (bf16 ? 2 : 4));
+            uint4 q[kGnUnroll];
+#pragma unroll
+            for (int j = 0; j < kGnUnroll; ++j) {
+                const int k = j * kGnThreads + (int)threadIdx.x;
+                q[j] = k < nv ? __ldg(v + k) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < kGnUnroll; ++j) sum += vector_squares(q[j], bf16);
+            done = e0 + (int64_t)nv * vec;
+        }
+        for (int64_t k = done + threadIdx.x; k < e1; k += kGnThreads) {
+            const float x[1] = {elem(t.in, k, bf16)};
+            sum += squares(x);
+        }
+    }
+    sum = block_sum(sum);
+    if (threadIdx.x == 0) partial[blockIdx.x] = sum;
+}
+
+// Every block that needs the norm adds the partial sums up itself, in the same
+// order, so all of them hold the same bits.
+__device__ __forceinline__ double norm_of(const double* partial, int n) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < n; i += kGnThreads) s += partial[i];
+    return sqrt(block_sum(s));
+}
+
+__global__ void __launch_bounds__(kGnThreads)
+    norm_kernel(const double* __restrict__ partial, int n, float* __restrict__ out,
+                int* __restrict__ dev_error) {
+    const float norm = (float)norm_of(partial, n);
+    if (threadIdx.x == 0) {
+        *out = norm;
+        if (!(norm < INFINITY) && dev_error) atomicOr(dev_error, PSTAT_DEV_NONFINITE);
+    }
+}
+
+template <int N>
+__global__ void __launch_bounds__(kGnThreads)
+    scale_kernel(const __grid_constant__ GradBatch<N> g, const double* __restrict__ partial, int n,
+                 float max_norm, float* __restrict__ out, int* __restrict__ dev_error) {
+    __shared__ float s_factor;
+    const double norm = norm_of(partial, n);
+    if (threadIdx.x == 0) {
+        const float f = (float)norm;
+        const bool finite = f < INFINITY;
+        s_factor = finite && norm > (double)max_norm ? (float)((double)max_norm / norm) : 1.f;
+        if (blockIdx.x == 0) {
+            *out = f;
+            if (!finite && dev_error) atomicOr(dev_error, PSTAT_DEV_NONFINITE);
+        }
+    }
+    __syncthreads();
+    const float factor = s_factor;
+    const uint32_t u0 = (uint32_t)((uint64_t)g.units * blockIdx.x / gridDim.x);
+    const uint32_t u1 = (uint32_t)((uint64_t)g.units * (blockIdx.x + 1) / gridDim.x);
+    int i = 0;
+    for (uint32_t u = u0; u < u1; ++u) {
+        while (i + 1 < g.count && g.t[i + 1].first_unit <= u) ++i;
+        const GradTensor& t = g.t[i];
+        if (factor == 1.f && t.out == t.in) continue;
+        const bool bf16 = t.bf16;
+        const int64_t per = kUnitBytes / (bf16 ? 2 : 4);
+        const int64_t e0 = (int64_t)(u - t.first_unit) * per;
+        const int64_t e1 = min(t.n, e0 + per);
+        const int vec = bf16 ? 8 : 4;
+        int64_t done = e0;
+        if (((reinterpret_cast<uintptr_t>(t.in) | reinterpret_cast<uintptr_t>(t.out)) & 15u) == 0) {
+            const int nv = (int)((e1 - e0) / vec);
+            const int64_t off = e0 * (bf16 ? 2 : 4);
+            const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(t.in) + off);
+            uint4* o = reinterpret_cast<uint4*>(static_cast<char*>(t.out) + off);
+            uint4 q[kGnUnroll];
+#pragma unroll
+            for (int j = 0; j < kGnUnroll; ++j) {
+                const int k = j * kGnThreads + (int)threadIdx.x;
+                if (k < nv) q[j] = v[k];
+            }
+#pragma unroll
+            for (int j = 0; j < kGnUnroll; ++j) {
+                const int k = j * kGnThreads + (int)threadIdx.x;
+                if (k >= nv) continue;
+                uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (factor == 1.f) continue;  // passed on bit for bit, NaNs included
+                    w[e] = bf16 ? bf2_pack_rn(bf2_lo(w[e]) * factor, bf2_hi(w[e]) * factor)
+                                : __float_as_uint(__uint_as_float(w[e]) * factor);
+                }
+                o[k] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            done = e0 + (int64_t)nv * vec;
+        }
+        for (int64_t k = done + threadIdx.x; k < e1; k += kGnThreads) {
+            if (bf16) {
+                const uint16_t x = static_cast<const uint16_t*>(t.in)[k];
+                static_cast<uint16_t*>(t.out)[k] =
+                    factor == 1.f ? x
+                                  : (uint16_t)(bf2_pack_rn(bf2_lo(x) * factor, 0.f) & 0xFFFFu);
+            } else {
+                const uint32_t x = static_cast<const uint32_t*>(t.in)[k];
+                static_cast<uint32_t*>(t.out)[k] =
+                    factor == 1.f ? x : __float_as_uint(__uint_as_float(x) * factor);
+            }
+        }
+    }
+}
+
+int check_tensors(const pstat_tensor* tensors, int64_t n, bool outputs) {
+    if (n < 0) return PSTAT_ERR_SHAPE;
+    if (n > 0 && !tensors) return PSTAT_ERR_NULLPTR;
+    for (int64_t i = 0; i < n; ++i) {
+        const pstat_tensor& t = tensors[i];
+        if (t.dtype != PSTAT_F32 && t.dtype != PSTAT_BF16) return PSTAT_ERR_DTYPE;
+        if (t.n < 0 || t.n > PSTAT_GRAD_MAX_ELEMENTS) return PSTAT_ERR_SHAPE;
+        if (t.n == 0) continue;
+        if (!t.data || (outputs && !t.out)) return PSTAT_ERR_NULLPTR;
+        const uintptr_t mask = t.dtype == PSTAT_BF16 ? 1 : 3;
+        if ((reinterpret_cast<uintptr_t>(t.data) & mask) ||
+            (outputs && (reinterpret_cast<uintptr_t>(t.out) & mask)))
+            return PSTAT_ERR_ALIGN;
+    }
+    return PSTAT_OK;
+}
+
+// Fills the next batch from tensors[i..]; returns how many of them it covers.
+template <int N>
+int64_t fill(GradBatch<N>& g, const pstat_tensor* tensors, int64_t i, int64_t n) {
+    g.count = 0;
+    uint64_t units = 0;
+    int64_t j = i;
+    for (; j < n && g.count < N; ++j) {
+        const pstat_tensor& t = tensors[j];
+        if (t.n == 0) continue;
+        const int64_t per = kUnitBytes / (t.dtype == PSTAT_BF16 ? 2 : 4);
+        const uint64_t add = (uint64_t)((t.n + per - 1) / per);
+        if (units + add > 0xFFFFFFFFull) break;
+        g.t[g.count++] = {t.data, t.out, t.n, (uint32_t)units, t.dtype == PSTAT_BF16 ? 1u : 0u};
+        units += add;
+    }
+    g.units = (uint32_t)units;
+    return j - i;
+}
+
+int blocks_for(uint32_t units, const DeviceInfo& dev) {
+    const uint32_t most = (uint32_t)(dev.sm_count * 4 < kMaxBlocks ? dev.sm_count * 4 : kMaxBlocks);
+    return (int)(units < most ? units : most);
+}
+
+template <int N>
+int run_norm(const pstat_tensor* tensors, int64_t n, bool clip, float max_norm, float* out_norm,
+             double* partial, int64_t max_partials, int* dev_error, cudaStream_t st) {
+    DeviceInfo dev;
+    const int rc = device_info(&dev);
+    if (rc != PSTAT_OK) return rc;
+    GradBatch<N> g;
+    int n_partial = 0;
+    for (int64_t i = 0; i < n;) {
+        i += fill(g, tensors, i, n);
+        if (g.units == 0) continue;
+        const int blocks = blocks_for(g.units, dev);
+        if (n_partial + blocks > max_partials) return PSTAT_ERR_WORKSPACE;
+        square_sums_kernel<N><<<blocks, kGnThreads, 0, st>>>(g, partial + n_partial);
+        n_partial += blocks;
+    }
+    if (!clip || n_partial == 0) {
+        norm_kernel<<<1, kGnThreads, 0, st>>>(partial, n_partial, out_norm, dev_error);
+    } else {
+        for (int64_t i = 0; i < n;) {
+            i += fill(g, tensors, i, n);
+            if (g.units == 0) continue;
+            scale_kernel<N><<<blocks_for(g.units, dev), kGnThreads, 0, st>>>(
+                g, partial, n_partial, max_norm, out_norm, dev_error);
+        }
+    }
+    return cudaGetLastError() == cudaSuccess ? PSTAT_OK : PSTAT_ERR_CUDA;
+}
+
+int64_t max_launches(const pstat_tensor* tensors, int64_t n, int per) {
+    // A batch ends when it is full or its unit index would pass 32 bits.
+    uint64_t units = 0;
+    for (int64_t i = 0; i < n; ++i) units += (uint64_t)(tensors[i].n / (kUnitBytes / 4) + 1);
+    return (n + per - 1) / per + (int64_t)(units >> 31) + 1;
+}
+
+int norm_entry(const pstat_tensor* tensors, int64_t n, bool clip, float max_norm, float* out_norm,
+               void* workspace, size_t ws_bytes, int* dev_error, pstat_stream_t stream) {
+    int rc = check_tensors(tensors, n, clip);
+    if (rc != PSTAT_OK) return rc;
+    if (clip && !(max_norm >= 0.f)) return PSTAT_ERR_PARAM;
+    if (!out_norm) return PSTAT_ERR_NULLPTR;
+    size_t need = 0;
+    rc = pstat_grad_workspace_size(tensors, n, &need);
+    if (rc != PSTAT_OK) return rc;
+    if (!workspace || ws_bytes < need) return PSTAT_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 7u) || (reinterpret_cast<uintptr_t>(out_norm) & 3u))
+        return PSTAT_ERR_ALIGN;
+    double* partial = static_cast<double*>(workspace);
+    const int64_t room = (int64_t)(ws_bytes / sizeof(double));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (n <= 32)
+        return run_norm<32>(tensors, n, clip, max_norm, out_norm, partial, room, dev_error, st);
+    return run_norm<kBatch>(tensors, n, clip, max_norm, out_norm, partial, room, dev_error, st);
+}
+
+}  // namespace
+}  // namespace pstat
+
+using namespace pstat;
+
+extern "C" {
+
+int pstat_grad_workspace_size(const pstat_tensor* tensors, int64_t n_tensors, size_t* bytes) {
+    if (!bytes) return PSTAT_ERR_NULLPTR;
+    const int rc = check_tensors(tensors, n_tensors, false);
+    if (rc != PSTAT_OK) return rc;
+    *bytes = (size_t)max_launches(tensors, n_tensors, n_tensors <= 32 ? 32 : kBatch) * kMaxBlocks *
+             sizeof(double);
+    return PSTAT_OK;
+}
+
+int pstat_grad_norm(const pstat_tensor* tensors, int64_t n_tensors, float* out_norm,
+                    void* workspace, size_t ws_bytes, int* dev_error, pstat_stream_t stream) {
+    return norm_entry(tensors, n_tensors, false, 0.f, out_norm, workspace, ws_bytes, dev_error,
+                      stream);
+}
+
+int pstat_clip_grad_norm(const pstat_tensor* tensors, int64_t n_tensors, float max_norm,
+                         float* out_norm, void* workspace, size_t ws_bytes, int* dev_error,
+                         pstat_stream_t stream) {
+    return norm_entry(tensors, n_tensors, true, max_norm, out_norm, workspace, ws_bytes, dev_error,
+                      stream);
+}
+
+}  // extern "C"

@@ -9,6 +9,7 @@ tensors.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -26,6 +27,13 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 # ---- C ABI prototypes -------------------------------------------------------
 _i64, _i32, _vp, _sz = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+
+
+class Filters(ctypes.Structure):
+    """pstat_filters of include/pstat.h."""
+    _fields_ = [("temperature", ctypes.c_float), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float), ("top_k", _i64), ("temperatures", _vp),
+                ("top_ks", _vp), ("top_ps", _vp), ("min_ps", _vp)]
 
 
 def declare_prototypes(lib: ctypes.CDLL) -> ctypes.CDLL:
@@ -72,6 +80,23 @@ def declare_prototypes(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.pstat_backward_shard.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64,
                                          _i64, _vp, _i32, _i64, _vp, _vp]
     lib.pstat_backward_shard.restype = _i32
+    lib.pstat_filter_workspace_size.argtypes = [_i64, _i64, _i32, ctypes.POINTER(_sz)]
+    lib.pstat_filter_workspace_size.restype = _i32
+    lib.pstat_sample.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp,
+                                 _vp]
+    lib.pstat_sample.restype = _i32
+    lib.pstat_filtered_forward.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp,
+                                           _vp, _vp, _vp, _vp, _sz, _vp, _vp]
+    lib.pstat_filtered_forward.restype = _i32
+    lib.pstat_filtered_backward.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp,
+                                            _vp, ctypes.c_float, _vp, _vp, _i32, _i64, _vp, _vp]
+    lib.pstat_filtered_backward.restype = _i32
+    lib.pstat_grad_workspace_size.argtypes = [_vp, _i64, ctypes.POINTER(_sz)]
+    lib.pstat_grad_workspace_size.restype = _i32
+    lib.pstat_grad_norm.argtypes = [_vp, _i64, _vp, _vp, _sz, _vp, _vp]
+    lib.pstat_grad_norm.restype = _i32
+    lib.pstat_clip_grad_norm.argtypes = [_vp, _i64, ctypes.c_float, _vp, _vp, _sz, _vp, _vp]
+    lib.pstat_clip_grad_norm.restype = _i32
     lib.pstat_noalloc_scratch_bytes.argtypes = []
     lib.pstat_noalloc_scratch_bytes.restype = _sz
     lib.pstat_selftest_wait_timeout.argtypes = [ctypes.c_uint64, _vp, _vp]
@@ -84,8 +109,9 @@ declare_prototypes(_lib)
 F32, BF16 = 0, 1
 OK = 0
 ERR = {-1: "NULLPTR", -2: "SHAPE", -3: "SHARDS", -4: "DTYPE", -5: "ALIGN", -6: "WORKSPACE",
-       -7: "CUDA", -8: "UNSUPPORTED"}
+       -7: "CUDA", -8: "UNSUPPORTED", -9: "PARAM"}
 DEV_BAD_LABEL, DEV_EMPTY_ROW, DEV_TIMEOUT, DEV_RANGE = 0x1, 0x2, 0x4, 0x8
+DEV_BAD_PARAM, DEV_NONFINITE = 0x10, 0x20
 CHUNK_BF16, CHUNK_F32 = 4096, 2048
 MAX_SHARDS = 64
 
@@ -646,6 +672,214 @@ def lmhead_backward(hidden, W, labels, weights, rowstats, ignore_index: int = -1
     return dhidden, dW
 
 
+# ---- tempered, truncated distributions -------------------------------------------
+
+def filter_workspace_size(T: int, V: int, dtype: torch.dtype) -> int:
+    """Workspace bytes of ``sample`` and ``filtered_forward``."""
+    n = ctypes.c_size_t(0)
+    code = BF16 if dtype == torch.bfloat16 else F32
+    _check(_lib.pstat_filter_workspace_size(T, V, code, ctypes.byref(n)),
+           "pstat_filter_workspace_size")
+    return int(n.value)
+
+
+def _per_row(x, dtype, T, dev, name):
+    """A setting as (number, None) or (unused, its [T] device tensor)."""
+    if isinstance(x, torch.Tensor):
+        return None, _tensor(x, dtype, (T,), dev, name)
+    return x, None
+
+
+def _filters(temperature, top_k, top_p, min_p, T, dev):
+    """The call's pstat_filters.  It holds the addresses of the caller's own
+    [T] tensors, which the caller's arguments keep alive until the launch."""
+    t, tt = _per_row(temperature, torch.float32, T, dev, "temperature")
+    k, kk = _per_row(top_k, torch.int32, T, dev, "top_k")
+    p, pp = _per_row(top_p, torch.float32, T, dev, "top_p")
+    m, mm = _per_row(min_p, torch.float32, T, dev, "min_p")
+
+    def ptr(a):
+        return None if a is None else a.data_ptr()
+
+    return Filters(1.0 if t is None else float(t), 1.0 if p is None else float(p),
+                   0.0 if m is None else float(m), 0 if k is None else int(k),
+                   ptr(tt), ptr(kk), ptr(pp), ptr(mm))
+
+
+def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0,
+           min_p=0.0, *, out=None, workspace=None, dev_error=None):
+    """One token per row, drawn with the given uniforms from the tempered,
+    truncated softmax of the row, and its log-probability there.
+
+    `uniform` is float32 [T] in [0, 1).  Each setting is a number, or a [T]
+    tensor (float32; int32 for top_k) with one value per row.  Temperature 0
+    takes the first maximum; top_k <= 0, top_p = 1 and min_p = 0 filter
+    nothing.  The token is the first in index order whose kept mass exceeds
+    `uniform` times the whole kept mass.  Returns (token [T] int64, logprob
+    [T] f32); `out` may supply the two.
+    """
+    T, V, ld = _rows(logits)
+    dev = logits.device
+    dt = _dtype_code(logits)
+    u = _tensor(uniform, torch.float32, (T,), dev, "uniform")
+    f = _filters(temperature, top_k, top_p, min_p, T, dev)
+    if out is None:
+        token = torch.empty(T, dtype=torch.int64, device=dev)
+        lp = torch.empty(T, dtype=torch.float32, device=dev)
+    else:
+        token = _tensor(out[0], torch.int64, (T,), dev, "out[0] (token)")
+        lp = _tensor(out[1], torch.float32, (T,), dev, "out[1] (logprob)")
+    dev_error = _error_flag(dev_error, dev)
+    workspace = _workspace(workspace, filter_workspace_size(T, V, logits.dtype), dev)
+    _call(dev, "pstat_sample", _lib.pstat_sample,
+          _ptr(logits), dt, T, V, ld, _ptr(u), ctypes.byref(f), _ptr(token), _ptr(lp),
+          _ptr(workspace), workspace.numel(), _ptr(dev_error), _stream(dev))
+    return token, lp
+
+
+def _filtered_outputs(out, T, dev):
+    if out is None:
+        return (*_row_outputs(None, T, dev), torch.empty(T, dtype=torch.float32, device=dev),
+                torch.empty(T, dtype=torch.int64, device=dev))
+    lp, ent, rs = _row_outputs(out[:3], T, dev)
+    return (lp, ent, rs, _tensor(out[3], torch.float32, (T,), dev, "out[3] (cut_logit)"),
+            _tensor(out[4], torch.int64, (T,), dev, "out[4] (cut_index)"))
+
+
+def filtered_forward(logits: torch.Tensor, labels: torch.Tensor | None, temperature=1.0, top_k=0,
+                     top_p=1.0, min_p=0.0, ignore_index: int = -100, *, out=None, workspace=None,
+                     dev_error=None):
+    """Policy statistics of `labels` under the distribution that ``sample``
+    draws from with the same settings (temperature > 0).
+
+    Returns (logprob [T] f32, -inf for a label outside the kept set; entropy
+    [T] f32; rowstats [T, 2] f32 (M, ln S of the kept set); cut_logit [T] f32;
+    cut_index [T] int64): column v is kept when its logit is above cut_logit,
+    or equal to it with v <= cut_index.
+    """
+    T, V, ld = _rows(logits)
+    dev = logits.device
+    dt = _dtype_code(logits)
+    lab = _labels(labels, T, dev)
+    f = _filters(temperature, top_k, top_p, min_p, T, dev)
+    lp, ent, rs, tau, index = _filtered_outputs(out, T, dev)
+    dev_error = _error_flag(dev_error, dev)
+    workspace = _workspace(workspace, filter_workspace_size(T, V, logits.dtype), dev)
+    _call(dev, "pstat_filtered_forward", _lib.pstat_filtered_forward,
+          _ptr(logits), dt, T, V, ld, _ptr(lab), int(ignore_index), ctypes.byref(f), _ptr(lp),
+          _ptr(ent), _ptr(rs), _ptr(tau), _ptr(index), _ptr(workspace), workspace.numel(),
+          _ptr(dev_error), _stream(dev))
+    return lp, ent, rs, tau, index
+
+
+def filtered_backward(logits: torch.Tensor, labels: torch.Tensor | None,
+                      weights: torch.Tensor | None, rowstats: torch.Tensor,
+                      cut_logit: torch.Tensor, cut_index: torch.Tensor, temperature=1.0,
+                      ignore_index: int = -100, out_dtype: torch.dtype | None = None, *, out=None,
+                      dev_error=None):
+    """dlogits = (w / temperature) (onehot(y) - p) with p the softmax over the
+    kept columns and 0 elsewhere, from the statistics of ``filtered_forward``
+    with the same settings; a zero row where the label is not kept."""
+    T, V, ld = _rows(logits)
+    dev = logits.device
+    dt = _dtype_code(logits)
+    lab = _labels(labels, T, dev)
+    out_dtype = out_dtype or logits.dtype
+    if out is None:
+        out = torch.empty(T, V, dtype=out_dtype, device=dev)
+    ld_out = _matrix_output(out, T, V, dev, "out")
+    w = _weights(weights, T, dev)
+    if rowstats is None:
+        raise ValueError("rowstats (from filtered_forward) is required")
+    rowstats = _rowstats(rowstats, T, dev)
+    tau = _tensor(cut_logit, torch.float32, (T,), dev, "cut_logit")
+    index = _tensor(cut_index, torch.int64, (T,), dev, "cut_index")
+    t, tt = _per_row(temperature, torch.float32, T, dev, "temperature")
+    dev_error = _error_flag(dev_error, dev)
+    _call(dev, "pstat_filtered_backward", _lib.pstat_filtered_backward,
+          _ptr(logits), dt, T, V, ld, _ptr(lab), int(ignore_index), _ptr(w), _ptr(rowstats),
+          _ptr(tau), _ptr(index), 1.0 if t is None else float(t), _ptr(tt), _ptr(out),
+          _dtype_code(out), ld_out, _ptr(dev_error), _stream(dev))
+    return out
+
+
+# ---- gradient norm and clipping ---------------------------------------------------
+
+_GRAD_CODES = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+def _grad_list(tensors, out, writes):
+    """(the outputs, the pstat_tensor array, the device) of a list of tensors
+    that must be contiguous, bf16 or fp32, on one CUDA device.  The array is
+    filled as 64-bit words (dtype is the low half of the fourth): a list of
+    hundreds of tensors is marshalled on every call, and a word costs less
+    than a ctypes field."""
+    tensors = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
+    if not tensors:
+        raise ValueError("tensors must not be empty")
+    index = tensors[0].get_device()
+    if index < 0:
+        raise ValueError("tensors must be CUDA tensors (no CPU path exists)")
+    dev = tensors[0].device
+    outs = tensors if out is None else [out] if isinstance(out, torch.Tensor) else list(out)
+    if len(outs) != len(tensors):
+        raise ValueError("out must have one tensor for each of tensors")
+    words = []
+    seen = set()
+    for x, o in zip(tensors, outs):
+        code = _GRAD_CODES.get(x.dtype)
+        if code is None:
+            raise TypeError(f"tensors must be bfloat16 or float32, got {x.dtype}")
+        if x.get_device() != index or not x.is_contiguous():
+            raise ValueError(f"tensors must be contiguous CUDA tensors on {dev}")
+        n, to = x.numel(), x.data_ptr()
+        words += (to, to, n, code)
+        if o is not x:
+            _tensor(o, x.dtype, x.shape, dev, "out")
+            to = words[-3] = o.data_ptr()
+        if writes and n:
+            if to in seen:
+                raise ValueError("a tensor may be written once only")
+            seen.add(to)
+    return outs, array.array("q", words), dev
+
+
+def _grad_call(words, workspace, dev):
+    """(address, count, workspace) of a marshalled list."""
+    at, n = words.buffer_info()[0], len(words) // 4
+    need = ctypes.c_size_t(0)
+    _check(_lib.pstat_grad_workspace_size(at, n, ctypes.byref(need)), "pstat_grad_workspace_size")
+    return at, n, _workspace(workspace, int(need.value), dev)
+
+
+def grad_norm(tensors, *, out=None, workspace=None, dev_error=None) -> torch.Tensor:
+    """The L2 norm over all elements of a list of gradients (bf16 or fp32, any
+    mix of sizes), as a float32 scalar tensor on their device."""
+    _, words, dev = _grad_list(tensors, None, False)
+    norm = (torch.empty((), dtype=torch.float32, device=dev) if out is None
+            else _tensor(out, torch.float32, (), dev, "out"))
+    dev_error = _error_flag(dev_error, dev)
+    at, n, workspace = _grad_call(words, workspace, dev)
+    _call(dev, "pstat_grad_norm", _lib.pstat_grad_norm,
+          at, n, _ptr(norm), _ptr(workspace), workspace.numel(), _ptr(dev_error), _stream(dev))
+    return norm
+
+
+def clip_grad_norm(tensors, max_norm: float, *, out=None, workspace=None, dev_error=None):
+    """Scales a list of gradients by min(1, max_norm / their global L2 norm),
+    in place or into the tensors of `out` (same shapes and dtypes).  Returns
+    (the norm before scaling, a float32 scalar tensor; the list of the scaled
+    tensors).  A norm that is not finite sets DEV_NONFINITE and scales nothing."""
+    outs, words, dev = _grad_list(tensors, out, True)
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    dev_error = _error_flag(dev_error, dev)
+    at, n, workspace = _grad_call(words, workspace, dev)
+    _call(dev, "pstat_clip_grad_norm", _lib.pstat_clip_grad_norm,
+          at, n, float(max_norm), _ptr(norm), _ptr(workspace), workspace.numel(),
+          _ptr(dev_error), _stream(dev))
+    return norm, outs
+
+
 def selftest_wait_timeout(device, limit_ns: int = 10_000_000) -> int:
     """Runs the library's bounded wait on a barrier that nothing arrives at
     (pstat_selftest_wait_timeout) and returns the device error bits it left:
@@ -717,3 +951,33 @@ class LmheadPolicyStats(torch.autograd.Function):
 def lmhead_policy_stats(hidden, W, labels, ignore_index: int = -100):
     """Differentiable (logprob, entropy) of hidden W^T through the fused lm_head."""
     return LmheadPolicyStats.apply(hidden, W, labels, ignore_index)
+
+
+class FilteredPolicyStats(torch.autograd.Function):
+    """logprob (differentiable) and entropy (a no-grad metric) of every row
+    under its tempered, truncated softmax; the kept set is held fixed."""
+
+    @staticmethod
+    def forward(ctx, logits, labels, temperature, top_k, top_p, min_p, ignore_index):
+        lp, ent, rs, tau, index = filtered_forward(logits, labels, temperature, top_k, top_p,
+                                                   min_p, ignore_index)
+        row_t = temperature if isinstance(temperature, torch.Tensor) else None
+        ctx.save_for_backward(logits, labels, rs, tau, index, row_t)
+        ctx.temperature = None if row_t is not None else temperature
+        ctx.ignore_index = ignore_index
+        ctx.mark_non_differentiable(ent)
+        return lp, ent
+
+    @staticmethod
+    def backward(ctx, grad_lp, grad_ent):
+        logits, labels, rs, tau, index, row_t = ctx.saved_tensors
+        g = filtered_backward(logits, labels, grad_lp.float().contiguous(), rs, tau, index,
+                              ctx.temperature if row_t is None else row_t, ctx.ignore_index)
+        return g, None, None, None, None, None, None
+
+
+def filtered_policy_stats(logits, labels, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
+                          ignore_index: int = -100):
+    """Differentiable (logprob, entropy) under the distribution of ``sample``."""
+    return FilteredPolicyStats.apply(logits, labels, temperature, top_k, top_p, min_p,
+                                     ignore_index)
