@@ -117,6 +117,7 @@ def test_filter_argument_checks(lib, call):
                 dict(temperature=2.0**-21), dict(top_p=0.0), dict(top_p=1.5), dict(top_p=math.nan),
                 dict(min_p=-0.1), dict(min_p=1.1), dict(min_p=math.nan)):
         assert call(lib, f=_f(**bad)) == -9, bad
+    assert call(lib, ws=0) == -6 and call(lib, ws_bytes=64) == -6 and call(lib, ws=0x5008) == -5
     for rows in ("temperatures", "top_ks", "top_ps", "min_ps"):
         assert call(lib, f=_f(**{rows: 0x6002})) == -5, rows
 

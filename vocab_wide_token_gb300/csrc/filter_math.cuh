@@ -19,6 +19,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "chunk_math.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -113,6 +114,176 @@ __device__ __forceinline__ float fixed_log(uint64_t S, int k) {
     const uint64_t one = 1ull << k;
     if (S < 2 * one) return log1pf((float)(S - one) * inv);
     return logf((float)S * inv);
+}
+
+// ---------------------------------------------------------------------------
+// fp32 statistics of one chunk (PSTAT_CHUNK_* columns, 16 vectors of 16 bytes
+// per lane), at the temperature's scale c = ch:
+//   m = max z,  m2 = RN(m c),  delta = m c - m2 (exact),
+//   a_i = RN(z_i c - m2),  s = sum 2^a_i,  u = sum 2^a_i a_i  (base 2),
+// the form of chunk_math.cuh with c for log2(e).  Moving a chunk to the row
+// maximum M multiplies by 2^((m - M) c - delta).  Where m c is so large that
+// delta could weigh in the exponent, a_i = (z_i - m) c and delta = 0.
+// -inf logits give 2^-inf = 0; only u needs them kept out (0 times -inf), so a
+// chunk whose u comes out NaN is summed again with a_i held above -1024.
+// A NaN or +inf logit makes the record's m NaN.
+// ---------------------------------------------------------------------------
+struct ChunkRecord {
+    float m, s, u, delta;
+};
+
+__device__ __forceinline__ uint32_t bf2_max_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float warp_max_nan(float m) {
+    float r;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(m));
+    return r;
+}
+
+// Maximum of one lane's vectors: the maximum of its group of columns.
+__device__ __forceinline__ float lane_max(const uint4 (&q)[kVecPerLane], uint16_t*) {
+    uint32_t a0 = q[0].x, a1 = q[0].y, a2 = q[0].z, a3 = q[0].w;
+#pragma unroll
+    for (int j = 1; j < kVecPerLane; ++j) {
+        a0 = bf2_max_nan(a0, q[j].x);
+        a1 = bf2_max_nan(a1, q[j].y);
+        a2 = bf2_max_nan(a2, q[j].z);
+        a3 = bf2_max_nan(a3, q[j].w);
+    }
+    const uint32_t a = bf2_max_nan(bf2_max_nan(a0, a1), bf2_max_nan(a2, a3));
+    return max_nan(bf2_lo(a), bf2_hi(a));
+}
+__device__ __forceinline__ float lane_max(const uint4 (&q)[kVecPerLane], float*) {
+    float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kVecPerLane; ++j) {
+        a0 = max_nan(a0, max_nan(__uint_as_float(q[j].x), __uint_as_float(q[j].y)));
+        a1 = max_nan(a1, max_nan(__uint_as_float(q[j].z), __uint_as_float(q[j].w)));
+    }
+    return max_nan(a0, a1);
+}
+
+// Pairs of floats of one 16-byte vector.
+__device__ __forceinline__ void vector_pairs(const uint4& q, uint64_t (&p)[4], uint16_t*) {
+    p[0] = f2_pack(bf2_lo(q.x), bf2_hi(q.x));
+    p[1] = f2_pack(bf2_lo(q.y), bf2_hi(q.y));
+    p[2] = f2_pack(bf2_lo(q.z), bf2_hi(q.z));
+    p[3] = f2_pack(bf2_lo(q.w), bf2_hi(q.w));
+}
+__device__ __forceinline__ void vector_pairs(const uint4& q, uint64_t (&p)[2], float*) {
+    p[0] = f2_pack(__uint_as_float(q.x), __uint_as_float(q.y));
+    p[1] = f2_pack(__uint_as_float(q.z), __uint_as_float(q.w));
+}
+
+// kDirect: a = (z - m) c; else a = z c - m2.  kFloor: a >= -1024.
+template <typename E, bool kU, bool kDirect, bool kFloor>
+__device__ __forceinline__ void chunk_sums(const uint4 (&q)[kVecPerLane], float m, float c,
+                                           float m2, float& s_out, float& u_out) {
+    constexpr int kPairs = 8 / sizeof(E);
+    const uint64_t cc = f2_pack(c, c), nm2 = f2_pack(-m2, -m2), nm = f2_pack(-m, -m);
+    uint64_t s[kPairs], u[kPairs];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) s[i] = u[i] = 0;
+#pragma unroll
+    for (int j = 0; j < kVecPerLane; ++j) {
+        uint64_t z[kPairs];
+        vector_pairs(q[j], z, (E*)nullptr);
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            uint64_t a = kDirect ? f2_mul(f2_add(z[i], nm), cc) : f2_fma(z[i], cc, nm2);
+            float a0, a1;
+            f2_unpack(a, a0, a1);
+            if (kFloor) {
+                a0 = fmaxf(a0, -1024.f);
+                a1 = fmaxf(a1, -1024.f);
+                a = f2_pack(a0, a1);
+            }
+            const uint64_t e = f2_pack(ex2_approx(a0), ex2_approx(a1));
+            s[i] = f2_add(s[i], e);
+            if (kU) u[i] = f2_fma(e, a, u[i]);
+        }
+    }
+    float st[kPairs], ut[kPairs];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        st[i] = hsum2(s[i]);
+        ut[i] = hsum2(u[i]);
+    }
+#pragma unroll
+    for (int w = kPairs / 2; w; w >>= 1)
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+            st[i] += st[i + w];
+            ut[i] += ut[i + w];
+        }
+    float ss = st[0], uu = ut[0];
+#pragma unroll
+    for (int off = 16; off; off >>= 1) {
+        ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
+        if (kU) uu += __shfl_xor_sync(0xFFFFFFFFu, uu, off);
+    }
+    s_out = ss;
+    u_out = kU ? uu : 0.f;
+}
+
+template <typename E, bool kU>
+__device__ __forceinline__ ChunkRecord chunk_record(const uint4 (&q)[kVecPerLane], float lane_m,
+                                                    float c) {
+    const float m = warp_max_nan(lane_m);
+    if (m == -INFINITY) return {m, 0.f, 0.f, 0.f};
+    if (!(m < INFINITY)) return {NAN, 0.f, 0.f, 0.f};
+    const float m2 = __fmul_rn(m, c);
+    const float delta = fmaf(m, c, -m2);
+    ChunkRecord r = {m, 0.f, 0.f, delta};
+    if (fabsf(delta) <= 4.f) {  // false where m c overflows
+        chunk_sums<E, kU, false, false>(q, m, c, m2, r.s, r.u);
+        if (kU && r.u != r.u) chunk_sums<E, kU, false, true>(q, m, c, m2, r.s, r.u);
+    } else {
+        chunk_sums<E, kU, true, kU>(q, m, c, m2, r.s, r.u);
+        r.delta = 0.f;
+    }
+    return r;
+}
+
+// Relative error of a sum of those records, and of its parts, against the
+// exact sum: in units of 2^-24, ex2 4, the rounding of a (|a| + 4) ln 2 with a
+// mass-weighted mean |a| of at most log2 V = 20, that of c half as much, 17
+// for a lane's sums, 3 for its tree, 5 for the lanes, and 12 for the move to M
+// and the fold: below 64, so 2^-18.  Measured errors are two orders smaller.
+constexpr float kSumError = 1.f / 262144.f;
+
+// The row's (M, S, U base 2) from its records, by one warp, every lane alike;
+// NaN M where a record is bad, -inf where every logit is masked.
+__device__ __forceinline__ float3 fold_records(const float4* __restrict__ rec, int n, float c,
+                                               int lane) {
+    float M = -INFINITY;
+    for (int i = lane; i < n; i += 32) M = max_nan(M, rec[i].x);
+    M = warp_max_nan(M);
+    float S = 0.f, U = 0.f;
+    if (M > -INFINITY) {
+        for (int i = lane; i < n; i += 32) {
+            const float4 r = rec[i];
+            if (r.x == -INFINITY) continue;
+            const float a = fmaf(r.x - M, c, -r.w);
+            const float f = exp2f(a);
+            S = fmaf(r.y, f, S);
+            U = fmaf(f, fmaf(fmaxf(a, -1024.f), r.y, r.z), U);
+        }
+#pragma unroll
+        for (int off = 16; off; off >>= 1) {
+            S += __shfl_xor_sync(0xFFFFFFFFu, S, off);
+            U += __shfl_xor_sync(0xFFFFFFFFu, U, off);
+        }
+    }
+    return make_float3(M, S, U);
 }
 
 }  // namespace pstat
