@@ -36,33 +36,50 @@ __device__ __forceinline__ float elem(const void* p, int64_t i, bool bf16) {
                 : static_cast<const float*>(p)[i];
 }
 
-// Sum of squares of up to 8 floats, as a double.  In fp32 it is used where no
-// square can have overflowed or lost its low bits (the sum is in [2^-60, 2^120];
-// then squares below 2^-126 are below 2^-66 of it); elsewhere in fp64.
+// Sum of squares of N floats, as a double.  In fp32 it is used where no square
+// can have overflowed or lost its low bits (the sum is in [2^-60, 2^120]; then
+// squares below 2^-126 are below 2^-66 of it); elsewhere in fp64.  One fp64
+// conversion and addition per N elements: fp64 runs at 2 operations per clock
+// and SM here, so one per 16-byte vector alone took 0.64 ms for 2.76 GB.
 template <int N>
 __device__ __forceinline__ double squares(const float (&x)[N]) {
-    float s = 0.f, any = 0.f;
+    float s[N < 4 ? N : 4];
+    constexpr int kParts = N < 4 ? N : 4;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        s = fmaf(x[i], x[i], s);
-        any = fmaxf(any, fabsf(x[i]));
-    }
-    if (s > 8.6736174e-19f && s < 1.3292280e36f) return (double)s;
-    if (s == 0.f && any == 0.f) return 0.0;
+    for (int i = 0; i < kParts; ++i) s[i] = x[i] * x[i];
+#pragma unroll
+    for (int i = kParts; i < N; ++i) s[i % kParts] = fmaf(x[i], x[i], s[i % kParts]);
+    float sum = s[0];
+#pragma unroll
+    for (int i = 1; i < kParts; ++i) sum += s[i];
+    if (sum > 8.6736174e-19f && sum < 1.3292280e36f) return (double)sum;
     double d = 0.0;
+    bool any = false;
 #pragma unroll
-    for (int i = 0; i < N; ++i) d = fma((double)x[i], (double)x[i], d);
+    for (int i = 0; i < N; ++i) any |= x[i] != 0.f;  // true for NaN
+    if (any)
+#pragma unroll 1
+        for (int i = 0; i < N; ++i) d = fma((double)x[i], (double)x[i], d);
     return d;
 }
 
-__device__ __forceinline__ double vector_squares(const uint4& q, bool bf16) {
-    if (bf16) {
-        const float x[8] = {bf2_lo(q.x), bf2_hi(q.x), bf2_lo(q.y), bf2_hi(q.y),
-                            bf2_lo(q.z), bf2_hi(q.z), bf2_lo(q.w), bf2_hi(q.w)};
-        return squares(x);
+template <bool kBf16>
+__device__ __forceinline__ double vectors_squares(const uint4 (&q)[kGnUnroll]) {
+    constexpr int kPer = kBf16 ? 8 : 4;
+    float x[kGnUnroll * kPer];
+#pragma unroll
+    for (int j = 0; j < kGnUnroll; ++j) {
+        const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (kBf16) {
+                x[j * kPer + 2 * i] = bf2_lo(w[i]);
+                x[j * kPer + 2 * i + 1] = bf2_hi(w[i]);
+            } else {
+                x[j * kPer + i] = __uint_as_float(w[i]);
+            }
+        }
     }
-    const float x[4] = {__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z),
-                        __uint_as_float(q.w)};
     return squares(x);
 }
 
@@ -104,8 +121,7 @@ __global__ void __launch_bounds__(kGnThreads)
                 const int k = j * kGnThreads + (int)threadIdx.x;
                 q[j] = k < nv ? __ldg(v + k) : make_uint4(0, 0, 0, 0);
             }
-#pragma unroll
-            for (int j = 0; j < kGnUnroll; ++j) sum += vector_squares(q[j], bf16);
+            sum += bf16 ? vectors_squares<true>(q) : vectors_squares<false>(q);
             done = e0 + (int64_t)nv * vec;
         }
         for (int64_t k = done + threadIdx.x; k < e1; k += kGnThreads) {

@@ -1266,7 +1266,12 @@ cudaError_t launch_filter(const FilterArgs& a, const DeviceInfo& dev, cudaStream
 }
 
 // ---------------------------------------------------------------------------
-// Gradient: dz_v = (w/t)(1[v = y] - kept_v e_v/S), elementwise.
+// Gradient: dz_v = (w/t)(1[v = y] - kept_v e_v/S), elementwise, one read and
+// one write of a row: bound by HBM.  Each thread keeps kU 8-column groups in
+// flight as raw 16-byte vectors.  A group without a logit of at least tau (all
+// but a few, once a filter cuts) is written as zeros without an exponential.
+// A row whose start is not on 16 bytes is taken from its first column that is,
+// when input and output agree on which that is, and column by column else.
 // ---------------------------------------------------------------------------
 constexpr int kFgThreads = 256;
 
@@ -1282,7 +1287,6 @@ __global__ void __launch_bounds__(kFgThreads)
                              int64_t ld_out, int segs, int* __restrict__ dev_error) {
     const int64_t t = blockIdx.x / segs;
     const int seg = (int)(blockIdx.x - t * segs);
-    const int64_t c0 = V * seg / segs, c1 = V * (seg + 1) / segs;
     const Ein* zin = logits + t * ld;
     Eout* zout = out + t * ld_out;
     const int64_t y = labels ? labels[t] : ignore_index;
@@ -1307,23 +1311,90 @@ __global__ void __launch_bounds__(kFgThreads)
         // a masked label is never kept, not even where nothing is filtered
         if (!(zy > -INFINITY && (zy > tau || (zy == tau && y <= last)))) mode = 0;
     }
-    float c = 0.f, off = 0.f, g = 0.f;
+    const float M = rs.x;
+    float c = 0.f, K = 0.f, g = 0.f;
     if (mode == 2) {
         c = kLog2e / temp;
-        off = rs.y * kLog2e;
+        K = exp2f(-rs.y * kLog2e);  // 1 / S
         g = w / temp;
     }
-    const float fill = mode == 0 ? 0.f : NAN;
-    for (int64_t col = c0 + threadIdx.x; col < c1; col += kFgThreads) {
-        float v = fill;
-        if (mode == 2) {
-            const float z = Elem<Ein>::to_float(zin[col]);
-            const bool kept = z > tau || (z == tau && col <= last);
-            const float p = kept ? exp2f(fmaf(z - rs.x, c, -off)) : 0.f;
-            v = col == y ? g * (1.f - p) : -(g * p);
-            if (!kept) v = 0.f;
+    const float ngK = -g * K;
+    const float fill = mode == 1 ? NAN : 0.f;
+    // Column y is kept, so its gradient is g (1 - p_y).
+    auto gradient = [&](float z, int64_t col) {
+        const float e = ex2_approx((z - M) * c);
+        const bool kept = z > tau || (z == tau && col <= last);
+        return col == y ? fmaf(-g, e * K, g) : kept ? e * ngK : 0.f;
+    };
+    auto scalar = [&](int64_t c0, int64_t c1) {
+        for (int64_t col = c0 + threadIdx.x; col < c1; col += kFgThreads)
+            zout[col] = out_cast(mode == 2 ? gradient(Elem<Ein>::to_float(zin[col]), col) : fill, zout);
+    };
+
+    // Columns before the first 16-byte boundary of both rows, -1 if there is none.
+    const int in_off = (int)((reinterpret_cast<uintptr_t>(zin) & 15u) / sizeof(Ein));
+    const int out_off = (int)((reinterpret_cast<uintptr_t>(zout) & 15u) / sizeof(Eout));
+    int head = -1;
+    for (int h = 0; h < 8; ++h)
+        if (((in_off + h) * sizeof(Ein)) % 16 == 0 && ((out_off + h) * sizeof(Eout)) % 16 == 0) {
+            head = h;
+            break;
         }
-        zout[col] = out_cast(v, zout);
+    if (head < 0 || head > V) return scalar(V * seg / segs, V * (seg + 1) / segs);
+    const int64_t groups = (V - head) >> 3;
+    const int64_t g0 = groups * seg / segs, g1 = groups * (seg + 1) / segs;
+    if (seg == 0) scalar(0, head);
+    if (seg == segs - 1) scalar(head + (groups << 3), V);
+    const Ein* vin = zin + head;
+    Eout* vout = zout + head;
+
+    constexpr int kVecs = (int)sizeof(Ein) / 2;  // 16-byte vectors per group
+    constexpr int kU = kVecs == 1 ? 6 : 4;
+    for (int64_t base = g0; base < g1; base += (int64_t)kFgThreads * kU) {
+        uint4 raw[kU][kVecs];
+#pragma unroll
+        for (int k = 0; k < kU; ++k) {
+            const int64_t i = base + k * kFgThreads + threadIdx.x;
+            if (i < g1 && mode == 2) {
+                const uint4* src = reinterpret_cast<const uint4*>(vin + (i << 3));
+#pragma unroll
+                for (int h = 0; h < kVecs; ++h) raw[k][h] = __ldcs(src + h);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kU; ++k) {
+            const int64_t i = base + k * kFgThreads + threadIdx.x;
+            if (i >= g1) continue;
+            float o[8];
+            bool any = false;
+            float x[8];
+            if (mode == 2) {
+                constexpr int kPer = 8 / kVecs;
+#pragma unroll
+                for (int h = 0; h < kVecs; ++h) {
+                    float part[kPer];
+                    RowReader<Ein>::unpack(raw[k][h], part);
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) x[h * kPer + e] = part[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) any |= x[e] >= tau;
+            }
+            if (any) {
+                const int64_t col = head + (i << 3);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = ex2_approx((x[e] - M) * c) * ngK;
+                // the few groups that the cut or the label falls into
+                if (tau > -INFINITY || (y >= col && y < col + 8)) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = gradient(x[e], col + e);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = fill;
+            }
+            Store8<Eout>::run(vout + (i << 3), o);
+        }
     }
 }
 
