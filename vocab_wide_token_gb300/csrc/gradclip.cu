@@ -12,9 +12,9 @@ namespace pstat {
 namespace {
 
 constexpr int kGnThreads = 256;
-constexpr int kGnUnroll = 4;                // 16-byte vectors in flight per thread
-constexpr int64_t kUnitBytes = (int64_t)kGnThreads * kGnUnroll * 16;  // 16 KiB of one tensor
-constexpr int kMaxBlocks = 1024;            // partial sums
+constexpr int kGnUnroll = 8;                // 16-byte vectors in flight per thread
+constexpr int64_t kUnitBytes = (int64_t)kGnThreads * kGnUnroll * 16;  // 32 KiB of one tensor
+constexpr int kMaxBlocks = 2048;            // partial sums
 constexpr int kBatch = 800;                 // tensors of one launch (they travel as its arguments)
 
 struct GradTensor {
@@ -36,51 +36,63 @@ __device__ __forceinline__ float elem(const void* p, int64_t i, bool bf16) {
                 : static_cast<const float*>(p)[i];
 }
 
-// Sum of squares of N floats, as a double.  In fp32 it is used where no square
-// can have overflowed or lost its low bits (the sum is in [2^-60, 2^120]; then
-// squares below 2^-126 are below 2^-66 of it); elsewhere in fp64.  One fp64
-// conversion and addition per N elements: fp64 runs at 2 operations per clock
-// and SM here, so one per 16-byte vector alone took 0.64 ms for 2.76 GB.
-template <int N>
-__device__ __forceinline__ double squares(const float (&x)[N]) {
-    float s[N < 4 ? N : 4];
-    constexpr int kParts = N < 4 ? N : 4;
-#pragma unroll
-    for (int i = 0; i < kParts; ++i) s[i] = x[i] * x[i];
-#pragma unroll
-    for (int i = kParts; i < N; ++i) s[i % kParts] = fmaf(x[i], x[i], s[i % kParts]);
-    float sum = s[0];
-#pragma unroll
-    for (int i = 1; i < kParts; ++i) sum += s[i];
-    if (sum > 8.6736174e-19f && sum < 1.3292280e36f) return (double)sum;
+// Whether an fp32 sum of squares stands: none of them can have overflowed or
+// lost its low bits (squares below 2^-126 are below 2^-66 of a sum of 2^-60).
+__device__ __forceinline__ bool in_range(float s) { return s > 8.6736174e-19f && s < 1.3292280e36f; }
+
+// The same elements in fp64: vectors `k`, `k + kGnThreads`, ... of `v` below
+// `nv`.  Rare, so the vectors are loaded again rather than kept.
+template <bool kBf16>
+__device__ __noinline__ double wide_squares(const uint4* v, int k, int nv) {
     double d = 0.0;
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < N; ++i) any |= x[i] != 0.f;  // true for NaN
-    if (any)
-#pragma unroll 1
-        for (int i = 0; i < N; ++i) d = fma((double)x[i], (double)x[i], d);
+    for (int j = 0; j < kGnUnroll && k < nv; ++j, k += kGnThreads) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(v + k);
+        for (int i = 0; i < 4; ++i) {
+            const double lo = kBf16 ? bf2_lo(w[i]) : __uint_as_float(w[i]);
+            const double hi = kBf16 ? bf2_hi(w[i]) : 0.f;
+            d = fma(lo, lo, fma(hi, hi, d));
+        }
+    }
     return d;
 }
 
+// Sum of the squares of one thread's vectors of a unit.  In fp32, with one fp64
+// addition for all of them: fp64 runs at about two operations per clock and SM.
 template <bool kBf16>
-__device__ __forceinline__ double vectors_squares(const uint4 (&q)[kGnUnroll]) {
-    constexpr int kPer = kBf16 ? 8 : 4;
-    float x[kGnUnroll * kPer];
+__device__ __forceinline__ double unit_squares(const uint4* __restrict__ v, int nv) {
+    uint4 q[kGnUnroll];
 #pragma unroll
     for (int j = 0; j < kGnUnroll; ++j) {
-        const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+        const int k = j * kGnThreads + (int)threadIdx.x;
+        q[j] = k < nv ? __ldg(v + k) : make_uint4(0, 0, 0, 0);
+    }
+    uint64_t s0 = 0, s1 = 0;
+    uint32_t any = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (kBf16) {
-                x[j * kPer + 2 * i] = bf2_lo(w[i]);
-                x[j * kPer + 2 * i + 1] = bf2_hi(w[i]);
-            } else {
-                x[j * kPer + i] = __uint_as_float(w[i]);
-            }
+    for (int j = 0; j < kGnUnroll; ++j) {
+        any |= q[j].x | q[j].y | q[j].z | q[j].w;
+        if (kBf16) {
+            const uint64_t a = f2_pack(bf2_lo(q[j].x), bf2_hi(q[j].x));
+            const uint64_t b = f2_pack(bf2_lo(q[j].y), bf2_hi(q[j].y));
+            const uint64_t c = f2_pack(bf2_lo(q[j].z), bf2_hi(q[j].z));
+            const uint64_t d = f2_pack(bf2_lo(q[j].w), bf2_hi(q[j].w));
+            s0 = f2_fma(a, a, s0);
+            s1 = f2_fma(b, b, s1);
+            s0 = f2_fma(c, c, s0);
+            s1 = f2_fma(d, d, s1);
+        } else {
+            const uint64_t a = f2_pack(__uint_as_float(q[j].x), __uint_as_float(q[j].y));
+            const uint64_t b = f2_pack(__uint_as_float(q[j].z), __uint_as_float(q[j].w));
+            s0 = f2_fma(a, a, s0);
+            s1 = f2_fma(b, b, s1);
         }
     }
-    return squares(x);
+    float x, y;
+    f2_unpack(f2_add(s0, s1), x, y);
+    const float s = x + y;
+    if (in_range(s)) return (double)s;
+    if (any == 0) return 0.0;
+    return wide_squares<kBf16>(v, (int)threadIdx.x, nv);
 }
 
 // Fixed-order sum of one double per thread; the result is valid in thread 0.
@@ -97,7 +109,7 @@ __device__ __forceinline__ double block_sum(double v) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(kGnThreads)
+__global__ void __launch_bounds__(kGnThreads, 6)
     square_sums_kernel(const __grid_constant__ GradBatch<N> g, double* __restrict__ partial) {
     const uint32_t u0 = (uint32_t)((uint64_t)g.units * blockIdx.x / gridDim.x);
     const uint32_t u1 = (uint32_t)((uint64_t)g.units * (blockIdx.x + 1) / gridDim.x);
@@ -115,18 +127,12 @@ __global__ void __launch_bounds__(kGnThreads)
         if ((reinterpret_cast<uintptr_t>(t.in) & 15u) == 0) {
             const int nv = (int)((e1 - e0) / vec);
             const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(t.in) + e0 * (bf16 ? 2 : 4));
-            uint4 q[kGnUnroll];
-#pragma unroll
-            for (int j = 0; j < kGnUnroll; ++j) {
-                const int k = j * kGnThreads + (int)threadIdx.x;
-                q[j] = k < nv ? __ldg(v + k) : make_uint4(0, 0, 0, 0);
-            }
-            sum += bf16 ? vectors_squares<true>(q) : vectors_squares<false>(q);
+            sum += bf16 ? unit_squares<true>(v, nv) : unit_squares<false>(v, nv);
             done = e0 + (int64_t)nv * vec;
         }
         for (int64_t k = done + threadIdx.x; k < e1; k += kGnThreads) {
-            const float x[1] = {elem(t.in, k, bf16)};
-            sum += squares(x);
+            const double x = elem(t.in, k, bf16);
+            sum = fma(x, x, sum);
         }
     }
     sum = block_sum(sum);
@@ -259,7 +265,7 @@ int64_t fill(GradBatch<N>& g, const pstat_tensor* tensors, int64_t i, int64_t n)
 }
 
 int blocks_for(uint32_t units, const DeviceInfo& dev) {
-    const uint32_t most = (uint32_t)(dev.sm_count * 4 < kMaxBlocks ? dev.sm_count * 4 : kMaxBlocks);
+    const uint32_t most = (uint32_t)(dev.sm_count * 6 < kMaxBlocks ? dev.sm_count * 6 : kMaxBlocks);
     return (int)(units < most ? units : most);
 }
 
