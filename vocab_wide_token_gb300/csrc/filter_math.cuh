@@ -30,8 +30,39 @@ constexpr float kFilterTempMin = 1.f / 1048576.f;  // 2^-20
 constexpr float kFilterTempMax = 1048576.f;        // 2^20
 
 // 2^(-j/64), j = 0..63, each as an unevaluated sum of two floats.
-struct ExpTable {
-    float2 v[64];
+__device__ const float2 kExp2Table[64] = {
+    {0x1p+0f, 0x0p+0f}, {0x1.fa7c18p-1f, 0x1.9e90d8p-29f},
+    {0x1.f50766p-1f, -0x1.246ebp-27f}, {0x1.efa1bep-1f, 0x1.cc2b44p-26f},
+    {0x1.ea4afap-1f, 0x1.52486cp-28f}, {0x1.e502eep-1f, 0x1.e2cffep-27f},
+    {0x1.dfc974p-1f, -0x1.908c94p-26f}, {0x1.da9e6p-1f, 0x1.ed9942p-28f},
+    {0x1.d5818ep-1f, -0x1.822dbcp-28f}, {0x1.d072d4p-1f, 0x1.40f13p-26f},
+    {0x1.cb720ep-1f, -0x1.8837ccp-28f}, {0x1.c67f12p-1f, 0x1.cafa2ap-26f},
+    {0x1.c199bep-1f, -0x1.3d56b2p-28f}, {0x1.bcc1eap-1f, -0x1.f687c6p-26f},
+    {0x1.b7f77p-1f, -0x1.a09438p-26f}, {0x1.b33a2cp-1f, -0x1.ec3a82p-27f},
+    {0x1.ae89fap-1f, -0x1.a94b14p-27f}, {0x1.a9e6b6p-1f, -0x1.50c048p-26f},
+    {0x1.a5503cp-1f, -0x1.b83b54p-26f}, {0x1.a0c668p-1f, -0x1.2886a6p-27f},
+    {0x1.9c4918p-1f, 0x1.51f848p-28f}, {0x1.97d82ap-1f, -0x1.0d8d84p-32f},
+    {0x1.93737cp-1f, -0x1.e64744p-26f}, {0x1.8f1aeap-1f, -0x1.baa232p-27f},
+    {0x1.8ace54p-1f, 0x1.15506ep-28f}, {0x1.868d9ap-1f, -0x1.2edb44p-27f},
+    {0x1.82589ap-1f, -0x1.accc7cp-27f}, {0x1.7e2f34p-1f, -0x1.261634p-26f},
+    {0x1.7a1148p-1f, -0x1.829fdp-26f}, {0x1.75feb6p-1f, -0x1.37b306p-26f},
+    {0x1.71f75ep-1f, 0x1.1d8beep-26f}, {0x1.6dfb24p-1f, -0x1.cd72e8p-28f},
+    {0x1.6a09e6p-1f, 0x1.9fcef4p-27f}, {0x1.662388p-1f, 0x1.2a9112p-28f},
+    {0x1.6247ecp-1f, -0x1.f8b55p-26f}, {0x1.5e76f2p-1f, -0x1.4a5bd6p-26f},
+    {0x1.5ab07ep-1f, -0x1.5bd5ecp-28f}, {0x1.56f474p-1f, -0x1.295b04p-26f},
+    {0x1.5342b6p-1f, -0x1.2c561p-26f}, {0x1.4f9b28p-1f, -0x1.2c5a6cp-26f},
+    {0x1.4bfdaep-1f, -0x1.593abcp-26f}, {0x1.486a2cp-1f, -0x1.47d866p-26f},
+    {0x1.44e086p-1f, 0x1.8624b4p-31f}, {0x1.4160a2p-1f, 0x1.f72e2ap-29f},
+    {0x1.3dea64p-1f, 0x1.824684p-26f}, {0x1.3a7db4p-1f, -0x1.634c02p-26f},
+    {0x1.371a74p-1f, -0x1.18aac6p-26f}, {0x1.33c08cp-1f, -0x1.b37d2p-26f},
+    {0x1.306fep-1f, 0x1.4636e2p-26f}, {0x1.2d285ap-1f, 0x1.b900c2p-27f},
+    {0x1.29e9ep-1f, -0x1.5c0424p-26f}, {0x1.26b456p-1f, 0x1.789f38p-27f},
+    {0x1.2387a6p-1f, 0x1.ceac48p-26f}, {0x1.2063b8p-1f, 0x1.0c519ap-26f},
+    {0x1.1d4874p-1f, -0x1.d2e8cap-26f}, {0x1.1a35bep-1f, 0x1.6df96ep-26f},
+    {0x1.172b84p-1f, -0x1.c15742p-28f}, {0x1.1429aap-1f, 0x1.d525bcp-26f},
+    {0x1.11301ep-1f, -0x1.fdb496p-26f}, {0x1.0e3ec4p-1f, -0x1.a585ccp-26f},
+    {0x1.0b5586p-1f, 0x1.9f3122p-26f}, {0x1.087452p-1f, -0x1.e2990ep-27f},
+    {0x1.059b0ep-1f, -0x1.9d4f52p-26f}, {0x1.02c9a4p-1f, -0x1.887fap-29f},
 };
 
 // Order-preserving map: a smaller key is a larger logit.  -0 and +0 are one
@@ -60,17 +91,19 @@ __device__ __forceinline__ TempScale temp_scale(float t) {
     return s;
 }
 
-// round(2^k e^((z - M)/t)) to about 2^-46 relative, 0 where e^((z-M)/t) is
-// below 2^-63.  With y = (M - z) log2(e)/t in double-float arithmetic, write
+// round(2^k e^((z - M)/t)) to about 2^-46 relative, k <= 60; 0 where that is
+// far below 1.  With y = (M - z) log2(e)/t in double-float arithmetic, write
 // y = j/64 + r, |r| <= 2^-7 (plus the low part); then 2^-y = 2^-(j/64) 2^-r:
 // the first factor from the table and a power of two, the second from
 // e^-s = 1 - s + s^2/2 - s^3/6 + s^4/24 - s^5/120, s = r ln 2 <= 2^-7.5,
 // whose next term s^6/720 is below 2^-54.  The first two terms are carried in
 // double-float, the others (below 2^-24) in fp32.  z = M gives 2^k exactly.
+// (A table-driven exponential, as in Tang, ACM TOMS 15, 1989.)
 __device__ __forceinline__ uint64_t fixed_weight(float z, float M, TempScale c, int k,
                                                  const float2* __restrict__ table) {
-    const float dh = M - z;
-    if (!(dh * c.ch < 63.f)) return 0;
+    const float d = M - z;
+    const bool far = !(d * c.ch < (float)(k + 2));
+    const float dh = far ? 0.f : d;  // no branch: callers weigh several at once
     const float bb = dh - M;
     const float dl = (M - (dh - bb)) - (z + bb);  // exact remainder of M - z
     // (rounding intrinsics where a product's own rounding error is used: the
@@ -96,8 +129,14 @@ __device__ __forceinline__ uint64_t fixed_weight(float z, float M, TempScale c, 
     const float pl = fmaf(tb.x, ah, -ph) + fmaf(tb.x, al, tb.y * ah);
     const float eh = tb.x + ph;
     const float el = (ph - (eh - tb.x)) + (tb.y + pl);
-    const float scale = __int_as_float((127 + k - (j >> 6)) << 23);
-    return (uint64_t)(__float2ll_rn(eh * scale) + __float2ll_rn(el * scale));
+    // (eh + el) 2^54 as an integer, eh >= 1/2 being a multiple of 2^-24 and el
+    // below 2^-24, then rounded to k - n digits: conversions to 64-bit integers
+    // run at a sixteenth of the rate of 32-bit ones.
+    const int64_t m = ((int64_t)__float2int_rn(eh * 16777216.f) << 30) +
+                      __float2int_rn(el * 18014398509481984.f);
+    const int drop = 60 - k + (j >> 6);  // in [0, 62]
+    const uint64_t w = (((uint64_t)m << 6) + ((1ull << drop) >> 1)) >> drop;
+    return far ? 0 : w;
 }
 
 // Binary digits after the point of the fixed weights of a row whose sum is

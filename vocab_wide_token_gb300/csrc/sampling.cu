@@ -31,9 +31,11 @@ constexpr int kExThreads = 512;
 constexpr int kExWarps = kExThreads / 32;
 constexpr int kBins = 2048;    // bins of one histogram level
 constexpr int kCand = 2048;    // elements that are sorted at once
-constexpr int kSpan = 4096;    // columns of one span of the index-order scan
+constexpr int kSpan = 1024;    // columns of one span of the index-order scan
 constexpr int kMaxSpans = (int)(kFilterMaxV / kSpan);
-static_assert(kBins % kExThreads == 0 && kCand % kExThreads == 0 && kSpan % kExThreads == 0, "");
+static_assert(kBins % kExThreads == 0 && kCand % kExThreads == 0 && kSpan % kExThreads == 0 &&
+                  kMaxSpans <= 2 * kExThreads && kMaxSpans <= kBins,
+              "");
 
 struct FilterArgs {
     const void* logits;
@@ -60,7 +62,6 @@ struct FilterArgs {
     void* group_max;            // [T, chunks, 32], the logits' type
     int* left_count;            // rows that the finish kernel leaves to the exact one
     int* left;                  // [T]
-    ExpTable table;
 };
 
 // One row's settings.
@@ -269,35 +270,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
 }
 
-// What one element selection found: the element (key, index), its rank in the
-// order (1-based) and the mass up to and including it.
-struct Selection {
-    uint32_t key, index;
-    uint32_t rank;
-    uint64_t mass;
-};
-
 struct Histogram {
     uint32_t count[kBins];
     unsigned long long mass[kBins];
-};
-
-struct ExactShared {
-    Histogram level0, level1;
-    unsigned long long cand[kCand];
-    unsigned long long span_mass[kMaxSpans];
-    float span_u[kMaxSpans];
-    float2 table[64];
-    unsigned long long scratch[2 * kExWarps];
-    // Team results, in the first CTA of a cluster.
-    uint32_t n_min;
-    uint32_t n_cand;
-    uint32_t first;
-    uint32_t first_kept;
-    // Decisions that the first CTA announces.
-    uint32_t klo, khi, n_in, count_before;
-    uint64_t mass_before;
-    Selection sel;
 };
 
 template <typename E>
@@ -325,25 +300,33 @@ struct RowReader<float> {
     }
 };
 
-// Calls f(column, logit) for every column of a row, shared out over `n`
-// threads of which this is thread `i`: whole 16-byte vectors between a head
-// and a tail that are read one by one.
-template <typename E, typename F>
-__device__ __forceinline__ void for_each_logit(const E* row, int V, int i, int n, F f) {
-    constexpr int kVec = RowReader<E>::kVec;
-    const int skew = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(E));
-    const int head = min(V, skew ? kVec - skew : 0);
-    const int nv = (V - head) / kVec;
-    const int tail = head + nv * kVec;
-    if (i < head) f(i, Elem<E>::to_float(row[i]));
-    const uint4* v = reinterpret_cast<const uint4*>(row + head);
-    for (int j = i; j < nv; j += n) {
-        float x[kVec];
-        RowReader<E>::unpack(__ldg(v + j), x);
+// Reads N times kVec columns from col[h] (multiples of kVec) of a row, all loads
+// before the first use; columns past V read as -inf.
+template <typename E, int N>
+__device__ __forceinline__ void load_columns(const E* row, const int (&col)[N], int V,
+                                             float (&x)[N][Elem<E>::kVec]) {
+    constexpr int kVec = Elem<E>::kVec;
+    if ((reinterpret_cast<uintptr_t>(row) & 15u) == 0) {
+        uint4 q[N];
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) f(head + j * kVec + e, x[e]);
+        for (int h = 0; h < N; ++h)
+            q[h] = col[h] + kVec <= V ? __ldg(reinterpret_cast<const uint4*>(row + col[h]))
+                                      : Elem<E>::neg_inf_vec();
+#pragma unroll
+        for (int h = 0; h < N; ++h) RowReader<E>::unpack(q[h], x[h]);
+#pragma unroll
+        for (int h = 0; h < N; ++h)
+            if (col[h] < V && col[h] + kVec > V)  // the row's last, partial vector
+#pragma unroll
+                for (int e = 0; e < kVec; ++e)
+                    if (col[h] + e < V) x[h][e] = Elem<E>::to_float(row[col[h] + e]);
+    } else {
+#pragma unroll
+        for (int h = 0; h < N; ++h)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e)
+                x[h][e] = col[h] + e < V ? Elem<E>::to_float(row[col[h] + e]) : -INFINITY;
     }
-    for (int c = tail + i; c < V; c += n) f(c, Elem<E>::to_float(row[c]));
 }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
@@ -387,53 +370,222 @@ __device__ __forceinline__ void block_scan(unsigned long long* scratch, T a, T b
     __syncthreads();
 }
 
-// Ascending bitonic sort of keys[0..n), padded in place to a power of two.
+// ---------------------------------------------------------------------------
+// Selection in a list of (key, weight) in shared memory, by one CTA.
+//
+// The list is ordered by its keys (descending logit in the high word, column
+// in the low one), or by the columns alone.  Among the keys in [kmin, kmax]
+// this finds the one at which the count reaches `want`, or the mass `target`:
+// histograms of the high word (or the column) narrow the range until few keys
+// are left, or all that are left have one high word (then the columns are
+// narrowed); each of those counts what lies before it.  Linear in the list,
+// where sorting 2048 keys costs a block 66 synchronised steps.
+// ---------------------------------------------------------------------------
+struct Selected {
+    unsigned long long key;
+    uint32_t rank;  // 1-based
+    uint64_t mass;  // up to and including it
+};
+
+constexpr int kListMembers = 128;
 template <int kThreads>
-__device__ __forceinline__ void sort_keys(unsigned long long* keys, int n) {
-    int m = 2;
-    while (m < n) m <<= 1;
-    for (int i = n + threadIdx.x; i < m; i += kThreads) keys[i] = ~0ull;
-    __syncthreads();
-    for (int size = 2; size <= m; size <<= 1) {
-        for (int stride = size >> 1; stride; stride >>= 1) {
-            for (int p = threadIdx.x; p < m / 2; p += kThreads) {
-                const int i = 2 * p - (p & (stride - 1));
-                const unsigned long long a = keys[i], b = keys[i + stride];
-                if ((a > b) == ((i & size) == 0)) {
-                    keys[i] = b;
-                    keys[i + stride] = a;
-                }
+struct ListShared {
+    static constexpr int kBins = 1024;
+    uint32_t count[kBins];
+    unsigned long long mass[kBins];
+    uint16_t member[kListMembers];
+    uint32_t lo, n_in, n_member, count_before;
+    unsigned long long mass_before;
+    unsigned long long scratch[2 * (kThreads / 32)];
+    Selected found;
+};
+
+template <int kThreads>
+__device__ __noinline__ Selected list_select(ListShared<kThreads>& ls,
+                                             const unsigned long long* keys,
+                                             const unsigned long long* weights, int n,
+                                             unsigned long long kmin, unsigned long long kmax,
+                                             bool by_column, bool by_count, uint32_t want,
+                                             uint64_t target, uint32_t count_before,
+                                             uint64_t mass_before) {
+    constexpr int kPer = ListShared<kThreads>::kBins / kThreads;
+    uint32_t lo = by_column ? 0u : (uint32_t)(kmin >> 32);
+    uint32_t hi = by_column ? (uint32_t)kFilterMaxV - 1 : (uint32_t)(kmax >> 32);
+    uint32_t n_in = (uint32_t)n;  // keys in the range, at most
+    auto inside = [&](unsigned long long key, uint32_t& p) {
+        p = by_column ? (uint32_t)key : (uint32_t)(key >> 32);
+        return key >= kmin && key <= kmax && p >= lo && p <= hi;
+    };
+    while (n_in > (uint32_t)kListMembers) {
+        if (lo == hi) {  // equal logits: by their columns from here on
+            if (!by_count) {
+                const uint64_t w = [&] {
+                    uint64_t one = 0;
+                    for (int i = 0; i < n && one == 0; ++i)
+                        if ((uint32_t)(keys[i] >> 32) == lo) one = weights[i];
+                    return one;
+                }();
+                const uint64_t short_of = target - mass_before;
+                want = count_before + (uint32_t)(w ? (short_of + w - 1) / w : n_in);
+                by_count = true;
             }
-            __syncthreads();
+            kmin = kmin > ((unsigned long long)lo << 32) ? kmin : (unsigned long long)lo << 32;
+            kmax = kmax < ((unsigned long long)lo << 32 | 0xFFFFFFFFu)
+                       ? kmax
+                       : ((unsigned long long)lo << 32 | 0xFFFFFFFFu);
+            by_column = true;
+            lo = 0;
+            hi = (uint32_t)kFilterMaxV - 1;
+        }
+        int shift = 0;
+        while (((hi - lo) >> shift) >= (uint32_t)ListShared<kThreads>::kBins) ++shift;
+        for (int i = threadIdx.x; i < ListShared<kThreads>::kBins; i += kThreads)
+            ls.count[i] = 0, ls.mass[i] = 0;
+        if (threadIdx.x == 0) ls.n_in = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            uint32_t p;
+            if (inside(keys[i], p)) {
+                atomicAdd(&ls.count[(p - lo) >> shift], 1u);
+                if (weights[i]) atomicAdd(&ls.mass[(p - lo) >> shift], weights[i]);
+            }
+        }
+        __syncthreads();
+        const int b0 = threadIdx.x * kPer;
+        uint64_t nc = 0, nm = 0;
+        for (int i = 0; i < kPer; ++i) {
+            nc += ls.count[b0 + i];
+            nm += ls.mass[b0 + i];
+        }
+        uint64_t nb, wb;
+        block_scan<kThreads, uint64_t>(ls.scratch, nc, nm, nb, wb);
+        nb += count_before;
+        wb += mass_before;
+        for (int i = 0; i < kPer; ++i) {
+            const uint64_t n1 = nb + ls.count[b0 + i], w1 = wb + ls.mass[b0 + i];
+            if (by_count ? (nb < want && want <= n1) : (wb < target && w1 >= target)) {
+                ls.lo = lo + ((uint32_t)(b0 + i) << shift);
+                ls.n_in = ls.count[b0 + i];
+                ls.count_before = (uint32_t)nb;
+                ls.mass_before = wb;
+            }
+            nb = n1;
+            wb = w1;
+        }
+        __syncthreads();
+        if (ls.n_in == 0) break;  // nothing reaches it: the caller asked for too much
+        lo = ls.lo;
+        hi = min(hi, lo + ((1u << shift) - 1u));
+        n_in = ls.n_in;
+        count_before = ls.count_before;
+        mass_before = ls.mass_before;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        ls.n_member = 0;
+        ls.found = {~0ull, 0u, 0};
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        uint32_t p;
+        if (inside(keys[i], p)) {
+            const uint32_t at = atomicAdd(&ls.n_member, 1u);
+            if (at < (uint32_t)kListMembers) ls.member[at] = (uint16_t)i;
         }
     }
+    __syncthreads();
+    const int m = min((int)ls.n_member, kListMembers);
+    if ((int)threadIdx.x < m) {
+        const int me = ls.member[threadIdx.x];
+        const unsigned long long mine = keys[me];
+        uint32_t rank = count_before;
+        uint64_t before = mass_before;
+#pragma unroll 4
+        for (int j = 0; j < m; ++j) {
+            const int o = ls.member[j];
+            const bool less = by_column ? (uint32_t)keys[o] < (uint32_t)mine : keys[o] < mine;
+            rank += less;
+            before += less ? weights[o] : 0;
+        }
+        const uint64_t after = before + weights[me];
+        if (by_count ? rank + 1 == want : (before < target && after >= target))
+            ls.found = {mine, rank + 1, after};
+    }
+    __syncthreads();
+    const Selected found = ls.found;
+    __syncthreads();
+    return found;
 }
 
-// One row, worked on by the CTAs of a cluster (the team): passes over the row
-// are shared out over all of them, decisions are taken in the first.
+struct ExactShared {
+    uint32_t level0[kBins];
+    Histogram level1;
+    unsigned long long cand[kCand];
+    unsigned long long weight[kCand];
+    unsigned long long span_mass[kMaxSpans];
+    float span_u[kMaxSpans];
+    float2 table[64];
+    unsigned long long scratch[2 * kExWarps];
+    ListShared<kExThreads> list;
+    // Team results, in the first CTA of a cluster.
+    uint32_t n_min, n_finite;
+    uint32_t n_cand;
+    uint32_t first;
+    uint32_t first_kept;
+    // Decisions that the first CTA announces.
+    uint32_t klo, khi, n_in, count_before, bin;
+    unsigned long long mass_before, mass_in, total, offset;
+    Selected sel;
+};
+
+// One row, worked on by a team of CTAs: those of a cluster, or one CTA alone.
+// Passes over the row are shared out over all of them, decisions are taken in
+// the first.
 template <typename E>
 struct Team {
-    ExactShared& sm;        // this CTA's
-    ExactShared& lead;      // the first CTA's
+    ExactShared& sm;         // this CTA's
+    ExactShared& lead;       // the first CTA's
     cg::cluster_group cluster;
     const E* row;
     int V;
     int thread, threads;     // of the team
-    bool first;              // this is the first CTA
+    bool first, alone;
     float M;
     TempScale c;
     int k;                   // digits of the fixed weights
     float bin_scale;
 
+    __device__ void sync() {
+        if (alone)
+            __syncthreads();
+        else
+            cluster.sync();
+    }
+    // f(first column, logits of one vector), columns past V as -inf.
     template <typename F>
-    __device__ void each(F f) const {
-        for_each_logit(row, V, thread, threads, f);
+    __device__ __forceinline__ void each_vector(F f) const {
+        constexpr int kVec = Elem<E>::kVec, kAhead = 2;
+        for (int c0 = thread * kVec; c0 < V; c0 += kAhead * threads * kVec) {
+            int col[kAhead];
+            float x[kAhead][kVec];
+#pragma unroll
+            for (int h = 0; h < kAhead; ++h) col[h] = c0 + h * threads * kVec;
+            load_columns<E, kAhead>(row, col, V, x);
+#pragma unroll
+            for (int h = 0; h < kAhead; ++h)
+                if (col[h] < V) f(col[h], x[h]);
+        }
     }
     __device__ uint64_t weight(float z) const { return fixed_weight(z, M, c, k, sm.table); }
     // Level-0 bins: equal steps of M - z, the last one open (the difference
     // and the product round monotonely, so bins are ranges of the order).
     __device__ int bin0(float z) const { return min(kBins - 1, __float2int_rd((M - z) * bin_scale)); }
 
+    // Adds one value per thread up over the team, into the first CTA's *to.
+    __device__ void add_to(unsigned long long* to, uint64_t v) const {
+        v = warp_sum(v);
+        if ((threadIdx.x & 31) == 0 && v) atomicAdd(to, (unsigned long long)v);
+    }
     __device__ void clear(Histogram& h) const {
         for (int i = threadIdx.x; i < kBins; i += kExThreads) {
             h.count[i] = 0;
@@ -441,29 +593,29 @@ struct Team {
         }
         __syncthreads();
     }
-    // Adds every CTA's histogram to the first one's.
-    __device__ void merge(Histogram ExactShared::*which) {
-        cluster.sync();
-        if (!first) {
-            Histogram& mine = sm.*which;
-            Histogram& all = lead.*which;
+    // Adds every CTA's histogram (masses optional) to the first one's.
+    __device__ void merge(const uint32_t* count, uint32_t* all_count,
+                          const unsigned long long* mass = nullptr,
+                          unsigned long long* all_mass = nullptr) {
+        sync();
+        if (!first)
             for (int i = threadIdx.x; i < kBins; i += kExThreads) {
-                if (mine.count[i]) atomicAdd(&all.count[i], mine.count[i]);
-                if (mine.mass[i]) atomicAdd(&all.mass[i], mine.mass[i]);
+                if (count[i]) atomicAdd(&all_count[i], count[i]);
+                if (mass && mass[i]) atomicAdd(&all_mass[i], mass[i]);
             }
-        }
-        cluster.sync();
+        sync();
     }
 
     // First CTA: the bin in which the count reaches `want` (by_count) or the
-    // mass reaches `target`; announces what lies before it and inside it.
-    __device__ int pick_bin(const Histogram& h, bool by_count, uint32_t want, double target) {
+    // mass `target`; announces the count and mass before it and the count inside.
+    __device__ int pick_bin(const uint32_t* count, const unsigned long long* mass, bool by_count,
+                            uint32_t want, uint64_t target) {
         constexpr int kPer = kBins / kExThreads;
         const int b0 = threadIdx.x * kPer;
         uint64_t n = 0, w = 0;
         for (int i = 0; i < kPer; ++i) {
-            n += h.count[b0 + i];
-            w += h.mass[b0 + i];
+            n += count[b0 + i];
+            w += mass ? mass[b0 + i] : 0;
         }
         uint64_t nb, wb;
         block_scan<kExThreads, uint64_t>(sm.scratch, n, w, nb, wb);
@@ -471,13 +623,11 @@ struct Team {
         wb += sm.mass_before;
         __syncthreads();
         for (int i = 0; i < kPer; ++i) {
-            const uint64_t n1 = nb + h.count[b0 + i], w1 = wb + h.mass[b0 + i];
-            const bool here = by_count ? (nb < want && want <= n1)
-                                       : ((double)wb < target && (double)w1 >= target);
-            if (here) {
+            const uint64_t n1 = nb + count[b0 + i], w1 = wb + (mass ? mass[b0 + i] : 0);
+            if (by_count ? (nb < want && want <= n1) : (wb < target && w1 >= target)) {
                 sm.count_before = (uint32_t)nb;
                 sm.mass_before = wb;
-                sm.n_in = h.count[b0 + i];
+                sm.n_in = count[b0 + i];
                 sm.first = b0 + i;
             }
             nb = n1;
@@ -487,117 +637,214 @@ struct Team {
         return (int)sm.first;
     }
 
+    // First CTA: the last of the level-0 bins [lo, hi] before which the
+    // estimated mass is below `target`.  A bin's mass is estimated by its count
+    // times the weight of its middle (steps of 1/32 of a binary order: 1.1% of
+    // it at most); `anchor`, if not negative, is a bin before which the mass is
+    // known.  Announces the bin and its counts.
+    __device__ int guess_bin(uint64_t target, int lo, int hi, int anchor, uint64_t known) {
+        constexpr int kPer = kBins / kExThreads;
+        const int b0 = threadIdx.x * kPer;
+        const float one = __int_as_float((127 + k) << 23);
+        uint64_t n = 0, w = 0, part[kPer];
+        for (int i = 0; i < kPer; ++i) {
+            n += sm.level0[b0 + i];
+            const float mid = exp2f(-((float)(b0 + i) + 0.5f) * (64.f / kBins));
+            part[i] = (uint64_t)((float)sm.level0[b0 + i] * mid * one);
+            w += part[i];
+        }
+        uint64_t nb, wb;
+        block_scan<kExThreads, uint64_t>(sm.scratch, n, w, nb, wb);
+        if (threadIdx.x == 0) sm.first = (uint32_t)lo;
+        uint64_t at = wb;
+        for (int i = 0; i < kPer; ++i) {
+            if (b0 + i == anchor) sm.offset = known - at;  // modulo 2^64
+            at += part[i];
+        }
+        if (threadIdx.x == 0 && anchor < 0) sm.offset = 0;
+        __syncthreads();
+        at = wb + sm.offset;
+        for (int i = 0; i < kPer; ++i) {
+            if (b0 + i > lo && b0 + i <= hi && (int64_t)(at - target) < 0 && sm.level0[b0 + i])
+                atomicMax(&sm.first, (uint32_t)(b0 + i));
+            at += part[i];
+        }
+        __syncthreads();
+        const int b = (int)sm.first;
+        uint64_t before = nb;
+        for (int i = 0; i < kPer; ++i) {
+            if (b0 + i == b) {
+                sm.count_before = (uint32_t)before;
+                sm.n_in = sm.level0[b0 + i];
+            }
+            before += sm.level0[b0 + i];
+        }
+        __syncthreads();
+        return b;
+    }
+
+    // First CTA: the keys of level-0 bin b.
+    __device__ void bin_range(int b) {
+        if (threadIdx.x < 2) {
+            // Smallest key whose bin is >= b (thread 0) and > b (thread 1).
+            const int edge = b + (int)threadIdx.x;
+            uint32_t lo = desc_key(M), hi = kKeyNegInf;  // answer in [lo, hi]
+            while (lo < hi) {
+                const uint32_t mid = lo + (hi - lo) / 2;
+                if (bin0(key_logit(mid)) >= edge)
+                    hi = mid;
+                else
+                    lo = mid + 1;
+            }
+            if (threadIdx.x == 0)
+                sm.klo = lo;
+            else
+                sm.khi = b == kBins - 1 ? kKeyNegInf - 1 : lo - 1;
+        }
+    }
+
+    // One pass: the exact masses before and inside the keys [klo, khi], and the
+    // elements inside, as far as they fit.
+    __device__ __noinline__ void weigh_and_gather(uint32_t klo, uint32_t khi) {
+        if (first && threadIdx.x == 0) {
+            sm.n_cand = 0;
+            sm.mass_before = sm.mass_in = 0;
+        }
+        sync();
+        uint64_t before = 0, inside = 0;
+        each_vector([&](int col, const float (&x)[Elem<E>::kVec]) {
+            bool any = false;
+#pragma unroll
+            for (int e = 0; e < Elem<E>::kVec; ++e) any |= desc_key(x[e]) <= khi;
+            if (!any) return;
+#pragma unroll
+            for (int e = 0; e < Elem<E>::kVec; ++e) {
+                const uint32_t dk = desc_key(x[e]);
+                const uint64_t w = weight(x[e]);
+                before += dk < klo ? w : 0;
+                if (dk >= klo && dk <= khi) {
+                    inside += w;
+                    const uint32_t at = atomicAdd(&lead.n_cand, 1u);
+                    if (at < (uint32_t)kCand) {
+                        lead.cand[at] = ((unsigned long long)dk << 32) | (uint32_t)(col + e);
+                        lead.weight[at] = w;
+                    }
+                }
+            }
+        });
+        add_to(&lead.mass_before, before);
+        add_to(&lead.mass_in, inside);
+        sync();
+    }
+
     // The element at which the count reaches `want`, or the mass `target`, in
-    // the order of the finite logits; level0 holds all of them.  Bins are
-    // narrowed until what is left can be sorted, or is one value.
-    __device__ Selection select(bool by_count, uint32_t want, double target) {
+    // the order of the finite logits, all of which level0 counts.
+    __device__ __noinline__ Selected select(bool by_count, uint32_t want, uint64_t target) {
         if (first) {
             if (threadIdx.x == 0) {
                 sm.count_before = 0;
                 sm.mass_before = 0;
             }
             __syncthreads();
-            const int b = pick_bin(sm.level0, by_count, want, target);
-            if (threadIdx.x < 2) {
-                // Smallest key whose bin is >= b (thread 0) and > b (thread 1).
-                const int edge = b + (int)threadIdx.x;
-                uint32_t lo = desc_key(M), hi = kKeyNegInf;  // answer in [lo, hi]
-                while (lo < hi) {
-                    const uint32_t mid = lo + (hi - lo) / 2;
-                    if (bin0(key_logit(mid)) >= edge)
-                        hi = mid;
-                    else
-                        lo = mid + 1;
-                }
-                if (threadIdx.x == 0)
-                    sm.klo = lo;
+            const int b = by_count ? pick_bin(sm.level0, nullptr, true, want, 0)
+                                   : guess_bin(target, 0, kBins - 1, -1, 0);
+            bin_range(b);
+            if (threadIdx.x == 0) sm.bin = (uint32_t)b;
+        }
+        sync();
+        uint32_t klo = lead.klo, khi = lead.khi, n_in = lead.n_in;
+        int b = (int)lead.bin, lo = 0, hi = kBins - 1;
+        weigh_and_gather(klo, khi);
+        if (!by_count) {
+            // A guess that missed narrows the bins that are left, so this ends.
+            while (true) {
+                const uint64_t before = lead.mass_before, in = lead.mass_in;
+                if (before >= target && b > lo)
+                    hi = b - 1;
+                else if (before + in < target && b < hi)
+                    lo = b + 1;
                 else
-                    sm.khi = b == kBins - 1 ? kKeyNegInf - 1 : lo - 1;
+                    break;
+                sync();
+                if (first) {
+                    const int anchor = b;
+                    b = guess_bin(target, lo, hi, anchor, before);
+                    bin_range(b);
+                    if (threadIdx.x == 0) sm.bin = (uint32_t)b;
+                }
+                sync();
+                klo = lead.klo;
+                khi = lead.khi;
+                n_in = lead.n_in;
+                b = (int)lead.bin;
+                weigh_and_gather(klo, khi);
             }
         }
-        cluster.sync();
-        uint32_t klo = lead.klo, khi = lead.khi, n_in = lead.n_in;
+        bool narrowed = false;
         while (n_in > kCand && klo < khi) {
+            narrowed = true;
             int shift = 0;
             while (((khi - klo) >> shift) >= (uint32_t)kBins) ++shift;
+            sync();
             clear(sm.level1);
-            each([&](int, float z) {
-                const uint32_t dk = desc_key(z);
-                if (dk >= klo && dk <= khi) {
-                    const int b = (int)((dk - klo) >> shift);
-                    atomicAdd(&sm.level1.count[b], 1u);
-                    atomicAdd(&sm.level1.mass[b], (unsigned long long)weight(z));
+            each_vector([&](int, const float (&x)[Elem<E>::kVec]) {
+#pragma unroll 1
+                for (int e = 0; e < Elem<E>::kVec; ++e) {
+                    const uint32_t dk = desc_key(x[e]);
+                    if (dk >= klo && dk <= khi) {
+                        const int i = (int)((dk - klo) >> shift);
+                        atomicAdd(&sm.level1.count[i], 1u);
+                        atomicAdd(&sm.level1.mass[i], (unsigned long long)weight(x[e]));
+                    }
                 }
             });
-            merge(&ExactShared::level1);
+            merge(sm.level1.count, lead.level1.count, sm.level1.mass, lead.level1.mass);
             if (first) {
-                const uint32_t b = (uint32_t)pick_bin(sm.level1, by_count, want, target);
+                const uint32_t i = (uint32_t)pick_bin(sm.level1.count, sm.level1.mass, by_count,
+                                                      want, target);
                 if (threadIdx.x == 0) {
-                    const uint32_t lo = klo + (b << shift);
-                    sm.klo = lo;
-                    sm.khi = min(khi, lo + ((1u << shift) - 1u));
+                    const uint32_t from = klo + (i << shift);
+                    sm.klo = from;
+                    sm.khi = min(khi, from + ((1u << shift) - 1u));
                 }
             }
-            cluster.sync();
+            sync();
             klo = lead.klo;
             khi = lead.khi;
             n_in = lead.n_in;
         }
-        if (n_in > kCand)
+        if (n_in > kCand) {
+            sync();
             select_tie(klo, by_count, want, target);
-        else
-            select_sorted(klo, khi, by_count, want, target);
-        cluster.sync();
-        return lead.sel;
-    }
-
-    // Few elements left: gather them into the first CTA, sort, scan.
-    __device__ void select_sorted(uint32_t klo, uint32_t khi, bool by_count, uint32_t want,
-                                  double target) {
-        if (first && threadIdx.x == 0) sm.n_cand = 0;
-        cluster.sync();
-        each([&](int col, float z) {
-            const uint32_t dk = desc_key(z);
-            if (dk >= klo && dk <= khi) {
-                const uint32_t at = atomicAdd(&lead.n_cand, 1u);
-                if (at < (uint32_t)kCand)
-                    lead.cand[at] = ((unsigned long long)dk << 32) | (uint32_t)col;
+        } else {
+            if (narrowed) {
+                sync();
+                weigh_and_gather(klo, khi);
             }
-        });
-        cluster.sync();
-        if (!first) return;
-        const int n = min((int)sm.n_cand, kCand);
-        sort_keys<kExThreads>(sm.cand, n);
-        constexpr int kPer = kCand / kExThreads;
-        const int i0 = threadIdx.x * kPer;
-        uint64_t w[kPer], sum = 0;
-        for (int i = 0; i < kPer; ++i) {
-            w[i] = i0 + i < n ? weight(key_logit((uint32_t)(sm.cand[i0 + i] >> 32))) : 0;
-            sum += w[i];
-        }
-        uint64_t wb, unused;
-        block_scan<kExThreads, uint64_t>(sm.scratch, sum, 0, wb, unused);
-        wb += sm.mass_before;
-        const uint32_t before = sm.count_before;
-        for (int i = 0; i < kPer && i0 + i < n; ++i) {
-            const uint64_t w1 = wb + w[i];
-            const uint32_t rank = before + i0 + i + 1;
-            if (by_count ? rank == want : ((double)wb < target && (double)w1 >= target)) {
-                const unsigned long long e = sm.cand[i0 + i];
-                sm.sel = {(uint32_t)(e >> 32), (uint32_t)e, rank, w1};
+            if (first) {
+                const Selected f = list_select<kExThreads>(
+                    sm.list, sm.cand, sm.weight, min((int)sm.n_cand, kCand),
+                    (unsigned long long)klo << 32, (unsigned long long)khi << 32 | 0xFFFFFFFFu,
+                    false, by_count, want, target, sm.count_before, sm.mass_before);
+                if (threadIdx.x == 0) sm.sel = f;
             }
-            wb = w1;
         }
+        sync();
+        const Selected found = lead.sel;
+        sync();
+        return found;
     }
 
     // Many equal logits: how many of them are taken follows from their common
     // weight; the last one taken is found by counting them in index order.
-    __device__ void select_tie(uint32_t key, bool by_count, uint32_t want, double target) {
+    __device__ void select_tie(uint32_t key, bool by_count, uint32_t want, uint64_t target) {
         clear(sm.level1);
-        each([&](int col, float z) {
-            if (desc_key(z) == key) atomicAdd(&sm.level1.count[col / kSpan], 1u);
+        each_vector([&](int col, const float (&x)[Elem<E>::kVec]) {
+#pragma unroll
+            for (int e = 0; e < Elem<E>::kVec; ++e)
+                if (desc_key(x[e]) == key) atomicAdd(&sm.level1.count[(col + e) / kSpan], 1u);
         });
-        merge(&ExactShared::level1);
+        merge(sm.level1.count, lead.level1.count);
         if (!first) return;
         const uint64_t w = weight(key_logit(key));
         const uint32_t before = sm.count_before, n_in = sm.n_in;
@@ -610,7 +857,7 @@ struct Team {
             uint32_t lo = 1, hi = n_in;
             while (lo < hi) {
                 const uint32_t mid = lo + (hi - lo) / 2;
-                if ((double)(mass_before + (uint64_t)mid * w) >= target)
+                if (mass_before + (uint64_t)mid * w >= target)
                     hi = mid;
                 else
                     lo = mid + 1;
@@ -620,11 +867,20 @@ struct Team {
         __syncthreads();
         const int spans = (V + kSpan - 1) / kSpan;
         uint64_t nb, unused;
-        const uint64_t mine = (int)threadIdx.x < spans ? sm.level1.count[threadIdx.x] : 0;
-        block_scan<kExThreads, uint64_t>(sm.scratch, mine, 0, nb, unused);
-        if (nb < take && take <= nb + mine) {
-            sm.first = threadIdx.x;
-            sm.n_in = (uint32_t)nb;
+        uint64_t mine[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int s = 2 * (int)threadIdx.x + i;
+            mine[i] = s < spans ? sm.level1.count[s] : 0;
+        }
+        block_scan<kExThreads, uint64_t>(sm.scratch, mine[0] + mine[1], 0, nb, unused);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (nb < take && take <= nb + mine[i]) {
+                sm.first = 2 * threadIdx.x + i;
+                sm.n_in = (uint32_t)nb;
+            }
+            nb += mine[i];
         }
         __syncthreads();
         constexpr int kPer = kSpan / kExThreads;
@@ -632,19 +888,19 @@ struct Team {
         const uint64_t skipped = sm.n_in;
         uint32_t hit = 0;
         for (int i = 0; i < kPer; ++i)
-            if (c0 >= 0 && c0 + i < V && desc_key(Elem<E>::to_float(row[c0 + i])) == key) hit |= 1u << i;
+            if (c0 >= 0 && c0 + i < V && desc_key(Elem<E>::to_float(row[c0 + i])) == key)
+                hit |= 1u << i;
         block_scan<kExThreads, uint64_t>(sm.scratch, __popc(hit), 0, nb, unused);
         nb += skipped;
         for (int i = 0; i < kPer; ++i) {
             if (!(hit >> i & 1u)) continue;
             if (++nb == take)
-                sm.sel = {key, (uint32_t)(c0 + i), before + take, mass_before + (uint64_t)take * w};
+                sm.sel = {(unsigned long long)key << 32 | (uint32_t)(c0 + i), before + take,
+                          mass_before + (uint64_t)take * w};
         }
         __syncthreads();
     }
 };
-
-static_assert(kMaxSpans <= kExThreads && kMaxSpans <= kBins, "one thread per span");
 
 // ---------------------------------------------------------------------------
 // Finish: one CTA per row.
@@ -654,20 +910,33 @@ static_assert(kMaxSpans <= kExThreads && kMaxSpans <= kBins, "one thread per spa
 // chunk alone.  It stands when the target u S lies further than the sums' error
 // bound from both ends of the column's interval.
 //
-// Filtered: a histogram of the group maxima over M - z gives a bin b such that
-// the groups whose maximum lies in bins <= b are sure (top-k: k maxima, so at
-// least k columns; min-p: the bin of its threshold) or likely (top-p: their
-// maxima alone hold the mass) to hold all kept columns.  Only those groups are
-// read again, and their columns in bins <= b sorted.  Their weights are exact;
-// a nucleus is measured against the fp32 sum with its error bound (against an
-// exact one after top-k), and the row is left to the exact kernel when the
+// Filtered: a histogram over M - z gives a bin b such that the columns in bins
+// <= b are sure or likely to hold all kept ones: of the group maxima (top-k: k
+// maxima, so at least k columns; top-p: their maxima alone hold the mass), of
+// the columns themselves in a row short enough to be read twice at little
+// cost, or simply the bin of min-p's threshold.  Only the groups whose maximum
+// lies in those bins are read again.  What is found has exact weights; a
+// nucleus is measured against the fp32 sum with its error bound (against an
+// exact one after top-k), and the row is left to the exact kernel where the
 // bound does not decide or the columns do not suffice.
+//
+// Up to one candidate per thread, every thread finds the rank and the mass
+// before its own by comparing with all others: for the usual 50 to 100 that
+// is a few hundred cycles, where a sort by a block needs 28 synchronised steps.
+// Among more the cut and the draw are selected by histograms (list_select).
 // ---------------------------------------------------------------------------
 constexpr int kFinThreads = 256;
 constexpr int kFinBins = 1024;     // 64 binary orders of e, in steps of 1/16
-constexpr int kFinCand = 1024;
+constexpr int kFinCand = 2048;
 constexpr int kFinGroups = 2048;
+constexpr int kFinAll = 1024;      // columns of a row that are all taken as candidates
+constexpr int kFinShort = 16384;   // columns of a row whose histogram is of its columns
 constexpr int kMaxChunks = (int)(kFilterMaxV / PSTAT_CHUNK_F32);
+
+struct Candidate {
+    unsigned long long key;  // (descending key, column)
+    unsigned long long weight;
+};
 
 struct FinishShared {
     union {
@@ -675,35 +944,24 @@ struct FinishShared {
             uint32_t count[kFinBins];
             uint32_t mass[kFinBins];
         } hist;
-        unsigned long long weight[kFinCand];  // inclusive sums
+        Candidate pair[kFinThreads];
+        ListShared<kFinThreads> list;
         float prefix[kMaxChunks];
     };
     unsigned long long cand[kFinCand];
-    uint16_t group[kFinGroups];
+    union {
+        unsigned long long weight[kFinCand];
+        uint16_t group[kFinGroups];
+    };
     float2 table[64];
     unsigned long long scratch[2 * (kFinThreads / 32)];
-    uint32_t n_group, n_cand, bin, found;
+    unsigned long long target0, target1, total, sum, cut, draw, ux;
+    uint32_t n_group, n_cand, bin, found, keep0, keep1;
 };
 static_assert(kMaxChunks * 32 <= 65536, "group indices are 16 bits");
 
 __device__ __forceinline__ void leave_row(const FilterArgs& a, int64_t t) {
     if (threadIdx.x == 0) a.left[atomicAdd(a.left_count, 1)] = (int)t;
-}
-
-// Reads kVec columns from `col` (a multiple of kVec) of a row; columns past V
-// read as -inf.
-template <typename E>
-__device__ __forceinline__ void load_columns(const E* row, int col, int V,
-                                             float (&x)[Elem<E>::kVec]) {
-    constexpr int kVec = Elem<E>::kVec;
-    const E* p = row + col;
-    if (col + kVec <= V && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-        RowReader<E>::unpack(__ldg(reinterpret_cast<const uint4*>(p)), x);
-    } else {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e)
-            x[e] = col + e < V ? Elem<E>::to_float(p[e]) : -INFINITY;
-    }
 }
 
 template <typename E>
@@ -766,12 +1024,16 @@ __device__ void finish_draw(const FilterArgs& a, int64_t t, const E* row, const 
     constexpr int kVec = Elem<E>::kVec, kPer = Elem<E>::kChunk / kFinThreads;
     const int col0 = chunk * Elem<E>::kChunk + threadIdx.x * kPer;
     float z[kPer], sum = 0.f;
+    {
+        int col[kPer / kVec];
+        float x[kPer / kVec][kVec];
 #pragma unroll
-    for (int v = 0; v < kPer / kVec; ++v) {
-        float x[kVec];
-        load_columns(row, col0 + v * kVec, (int)a.V, x);
+        for (int v = 0; v < kPer / kVec; ++v) col[v] = col0 + v * kVec;
+        load_columns<E, kPer / kVec>(row, col, (int)a.V, x);
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) z[v * kVec + e] = x[e];
+        for (int v = 0; v < kPer / kVec; ++v)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) z[v * kVec + e] = x[v][e];
     }
     float ex[kPer];
 #pragma unroll
@@ -797,22 +1059,283 @@ __device__ void finish_draw(const FilterArgs& a, int64_t t, const E* row, const 
     if (!sm.found) leave_row(a, t);
 }
 
+// Calls f(group, maximum) for a row's groups, eight loads ahead.
+template <typename E, typename F>
+__device__ __forceinline__ void for_each_group(const E* __restrict__ gm, int groups, F f) {
+    constexpr int kAhead = 8;
+    for (int i0 = threadIdx.x; i0 < groups; i0 += kAhead * kFinThreads) {
+        E g[kAhead];
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h)
+            g[h] = i0 + h * kFinThreads < groups ? gm[i0 + h * kFinThreads] : Elem<E>::neg_inf();
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h)
+            if (i0 + h * kFinThreads < groups) f(i0 + h * kFinThreads, Elem<E>::to_float(g[h]));
+    }
+}
+
+// ln(min_p) t + M with the bounds of its fp32 error: the product of a logarithm
+// of 2 ulp with t, and the sum.
+struct MinP {
+    float lo, hi;
+};
+__device__ __forceinline__ MinP min_p_bounds(float M, const RowSettings& rs) {
+    if (!rs.cut_m) return {-INFINITY, -INFINITY};
+    if (rs.min_p == 1.f) return {M, M};
+    const float d = rs.temp * logf(rs.min_p);
+    const float z = M + d;
+    const float err = (fabsf(d) * 4.f + fabsf(z)) * 1.1920929e-7f;
+    return {__fadd_rd(z, -err), fminf(M, __fadd_ru(z, err))};
+}
+
+struct FinishRow {
+    int64_t t;
+    RowSettings rs;
+    float M, Sf;
+    TempScale c;
+    MinP mp;
+    int k;         // top-k's, 0 if it does not cut
+    int n;         // candidates
+    bool all;      // they are all finite columns of the row
+    bool all_min;  // they hold every column that min-p keeps
+    int scale;     // digits of their weights
+};
+
+// e x in units of 2^-44, x in fp32: every term is at most 1/e, so that they add
+// up as integers, in any order.
+__device__ __forceinline__ long long entropy_term(unsigned long long key, uint64_t w, float M,
+                                                  float temp, int scale) {
+    const float x = (key_logit((uint32_t)(key >> 32)) - M) / temp;
+    const float e = (float)w * __int_as_float((127 - scale) << 23);
+    return w ? __float2ll_rn(e * x * 1.7592186e13f) : 0;
+}
+
+template <typename E, bool kSample>
+__device__ __forceinline__ void write_token(const FilterArgs& a, const E* row, const FinishRow& r,
+                                            uint32_t col, uint64_t S) {
+    a.token[r.t] = (int64_t)col;
+    a.logprob[r.t] = (Elem<E>::to_float(row[col]) - r.M) / r.rs.temp - fixed_log(S, r.scale);
+}
+
+template <typename E>
+__device__ __forceinline__ void write_kept(const FilterArgs& a, const E* row, const FinishRow& r,
+                                           unsigned long long cut, uint64_t S, long long ux) {
+    const float lnS = fixed_log(S, r.scale);
+    const float U = (float)ux * 5.6843419e-14f;  // 2^-44
+    const float Sr = (float)S * __int_as_float((127 - r.scale) << 23);
+    write_statistics(a, r.t, row, r.M, lnS, lnS - U / Sr, r.rs.temp, (uint32_t)(cut >> 32),
+                     (uint32_t)cut);
+}
+
+// Targets of a nucleus that is measured against the fp32 sum: p S with the
+// error bound taken off and added.
+__device__ __forceinline__ void nucleus_targets(const FinishRow& r, FinishShared& sm) {
+    const double target = (double)r.rs.top_p * (double)r.Sf * (double)(1ull << r.scale);
+    sm.target0 = __double2ull_rd(target * (1.0 - (double)kSumError));
+    sm.target1 = __double2ull_ru(target * (1.0 + (double)kSumError));
+}
+
+// Decides a row from at most kFinThreads candidates.
+template <typename E, bool kSample>
+__device__ __forceinline__ void finish_few(const FilterArgs& a, const E* row, const FinishRow& r,
+                                           FinishShared& sm) {
+    const int lane = threadIdx.x & 31, n = r.n;
+    // `parts` neighbouring lanes share a candidate, each comparing it with its
+    // share of the others.
+    const int parts = n <= kFinThreads / 4 ? 4 : n <= kFinThreads / 2 ? 2 : 1;
+    const int item = (int)threadIdx.x / parts, part = (int)threadIdx.x % parts;
+    // (number, mass) of the candidates that `less` accepts
+    auto count_before = [&](auto less, int& number, uint64_t& mass) {
+        number = 0;
+        mass = 0;
+        if ((int)(threadIdx.x & ~31u) / parts < n) {
+#pragma unroll 4
+            for (int j = part; j < n; j += parts) {
+                const Candidate o = sm.pair[j];
+                const bool yes = less(o.key);
+                number += yes;
+                mass += yes ? o.weight : 0;
+            }
+            for (int off = 1; off < parts; off <<= 1) {
+                number += __shfl_xor_sync(0xFFFFFFFFu, number, off);
+                mass += __shfl_xor_sync(0xFFFFFFFFu, mass, off);
+            }
+        }
+    };
+    if ((int)threadIdx.x < n) {
+        const unsigned long long mine = sm.cand[threadIdx.x];
+        sm.pair[threadIdx.x] = {
+            mine, fixed_weight(key_logit((uint32_t)(mine >> 32)), r.M, r.c, r.scale, sm.table)};
+    }
+    const bool whole = r.k > 0 || r.all;  // the whole mass is among the candidates'
+    if (r.rs.cut_p && !whole && threadIdx.x == 0) nucleus_targets(r, sm);
+    __syncthreads();
+    const bool mine = item < n && part == 0;  // one thread speaks for a candidate
+    const unsigned long long key = item < n ? sm.pair[item].key : ~0ull;
+    const uint64_t w = item < n ? sm.pair[item].weight : 0;
+    int rank;
+    uint64_t before;
+    count_before([&](unsigned long long o) { return o < key; }, rank, before);
+    if (mine && rank == n - 1) sm.total = before + w;
+    if (r.rs.cut_p && whole && mine && rank == (r.k > 0 && r.k < n ? r.k : n) - 1) {
+        const uint64_t target = __double2ull_ru((double)r.rs.top_p * (double)(before + w));
+        sm.target0 = sm.target1 = target ? target : 1;
+    }
+    __syncthreads();
+    // A column is kept when its rank, the mass before it and its logit pass
+    // every filter; by the narrow and by the wide bounds.
+    const float z = key_logit((uint32_t)(key >> 32));
+    const bool in = mine && (r.k == 0 || rank < r.k);
+    const int keep = __syncthreads_count(in && (!r.rs.cut_m || z >= r.mp.hi) &&
+                                         (!r.rs.cut_p || before < sm.target0));
+    const int most = __syncthreads_count(in && (!r.rs.cut_m || z >= r.mp.lo) &&
+                                         (!r.rs.cut_p || before < sm.target1));
+    // All candidates kept: then a filter must end here, or there are no others.
+    const bool ends = keep < n || r.all || (r.k > 0 && r.k <= n) || r.all_min ||
+                      (r.rs.cut_p && sm.total >= sm.target1);
+    if (keep == 0 || keep != most || !ends) return leave_row(a, r.t);
+    if (mine && rank == keep - 1) {
+        sm.sum = before + w;
+        sm.cut = key;
+        if (kSample) sm.draw = __double2ull_rd((double)r.rs.u * (double)(before + w));
+    }
+    __syncthreads();
+    const uint64_t S = sm.sum;
+    const unsigned long long cut = sm.cut;
+    if (!kSample) {
+        const long long ux = (long long)warp_sum(
+            mine && key <= cut ? (uint64_t)entropy_term(key, w, r.M, r.rs.temp, r.scale) : 0);
+        if (lane == 0 && ux) atomicAdd(&sm.ux, (unsigned long long)ux);
+        __syncthreads();
+        if (threadIdx.x == 0) write_kept(a, row, r, cut, S, (long long)sm.ux);
+        return;
+    }
+    // The draw: the kept columns in index order.  u = 0 takes the first of
+    // them, however small its weight.
+    const uint32_t col = (uint32_t)key;
+    int less;
+    uint64_t mass;
+    count_before([&](unsigned long long o) { return o <= cut && (uint32_t)o < col; }, less, mass);
+    const uint64_t target = sm.draw;
+    if (mine && key <= cut &&
+        (r.rs.u == 0.f ? less == 0 : (mass <= target && mass + w > target)))
+        write_token<E, kSample>(a, row, r, col, S);
+}
+
+// Decides a row from more candidates, by selections in their list.
+template <typename E, bool kSample>
+__device__ __noinline__ void finish_many(const FilterArgs& a, const E* row, const FinishRow& r,
+                                         FinishShared& sm) {
+    const int lane = threadIdx.x & 31, n = r.n;
+    uint64_t total = 0;
+    int n_hi = 0, n_lo = 0;  // columns that min-p keeps, by both bounds
+    for (int i = threadIdx.x; i < n; i += kFinThreads) {
+        const float z = key_logit((uint32_t)(sm.cand[i] >> 32));
+        const uint64_t w = fixed_weight(z, r.M, r.c, r.scale, sm.table);
+        sm.weight[i] = w;
+        total += w;
+        n_hi += z >= r.mp.hi;
+        n_lo += z >= r.mp.lo;
+    }
+    total = warp_sum(total);
+    n_hi = __reduce_add_sync(0xFFFFFFFFu, n_hi);
+    n_lo = __reduce_add_sync(0xFFFFFFFFu, n_lo);
+    if (lane == 0) {
+        atomicAdd(&sm.total, (unsigned long long)total);
+        atomicAdd(&sm.keep0, (uint32_t)n_hi);
+        atomicAdd(&sm.keep1, (uint32_t)n_lo);
+    }
+    if (threadIdx.x == 0) nucleus_targets(r, sm);
+    __syncthreads();
+    total = sm.total;
+    n_hi = (int)sm.keep0;
+    n_lo = (int)sm.keep1;
+    auto select = [&](bool by_count, uint32_t want, uint64_t target) {
+        return list_select<kFinThreads>(sm.list, sm.cand, sm.weight, n, 0, ~0ull, false, by_count,
+                                        want, target, 0, 0);
+    };
+    const bool whole = r.k > 0 || r.all;
+    int keep = n + 1;  // n + 1: all of these, and perhaps more
+    Selected end = {0, 0, 0};
+    if (r.k > 0 && r.k <= n) {
+        keep = r.k;
+        end = select(true, (uint32_t)r.k, 0);
+    }
+    if (r.rs.cut_p) {
+        uint64_t t0 = sm.target0, t1 = sm.target1;
+        if (whole) {
+            t0 = __double2ull_ru((double)r.rs.top_p * (double)(keep <= n ? end.mass : total));
+            t0 = t1 = t0 ? t0 : 1;
+        }
+        if (t0 == 0) return leave_row(a, r.t);
+        if (total >= t0) {
+            const Selected s = select(false, 0, t0);
+            if (s.mass < t1) {
+                // between the bounds, unless min-p ends before it
+                if (!(r.rs.cut_m && n_lo < (int)s.rank)) return leave_row(a, r.t);
+            } else if ((int)s.rank < keep) {
+                keep = (int)s.rank;
+                end = s;
+            }
+        }
+    }
+    if (r.rs.cut_m && n_hi < keep && n_hi != n_lo) return leave_row(a, r.t);
+    if (r.rs.cut_m && n_lo < keep && (n_lo < n || r.all_min || r.all)) {
+        keep = n_lo;
+        end = select(true, (uint32_t)keep, 0);
+    }
+    if (keep > n && r.all) {
+        keep = n;
+        end = select(true, (uint32_t)n, 0);
+    }
+    if (keep > n || keep == 0 || (int)end.rank != keep) return leave_row(a, r.t);
+    const uint64_t S = end.mass;
+    const unsigned long long cut = end.key;
+    if (!kSample) {
+        long long ux = 0;
+        for (int i = threadIdx.x; i < n; i += kFinThreads)
+            if (sm.cand[i] <= cut)
+                ux += entropy_term(sm.cand[i], sm.weight[i], r.M, r.rs.temp, r.scale);
+        ux = (long long)warp_sum((uint64_t)ux);
+        if (lane == 0 && ux) atomicAdd(&sm.ux, (unsigned long long)ux);
+        __syncthreads();
+        if (threadIdx.x == 0) write_kept(a, row, r, cut, S, (long long)sm.ux);
+        return;
+    }
+    const bool lowest = r.rs.u == 0.f;
+    const Selected s = list_select<kFinThreads>(
+        sm.list, sm.cand, sm.weight, n, 0, cut, true, lowest, 1,
+        __double2ull_rd((double)r.rs.u * (double)S) + 1, 0, 0);
+    if (threadIdx.x == 0) write_token<E, kSample>(a, row, r, (uint32_t)s.key, S);
+}
+
 template <typename E, bool kSample>
 __global__ void __launch_bounds__(kFinThreads)
     filter_finish_kernel(const __grid_constant__ FilterArgs a) {
     __shared__ FinishShared sm;
+    constexpr int kVec = Elem<E>::kVec;
     const int64_t t = blockIdx.x;
     const int V = (int)a.V, lane = threadIdx.x & 31;
     const E* row = static_cast<const E*>(a.logits) + t * a.ld;
     const float4* rec = a.records + t * a.chunks;
-    const RowSettings rs = row_settings<kSample>(a, t);
+    for (int i = threadIdx.x; i < kFinBins; i += kFinThreads) sm.hist.count[i] = sm.hist.mass[i] = 0;
+    if (threadIdx.x < 64) sm.table[threadIdx.x] = kExp2Table[threadIdx.x];
+    if (threadIdx.x == 0) {
+        sm.n_group = sm.n_cand = sm.keep0 = sm.keep1 = 0;
+        sm.ux = sm.total = 0;
+        sm.bin = kFinBins;
+    }
+    FinishRow r;
+    r.t = t;
+    r.rs = row_settings<kSample>(a, t);
+    const RowSettings& rs = r.rs;
     if (!rs.valid) {
         if (threadIdx.x == 0) write_undefined<kSample>(a, t, PSTAT_DEV_BAD_PARAM);
         return;
     }
-    const TempScale c = temp_scale(rs.greedy ? 1.f : rs.temp);
-    const float3 st = fold_records(rec, a.chunks, c.ch, lane);
-    const float M = st.x + 0.f, Sf = st.y;
+    r.c = temp_scale(rs.greedy ? 1.f : rs.temp);
+    const float3 st = fold_records(rec, a.chunks, r.c.ch, lane);
+    const float M = r.M = st.x + 0.f, Sf = r.Sf = st.y;
     if (!(M > -INFINITY)) {
         if (threadIdx.x == 0) write_undefined<kSample>(a, t, PSTAT_DEV_EMPTY_ROW);
         return;
@@ -820,37 +1343,52 @@ __global__ void __launch_bounds__(kFinThreads)
     if (rs.greedy) return finish_greedy(a, t, row, rec, M, sm);
     if (!rs.cut_k && !rs.cut_p && !rs.cut_m) {
         const float lnS = logf(Sf);
-        if (kSample) return finish_draw(a, t, row, rec, M, c.ch, rs, lnS, sm);
+        if (kSample) {
+            __syncthreads();  // the histogram's zeros share memory with the prefix sums
+            return finish_draw(a, t, row, rec, M, r.c.ch, rs, lnS, sm);
+        }
         if (threadIdx.x == 0)
             write_statistics(a, t, row, M, lnS, lnS - kLn2 * (st.z / Sf), rs.temp, 0xFFFFFFFFu,
                              (uint32_t)V - 1);
         return;
     }
 
-    // ---- which groups are read again
-    const bool by_mass = rs.cut_p && !rs.cut_k;
-    const int k = rs.cut_k ? (int)rs.top_k : 0;
-    if (threadIdx.x < 64) sm.table[threadIdx.x] = a.table.v[threadIdx.x];
-    if (threadIdx.x == 0) {
-        sm.n_group = sm.n_cand = 0;
-        sm.bin = kFinBins;
-    }
-    const float bin_scale = c.ch * ((float)kFinBins / 64.f);
+    r.k = rs.cut_k ? (int)rs.top_k : 0;
+    r.mp = min_p_bounds(M, rs);
+    r.all = V <= kFinAll;
+    const float bin_scale = r.c.ch * ((float)kFinBins / 64.f);
+    const float ch = r.c.ch;
     auto bin_of = [&](float z) { return min(kFinBins - 1, __float2int_rd((M - z) * bin_scale)); };
     const E* gm = static_cast<const E*>(a.group_max) + t * a.chunks * 32;
     const int groups = a.chunks * 32;
-    const float z_min = min_p_logit(M, rs);
-    const int bin_m = rs.cut_m ? bin_of(z_min) : kFinBins;
-    if (rs.cut_k || rs.cut_p) {
-        for (int i = threadIdx.x; i < kFinBins; i += kFinThreads) sm.hist.count[i] = sm.hist.mass[i] = 0;
-        __syncthreads();
-        constexpr float kUnit = 131072.f;  // 2^17: the maxima of all groups stay below 2^32
-        for (int i = threadIdx.x; i < groups; i += kFinThreads) {
-            const float g = Elem<E>::to_float(gm[i]);
-            if (g == -INFINITY) continue;
-            const int b = bin_of(g);
-            atomicAdd(&sm.hist.count[b], 1u);
-            if (by_mass) atomicAdd(&sm.hist.mass[b], (uint32_t)(ex2_approx((g - M) * c.ch) * kUnit));
+    const int bin_m = rs.cut_m ? bin_of(r.mp.lo) : kFinBins;
+    // Columns up to this bin are gathered; the last bin is open.
+    int b = kFinBins;
+    __syncthreads();
+    if (!r.all && (rs.cut_k || rs.cut_p)) {
+        const bool by_mass = rs.cut_p && !rs.cut_k, short_row = V <= kFinShort;
+        constexpr float kUnit = 131072.f;  // 2^17: of all groups together below 2^32
+        auto add = [&](float z) {
+            if (z == -INFINITY) return;
+            const int i = bin_of(z);
+            atomicAdd(&sm.hist.count[i], 1u);
+            if (by_mass) atomicAdd(&sm.hist.mass[i], __float2uint_rn(ex2_approx((z - M) * ch) * kUnit));
+        };
+        if (short_row) {
+            constexpr int kAhead = 2;
+            for (int c0 = threadIdx.x * kVec; c0 < V; c0 += kAhead * kFinThreads * kVec) {
+                int col[kAhead];
+                float x[kAhead][kVec];
+#pragma unroll
+                for (int h = 0; h < kAhead; ++h) col[h] = c0 + h * kFinThreads * kVec;
+                load_columns<E, kAhead>(row, col, V, x);
+#pragma unroll
+                for (int h = 0; h < kAhead; ++h)
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) add(x[h][e]);
+            }
+        } else {
+            for_each_group(gm, groups, [&](int, float g) { add(g); });
         }
         __syncthreads();
         constexpr int kPer = kFinBins / kFinThreads;
@@ -863,176 +1401,88 @@ __global__ void __launch_bounds__(kFinThreads)
         }
         uint32_t cb, mb;
         block_scan<kFinThreads, uint32_t>(sm.scratch, nc, nm, cb, mb);
-        const float need = rs.top_p * Sf * kUnit;
+        // a little more than the nucleus, so that roundings cannot fall short of it
+        const float need = (rs.top_p + (1.f - rs.top_p) * 0.05f) * Sf * kUnit;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const uint32_t c1 = cb + sm.hist.count[b0 + i], m1 = mb + sm.hist.mass[b0 + i];
             if (by_mass ? ((float)mb < need && (float)m1 >= need)
-                        : (cb < (uint32_t)k && (uint32_t)k <= c1))
+                        : (cb < (uint32_t)r.k && (uint32_t)r.k <= c1))
                 sm.bin = b0 + i;
             cb = c1;
             mb = m1;
         }
-    }
-    __syncthreads();
-    int b = (int)sm.bin;
-    // top-p after top-k needs the whole top-k mass, so min-p may not shorten it
-    if (!(rs.cut_k && rs.cut_p)) b = min(b, bin_m);
-    if (b >= kFinBins - 1) return leave_row(a, t);
-
-    // ---- gather
-    for (int i = threadIdx.x; i < groups; i += kFinThreads)
-        if (bin_of(Elem<E>::to_float(gm[i])) <= b) {
-            const uint32_t at = atomicAdd(&sm.n_group, 1u);
-            if (at < (uint32_t)kFinGroups) sm.group[at] = (uint16_t)i;
-        }
-    __syncthreads();
-    const int n_group = (int)sm.n_group;
-    if (n_group > kFinGroups) return leave_row(a, t);
-    {
-        constexpr int kVec = Elem<E>::kVec;
-        const int j = threadIdx.x & 15;
-        for (int gi = threadIdx.x >> 4; gi < n_group; gi += kFinThreads / 16) {
-            const int g = sm.group[gi];
-            const int col = (g >> 5) * Elem<E>::kChunk + ((g & 31) + 32 * j) * kVec;
-            float x[kVec];
-            load_columns(row, col, V, x);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                if (x[e] > -INFINITY && bin_of(x[e]) <= b) {
-                    const uint32_t at = atomicAdd(&sm.n_cand, 1u);
-                    if (at < (uint32_t)kFinCand)
-                        sm.cand[at] = ((unsigned long long)desc_key(x[e]) << 32) | (uint32_t)(col + e);
-                }
-            }
-        }
-    }
-    __syncthreads();
-    const int n = (int)sm.n_cand;
-    if (n > kFinCand) return leave_row(a, t);
-    sort_keys<kFinThreads>(sm.cand, n);
-
-    // ---- inclusive sums of the exact weights, in order
-    const int scale = fixed_scale(Sf * (1.f + 2.f * kSumError));
-    constexpr int kPer = kFinCand / kFinThreads;
-    {
-        uint64_t w[kPer], sum = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int at = threadIdx.x * kPer + i;
-            w[i] = at < n ? fixed_weight(key_logit((uint32_t)(sm.cand[at] >> 32)), M, c, scale, sm.table)
-                          : 0;
-            sum += w[i];
-        }
-        uint64_t wb, unused;
-        block_scan<kFinThreads, uint64_t>(sm.scratch, sum, 0, wb, unused);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            wb += w[i];
-            if (threadIdx.x * kPer + i < n) sm.weight[threadIdx.x * kPer + i] = wb;
-        }
-    }
-    __syncthreads();
-
-    // ---- how many are kept; n + 1 where a filter keeps all of these or more
-    auto first_mass = [&](double target) {  // first i with weight[i] >= target, n if none
-        int lo = 0, hi = n;
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if ((double)sm.weight[mid] >= target)
-                hi = mid;
-            else
-                lo = mid + 1;
-        }
-        return lo;
-    };
-    int keep = n + 1;
-    if (rs.cut_m) {
-        const uint32_t km = desc_key(z_min);
-        int lo = 0, hi = n;
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if ((uint32_t)(sm.cand[mid] >> 32) > km)
-                hi = mid;
-            else
-                lo = mid + 1;
-        }
-        if (lo < n || b >= bin_m) keep = lo;
-    }
-    if (rs.cut_p) {
-        if (rs.cut_k) {
-            if (n < k) return leave_row(a, t);
-            keep = min(keep, min(k, 1 + first_mass((double)rs.top_p * (double)sm.weight[k - 1])));
-        } else {
-            const double one = (double)(1ull << scale);
-            const double target = (double)rs.top_p * (double)Sf * one;
-            const int i0 = first_mass(target * (1.0 - (double)kSumError));
-            const int i1 = first_mass(target * (1.0 + (double)kSumError));
-            if (keep > i0) {  // else min-p ends before the nucleus can
-                if (i0 != i1 || i0 == n) return leave_row(a, t);
-                keep = i0 + 1;
-            }
-        }
-    } else if (rs.cut_k && n >= k) {
-        keep = min(keep, k);
-    }
-    if (keep > n) return leave_row(a, t);
-
-    const uint64_t S = sm.weight[keep - 1];
-    const float lnS = fixed_log(S, scale);
-    if (!kSample) {
-        float ux = 0.f;
-        for (int i = threadIdx.x; i < keep; i += kFinThreads) {
-            const uint64_t w = sm.weight[i] - (i ? sm.weight[i - 1] : 0);
-            const float x = (key_logit((uint32_t)(sm.cand[i] >> 32)) - M) / rs.temp;
-            if (w) ux = fmaf((float)w * __int_as_float((127 - scale) << 23), x, ux);
-        }
-#pragma unroll
-        for (int off = 16; off; off >>= 1) ux += __shfl_xor_sync(0xFFFFFFFFu, ux, off);
-        float* part = reinterpret_cast<float*>(sm.scratch);
-        if (lane == 0) part[threadIdx.x >> 5] = ux;
         __syncthreads();
-        if (threadIdx.x == 0) {
-            float U = 0.f;
-            for (int w = 0; w < kFinThreads / 32; ++w) U += part[w];
-            const unsigned long long cut = sm.cand[keep - 1];
-            const float Sr = (float)S * __int_as_float((127 - scale) << 23);
-            write_statistics(a, t, row, M, lnS, lnS - U / Sr, rs.temp, (uint32_t)(cut >> 32),
-                             (uint32_t)cut);
-        }
-        return;
+        b = (int)sm.bin;
     }
-    // ---- draw: the kept columns in index order
+    // top-p after top-k needs the whole top-k mass, so min-p may not shorten it
+    if (!r.all) {
+        if (!(rs.cut_k && rs.cut_p)) b = min(b, bin_m);
+        if (b >= kFinBins - 1) return leave_row(a, t);
+    }
+    r.all_min = rs.cut_m && b >= bin_m;
+
+    // ---- gather.  bin_of(z) <= b  <=>  (M - z) bin_scale < b + 1
+    const float edge = r.all ? INFINITY : (float)(b + 1);
+    int n_vec;  // vectors of kVec columns to look through
+    if (r.all) {
+        n_vec = (V + kVec - 1) / kVec;
+    } else {
+        for_each_group(gm, groups, [&](int i, float g) {
+            if (g > -INFINITY && (M - g) * bin_scale < edge) {
+                const uint32_t at = atomicAdd(&sm.n_group, 1u);
+                if (at < (uint32_t)kFinGroups) sm.group[at] = (uint16_t)i;
+            }
+        });
+        __syncthreads();
+        const int n_group = (int)sm.n_group;
+        if (n_group > kFinGroups) return leave_row(a, t);
+        n_vec = n_group * kVecPerLane;
+    }
+    // One vector per thread, four ahead; what passes is rare, so it is picked
+    // out of a bit mask and read again.
+    constexpr int kAhead = 4;
+    for (int i0 = threadIdx.x; i0 < n_vec; i0 += kAhead * kFinThreads) {
+        float x[kAhead][kVec];
+        int col[kAhead];
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h) {
+            const int i = i0 + h * kFinThreads;
+            if (r.all) {
+                col[h] = i * kVec;
+            } else {
+                const int g = sm.group[min(i, n_vec - 1) / kVecPerLane], j = i % kVecPerLane;
+                col[h] = (g >> 5) * Elem<E>::kChunk + ((g & 31) + 32 * j) * kVec;
+            }
+            if (i >= n_vec) col[h] = V;
+        }
+        load_columns<E, kAhead>(row, col, V, x);
+        uint32_t hits = 0;
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e)
+                hits |= (uint32_t)(x[h][e] > -INFINITY && (r.all || (M - x[h][e]) * bin_scale < edge))
+                        << (h * kVec + e);
+        if (hits == 0) continue;
+        uint32_t at = atomicAdd(&sm.n_cand, (uint32_t)__popc(hits));
+#pragma unroll 1
+        for (; hits; hits &= hits - 1, ++at) {
+            const int bit = __ffs(hits) - 1, h = bit / kVec;
+            const int c = (h == 0 ? col[0] : h == 1 ? col[1] : h == 2 ? col[2] : col[3]) + bit % kVec;
+            if (at < (uint32_t)kFinCand)
+                sm.cand[at] = ((unsigned long long)desc_key(Elem<E>::to_float(row[c])) << 32) |
+                              (uint32_t)c;
+        }
+    }
     __syncthreads();
-    for (int i = threadIdx.x; i < keep; i += kFinThreads)
-        sm.cand[i] = (sm.cand[i] << 32) | (uint32_t)i;
-    sort_keys<kFinThreads>(sm.cand, keep);
-    const double target = (double)rs.u * (double)S;
-    uint64_t w[kPer], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int at = threadIdx.x * kPer + i;
-        w[i] = 0;
-        if (at < keep) {
-            const uint32_t from = (uint32_t)sm.cand[at];
-            w[i] = sm.weight[from] - (from ? sm.weight[from - 1] : 0);
-        }
-        sum += w[i];
-    }
-    uint64_t wb, unused;
-    block_scan<kFinThreads, uint64_t>(sm.scratch, sum, 0, wb, unused);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int at = threadIdx.x * kPer + i;
-        const uint64_t w1 = wb + w[i];
-        // u = 0 takes the first kept column, however small its weight
-        if (at < keep && (rs.u == 0.f ? at == 0 : ((double)wb <= target && (double)w1 > target))) {
-            const int col = (int)(sm.cand[at] >> 32);
-            a.token[t] = col;
-            a.logprob[t] = (Elem<E>::to_float(row[col]) - M) / rs.temp - lnS;
-        }
-        wb = w1;
-    }
+    r.n = (int)sm.n_cand;
+    if (r.n > kFinCand || (rs.cut_p && r.k > r.n && !r.all)) return leave_row(a, t);
+    r.scale = fixed_scale(Sf * (1.f + 2.f * kSumError));
+    if (r.n <= kFinThreads)
+        finish_few<E, kSample>(a, row, r, sm);
+    else
+        finish_many<E, kSample>(a, row, r, sm);
 }
 
 // ---------------------------------------------------------------------------
@@ -1040,7 +1490,7 @@ __global__ void __launch_bounds__(kFinThreads)
 // ---------------------------------------------------------------------------
 template <typename E, bool kSample>
 __device__ void exact_row(const FilterArgs& a, int64_t t, Team<E>& tm, ExactShared& sm,
-                          ExactShared& lead, cg::cluster_group& cluster) {
+                          ExactShared& lead) {
     const int V = (int)a.V, lane = threadIdx.x & 31;
     const bool first = tm.first;
     const E* row = tm.row;
@@ -1052,61 +1502,59 @@ __device__ void exact_row(const FilterArgs& a, int64_t t, Team<E>& tm, ExactShar
     tm.bin_scale = tm.c.ch * ((float)kBins / 64.f);
     tm.k = fixed_scale(st.y * (1.f + 2.f * kSumError));
     if (threadIdx.x == 0) {
-        sm.n_min = 0;
+        sm.n_min = sm.n_finite = 0;
+        sm.total = 0;
         sm.first = sm.first_kept = 0xFFFFFFFFu;
     }
-    cluster.sync();
+    tm.sync();
 
     const float z_min = min_p_logit(M, rs);
     uint32_t cut_key = 0xFFFFFFFFu, cut_index = (uint32_t)V - 1;
     if (rs.cut_k || rs.cut_p || (rs.cut_m && !kSample)) {
-        tm.clear(sm.level0);
-        uint32_t n_min = 0;
-        tm.each([&](int, float z) {
-            if (z == -INFINITY) return;
-            const int b = tm.bin0(z);
-            atomicAdd(&sm.level0.count[b], 1u);
-            const uint64_t w = tm.weight(z);
-            if (w) atomicAdd(&sm.level0.mass[b], (unsigned long long)w);
-            n_min += z >= z_min;
+        // Counts of the level-0 bins, and the whole mass where top-p refers to it.
+        for (int i = threadIdx.x; i < kBins; i += kExThreads) sm.level0[i] = 0;
+        __syncthreads();
+        uint32_t n_min = 0, n_fin = 0;
+        uint64_t mass = 0;
+        const bool weigh = rs.cut_p;
+        tm.each_vector([&](int, const float (&x)[Elem<E>::kVec]) {
+#pragma unroll
+            for (int e = 0; e < Elem<E>::kVec; ++e) {
+                if (x[e] > -INFINITY) {
+                    atomicAdd(&sm.level0[tm.bin0(x[e])], 1u);
+                    n_min += x[e] >= z_min;
+                    ++n_fin;
+                }
+            }
+            if (weigh)
+#pragma unroll
+                for (int e = 0; e < Elem<E>::kVec; ++e) mass += tm.weight(x[e]);
         });
         n_min = __reduce_add_sync(0xFFFFFFFFu, n_min);
-        if (lane == 0) atomicAdd(&lead.n_min, n_min);
-        tm.merge(&ExactShared::level0);
-        if (first) {
-            uint64_t n = 0, w = 0, nb, wb;
-            for (int i = threadIdx.x; i < kBins; i += kExThreads) {
-                n += sm.level0.count[i];
-                w += sm.level0.mass[i];
-            }
-            block_scan<kExThreads, uint64_t>(sm.scratch, n, w, nb, wb);
-            if (threadIdx.x == kExThreads - 1) {
-                sm.sel.rank = (uint32_t)(nb + n);
-                sm.sel.mass = wb + w;
-            }
+        n_fin = __reduce_add_sync(0xFFFFFFFFu, n_fin);
+        if (lane == 0) {
+            atomicAdd(&lead.n_min, n_min);
+            atomicAdd(&lead.n_finite, n_fin);
         }
-        cluster.sync();
-        const uint32_t n_finite = lead.sel.rank;
-        uint64_t total = lead.sel.mass;
+        tm.add_to(&lead.total, mass);
+        tm.merge(sm.level0, lead.level0);
+        const uint32_t n_finite = lead.n_finite;
+        uint64_t total = lead.total;
         const uint32_t n_keep_min = rs.cut_m ? lead.n_min : n_finite;
-        cluster.sync();
         uint32_t want = rs.cut_k && rs.top_k < (int64_t)n_finite ? (uint32_t)rs.top_k : n_finite;
-        Selection sel;
+        Selected sel;
         bool have = false;
         if (rs.cut_p) {
-            if (want < n_finite) total = tm.select(true, want, 0.0).mass;
-            cluster.sync();
-            sel = tm.select(false, 0, (double)rs.top_p * (double)total);
+            if (want < n_finite) total = tm.select(true, want, 0).mass;
+            // C >= p S in whole numbers; at least 1, so that a token is kept
+            const uint64_t target = __double2ull_ru((double)rs.top_p * (double)total);
+            sel = tm.select(false, 0, target ? target : 1);
             want = sel.rank;
             have = n_keep_min >= want;
-            cluster.sync();
         }
-        if (!have) {
-            sel = tm.select(true, min(want, n_keep_min), 0.0);
-            cluster.sync();
-        }
-        cut_key = sel.key;
-        cut_index = sel.index;
+        if (!have) sel = tm.select(true, min(want, n_keep_min), 0);
+        cut_key = (uint32_t)(sel.key >> 32);
+        cut_index = (uint32_t)sel.key;
     } else if (rs.cut_m) {
         cut_key = desc_key(z_min);
     }
@@ -1114,19 +1562,34 @@ __device__ void exact_row(const FilterArgs& a, int64_t t, Team<E>& tm, ExactShar
     // Kept mass (and sum of e x) of every span of the index order.
     const int spans = (V + kSpan - 1) / kSpan;
     uint32_t lowest = 0xFFFFFFFFu;
+    const float inv_t = 1.f / rs.temp;
+    constexpr int kVec = Elem<E>::kVec, kVecs = kSpan / (32 * kVec);
     for (int s = tm.thread >> 5; s < spans; s += tm.threads >> 5) {
         uint64_t w = 0;
         float ux = 0.f;
-        const int c1 = min(V, (s + 1) * kSpan);
-        for (int col = s * kSpan + lane; col < c1; col += 32) {
-            const float z = Elem<E>::to_float(row[col]);
-            if (is_kept(z, col, cut_key, cut_index)) {
-                const uint64_t e = tm.weight(z);
-                w += e;
-                if (z > -INFINITY) lowest = min(lowest, (uint32_t)col);
-                if (!kSample && e)
-                    ux = fmaf((float)e * __int_as_float((127 - tm.k) << 23), (z - M) / rs.temp, ux);
-            }
+        constexpr int kAhead = 2;
+#pragma unroll 1
+        for (int j0 = 0; j0 < kVecs; j0 += kAhead) {
+            int at[kAhead];
+            float x[kAhead][kVec];
+#pragma unroll
+            for (int h = 0; h < kAhead; ++h) at[h] = s * kSpan + ((j0 + h) * 32 + lane) * kVec;
+            load_columns<E, kAhead>(row, at, V, x);
+#pragma unroll
+            for (int h = 0; h < kAhead; ++h)
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) {
+                    const int col = at[h] + i;
+                    const float z = x[h][i];
+                    const bool kept = z > -INFINITY && is_kept(z, col, cut_key, cut_index);
+                    const uint64_t e = kept ? tm.weight(z) : 0;
+                    w += e;
+                    if (kSample)
+                        lowest = min(lowest, kept ? (uint32_t)col : 0xFFFFFFFFu);
+                    else if (e)
+                        ux = fmaf((float)e * __int_as_float((127 - tm.k) << 23), (z - M) * inv_t,
+                                  ux);
+                }
         }
         w = warp_sum(w);
         if (!kSample) {
@@ -1142,13 +1605,18 @@ __device__ void exact_row(const FilterArgs& a, int64_t t, Team<E>& tm, ExactShar
         lowest = __reduce_min_sync(0xFFFFFFFFu, lowest);
         if (lane == 0) atomicMin(&lead.first_kept, lowest);
     }
-    cluster.sync();
+    tm.sync();
     if (!first) return;
 
-    const uint64_t mine = (int)threadIdx.x < spans ? sm.span_mass[threadIdx.x] : 0;
+    uint64_t mine[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int s = 2 * (int)threadIdx.x + i;
+        mine[i] = s < spans ? sm.span_mass[s] : 0;
+    }
     uint64_t before, unused;
-    block_scan<kExThreads, uint64_t>(sm.scratch, mine, 0, before, unused);
-    if (threadIdx.x == kExThreads - 1) sm.mass_before = before + mine;
+    block_scan<kExThreads, uint64_t>(sm.scratch, mine[0] + mine[1], 0, before, unused);
+    if (threadIdx.x == kExThreads - 1) sm.mass_before = before + mine[0] + mine[1];
     __syncthreads();
     const uint64_t S = sm.mass_before;
     const float lnS = fixed_log(S, tm.k);
@@ -1169,11 +1637,16 @@ __device__ void exact_row(const FilterArgs& a, int64_t t, Team<E>& tm, ExactShar
         }
         return;
     }
-    const double target = (double)rs.u * (double)S;
+    // C > u S in whole numbers
+    const uint64_t target = __double2ull_rd((double)rs.u * (double)S);
     __syncthreads();
-    if ((double)before <= target && (double)(before + mine) > target) {
-        sm.first = threadIdx.x;
-        sm.mass_before = before;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (before <= target && before + mine[i] > target) {
+            sm.first = 2 * threadIdx.x + i;
+            sm.mass_before = before;
+        }
+        before += mine[i];
     }
     __syncthreads();
     constexpr int kPer = kSpan / kExThreads;
@@ -1192,12 +1665,11 @@ __device__ void exact_row(const FilterArgs& a, int64_t t, Team<E>& tm, ExactShar
     block_scan<kExThreads, uint64_t>(sm.scratch, sum, 0, wb, unused);
     wb += base;
     for (int i = 0; i < kPer; ++i) {
-        const uint64_t w1 = wb + w[i];
-        if (w[i] && (double)wb <= target && (double)w1 > target) {
+        if (wb <= target && wb + w[i] > target) {
             a.token[t] = c0 + i;
             a.logprob[t] = (Elem<E>::to_float(row[c0 + i]) - M) / rs.temp - lnS;
         }
-        wb = w1;
+        wb += w[i];
     }
 }
 
@@ -1208,17 +1680,22 @@ __global__ void __launch_bounds__(kExThreads)
     cg::cluster_group cluster = cg::this_cluster();
     ExactShared& sm = *reinterpret_cast<ExactShared*>(smem_raw);
     ExactShared& lead = *cluster.map_shared_rank(&sm, 0);
-    const int team = (int)cluster.num_blocks();
     const int n = *a.left_count;
-    if (threadIdx.x < 64) sm.table[threadIdx.x] = a.table.v[threadIdx.x];
+    if (n == 0) return;
+    if (threadIdx.x < 64) sm.table[threadIdx.x] = kExp2Table[threadIdx.x];
     __syncthreads();
+    // A cluster to a row, or, with more rows than a few for every cluster, a
+    // CTA: what a team saves in a pass it loses again in synchronisation.
+    const bool alone = n >= 4 * (int)(gridDim.x / cluster.num_blocks());
+    const int team = alone ? 1 : (int)cluster.num_blocks();
+    const int rank = alone ? 0 : (int)cluster.block_rank();
     for (int i = blockIdx.x / team; i < n; i += gridDim.x / team) {
         const int64_t t = a.left[i];
-        Team<E> tm{sm, lead, cluster, static_cast<const E*>(a.logits) + t * a.ld, (int)a.V,
-                   (int)(cluster.block_rank() * kExThreads + threadIdx.x), team * kExThreads,
-                   cluster.block_rank() == 0, 0.f, {0.f, 0.f}, 0, 0.f};
-        exact_row<E, kSample>(a, t, tm, sm, lead, cluster);
-        cluster.sync();  // the next row writes what this one reads
+        Team<E> tm{sm, alone ? sm : lead, cluster, static_cast<const E*>(a.logits) + t * a.ld,
+                   (int)a.V, rank * kExThreads + (int)threadIdx.x, team * kExThreads, rank == 0,
+                   alone, 0.f, {0.f, 0.f}, 0, 0.f};
+        exact_row<E, kSample>(a, t, tm, sm, tm.lead);
+        tm.sync();  // the next row writes what this one reads
     }
 }
 
@@ -1414,20 +1891,6 @@ cudaError_t launch_filtered_backward(const void* logits, int64_t T, int64_t V, i
     return cudaGetLastError();
 }
 
-ExpTable make_table() {
-    ExpTable t;
-    for (int j = 0; j < 64; ++j) {
-        const double v = std::exp2(-j / 64.0);
-        t.v[j].x = (float)v;
-        t.v[j].y = (float)(v - (double)t.v[j].x);
-    }
-    return t;
-}
-const ExpTable& exp_table() {
-    static const ExpTable t = make_table();
-    return t;
-}
-
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 struct FilterWorkspace {
@@ -1491,7 +1954,6 @@ FilterArgs filter_args(const void* logits, pstat_dtype dt, int64_t T, int64_t V,
     a.top_ps = f->top_ps;
     a.min_ps = f->min_ps;
     a.dev_error = dev_error;
-    a.table = exp_table();
     return a;
 }
 
