@@ -212,7 +212,7 @@ def test_binding_refusals(lib):
             pstat._filters(bad, 0, 1.0, 0.0, T, cpu)
     with pytest.raises(ValueError):
         pstat._filters(1.0, torch.ones(T, dtype=torch.int64), 1.0, 0.0, T, cpu)
-    f = pstat._filters(0.5, 7, 0.9, torch.zeros(T), T, cpu)
+    f = pstat._filters(0.5, 7, 0.9, torch.zeros(T), T, cpu)._obj
     assert f.temperature == 0.5 and f.top_k == 7 and f.min_ps and not f.top_ps
     with pytest.raises(ValueError):
         pstat._filtered_outputs((torch.empty(T), torch.empty(T), torch.empty(T, 2), torch.empty(T),

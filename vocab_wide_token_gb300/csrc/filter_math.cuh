@@ -303,19 +303,26 @@ constexpr float kSumError = 1.f / 262144.f;
 // NaN M where a record is bad, -inf where every logit is masked.
 __device__ __forceinline__ float3 fold_records(const float4* __restrict__ rec, int n, float c,
                                                int lane) {
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = max_nan(M, rec[i].x);
+    // The usual rows have at most 64 chunks: both of a lane's records are loaded
+    // before either is used.
+    const float4 none = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    const float4 r0 = lane < n ? rec[lane] : none;
+    const float4 r1 = lane + 32 < n ? rec[lane + 32] : none;
+    float M = max_nan(r0.x, r1.x);
+    for (int i = lane + 64; i < n; i += 32) M = max_nan(M, rec[i].x);
     M = warp_max_nan(M);
     float S = 0.f, U = 0.f;
     if (M > -INFINITY) {
-        for (int i = lane; i < n; i += 32) {
-            const float4 r = rec[i];
-            if (r.x == -INFINITY) continue;
+        auto add = [&](const float4& r) {
+            if (r.x == -INFINITY) return;
             const float a = fmaf(r.x - M, c, -r.w);
             const float f = exp2f(a);
             S = fmaf(r.y, f, S);
             U = fmaf(f, fmaf(fmaxf(a, -1024.f), r.y, r.z), U);
-        }
+        };
+        add(r0);
+        add(r1);
+        for (int i = lane + 64; i < n; i += 32) add(rec[i]);
 #pragma unroll
         for (int off = 16; off; off >>= 1) {
             S += __shfl_xor_sync(0xFFFFFFFFu, S, off);

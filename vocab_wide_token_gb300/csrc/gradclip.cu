@@ -111,6 +111,7 @@ __device__ __forceinline__ double block_sum(double v) {
 template <int N>
 __global__ void __launch_bounds__(kGnThreads, 6)
     square_sums_kernel(const __grid_constant__ GradBatch<N> g, double* __restrict__ partial) {
+    grid_launch_dependents();
     const uint32_t u0 = (uint32_t)((uint64_t)g.units * blockIdx.x / gridDim.x);
     const uint32_t u1 = (uint32_t)((uint64_t)g.units * (blockIdx.x + 1) / gridDim.x);
     double sum = 0.0;
@@ -150,6 +151,7 @@ __device__ __forceinline__ double norm_of(const double* partial, int n) {
 __global__ void __launch_bounds__(kGnThreads)
     norm_kernel(const double* __restrict__ partial, int n, float* __restrict__ out,
                 int* __restrict__ dev_error) {
+    grid_wait();
     const float norm = (float)norm_of(partial, n);
     if (threadIdx.x == 0) {
         *out = norm;
@@ -162,6 +164,7 @@ __global__ void __launch_bounds__(kGnThreads)
     scale_kernel(const __grid_constant__ GradBatch<N> g, const double* __restrict__ partial, int n,
                  float max_norm, float* __restrict__ out, int* __restrict__ dev_error) {
     __shared__ float s_factor;
+    grid_wait();
     const double norm = norm_of(partial, n);
     if (threadIdx.x == 0) {
         const float f = (float)norm;
@@ -286,13 +289,17 @@ int run_norm(const pstat_tensor* tensors, int64_t n, bool clip, float max_norm, 
         n_partial += blocks;
     }
     if (!clip || n_partial == 0) {
-        norm_kernel<<<1, kGnThreads, 0, st>>>(partial, n_partial, out_norm, dev_error);
+        if (launch_behind(norm_kernel, 1, kGnThreads, 0, st, 1, (const double*)partial, n_partial,
+                          out_norm, dev_error) != cudaSuccess)
+            return PSTAT_ERR_CUDA;
     } else {
         for (int64_t i = 0; i < n;) {
             i += fill(g, tensors, i, n);
             if (g.units == 0) continue;
-            scale_kernel<N><<<blocks_for(g.units, dev), kGnThreads, 0, st>>>(
-                g, partial, n_partial, max_norm, out_norm, dev_error);
+            if (launch_behind(scale_kernel<N>, (unsigned)blocks_for(g.units, dev), kGnThreads, 0, st,
+                              1, g, (const double*)partial, n_partial, max_norm, out_norm,
+                              dev_error) != cudaSuccess)
+                return PSTAT_ERR_CUDA;
         }
     }
     return cudaGetLastError() == cudaSuccess ? PSTAT_OK : PSTAT_ERR_CUDA;

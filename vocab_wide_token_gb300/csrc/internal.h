@@ -66,6 +66,29 @@ struct ContextSeen {
 // device and context.
 cudaError_t ensure_smem_optin(const void* func, int bytes, ContextSeen& seen);
 
+// Launches `kernel` behind the stream's previous kernel by programmatic
+// dependent launch: its blocks may start early and call grid_wait() before they
+// touch anything that kernel writes.  `cluster` > 1 groups the blocks.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
+                          cudaStream_t stream, unsigned cluster, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Kernel launchers (stats_kernels.cu).  They assume validated arguments.
 cudaError_t launch_chunk_stats(const void* logits, pstat_dtype dt, int64_t T, int64_t ld,
                                const ShardPlan& plan, float4* chunk_stats, int* dev_error,

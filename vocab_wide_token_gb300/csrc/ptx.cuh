@@ -98,6 +98,15 @@ __device__ __forceinline__ uint64_t policy_evict_last() {
     return p;
 }
 
+// ---- programmatic dependent launch -----------------------------------------
+// wait: until the grid this one was launched behind has completed and its
+// memory is visible.  launch: lets the grid behind this one start (it waits
+// itself).  Both do nothing in a grid launched without the attribute.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---- packed f32x2 arithmetic (sm_100+) --------------------------------------
 __device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
     uint64_t r;

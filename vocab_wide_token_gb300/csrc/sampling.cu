@@ -16,6 +16,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "chunk_math.cuh"
 #include "filter_math.cuh"
@@ -31,11 +32,11 @@ constexpr int kExThreads = 512;
 constexpr int kExWarps = kExThreads / 32;
 constexpr int kBins = 2048;    // bins of one histogram level
 constexpr int kCand = 2048;    // elements that are sorted at once
-constexpr int kSpan = 1024;    // columns of one span of the index-order scan
+constexpr int kSpan = 256;     // columns of one span of the index-order scan, a warp's
 constexpr int kMaxSpans = (int)(kFilterMaxV / kSpan);
-static_assert(kBins % kExThreads == 0 && kCand % kExThreads == 0 && kSpan % kExThreads == 0 &&
-                  kMaxSpans <= 2 * kExThreads && kMaxSpans <= kBins,
-              "");
+constexpr int kSpansPer = kMaxSpans / kExThreads;
+static_assert(kBins % kExThreads == 0 && kMaxSpans % kExThreads == 0 && kSpan <= kExThreads, "");
+constexpr int kMaxTeam = 8;
 
 struct FilterArgs {
     const void* logits;
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     E* group_max = static_cast<E*>(a.group_max);
     const int V = (int)a.V, chunks = a.chunks;
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.left_count = 0;
+    grid_launch_dependents();
 
     const int64_t n_items = a.T * chunks;
     const int64_t gw = (int64_t)blockIdx.x * warps + warp;
@@ -329,6 +331,17 @@ __device__ __forceinline__ void load_columns(const E* row, const int (&col)[N], 
     }
 }
 
+// *p += v in shared memory.  64-bit adds there are compare-and-swap loops, which
+// crawl when lanes meet on one address; two 32-bit adds with the carry between
+// them are not (nobody reads the sum before the next barrier).
+__device__ __forceinline__ void add_wide(unsigned long long* p, uint64_t v) {
+    uint32_t* half = reinterpret_cast<uint32_t*>(p);
+    const uint32_t lo = (uint32_t)v, hi = (uint32_t)(v >> 32);
+    const uint32_t old = atomicAdd(half, lo);
+    const uint32_t carry = old + lo < old;
+    if (hi + carry) atomicAdd(half + 1, hi + carry);
+}
+
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 #pragma unroll
     for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
@@ -447,7 +460,7 @@ __device__ __noinline__ Selected list_select(ListShared<kThreads>& ls,
             uint32_t p;
             if (inside(keys[i], p)) {
                 atomicAdd(&ls.count[(p - lo) >> shift], 1u);
-                if (weights[i]) atomicAdd(&ls.mass[(p - lo) >> shift], weights[i]);
+                if (weights[i]) add_wide(&ls.mass[(p - lo) >> shift], weights[i]);
             }
         }
         __syncthreads();
@@ -517,24 +530,38 @@ __device__ __noinline__ Selected list_select(ListShared<kThreads>& ls,
     return found;
 }
 
+// e x in units of 2^-44, x in fp32: every term is at most 1/e, so that they add
+// up as integers, in any order.
+__device__ __forceinline__ long long entropy_term(unsigned long long key, uint64_t w, float M,
+                                                  float temp, int scale) {
+    const float x = (key_logit((uint32_t)(key >> 32)) - M) / temp;
+    const float e = (float)w * __int_as_float((127 - scale) << 23);
+    return w ? __float2ll_rn(e * x * 1.7592186e13f) : 0;
+}
+
+// C >= p S in whole numbers; at least 1, so that a token is kept.
+__device__ __forceinline__ uint64_t share_of(float p, uint64_t S) {
+    const uint64_t target = __double2ull_ru((double)p * (double)S);
+    return target ? target : 1;
+}
+
 struct ExactShared {
     uint32_t level0[kBins];
     Histogram level1;
     unsigned long long cand[kCand];
     unsigned long long weight[kCand];
     unsigned long long span_mass[kMaxSpans];
-    float span_u[kMaxSpans];
     float2 table[64];
     unsigned long long scratch[2 * kExWarps];
     ListShared<kExThreads> list;
     // Team results, in the first CTA of a cluster.
-    uint32_t n_min, n_finite;
+    unsigned long long part[kMaxTeam][3];
     uint32_t n_cand;
     uint32_t first;
     uint32_t first_kept;
     // Decisions that the first CTA announces.
     uint32_t klo, khi, n_in, count_before, bin;
-    unsigned long long mass_before, mass_in, total, offset;
+    unsigned long long mass_before, mass_in, total, offset, ux;
     Selected sel;
 };
 
@@ -550,10 +577,12 @@ struct Team {
     int V;
     int thread, threads;     // of the team
     bool first, alone;
-    float M;
+    bool entropy;            // the entropy's sum is wanted
+    float M, temp;
     TempScale c;
     int k;                   // digits of the fixed weights
     float bin_scale;
+    bool ties;               // the last selection ended among too many equal logits
 
     __device__ void sync() {
         if (alone)
@@ -561,19 +590,25 @@ struct Team {
         else
             cluster.sync();
     }
-    // f(first column, logits of one vector), columns past V as -inf.
+    // f(span, this lane's first column of it, its logits): a warp goes through a
+    // span of kSpan columns together, kVec neighbouring ones (twice, in fp32) to a
+    // lane; columns past V are -inf.
+    static constexpr int kLane = kSpan / 32;
     template <typename F>
-    __device__ __forceinline__ void each_vector(F f) const {
-        constexpr int kVec = Elem<E>::kVec, kAhead = 2;
-        for (int c0 = thread * kVec; c0 < V; c0 += kAhead * threads * kVec) {
-            int col[kAhead];
-            float x[kAhead][kVec];
+    __device__ __forceinline__ void each_span(F f) const {
+        constexpr int kVec = Elem<E>::kVec, kVecs = kLane / kVec;
+        const int lane = thread & 31, warps = threads >> 5;
+        for (int s = thread >> 5; s * kSpan < V; s += warps) {
+            int col[kVecs];
+            float part[kVecs][kVec], x[kLane];
 #pragma unroll
-            for (int h = 0; h < kAhead; ++h) col[h] = c0 + h * threads * kVec;
-            load_columns<E, kAhead>(row, col, V, x);
+            for (int h = 0; h < kVecs; ++h) col[h] = s * kSpan + lane * kLane + h * kVec;
+            load_columns<E, kVecs>(row, col, V, part);
 #pragma unroll
-            for (int h = 0; h < kAhead; ++h)
-                if (col[h] < V) f(col[h], x[h]);
+            for (int h = 0; h < kVecs; ++h)
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) x[h * kVec + e] = part[h][e];
+            f(s, col[0], x);
         }
     }
     __device__ uint64_t weight(float z) const { return fixed_weight(z, M, c, k, sm.table); }
@@ -581,10 +616,23 @@ struct Team {
     // and the product round monotonely, so bins are ranges of the order).
     __device__ int bin0(float z) const { return min(kBins - 1, __float2int_rd((M - z) * bin_scale)); }
 
-    // Adds one value per thread up over the team, into the first CTA's *to.
-    __device__ void add_to(unsigned long long* to, uint64_t v) const {
+    // Sum over the team of one value per thread, through slot `which` (of three):
+    // put() everywhere, sync(), then get() in any CTA.
+    __device__ void put(int which, uint64_t v) {
         v = warp_sum(v);
-        if ((threadIdx.x & 31) == 0 && v) atomicAdd(to, (unsigned long long)v);
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) sm.scratch[threadIdx.x >> 5] = v;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            uint64_t all = 0;
+            for (int i = 0; i < kExWarps; ++i) all += sm.scratch[i];
+            lead.part[thread / kExThreads][which] = all;
+        }
+    }
+    __device__ uint64_t get(int which) const {
+        uint64_t all = 0;
+        for (int i = 0; i < threads / kExThreads; ++i) all += lead.part[i][which];
+        return all;
     }
     __device__ void clear(Histogram& h) const {
         for (int i = threadIdx.x; i < kBins; i += kExThreads) {
@@ -601,7 +649,7 @@ struct Team {
         if (!first)
             for (int i = threadIdx.x; i < kBins; i += kExThreads) {
                 if (count[i]) atomicAdd(&all_count[i], count[i]);
-                if (mass && mass[i]) atomicAdd(&all_mass[i], mass[i]);
+                if (mass && mass[i]) add_wide(&all_mass[i], mass[i]);
             }
         sync();
     }
@@ -703,43 +751,86 @@ struct Team {
         }
     }
 
-    // One pass: the exact masses before and inside the keys [klo, khi], and the
-    // elements inside, as far as they fit.
-    __device__ __noinline__ void weigh_and_gather(uint32_t klo, uint32_t khi) {
-        if (first && threadIdx.x == 0) {
-            sm.n_cand = 0;
-            sm.mass_before = sm.mass_in = 0;
-        }
+    // One pass: the exact masses before and inside the keys [klo, khi], what lies
+    // before by spans of the index order, and the elements inside, as far as
+    // they fit; with `all` the mass of the whole row as well.
+    __device__ __noinline__ void weigh_and_gather(uint32_t klo, uint32_t khi, bool all) {
+        if (first && threadIdx.x == 0) sm.n_cand = 0;
         sync();
-        uint64_t before = 0, inside = 0;
-        each_vector([&](int col, const float (&x)[Elem<E>::kVec]) {
-            bool any = false;
+        uint64_t outside = 0, inside = 0, ux = 0;
+        // in registers: this function writes memory that could be *this
+        const float M = this->M, temp = this->temp;
+        const TempScale c = this->c;
+        const int k = this->k;
+        const bool entropy = this->entropy;
+        const E* const row = this->row;
+        ExactShared& lead = this->lead;
+        const float2* const table = sm.table;
+        auto weight = [&](float z) { return fixed_weight(z, M, c, k, table); };
+        each_span([&](int s, int col, const float (&x)[kLane]) {
+            bool any = all;
 #pragma unroll
-            for (int e = 0; e < Elem<E>::kVec; ++e) any |= desc_key(x[e]) <= khi;
-            if (!any) return;
+            for (int e = 0; e < kLane; ++e) any |= desc_key(x[e]) <= khi;
+            uint64_t before = 0;
+            uint32_t hits = 0;
+            if (__any_sync(0xFFFFFFFFu, any)) {
 #pragma unroll
-            for (int e = 0; e < Elem<E>::kVec; ++e) {
-                const uint32_t dk = desc_key(x[e]);
-                const uint64_t w = weight(x[e]);
-                before += dk < klo ? w : 0;
-                if (dk >= klo && dk <= khi) {
+                for (int e = 0; e < kLane; ++e) {
+                    const uint32_t dk = desc_key(x[e]);
+                    const uint64_t w = weight(x[e]);
+                    before += dk < klo ? w : 0;
+                    outside += dk > khi ? w : 0;
+                    hits |= (uint32_t)(dk >= klo && dk <= khi) << e;
+                    if (entropy && dk < klo)
+                        ux += (uint64_t)entropy_term((unsigned long long)dk << 32, w, M, temp, k);
+                }
+                before = warp_sum(before);
+            }
+            if ((threadIdx.x & 31) == 0) lead.span_mass[s] = before;
+            if (hits) {
+                uint32_t at = atomicAdd(&lead.n_cand, (uint32_t)__popc(hits));
+#pragma unroll 1
+                for (; hits; hits &= hits - 1, ++at) {
+                    const int c = col + __ffs(hits) - 1;
+                    const float z = Elem<E>::to_float(row[c]);
+                    const uint64_t w = weight(z);
                     inside += w;
-                    const uint32_t at = atomicAdd(&lead.n_cand, 1u);
                     if (at < (uint32_t)kCand) {
-                        lead.cand[at] = ((unsigned long long)dk << 32) | (uint32_t)(col + e);
+                        lead.cand[at] = ((unsigned long long)desc_key(z) << 32) | (uint32_t)c;
                         lead.weight[at] = w;
                     }
                 }
             }
         });
-        add_to(&lead.mass_before, before);
-        add_to(&lead.mass_in, inside);
+        put(0, inside);
+        if (all) put(1, outside);
+        if (entropy) put(2, ux);
+        sync();
+        if (first) {
+            uint64_t before = 0;
+            for (int i = threadIdx.x; i * kSpan < V; i += kExThreads) before += sm.span_mass[i];
+            before = warp_sum(before);
+            if ((threadIdx.x & 31) == 0) sm.scratch[threadIdx.x >> 5] = before;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                before = 0;
+                for (int i = 0; i < kExWarps; ++i) before += sm.scratch[i];
+                sm.mass_before = before;
+                sm.mass_in = get(0);
+                sm.total = before + sm.mass_in + (all ? get(1) : 0);
+                sm.ux = entropy ? get(2) : 0;
+            }
+        }
         sync();
     }
 
     // The element at which the count reaches `want`, or the mass `target`, in
-    // the order of the finite logits, all of which level0 counts.
-    __device__ __noinline__ Selected select(bool by_count, uint32_t want, uint64_t target) {
+    // the order of the finite logits, all of which level0 counts.  With `share`
+    // the target is that share of the whole mass, which this takes as well;
+    // `target` is then an estimate.  Afterwards, unless `ties`, the spans hold
+    // the mass of what was kept.
+    __device__ __noinline__ Selected select(bool by_count, uint32_t want, uint64_t target,
+                                            float share = 0.f) {
         if (first) {
             if (threadIdx.x == 0) {
                 sm.count_before = 0;
@@ -754,8 +845,9 @@ struct Team {
         sync();
         uint32_t klo = lead.klo, khi = lead.khi, n_in = lead.n_in;
         int b = (int)lead.bin, lo = 0, hi = kBins - 1;
-        weigh_and_gather(klo, khi);
+        weigh_and_gather(klo, khi, share > 0.f);
         if (!by_count) {
+            if (share > 0.f) target = share_of(share, lead.total);
             // A guess that missed narrows the bins that are left, so this ends.
             while (true) {
                 const uint64_t before = lead.mass_before, in = lead.mass_in;
@@ -777,7 +869,7 @@ struct Team {
                 khi = lead.khi;
                 n_in = lead.n_in;
                 b = (int)lead.bin;
-                weigh_and_gather(klo, khi);
+                weigh_and_gather(klo, khi, false);
             }
         }
         bool narrowed = false;
@@ -787,14 +879,19 @@ struct Team {
             while (((khi - klo) >> shift) >= (uint32_t)kBins) ++shift;
             sync();
             clear(sm.level1);
-            each_vector([&](int, const float (&x)[Elem<E>::kVec]) {
+            each_span([&](int, int col, const float (&x)[kLane]) {
+                uint32_t hits = 0;
+#pragma unroll
+                for (int e = 0; e < kLane; ++e)
+                    hits |= (uint32_t)(desc_key(x[e]) >= klo && desc_key(x[e]) <= khi) << e;
 #pragma unroll 1
-                for (int e = 0; e < Elem<E>::kVec; ++e) {
-                    const uint32_t dk = desc_key(x[e]);
-                    if (dk >= klo && dk <= khi) {
+                for (; hits; hits &= hits - 1) {
+                    const float z = Elem<E>::to_float(row[col + __ffs(hits) - 1]);
+                    const uint32_t dk = desc_key(z);
+                    {
                         const int i = (int)((dk - klo) >> shift);
                         atomicAdd(&sm.level1.count[i], 1u);
-                        atomicAdd(&sm.level1.mass[i], (unsigned long long)weight(x[e]));
+                        add_wide(&sm.level1.mass[i], weight(z));
                     }
                 }
             });
@@ -813,13 +910,14 @@ struct Team {
             khi = lead.khi;
             n_in = lead.n_in;
         }
-        if (n_in > kCand) {
+        ties = n_in > kCand;
+        if (ties) {
             sync();
             select_tie(klo, by_count, want, target);
         } else {
             if (narrowed) {
                 sync();
-                weigh_and_gather(klo, khi);
+                weigh_and_gather(klo, khi, false);
             }
             if (first) {
                 const Selected f = list_select<kExThreads>(
@@ -827,6 +925,14 @@ struct Team {
                     (unsigned long long)klo << 32, (unsigned long long)khi << 32 | 0xFFFFFFFFu,
                     false, by_count, want, target, sm.count_before, sm.mass_before);
                 if (threadIdx.x == 0) sm.sel = f;
+                // what is kept of the candidates joins the spans
+                for (int i = threadIdx.x; i < min((int)sm.n_cand, kCand); i += kExThreads) {
+                    if (sm.cand[i] > f.key) continue;
+                    const uint64_t w = sm.weight[i];
+                    add_wide(&sm.span_mass[(uint32_t)sm.cand[i] / kSpan], w);
+                    if (entropy)
+                        add_wide(&sm.ux, (uint64_t)entropy_term(sm.cand[i], w, M, temp, k));
+                }
             }
         }
         sync();
@@ -838,13 +944,14 @@ struct Team {
     // Many equal logits: how many of them are taken follows from their common
     // weight; the last one taken is found by counting them in index order.
     __device__ void select_tie(uint32_t key, bool by_count, uint32_t want, uint64_t target) {
-        clear(sm.level1);
-        each_vector([&](int col, const float (&x)[Elem<E>::kVec]) {
+        each_span([&](int s, int, const float (&x)[kLane]) {
+            uint32_t n = 0;
 #pragma unroll
-            for (int e = 0; e < Elem<E>::kVec; ++e)
-                if (desc_key(x[e]) == key) atomicAdd(&sm.level1.count[(col + e) / kSpan], 1u);
+            for (int e = 0; e < kLane; ++e) n += desc_key(x[e]) == key;
+            n = __reduce_add_sync(0xFFFFFFFFu, n);
+            if ((threadIdx.x & 31) == 0) lead.span_mass[s] = n;
         });
-        merge(sm.level1.count, lead.level1.count);
+        sync();
         if (!first) return;
         const uint64_t w = weight(key_logit(key));
         const uint32_t before = sm.count_before, n_in = sm.n_in;
@@ -866,38 +973,30 @@ struct Team {
         }
         __syncthreads();
         const int spans = (V + kSpan - 1) / kSpan;
-        uint64_t nb, unused;
-        uint64_t mine[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int s = 2 * (int)threadIdx.x + i;
-            mine[i] = s < spans ? sm.level1.count[s] : 0;
+        uint64_t nb, unused, mine = 0;
+        for (int i = 0; i < kSpansPer; ++i) {
+            const int s = kSpansPer * (int)threadIdx.x + i;
+            mine += s < spans ? sm.span_mass[s] : 0;
         }
-        block_scan<kExThreads, uint64_t>(sm.scratch, mine[0] + mine[1], 0, nb, unused);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (nb < take && take <= nb + mine[i]) {
-                sm.first = 2 * threadIdx.x + i;
+        block_scan<kExThreads, uint64_t>(sm.scratch, mine, 0, nb, unused);
+        for (int i = 0; i < kSpansPer; ++i) {
+            const int s = kSpansPer * (int)threadIdx.x + i;
+            const uint64_t n = s < spans ? sm.span_mass[s] : 0;
+            if (nb < take && take <= nb + n) {
+                sm.first = (uint32_t)s;
                 sm.n_in = (uint32_t)nb;
             }
-            nb += mine[i];
+            nb += n;
         }
         __syncthreads();
-        constexpr int kPer = kSpan / kExThreads;
-        const int c0 = (int)sm.first * kSpan + threadIdx.x * kPer;
+        const int c = (int)sm.first * kSpan + (int)threadIdx.x;
         const uint64_t skipped = sm.n_in;
-        uint32_t hit = 0;
-        for (int i = 0; i < kPer; ++i)
-            if (c0 >= 0 && c0 + i < V && desc_key(Elem<E>::to_float(row[c0 + i])) == key)
-                hit |= 1u << i;
-        block_scan<kExThreads, uint64_t>(sm.scratch, __popc(hit), 0, nb, unused);
-        nb += skipped;
-        for (int i = 0; i < kPer; ++i) {
-            if (!(hit >> i & 1u)) continue;
-            if (++nb == take)
-                sm.sel = {(unsigned long long)key << 32 | (uint32_t)(c0 + i), before + take,
-                          mass_before + (uint64_t)take * w};
-        }
+        const bool hit = (int)threadIdx.x < kSpan && c >= 0 && c < V &&
+                         desc_key(Elem<E>::to_float(row[c])) == key;
+        block_scan<kExThreads, uint64_t>(sm.scratch, hit ? 1 : 0, 0, nb, unused);
+        if (hit && skipped + nb + 1 == take)
+            sm.sel = {(unsigned long long)key << 32 | (uint32_t)c, before + take,
+                      mass_before + (uint64_t)take * w};
         __syncthreads();
     }
 };
@@ -938,6 +1037,13 @@ struct Candidate {
     unsigned long long weight;
 };
 
+// What a row without filters needs.
+struct DrawShared {
+    float prefix[kMaxChunks];
+    unsigned long long scratch[2 * (kFinThreads / 32)];
+    uint32_t bin, found;
+};
+
 struct FinishShared {
     union {
         struct {
@@ -964,9 +1070,9 @@ __device__ __forceinline__ void leave_row(const FilterArgs& a, int64_t t) {
     if (threadIdx.x == 0) a.left[atomicAdd(a.left_count, 1)] = (int)t;
 }
 
-template <typename E>
+template <typename E, typename Shared>
 __device__ void finish_greedy(const FilterArgs& a, int64_t t, const E* row, const float4* rec,
-                              float M, FinishShared& sm) {
+                              float M, Shared& sm) {
     constexpr int kChunk = Elem<E>::kChunk;
     if (threadIdx.x == 0) sm.bin = sm.found = 0xFFFFFFFFu;
     __syncthreads();
@@ -986,10 +1092,9 @@ __device__ void finish_greedy(const FilterArgs& a, int64_t t, const E* row, cons
     }
 }
 
-template <typename E>
+template <typename E, typename Shared>
 __device__ void finish_draw(const FilterArgs& a, int64_t t, const E* row, const float4* rec,
-                            float M, float c, const RowSettings& rs, float lnS,
-                            FinishShared& sm) {
+                            float M, float c, const RowSettings& rs, float lnS, Shared& sm) {
     const int lane = threadIdx.x & 31, n = a.chunks;
     if (threadIdx.x < 32) {
         float carry = 0.f;
@@ -1101,15 +1206,6 @@ struct FinishRow {
     int scale;     // digits of their weights
 };
 
-// e x in units of 2^-44, x in fp32: every term is at most 1/e, so that they add
-// up as integers, in any order.
-__device__ __forceinline__ long long entropy_term(unsigned long long key, uint64_t w, float M,
-                                                  float temp, int scale) {
-    const float x = (key_logit((uint32_t)(key >> 32)) - M) / temp;
-    const float e = (float)w * __int_as_float((127 - scale) << 23);
-    return w ? __float2ll_rn(e * x * 1.7592186e13f) : 0;
-}
-
 template <typename E, bool kSample>
 __device__ __forceinline__ void write_token(const FilterArgs& a, const E* row, const FinishRow& r,
                                             uint32_t col, uint64_t S) {
@@ -1178,8 +1274,7 @@ __device__ __forceinline__ void finish_few(const FilterArgs& a, const E* row, co
     count_before([&](unsigned long long o) { return o < key; }, rank, before);
     if (mine && rank == n - 1) sm.total = before + w;
     if (r.rs.cut_p && whole && mine && rank == (r.k > 0 && r.k < n ? r.k : n) - 1) {
-        const uint64_t target = __double2ull_ru((double)r.rs.top_p * (double)(before + w));
-        sm.target0 = sm.target1 = target ? target : 1;
+        sm.target0 = sm.target1 = share_of(r.rs.top_p, before + w);
     }
     __syncthreads();
     // A column is kept when its rank, the mass before it and its logit pass
@@ -1205,7 +1300,7 @@ __device__ __forceinline__ void finish_few(const FilterArgs& a, const E* row, co
     if (!kSample) {
         const long long ux = (long long)warp_sum(
             mine && key <= cut ? (uint64_t)entropy_term(key, w, r.M, r.rs.temp, r.scale) : 0);
-        if (lane == 0 && ux) atomicAdd(&sm.ux, (unsigned long long)ux);
+        if (lane == 0 && ux) add_wide(&sm.ux, (uint64_t)ux);
         __syncthreads();
         if (threadIdx.x == 0) write_kept(a, row, r, cut, S, (long long)sm.ux);
         return;
@@ -1241,7 +1336,7 @@ __device__ __noinline__ void finish_many(const FilterArgs& a, const E* row, cons
     n_hi = __reduce_add_sync(0xFFFFFFFFu, n_hi);
     n_lo = __reduce_add_sync(0xFFFFFFFFu, n_lo);
     if (lane == 0) {
-        atomicAdd(&sm.total, (unsigned long long)total);
+        add_wide(&sm.total, total);
         atomicAdd(&sm.keep0, (uint32_t)n_hi);
         atomicAdd(&sm.keep1, (uint32_t)n_lo);
     }
@@ -1264,8 +1359,7 @@ __device__ __noinline__ void finish_many(const FilterArgs& a, const E* row, cons
     if (r.rs.cut_p) {
         uint64_t t0 = sm.target0, t1 = sm.target1;
         if (whole) {
-            t0 = __double2ull_ru((double)r.rs.top_p * (double)(keep <= n ? end.mass : total));
-            t0 = t1 = t0 ? t0 : 1;
+            t0 = t1 = share_of(r.rs.top_p, keep <= n ? end.mass : total);
         }
         if (t0 == 0) return leave_row(a, r.t);
         if (total >= t0) {
@@ -1297,7 +1391,7 @@ __device__ __noinline__ void finish_many(const FilterArgs& a, const E* row, cons
             if (sm.cand[i] <= cut)
                 ux += entropy_term(sm.cand[i], sm.weight[i], r.M, r.rs.temp, r.scale);
         ux = (long long)warp_sum((uint64_t)ux);
-        if (lane == 0 && ux) atomicAdd(&sm.ux, (unsigned long long)ux);
+        if (lane == 0 && ux) add_wide(&sm.ux, (uint64_t)ux);
         __syncthreads();
         if (threadIdx.x == 0) write_kept(a, row, r, cut, S, (long long)sm.ux);
         return;
@@ -1309,26 +1403,35 @@ __device__ __noinline__ void finish_many(const FilterArgs& a, const E* row, cons
     if (threadIdx.x == 0) write_token<E, kSample>(a, row, r, (uint32_t)s.key, S);
 }
 
-template <typename E, bool kSample>
-__global__ void __launch_bounds__(kFinThreads)
+// kFiltered: some row may have a filter; without, the kernel needs neither the
+// registers nor the shared memory of the candidates.
+template <typename E, bool kSample, bool kFiltered>
+__global__ void __launch_bounds__(kFinThreads, kFiltered ? 4 : 6)
     filter_finish_kernel(const __grid_constant__ FilterArgs a) {
-    __shared__ FinishShared sm;
+    __shared__ typename std::conditional<kFiltered, FinishShared, DrawShared>::type sm;
     constexpr int kVec = Elem<E>::kVec;
     const int64_t t = blockIdx.x;
     const int V = (int)a.V, lane = threadIdx.x & 31;
     const E* row = static_cast<const E*>(a.logits) + t * a.ld;
     const float4* rec = a.records + t * a.chunks;
-    for (int i = threadIdx.x; i < kFinBins; i += kFinThreads) sm.hist.count[i] = sm.hist.mass[i] = 0;
-    if (threadIdx.x < 64) sm.table[threadIdx.x] = kExp2Table[threadIdx.x];
-    if (threadIdx.x == 0) {
-        sm.n_group = sm.n_cand = sm.keep0 = sm.keep1 = 0;
-        sm.ux = sm.total = 0;
-        sm.bin = kFinBins;
+    if constexpr (kFiltered) {
+        for (int i = threadIdx.x; i < kFinBins; i += kFinThreads)
+            sm.hist.count[i] = sm.hist.mass[i] = 0;
+        if (threadIdx.x < 64) sm.table[threadIdx.x] = kExp2Table[threadIdx.x];
+        if (threadIdx.x == 0) {
+            sm.n_group = sm.n_cand = sm.keep0 = sm.keep1 = 0;
+            sm.ux = sm.total = 0;
+            sm.bin = kFinBins;
+        }
     }
     FinishRow r;
     r.t = t;
     r.rs = row_settings<kSample>(a, t);
     const RowSettings& rs = r.rs;
+    // Up to here only what the caller gave was read.  Every block waits, so that
+    // this grid cannot complete before the records are.
+    grid_wait();
+    grid_launch_dependents();
     if (!rs.valid) {
         if (threadIdx.x == 0) write_undefined<kSample>(a, t, PSTAT_DEV_BAD_PARAM);
         return;
@@ -1341,7 +1444,7 @@ __global__ void __launch_bounds__(kFinThreads)
         return;
     }
     if (rs.greedy) return finish_greedy(a, t, row, rec, M, sm);
-    if (!rs.cut_k && !rs.cut_p && !rs.cut_m) {
+    if (!kFiltered || (!rs.cut_k && !rs.cut_p && !rs.cut_m)) {
         const float lnS = logf(Sf);
         if (kSample) {
             __syncthreads();  // the histogram's zeros share memory with the prefix sums
@@ -1352,6 +1455,7 @@ __global__ void __launch_bounds__(kFinThreads)
                              (uint32_t)V - 1);
         return;
     }
+    if constexpr (kFiltered) {
 
     r.k = rs.cut_k ? (int)rs.top_k : 0;
     r.mp = min_p_bounds(M, rs);
@@ -1483,6 +1587,8 @@ __global__ void __launch_bounds__(kFinThreads)
         finish_few<E, kSample>(a, row, r, sm);
     else
         finish_many<E, kSample>(a, row, r, sm);
+
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -1499,131 +1605,110 @@ __device__ void exact_row(const FilterArgs& a, int64_t t, Team<E>& tm, ExactShar
     const float3 st = fold_records(a.records + t * a.chunks, a.chunks, tm.c.ch, lane);
     const float M = st.x + 0.f;
     tm.M = M;
+    tm.temp = rs.temp;
     tm.bin_scale = tm.c.ch * ((float)kBins / 64.f);
     tm.k = fixed_scale(st.y * (1.f + 2.f * kSumError));
     if (threadIdx.x == 0) {
-        sm.n_min = sm.n_finite = 0;
-        sm.total = 0;
         sm.first = sm.first_kept = 0xFFFFFFFFu;
     }
     tm.sync();
 
     const float z_min = min_p_logit(M, rs);
     uint32_t cut_key = 0xFFFFFFFFu, cut_index = (uint32_t)V - 1;
+    bool spans_ready = false;
     if (rs.cut_k || rs.cut_p || (rs.cut_m && !kSample)) {
-        // Counts of the level-0 bins, and the whole mass where top-p refers to it.
+        // Counts of the level-0 bins.
         for (int i = threadIdx.x; i < kBins; i += kExThreads) sm.level0[i] = 0;
         __syncthreads();
         uint32_t n_min = 0, n_fin = 0;
-        uint64_t mass = 0;
-        const bool weigh = rs.cut_p;
-        tm.each_vector([&](int, const float (&x)[Elem<E>::kVec]) {
+        tm.each_span([&](int, int, const float (&x)[Team<E>::kLane]) {
 #pragma unroll
-            for (int e = 0; e < Elem<E>::kVec; ++e) {
+            for (int e = 0; e < Team<E>::kLane; ++e) {
                 if (x[e] > -INFINITY) {
                     atomicAdd(&sm.level0[tm.bin0(x[e])], 1u);
                     n_min += x[e] >= z_min;
                     ++n_fin;
                 }
             }
-            if (weigh)
-#pragma unroll
-                for (int e = 0; e < Elem<E>::kVec; ++e) mass += tm.weight(x[e]);
         });
-        n_min = __reduce_add_sync(0xFFFFFFFFu, n_min);
-        n_fin = __reduce_add_sync(0xFFFFFFFFu, n_fin);
-        if (lane == 0) {
-            atomicAdd(&lead.n_min, n_min);
-            atomicAdd(&lead.n_finite, n_fin);
-        }
-        tm.add_to(&lead.total, mass);
+        tm.put(0, n_min);
+        tm.put(1, n_fin);
         tm.merge(sm.level0, lead.level0);
-        const uint32_t n_finite = lead.n_finite;
-        uint64_t total = lead.total;
-        const uint32_t n_keep_min = rs.cut_m ? lead.n_min : n_finite;
+        const uint32_t n_finite = (uint32_t)tm.get(1);
+        const uint32_t n_keep_min = rs.cut_m ? (uint32_t)tm.get(0) : n_finite;
+        tm.sync();
         uint32_t want = rs.cut_k && rs.top_k < (int64_t)n_finite ? (uint32_t)rs.top_k : n_finite;
         Selected sel;
         bool have = false;
         if (rs.cut_p) {
-            if (want < n_finite) total = tm.select(true, want, 0).mass;
-            // C >= p S in whole numbers; at least 1, so that a token is kept
-            const uint64_t target = __double2ull_ru((double)rs.top_p * (double)total);
-            sel = tm.select(false, 0, target ? target : 1);
+            if (want < n_finite) {
+                const uint64_t total = tm.select(true, want, 0).mass;
+                sel = tm.select(false, 0, share_of(rs.top_p, total));
+            } else {
+                const float about = rs.top_p * st.y * __int_as_float((127 + tm.k) << 23);
+                sel = tm.select(false, 0, (uint64_t)about, rs.top_p);
+            }
             want = sel.rank;
             have = n_keep_min >= want;
         }
         if (!have) sel = tm.select(true, min(want, n_keep_min), 0);
+        spans_ready = !tm.ties;
         cut_key = (uint32_t)(sel.key >> 32);
         cut_index = (uint32_t)sel.key;
     } else if (rs.cut_m) {
         cut_key = desc_key(z_min);
     }
 
-    // Kept mass (and sum of e x) of every span of the index order.
+    // Kept mass of every span of the index order (and the sum of e x), where no
+    // selection has left it.
     const int spans = (V + kSpan - 1) / kSpan;
-    uint32_t lowest = 0xFFFFFFFFu;
-    const float inv_t = 1.f / rs.temp;
-    constexpr int kVec = Elem<E>::kVec, kVecs = kSpan / (32 * kVec);
-    for (int s = tm.thread >> 5; s < spans; s += tm.threads >> 5) {
-        uint64_t w = 0;
-        float ux = 0.f;
-        constexpr int kAhead = 2;
-#pragma unroll 1
-        for (int j0 = 0; j0 < kVecs; j0 += kAhead) {
-            int at[kAhead];
-            float x[kAhead][kVec];
+    constexpr int kLane = Team<E>::kLane;
+    if (!spans_ready) {
+        uint64_t ux = 0;
+        tm.each_span([&](int s, int col, const float (&x)[kLane]) {
+            uint64_t w = 0;
 #pragma unroll
-            for (int h = 0; h < kAhead; ++h) at[h] = s * kSpan + ((j0 + h) * 32 + lane) * kVec;
-            load_columns<E, kAhead>(row, at, V, x);
-#pragma unroll
-            for (int h = 0; h < kAhead; ++h)
-#pragma unroll
-                for (int i = 0; i < kVec; ++i) {
-                    const int col = at[h] + i;
-                    const float z = x[h][i];
-                    const bool kept = z > -INFINITY && is_kept(z, col, cut_key, cut_index);
-                    const uint64_t e = kept ? tm.weight(z) : 0;
-                    w += e;
-                    if (kSample)
-                        lowest = min(lowest, kept ? (uint32_t)col : 0xFFFFFFFFu);
-                    else if (e)
-                        ux = fmaf((float)e * __int_as_float((127 - tm.k) << 23), (z - M) * inv_t,
-                                  ux);
-                }
-        }
-        w = warp_sum(w);
-        if (!kSample) {
-#pragma unroll
-            for (int off = 16; off; off >>= 1) ux += __shfl_xor_sync(0xFFFFFFFFu, ux, off);
-        }
-        if (lane == 0) {
-            lead.span_mass[s] = w;
-            if (!kSample) lead.span_u[s] = ux;
-        }
+            for (int e = 0; e < kLane; ++e) {
+                const uint64_t we = tm.weight(x[e]);
+                const bool kept = is_kept(x[e], col + e, cut_key, cut_index);
+                w += kept ? we : 0;
+                if (!kSample && kept)
+                    ux += (uint64_t)entropy_term((unsigned long long)desc_key(x[e]) << 32, we, M,
+                                                 rs.temp, tm.k);
+            }
+            w = warp_sum(w);
+            if (lane == 0) lead.span_mass[s] = w;
+        });
+        if (!kSample) tm.put(2, ux);
     }
     if (kSample && rs.u == 0.f) {
+        uint32_t lowest = 0xFFFFFFFFu;
+        tm.each_span([&](int, int col, const float (&x)[kLane]) {
+#pragma unroll
+            for (int e = 0; e < kLane; ++e)
+                if (x[e] > -INFINITY && is_kept(x[e], col + e, cut_key, cut_index))
+                    lowest = min(lowest, (uint32_t)(col + e));
+        });
         lowest = __reduce_min_sync(0xFFFFFFFFu, lowest);
         if (lane == 0) atomicMin(&lead.first_kept, lowest);
     }
     tm.sync();
     if (!first) return;
 
-    uint64_t mine[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int s = 2 * (int)threadIdx.x + i;
-        mine[i] = s < spans ? sm.span_mass[s] : 0;
+    uint64_t before, unused, mine = 0;
+    for (int i = 0; i < kSpansPer; ++i) {
+        const int s = kSpansPer * (int)threadIdx.x + i;
+        mine += s < spans ? sm.span_mass[s] : 0;
     }
-    uint64_t before, unused;
-    block_scan<kExThreads, uint64_t>(sm.scratch, mine[0] + mine[1], 0, before, unused);
-    if (threadIdx.x == kExThreads - 1) sm.mass_before = before + mine[0] + mine[1];
+    block_scan<kExThreads, uint64_t>(sm.scratch, mine, 0, before, unused);
+    if (threadIdx.x == kExThreads - 1) sm.mass_before = before + mine;
+    if (threadIdx.x == 0 && !kSample && !spans_ready) sm.ux = tm.get(2);
     __syncthreads();
     const uint64_t S = sm.mass_before;
     const float lnS = fixed_log(S, tm.k);
     if (!kSample) {
         if (threadIdx.x == 0) {
-            float U = 0.f;
-            for (int s = 0; s < spans; ++s) U += sm.span_u[s];
+            const float U = (float)(long long)sm.ux * 5.6843419e-14f;  // 2^-44
             const float Sr = (float)S * __int_as_float((127 - tm.k) << 23);
             write_statistics(a, t, row, M, lnS, lnS - U / Sr, rs.temp, cut_key, cut_index);
         }
@@ -1640,50 +1725,45 @@ __device__ void exact_row(const FilterArgs& a, int64_t t, Team<E>& tm, ExactShar
     // C > u S in whole numbers
     const uint64_t target = __double2ull_rd((double)rs.u * (double)S);
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (before <= target && before + mine[i] > target) {
-            sm.first = 2 * threadIdx.x + i;
+    for (int i = 0; i < kSpansPer; ++i) {
+        const int s = kSpansPer * (int)threadIdx.x + i;
+        const uint64_t w = s < spans ? sm.span_mass[s] : 0;
+        if (before <= target && before + w > target) {
+            sm.first = (uint32_t)s;
             sm.mass_before = before;
         }
-        before += mine[i];
+        before += w;
     }
     __syncthreads();
-    constexpr int kPer = kSpan / kExThreads;
-    const int c0 = (int)sm.first * kSpan + threadIdx.x * kPer;
+    const int c = (int)sm.first * kSpan + (int)threadIdx.x;
     const uint64_t base = sm.mass_before;
-    uint64_t w[kPer], sum = 0;
-    for (int i = 0; i < kPer; ++i) {
-        w[i] = 0;
-        if (c0 >= 0 && c0 + i < V) {
-            const float z = Elem<E>::to_float(row[c0 + i]);
-            if (is_kept(z, c0 + i, cut_key, cut_index)) w[i] = tm.weight(z);
-        }
-        sum += w[i];
+    uint64_t w = 0;
+    float z = 0.f;
+    if ((int)threadIdx.x < kSpan && c >= 0 && c < V) {
+        z = Elem<E>::to_float(row[c]);
+        if (is_kept(z, c, cut_key, cut_index)) w = tm.weight(z);
     }
     uint64_t wb;
-    block_scan<kExThreads, uint64_t>(sm.scratch, sum, 0, wb, unused);
+    block_scan<kExThreads, uint64_t>(sm.scratch, w, 0, wb, unused);
     wb += base;
-    for (int i = 0; i < kPer; ++i) {
-        if (wb <= target && wb + w[i] > target) {
-            a.token[t] = c0 + i;
-            a.logprob[t] = (Elem<E>::to_float(row[c0 + i]) - M) / rs.temp - lnS;
-        }
-        wb += w[i];
+    if (wb <= target && wb + w > target) {
+        a.token[t] = c;
+        a.logprob[t] = (z - M) / rs.temp - lnS;
     }
 }
 
 template <typename E, bool kSample>
-__global__ void __launch_bounds__(kExThreads)
+__global__ void __launch_bounds__(kExThreads, 2)
     filter_exact_kernel(const __grid_constant__ FilterArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     cg::cluster_group cluster = cg::this_cluster();
     ExactShared& sm = *reinterpret_cast<ExactShared*>(smem_raw);
     ExactShared& lead = *cluster.map_shared_rank(&sm, 0);
-    const int n = *a.left_count;
-    if (n == 0) return;
     if (threadIdx.x < 64) sm.table[threadIdx.x] = kExp2Table[threadIdx.x];
     __syncthreads();
+    grid_wait();
+    const int n = *a.left_count;
+    if (n == 0) return;
     // A cluster to a row, or, with more rows than a few for every cluster, a
     // CTA: what a team saves in a pass it loses again in synchronisation.
     const bool alone = n >= 4 * (int)(gridDim.x / cluster.num_blocks());
@@ -1693,7 +1773,7 @@ __global__ void __launch_bounds__(kExThreads)
         const int64_t t = a.left[i];
         Team<E> tm{sm, alone ? sm : lead, cluster, static_cast<const E*>(a.logits) + t * a.ld,
                    (int)a.V, rank * kExThreads + (int)threadIdx.x, team * kExThreads, rank == 0,
-                   alone, 0.f, {0.f, 0.f}, 0, 0.f};
+                   alone, !kSample, 0.f, 0.f, {0.f, 0.f}, 0, 0.f, false};
         exact_row<E, kSample>(a, t, tm, sm, tm.lead);
         tm.sync();  // the next row writes what this one reads
     }
@@ -1719,27 +1799,19 @@ cudaError_t launch_filter(const FilterArgs& a, const DeviceInfo& dev, cudaStream
                                          stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    filter_finish_kernel<E, kSample><<<(unsigned)a.T, kFinThreads, 0, stream>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-
+    const bool filtered = a.top_ks || a.top_ps || a.min_ps || (a.top_k > 0 && a.top_k < a.V) ||
+                          a.top_p < 1.f || a.min_p > 0.f;
+    e = launch_behind(filtered ? filter_finish_kernel<E, kSample, true>
+                               : filter_finish_kernel<E, kSample, false>,
+                      (unsigned)a.T, kFinThreads, 0, stream, 1, a);
+    // Without filters only a draw can be left over.
+    if (e != cudaSuccess || (!filtered && !kSample)) return e;
     int team = 1;
-    while (team < 8 && a.V >= (int64_t)team * 8192) team *= 2;
-    int64_t teams = (int64_t)dev.sm_count * 3 / team;
+    while (team < kMaxTeam && a.V >= (int64_t)team * 8192) team *= 2;
+    int64_t teams = (int64_t)dev.sm_count * 2 / team;
     if (teams > a.T) teams = a.T;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(teams * team));
-    cfg.blockDim = dim3(kExThreads);
-    cfg.dynamicSmemBytes = sizeof(ExactShared);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)team;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, filter_exact_kernel<E, kSample>, a);
+    return launch_behind(filter_exact_kernel<E, kSample>, (unsigned)(teams * team), kExThreads,
+                         sizeof(ExactShared), stream, (unsigned)team, a);
 }
 
 // ---------------------------------------------------------------------------

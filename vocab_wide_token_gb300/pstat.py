@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import functools
 import operator
 import os
 
@@ -160,11 +161,18 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+# The current stream's handle; torch's accessor for it, where there is one, costs
+# a twentieth of building a Stream object (2 us of a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _rows(logits: torch.Tensor):
@@ -680,6 +688,7 @@ def lmhead_backward(hidden, W, labels, weights, rowstats, ignore_index: int = -1
 
 # ---- tempered, truncated distributions -------------------------------------------
 
+@functools.lru_cache(maxsize=256)
 def filter_workspace_size(T: int, V: int, dtype: torch.dtype) -> int:
     """Workspace bytes of ``sample`` and ``filtered_forward``."""
     n = ctypes.c_size_t(0)
@@ -689,27 +698,31 @@ def filter_workspace_size(T: int, V: int, dtype: torch.dtype) -> int:
     return int(n.value)
 
 
-def _per_row(x, dtype, T, dev, name):
-    """A setting as (number, None) or (unused, its [T] device tensor)."""
-    if isinstance(x, torch.Tensor):
-        return None, _tensor(x, dtype, (T,), dev, name)
-    return x, None
+@functools.lru_cache(maxsize=256)
+def _plain_filters(temperature, top_k, top_p, min_p):
+    """A pstat_filters of numbers alone, by reference (the library only reads it)."""
+    return ctypes.byref(Filters(float(temperature), float(top_p), float(min_p), int(top_k)))
 
 
 def _filters(temperature, top_k, top_p, min_p, T, dev):
-    """The call's pstat_filters.  It holds the addresses of the caller's own
-    [T] tensors, which the caller's arguments keep alive until the launch."""
-    t, tt = _per_row(temperature, torch.float32, T, dev, "temperature")
-    k, kk = _per_row(top_k, torch.int32, T, dev, "top_k")
-    p, pp = _per_row(top_p, torch.float32, T, dev, "top_p")
-    m, mm = _per_row(min_p, torch.float32, T, dev, "min_p")
-
-    def ptr(a):
-        return None if a is None else a.data_ptr()
-
-    return Filters(1.0 if t is None else float(t), 1.0 if p is None else float(p),
-                   0.0 if m is None else float(m), 0 if k is None else int(k),
-                   ptr(tt), ptr(kk), ptr(pp), ptr(mm))
+    """The call's pstat_filters, by reference: each setting a number, or the
+    address of the caller's own [T] tensor, which its argument keeps alive
+    until the launch."""
+    row = torch.Tensor
+    if not (isinstance(temperature, row) or isinstance(top_k, row) or isinstance(top_p, row)
+            or isinstance(min_p, row)):
+        return _plain_filters(temperature, top_k, top_p, min_p)
+    f = Filters(1.0, 1.0, 0.0, 0)
+    for x, dtype, name, one, many in ((temperature, torch.float32, "temperature", "temperature",
+                                       "temperatures"),
+                                      (top_k, torch.int32, "top_k", "top_k", "top_ks"),
+                                      (top_p, torch.float32, "top_p", "top_p", "top_ps"),
+                                      (min_p, torch.float32, "min_p", "min_p", "min_ps")):
+        if isinstance(x, row):
+            setattr(f, many, _tensor(x, dtype, (T,), dev, name).data_ptr())
+        else:
+            setattr(f, one, int(x) if one == "top_k" else float(x))
+    return ctypes.byref(f)
 
 
 def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0,
@@ -738,7 +751,7 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, top_k=0
     dev_error = _error_flag(dev_error, dev)
     workspace = _workspace(workspace, filter_workspace_size(T, V, logits.dtype), dev)
     _call(dev, "pstat_sample", _lib.pstat_sample,
-          _ptr(logits), dt, T, V, ld, _ptr(u), ctypes.byref(f), _ptr(token), _ptr(lp),
+          _ptr(logits), dt, T, V, ld, _ptr(u), f, _ptr(token), _ptr(lp),
           _ptr(workspace), workspace.numel(), _ptr(dev_error), _stream(dev))
     return token, lp
 
@@ -772,7 +785,7 @@ def filtered_forward(logits: torch.Tensor, labels: torch.Tensor | None, temperat
     dev_error = _error_flag(dev_error, dev)
     workspace = _workspace(workspace, filter_workspace_size(T, V, logits.dtype), dev)
     _call(dev, "pstat_filtered_forward", _lib.pstat_filtered_forward,
-          _ptr(logits), dt, T, V, ld, _ptr(lab), int(ignore_index), ctypes.byref(f), _ptr(lp),
+          _ptr(logits), dt, T, V, ld, _ptr(lab), int(ignore_index), f, _ptr(lp),
           _ptr(ent), _ptr(rs), _ptr(tau), _ptr(index), _ptr(workspace), workspace.numel(),
           _ptr(dev_error), _stream(dev))
     return lp, ent, rs, tau, index
@@ -800,18 +813,20 @@ def filtered_backward(logits: torch.Tensor, labels: torch.Tensor | None,
     rowstats = _rowstats(rowstats, T, dev)
     tau = _tensor(cut_logit, torch.float32, (T,), dev, "cut_logit")
     index = _tensor(cut_index, torch.int64, (T,), dev, "cut_index")
-    t, tt = _per_row(temperature, torch.float32, T, dev, "temperature")
+    row_t = isinstance(temperature, torch.Tensor)
+    if row_t:
+        _tensor(temperature, torch.float32, (T,), dev, "temperature")
     dev_error = _error_flag(dev_error, dev)
     _call(dev, "pstat_filtered_backward", _lib.pstat_filtered_backward,
           _ptr(logits), dt, T, V, ld, _ptr(lab), int(ignore_index), _ptr(w), _ptr(rowstats),
-          _ptr(tau), _ptr(index), 1.0 if t is None else float(t), _ptr(tt), _ptr(out),
+          _ptr(tau), _ptr(index), 1.0 if row_t else float(temperature),
+          _ptr(temperature) if row_t else None, _ptr(out),
           _dtype_code(out), ld_out, _ptr(dev_error), _stream(dev))
     return out
 
 
 # ---- gradient norm and clipping ---------------------------------------------------
 
-_GRAD_CODES = {torch.bfloat16: BF16, torch.float32: F32}
 _dtype_of = operator.attrgetter("dtype")
 
 
@@ -833,15 +848,16 @@ def _grad_list(tensors, out, writes):
     if not all(map(T.is_contiguous, tensors)):
         raise ValueError("tensors must be contiguous")
     dtypes = list(map(_dtype_of, tensors))
-    if not _GRAD_CODES.keys() >= set(dtypes):
-        raise TypeError("tensors must be bfloat16 or float32")
     n = len(tensors)
+    if dtypes.count(torch.bfloat16) + dtypes.count(torch.float32) != n:
+        raise TypeError("tensors must be bfloat16 or float32")
     words = array.array("q", bytes(32 * n))
     at = array.array("q", map(T.data_ptr, tensors))
     sizes = array.array("q", map(T.numel, tensors))
     words[0::4] = at
     words[2::4] = sizes
-    words[3::4] = array.array("q", map(_GRAD_CODES.__getitem__, dtypes))
+    bf16 = torch.bfloat16
+    words[3::4] = array.array("q", [BF16 if d is bf16 else F32 for d in dtypes])
     outs = tensors
     if out is not None:
         outs = [out] if isinstance(out, torch.Tensor) else list(out)
