@@ -91,52 +91,91 @@ __device__ __forceinline__ TempScale temp_scale(float t) {
     return s;
 }
 
-// round(2^k e^((z - M)/t)) to about 2^-46 relative, k <= 60; 0 where that is
-// far below 1.  With y = (M - z) log2(e)/t in double-float arithmetic, write
-// y = j/64 + r, |r| <= 2^-7 (plus the low part); then 2^-y = 2^-(j/64) 2^-r:
-// the first factor from the table and a power of two, the second from
-// e^-s = 1 - s + s^2/2 - s^3/6 + s^4/24 - s^5/120, s = r ln 2 <= 2^-7.5,
-// whose next term s^6/720 is below 2^-54.  The first two terms are carried in
-// double-float, the others (below 2^-24) in fp32.  z = M gives 2^k exactly.
-// (A table-driven exponential, as in Tang, ACM TOMS 15, 1989.)
-__device__ __forceinline__ uint64_t fixed_weight(float z, float M, TempScale c, int k,
-                                                 const float2* __restrict__ table) {
-    const float d = M - z;
-    const bool far = !(d * c.ch < (float)(k + 2));
-    const float dh = far ? 0.f : d;  // no branch: callers weigh several at once
-    const float bb = dh - M;
-    const float dl = (M - (dh - bb)) - (z + bb);  // exact remainder of M - z
-    // (rounding intrinsics where a product's own rounding error is used: the
-    // compiler may not fuse those into a later addition)
-    const float y0 = __fmul_rn(dh, c.ch);
-    const float y1 = fmaf(dh, c.ch, -y0) + fmaf(dh, c.cl, dl * c.ch);
-    const int j = __float2int_rn(y0 * 64.f);
-    const float r0 = fmaf((float)j, -0.015625f, y0);  // exact
-    const float rh = r0 + y1;
-    const float rb = rh - r0;
-    const float rl = (r0 - (rh - rb)) + (y1 - rb);
+// a - b, as one packed FMA.
+__device__ __forceinline__ uint64_t f2_set(float v) { return f2_pack(v, v); }
+__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
+    return f2_fma(b, f2_set(-1.f), a);
+}
+__device__ __forceinline__ uint64_t f2_neg(uint64_t v) { return v ^ 0x8000000080000000ull; }
+
+// round(2^k e^((z - M)/t)) of two logits, to about 2^-46 relative, k <= 60; 0
+// where that is far below 1.  With y = (M - z) log2(e)/t in double-float
+// arithmetic, write y = j/64 + r, |r| <= 2^-7 (plus the low part); then 2^-y =
+// 2^-(j/64) 2^-r: the first factor from the table and a power of two, the
+// second from e^-s = 1 - s + s^2/2 - s^3/6 + s^4/24 - s^5/120, s = r ln 2 <=
+// 2^-7.5, whose next term s^6/720 is below 2^-54.  The first two terms are
+// carried in double-float, the others (below 2^-24) in fp32.  z = M gives 2^k
+// exactly.  (A table-driven exponential, as in Tang, ACM TOMS 15, 1989.)
+// Packed arithmetic on both: a pass that weighs a whole row is bound by issued
+// instructions, of which this takes about 80 for a pair and scalar arithmetic
+// over 100 for each.
+__device__ __forceinline__ void fixed_weights(float z0, float z1, float M, TempScale c, int k,
+                                              const float2* __restrict__ table, uint64_t& w0,
+                                              uint64_t& w1) {
+    const float limit = (float)(k + 2);
+    float d0 = M - z0, d1 = M - z1;
+    const bool far0 = !(d0 * c.ch < limit), far1 = !(d1 * c.ch < limit);
+    if (far0) {  // selects
+        d0 = 0.f;
+        z0 = M;
+    }
+    if (far1) {
+        d1 = 0.f;
+        z1 = M;
+    }
+    const uint64_t Mp = f2_set(M), ch = f2_set(c.ch);
+    const uint64_t z = f2_pack(z0, z1), dh = f2_pack(d0, d1);
+    const uint64_t bb = f2_sub(dh, Mp);
+    const uint64_t dl = f2_sub(f2_sub(Mp, f2_sub(dh, bb)), f2_add(z, bb));  // rest of M - z
+    const uint64_t y0 = f2_mul(dh, ch);
+    const uint64_t y1 = f2_add(f2_fma(dh, ch, f2_neg(y0)), f2_fma(dh, f2_set(c.cl), f2_mul(dl, ch)));
+    float ja, jb;
+    f2_unpack(f2_mul(y0, f2_set(64.f)), ja, jb);
+    const int j0 = __float2int_rn(ja), j1 = __float2int_rn(jb);
+    const uint64_t r0 = f2_fma(f2_pack((float)j0, (float)j1), f2_set(-0.015625f), y0);  // exact
+    const uint64_t rh = f2_add(r0, y1);
+    const uint64_t rb = f2_sub(rh, r0);
+    const uint64_t rl = f2_add(f2_sub(r0, f2_sub(rh, rb)), f2_sub(y1, rb));
     constexpr float kLn2H = 0.69314718055994531f;
     constexpr float kLn2L = (float)(0.69314718055994530942 - (double)kLn2H);
-    const float sh = __fmul_rn(rh, kLn2H);
-    const float sl = fmaf(rh, kLn2H, -sh) + fmaf(rh, kLn2L, rl * kLn2H);
-    const float p = __fmul_rn(sh, sh);
-    const float pe = fmaf(2.f * sh, sl, fmaf(sh, sh, -p));
-    const float q = p * sh * fmaf(sh, fmaf(sh, -1.f / 120.f, 1.f / 24.f), -1.f / 6.f);
-    const float ah = fmaf(p, 0.5f, -sh);
-    const float al = fmaf(p, 0.5f, -__fadd_rn(ah, sh)) + (q + fmaf(0.5f, pe, -sl));
-    const float2 tb = table[j & 63];
-    const float ph = __fmul_rn(tb.x, ah);
-    const float pl = fmaf(tb.x, ah, -ph) + fmaf(tb.x, al, tb.y * ah);
-    const float eh = tb.x + ph;
-    const float el = (ph - (eh - tb.x)) + (tb.y + pl);
+    const uint64_t lh = f2_set(kLn2H);
+    const uint64_t sh = f2_mul(rh, lh), nsh = f2_neg(sh);
+    const uint64_t sl = f2_add(f2_fma(rh, lh, nsh), f2_fma(rh, f2_set(kLn2L), f2_mul(rl, lh)));
+    const uint64_t p = f2_mul(sh, sh);
+    const uint64_t pe = f2_fma(f2_add(sh, sh), sl, f2_fma(sh, sh, f2_neg(p)));
+    const uint64_t q =
+        f2_mul(f2_mul(p, sh), f2_fma(sh, f2_fma(sh, f2_set(-1.f / 120.f), f2_set(1.f / 24.f)),
+                                     f2_set(-1.f / 6.f)));
+    const uint64_t half = f2_set(0.5f);
+    const uint64_t ah = f2_fma(p, half, nsh);
+    const uint64_t al = f2_add(f2_fma(p, half, f2_neg(f2_add(ah, sh))),
+                               f2_add(q, f2_sub(f2_mul(half, pe), sl)));
+    const float2 t0 = table[j0 & 63], t1 = table[j1 & 63];
+    const uint64_t th = f2_pack(t0.x, t1.x), tl = f2_pack(t0.y, t1.y);
+    const uint64_t ph = f2_mul(th, ah);
+    const uint64_t pl = f2_add(f2_fma(th, ah, f2_neg(ph)), f2_fma(th, al, f2_mul(tl, ah)));
+    const uint64_t eh = f2_add(th, ph);
+    const uint64_t el = f2_add(f2_sub(ph, f2_sub(eh, th)), f2_add(tl, pl));
     // (eh + el) 2^54 as an integer, eh >= 1/2 being a multiple of 2^-24 and el
-    // below 2^-24, then rounded to k - n digits: conversions to 64-bit integers
+    // below 2^-23, then rounded to k - n digits: conversions to 64-bit integers
     // run at a sixteenth of the rate of 32-bit ones.
-    const int64_t m = ((int64_t)__float2int_rn(eh * 16777216.f) << 30) +
-                      __float2int_rn(el * 18014398509481984.f);
-    const int drop = 60 - k + (j >> 6);  // in [0, 62]
-    const uint64_t w = (((uint64_t)m << 6) + ((1ull << drop) >> 1)) >> drop;
-    return far ? 0 : w;
+    float a0, a1, b0, b1;
+    f2_unpack(f2_mul(eh, f2_set(16777216.f)), a0, a1);
+    f2_unpack(f2_mul(el, f2_set(18014398509481984.f)), b0, b1);
+    auto fixed = [&](float a, float b, int j, bool far) -> uint64_t {
+        const int64_t m = ((int64_t)__float2int_rn(a) << 30) + __float2int_rn(b);
+        const int drop = 60 - k + (j >> 6);  // in [0, 62]
+        const uint64_t w = (((uint64_t)m << 6) + ((1ull << drop) >> 1)) >> drop;
+        return far ? 0 : w;
+    };
+    w0 = fixed(a0, b0, j0, far0);
+    w1 = fixed(a1, b1, j1, far1);
+}
+__device__ __forceinline__ uint64_t fixed_weight(float z, float M, TempScale c, int k,
+                                                 const float2* __restrict__ table) {
+    uint64_t w, same;
+    fixed_weights(z, z, M, c, k, table, w, same);
+    return w;
 }
 
 // Binary digits after the point of the fixed weights of a row whose sum is

@@ -66,6 +66,10 @@ struct ContextSeen {
 // device and context.
 cudaError_t ensure_smem_optin(const void* func, int bytes, ContextSeen& seen);
 
+// cudaFuncSetAttribute(func, NonPortableClusterSizeAllowed, 1), run once per
+// device and context.
+cudaError_t ensure_large_cluster(const void* func, ContextSeen& seen);
+
 // Launches `kernel` behind the stream's previous kernel by programmatic
 // dependent launch: its blocks may start early and call grid_wait() before they
 // touch anything that kernel writes.  `cluster` > 1 groups the blocks.

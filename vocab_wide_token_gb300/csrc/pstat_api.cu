@@ -41,20 +41,28 @@ uint64_t current_context_id() {
     return (uint64_t)id;
 }
 
-cudaError_t ensure_smem_optin(const void* func, int bytes, ContextSeen& seen) {
+static cudaError_t ensure_attribute(const void* func, cudaFuncAttribute attr, int value,
+                                    ContextSeen& seen) {
     int d = 0;
     const cudaError_t ge = cudaGetDevice(&d);
     if (ge != cudaSuccess) return ge;
     const bool slot = d >= 0 && d < kMaxDevices;
     const uint64_t id = current_context_id();
     if (slot && id != 0 && seen.id[d].load(std::memory_order_acquire) == id) return cudaSuccess;
-    const cudaError_t e =
-        cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = cudaFuncSetAttribute(func, attr, value);
     if (e != cudaSuccess) return e;
     // The call above has made the device's primary context current if it was not.
     const uint64_t now = current_context_id();
     if (slot && now != 0) seen.id[d].store(now, std::memory_order_release);
     return cudaSuccess;
+}
+
+cudaError_t ensure_smem_optin(const void* func, int bytes, ContextSeen& seen) {
+    return ensure_attribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes, seen);
+}
+
+cudaError_t ensure_large_cluster(const void* func, ContextSeen& seen) {
+    return ensure_attribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1, seen);
 }
 
 int make_plan(int64_t V, int chunk, const int64_t* bounds, int n_shards, ShardPlan* plan) {

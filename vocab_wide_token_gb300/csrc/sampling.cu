@@ -36,7 +36,7 @@ constexpr int kSpan = 256;     // columns of one span of the index-order scan, a
 constexpr int kMaxSpans = (int)(kFilterMaxV / kSpan);
 constexpr int kSpansPer = kMaxSpans / kExThreads;
 static_assert(kBins % kExThreads == 0 && kMaxSpans % kExThreads == 0 && kSpan <= kExThreads, "");
-constexpr int kMaxTeam = 8;
+constexpr int kMaxTeam = 16;
 
 struct FilterArgs {
     const void* logits;
@@ -371,11 +371,21 @@ __device__ __forceinline__ void block_scan(unsigned long long* scratch, T a, T b
         wb[warp] = sb;
     }
     __syncthreads();
-    T oa = 0, ob = 0;
-    for (int w = 0; w < warp; ++w) {
-        oa += wa[w];
-        ob += wb[w];
+    // every warp scans the warps' totals, in the same order
+    constexpr int kW = kThreads / 32;
+    T ta = lane < kW ? wa[lane] : T(0), tb = lane < kW ? wb[lane] : T(0);
+#pragma unroll
+    for (int off = 1; off < kW; off <<= 1) {
+        const T ua = __shfl_up_sync(0xFFFFFFFFu, ta, off);
+        const T ub = __shfl_up_sync(0xFFFFFFFFu, tb, off);
+        if (lane >= off) {
+            ta += ua;
+            tb += ub;
+        }
     }
+    const int prior = warp ? warp - 1 : 0;
+    T oa = __shfl_sync(0xFFFFFFFFu, ta, prior), ob = __shfl_sync(0xFFFFFFFFu, tb, prior);
+    if (warp == 0) oa = ob = T(0);
     // exclusive sum of the lanes, without taking a back out of a sum
     T pa = __shfl_up_sync(0xFFFFFFFFu, sa, 1), pb = __shfl_up_sync(0xFFFFFFFFu, sb, 1);
     a_ex = lane ? oa + pa : oa;
@@ -432,15 +442,14 @@ __device__ __noinline__ Selected list_select(ListShared<kThreads>& ls,
     while (n_in > (uint32_t)kListMembers) {
         if (lo == hi) {  // equal logits: by their columns from here on
             if (!by_count) {
-                const uint64_t w = [&] {
-                    uint64_t one = 0;
-                    for (int i = 0; i < n && one == 0; ++i)
-                        if ((uint32_t)(keys[i] >> 32) == lo) one = weights[i];
-                    return one;
-                }();
+                for (int i = threadIdx.x; i < n; i += kThreads)
+                    if ((uint32_t)(keys[i] >> 32) == lo) ls.mass[0] = weights[i];  // all alike
+                __syncthreads();
+                const uint64_t w = ls.mass[0];
                 const uint64_t short_of = target - mass_before;
                 want = count_before + (uint32_t)(w ? (short_of + w - 1) / w : n_in);
                 by_count = true;
+                __syncthreads();
             }
             kmin = kmin > ((unsigned long long)lo << 32) ? kmin : (unsigned long long)lo << 32;
             kmax = kmax < ((unsigned long long)lo << 32 | 0xFFFFFFFFu)
@@ -507,22 +516,33 @@ __device__ __noinline__ Selected list_select(ListShared<kThreads>& ls,
         }
     }
     __syncthreads();
+    // Two (four, in a CTA of 512) neighbouring lanes share a member.
+    constexpr int kParts = kThreads / kListMembers;
     const int m = min((int)ls.n_member, kListMembers);
-    if ((int)threadIdx.x < m) {
-        const int me = ls.member[threadIdx.x];
+    const int item = (int)threadIdx.x / kParts;
+    if ((int)(threadIdx.x & ~31u) / kParts < m) {
+        const int me = ls.member[min(item, m - 1)];
         const unsigned long long mine = keys[me];
-        uint32_t rank = count_before;
-        uint64_t before = mass_before;
+        uint32_t less = 0;
+        uint64_t before = 0;
 #pragma unroll 4
-        for (int j = 0; j < m; ++j) {
+        for (int j = (int)threadIdx.x % kParts; j < m; j += kParts) {
             const int o = ls.member[j];
-            const bool less = by_column ? (uint32_t)keys[o] < (uint32_t)mine : keys[o] < mine;
-            rank += less;
-            before += less ? weights[o] : 0;
+            const bool yes = by_column ? (uint32_t)keys[o] < (uint32_t)mine : keys[o] < mine;
+            less += yes;
+            before += yes ? weights[o] : 0;
         }
+#pragma unroll
+        for (int off = 1; off < kParts; off <<= 1) {
+            less += __shfl_xor_sync(0xFFFFFFFFu, less, off);
+            before += __shfl_xor_sync(0xFFFFFFFFu, before, off);
+        }
+        const uint32_t rank = count_before + less + 1;
+        before += mass_before;
         const uint64_t after = before + weights[me];
-        if (by_count ? rank + 1 == want : (before < target && after >= target))
-            ls.found = {mine, rank + 1, after};
+        if (item < m && threadIdx.x % kParts == 0 &&
+            (by_count ? rank == want : (before < target && after >= target)))
+            ls.found = {mine, rank, after};
     }
     __syncthreads();
     const Selected found = ls.found;
@@ -555,7 +575,8 @@ struct ExactShared {
     unsigned long long scratch[2 * kExWarps];
     ListShared<kExThreads> list;
     // Team results, in the first CTA of a cluster.
-    unsigned long long part[kMaxTeam][3];
+    unsigned long long part[kMaxTeam][4];
+    unsigned long long sums[3][kExWarps];
     uint32_t n_cand;
     uint32_t first;
     uint32_t first_kept;
@@ -616,23 +637,27 @@ struct Team {
     // and the product round monotonely, so bins are ranges of the order).
     __device__ int bin0(float z) const { return min(kBins - 1, __float2int_rd((M - z) * bin_scale)); }
 
-    // Sum over the team of one value per thread, through slot `which` (of three):
-    // put() everywhere, sync(), then get() in any CTA.
-    __device__ void put(int which, uint64_t v) {
-        v = warp_sum(v);
+    // Sums over the team of two or three values per thread: put() everywhere,
+    // sync(), then get() in any CTA, by a whole warp.  The fourth slot is for
+    // the candidates' number.
+    template <int N>
+    __device__ void put(const uint64_t (&v)[N]) {
         __syncthreads();
-        if ((threadIdx.x & 31) == 0) sm.scratch[threadIdx.x >> 5] = v;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint64_t w = warp_sum(v[i]);
+            if ((threadIdx.x & 31) == 0) sm.sums[i][threadIdx.x >> 5] = w;
+        }
         __syncthreads();
-        if (threadIdx.x == 0) {
-            uint64_t all = 0;
-            for (int i = 0; i < kExWarps; ++i) all += sm.scratch[i];
-            lead.part[thread / kExThreads][which] = all;
+        const int i = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if (i < N) {
+            const uint64_t all = warp_sum(lane < kExWarps ? sm.sums[i][lane] : 0);
+            if (lane == 0) lead.part[thread / kExThreads][i] = all;
         }
     }
     __device__ uint64_t get(int which) const {
-        uint64_t all = 0;
-        for (int i = 0; i < threads / kExThreads; ++i) all += lead.part[i][which];
-        return all;
+        const int lane = threadIdx.x & 31;
+        return warp_sum(lane < threads / kExThreads ? lead.part[lane][which] : 0);
     }
     __device__ void clear(Histogram& h) const {
         for (int i = threadIdx.x; i < kBins; i += kExThreads) {
@@ -755,8 +780,9 @@ struct Team {
     // before by spans of the index order, and the elements inside, as far as
     // they fit; with `all` the mass of the whole row as well.
     __device__ __noinline__ void weigh_and_gather(uint32_t klo, uint32_t khi, bool all) {
-        if (first && threadIdx.x == 0) sm.n_cand = 0;
-        sync();
+        // Candidates are collected in each CTA and then moved to the first.
+        if (threadIdx.x == 0) sm.n_cand = 0;
+        __syncthreads();
         uint64_t outside = 0, inside = 0, ux = 0;
         // in registers: this function writes memory that could be *this
         const float M = this->M, temp = this->temp;
@@ -767,6 +793,9 @@ struct Team {
         ExactShared& lead = this->lead;
         const float2* const table = sm.table;
         auto weight = [&](float z) { return fixed_weight(z, M, c, k, table); };
+        auto weights = [&](float z0, float z1, uint64_t& w0, uint64_t& w1) {
+            fixed_weights(z0, z1, M, c, k, table, w0, w1);
+        };
         each_span([&](int s, int col, const float (&x)[kLane]) {
             bool any = all;
 #pragma unroll
@@ -774,10 +803,13 @@ struct Team {
             uint64_t before = 0;
             uint32_t hits = 0;
             if (__any_sync(0xFFFFFFFFu, any)) {
+                uint64_t we[kLane];
+#pragma unroll
+                for (int e = 0; e < kLane; e += 2) weights(x[e], x[e + 1], we[e], we[e + 1]);
 #pragma unroll
                 for (int e = 0; e < kLane; ++e) {
                     const uint32_t dk = desc_key(x[e]);
-                    const uint64_t w = weight(x[e]);
+                    const uint64_t w = we[e];
                     before += dk < klo ? w : 0;
                     outside += dk > khi ? w : 0;
                     hits |= (uint32_t)(dk >= klo && dk <= khi) << e;
@@ -788,7 +820,7 @@ struct Team {
             }
             if ((threadIdx.x & 31) == 0) lead.span_mass[s] = before;
             if (hits) {
-                uint32_t at = atomicAdd(&lead.n_cand, (uint32_t)__popc(hits));
+                uint32_t at = atomicAdd(&sm.n_cand, (uint32_t)__popc(hits));
 #pragma unroll 1
                 for (; hits; hits &= hits - 1, ++at) {
                     const int c = col + __ffs(hits) - 1;
@@ -796,29 +828,42 @@ struct Team {
                     const uint64_t w = weight(z);
                     inside += w;
                     if (at < (uint32_t)kCand) {
-                        lead.cand[at] = ((unsigned long long)desc_key(z) << 32) | (uint32_t)c;
-                        lead.weight[at] = w;
+                        sm.cand[at] = ((unsigned long long)desc_key(z) << 32) | (uint32_t)c;
+                        sm.weight[at] = w;
                     }
                 }
             }
         });
-        put(0, inside);
-        if (all) put(1, outside);
-        if (entropy) put(2, ux);
+        put<3>({inside, outside, ux});
+        if (threadIdx.x == 0) lead.part[thread / kExThreads][3] = sm.n_cand;
         sync();
+        const int rank = thread / kExThreads;
+        if (rank > 0) {
+            uint32_t to = 0;
+#pragma unroll
+            for (int i = 0; i < kMaxTeam; ++i) to += i < rank ? (uint32_t)lead.part[i][3] : 0;
+            const uint32_t mine = min(sm.n_cand, (uint32_t)kCand);
+            for (uint32_t i = threadIdx.x; i < mine && to + i < (uint32_t)kCand; i += kExThreads) {
+                lead.cand[to + i] = sm.cand[i];
+                lead.weight[to + i] = sm.weight[i];
+            }
+        }
         if (first) {
             uint64_t before = 0;
             for (int i = threadIdx.x; i * kSpan < V; i += kExThreads) before += sm.span_mass[i];
             before = warp_sum(before);
             if ((threadIdx.x & 31) == 0) sm.scratch[threadIdx.x >> 5] = before;
             __syncthreads();
-            if (threadIdx.x == 0) {
-                before = 0;
-                for (int i = 0; i < kExWarps; ++i) before += sm.scratch[i];
-                sm.mass_before = before;
-                sm.mass_in = get(0);
-                sm.total = before + sm.mass_in + (all ? get(1) : 0);
-                sm.ux = entropy ? get(2) : 0;
+            if (threadIdx.x < 32) {
+                before = warp_sum(threadIdx.x < kExWarps ? sm.scratch[threadIdx.x] : 0);
+                const uint64_t in = get(0), out = get(1), sum = get(2), n = get(3);
+                if (threadIdx.x == 0) {
+                    sm.n_cand = (uint32_t)n;
+                    sm.mass_before = before;
+                    sm.mass_in = in;
+                    sm.total = before + in + out;
+                    sm.ux = sum;
+                }
             }
         }
         sync();
@@ -1631,8 +1676,7 @@ __device__ void exact_row(const FilterArgs& a, int64_t t, Team<E>& tm, ExactShar
                 }
             }
         });
-        tm.put(0, n_min);
-        tm.put(1, n_fin);
+        tm.template put<2>({n_min, n_fin});
         tm.merge(sm.level0, lead.level0);
         const uint32_t n_finite = (uint32_t)tm.get(1);
         const uint32_t n_keep_min = rs.cut_m ? (uint32_t)tm.get(0) : n_finite;
@@ -1666,10 +1710,13 @@ __device__ void exact_row(const FilterArgs& a, int64_t t, Team<E>& tm, ExactShar
     if (!spans_ready) {
         uint64_t ux = 0;
         tm.each_span([&](int s, int col, const float (&x)[kLane]) {
-            uint64_t w = 0;
+            uint64_t w = 0, ws[kLane];
+#pragma unroll
+            for (int e = 0; e < kLane; e += 2)
+                fixed_weights(x[e], x[e + 1], M, tm.c, tm.k, sm.table, ws[e], ws[e + 1]);
 #pragma unroll
             for (int e = 0; e < kLane; ++e) {
-                const uint64_t we = tm.weight(x[e]);
+                const uint64_t we = ws[e];
                 const bool kept = is_kept(x[e], col + e, cut_key, cut_index);
                 w += kept ? we : 0;
                 if (!kSample && kept)
@@ -1679,7 +1726,7 @@ __device__ void exact_row(const FilterArgs& a, int64_t t, Team<E>& tm, ExactShar
             w = warp_sum(w);
             if (lane == 0) lead.span_mass[s] = w;
         });
-        if (!kSample) tm.put(2, ux);
+        if (!kSample) tm.template put<3>({0, 0, ux});
     }
     if (kSample && rs.u == 0.f) {
         uint32_t lowest = 0xFFFFFFFFu;
@@ -1702,7 +1749,10 @@ __device__ void exact_row(const FilterArgs& a, int64_t t, Team<E>& tm, ExactShar
     }
     block_scan<kExThreads, uint64_t>(sm.scratch, mine, 0, before, unused);
     if (threadIdx.x == kExThreads - 1) sm.mass_before = before + mine;
-    if (threadIdx.x == 0 && !kSample && !spans_ready) sm.ux = tm.get(2);
+    if (threadIdx.x < 32 && !kSample && !spans_ready) {
+        const uint64_t ux = tm.get(2);
+        if (threadIdx.x == 0) sm.ux = ux;
+    }
     __syncthreads();
     const uint64_t S = sm.mass_before;
     const float lnS = fixed_log(S, tm.k);
@@ -1806,8 +1856,13 @@ cudaError_t launch_filter(const FilterArgs& a, const DeviceInfo& dev, cudaStream
                       (unsigned)a.T, kFinThreads, 0, stream, 1, a);
     // Without filters only a draw can be left over.
     if (e != cudaSuccess || (!filtered && !kSample)) return e;
+    // Large teams where few rows can be left over; 16 is beyond the portable size.
+    static ContextSeen large_set;
+    e = ensure_large_cluster(ex_fn, large_set);
+    if (e != cudaSuccess) return e;
+    const int most = a.T <= 64 ? kMaxTeam : kMaxTeam / 2;
     int team = 1;
-    while (team < kMaxTeam && a.V >= (int64_t)team * 8192) team *= 2;
+    while (team < most && a.V >= (int64_t)team * 8192) team *= 2;
     int64_t teams = (int64_t)dev.sm_count * 2 / team;
     if (teams > a.T) teams = a.T;
     return launch_behind(filter_exact_kernel<E, kSample>, (unsigned)(teams * team), kExThreads,
