@@ -179,9 +179,10 @@ __global__ void __launch_bounds__(kGnThreads)
     const float factor = s_factor;
     const uint32_t u0 = (uint32_t)((uint64_t)g.units * blockIdx.x / gridDim.x);
     const uint32_t u1 = (uint32_t)((uint64_t)g.units * (blockIdx.x + 1) / gridDim.x);
-    int i = 0;
-    for (uint32_t u = u0; u < u1; ++u) {
-        while (i + 1 < g.count && g.t[i + 1].first_unit <= u) ++i;
+    // Backwards: what the norm read last is still in L2.
+    int i = g.count - 1;
+    for (uint32_t u = u1; u-- > u0;) {
+        while (i > 0 && g.t[i].first_unit > u) --i;
         const GradTensor& t = g.t[i];
         if (factor == 1.f && t.out == t.in) continue;
         const bool bf16 = t.bf16;
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kGnThreads)
 #pragma unroll
             for (int j = 0; j < kGnUnroll; ++j) {
                 const int k = j * kGnThreads + (int)threadIdx.x;
-                if (k < nv) q[j] = v[k];
+                if (k < nv) q[j] = __ldcs(v + k);
             }
 #pragma unroll
             for (int j = 0; j < kGnUnroll; ++j) {
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kGnThreads)
                     w[e] = bf16 ? bf2_pack_rn(bf2_lo(w[e]) * factor, bf2_hi(w[e]) * factor)
                                 : __float_as_uint(__uint_as_float(w[e]) * factor);
                 }
-                o[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                __stcs(o + k, make_uint4(w[0], w[1], w[2], w[3]));
             }
             done = e0 + (int64_t)nv * vec;
         }

@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         fence_mbar_init();
     }
     __syncwarp();
-    const uint64_t policy = policy_evict_normal();
+    const uint64_t policy = a.stream_once ? policy_evict_first() : policy_evict_normal();
 
     struct Item {
         int64_t t;
@@ -746,32 +746,42 @@ __global__ void __launch_bounds__(kFinThreads, kFiltered ? 4 : 6)
     }
 }
 
-template <typename E, bool kSample>
-cudaError_t launch_filter(const FilterArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
-    static ContextSeen records_set;
-    const void* rec_fn = reinterpret_cast<const void*>(filter_records_kernel<E, !kSample>);
-    cudaError_t e = ensure_smem_optin(rec_fn, (int)chunk_stats_smem_bytes(), records_set);
+template <typename E, bool kU>
+cudaError_t launch_records(const FilterArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
+    static ContextSeen configured;
+    const cudaError_t e =
+        ensure_smem_optin(reinterpret_cast<const void*>(filter_records_kernel<E, kU>),
+                          (int)chunk_stats_smem_bytes(), configured);
     if (e != cudaSuccess) return e;
-
     // Few items are spread over as many SMs as there are, one warp each at first.
     const int64_t items = a.T * a.chunks;
     int64_t warps = (items + dev.sm_count - 1) / dev.sm_count;
     warps = warps < kWarps ? warps : kWarps;
     int64_t grid = (items + warps - 1) / warps;
     grid = grid < dev.sm_count ? grid : dev.sm_count;
-    filter_records_kernel<E, !kSample><<<(unsigned)grid, (unsigned)warps * 32,
-                                         (size_t)warps * kStages * (kSlotBytes + sizeof(uint64_t)),
-                                         stream>>>(a);
-    e = cudaGetLastError();
+    filter_records_kernel<E, kU><<<(unsigned)grid, (unsigned)warps * 32,
+                                   (size_t)warps * kStages * (kSlotBytes + sizeof(uint64_t)),
+                                   stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename E, bool kSample>
+cudaError_t launch_filter(FilterArgs a, const DeviceInfo& dev, cudaStream_t stream) {
+    // A row without filters takes its entropy from the records; a filtered one
+    // from what it keeps.  So sums of e x are formed unless every row is filtered.
+    const bool every = (!a.top_ks && a.top_k > 0 && a.top_k < a.V) || (!a.top_ps && a.top_p < 1.f) ||
+                       (!a.min_ps && a.min_p > 0.f);
+    const bool some = every || a.top_ks || a.top_ps || a.min_ps;
+    a.stream_once = a.T * a.V * (int64_t)sizeof(E) > dev.l2_bytes / 2;
+    cudaError_t e = kSample || every ? launch_records<E, false>(a, dev, stream)
+                                     : launch_records<E, true>(a, dev, stream);
     if (e != cudaSuccess) return e;
-    const bool filtered = a.top_ks || a.top_ps || a.min_ps || (a.top_k > 0 && a.top_k < a.V) ||
-                          a.top_p < 1.f || a.min_p > 0.f;
-    e = launch_behind(filtered ? filter_finish_kernel<E, kSample, true>
-                               : filter_finish_kernel<E, kSample, false>,
+    e = launch_behind(some ? filter_finish_kernel<E, kSample, true>
+                           : filter_finish_kernel<E, kSample, false>,
                       (unsigned)a.T, kFinThreads, 0, stream, 1, a);
     // Without filters only a draw can be left over.
-    if (e != cudaSuccess || (!filtered && !kSample)) return e;
-    return launch_exact<E, kSample>(a, dev, stream);
+    if (e != cudaSuccess || (!some && !kSample)) return e;
+    return launch_exact<E, kSample>(a, some, dev, stream);
 }
 
 struct FilterWorkspace {

@@ -21,6 +21,7 @@ struct FilterArgs {
     const void* logits;
     int64_t T, V, ld;
     int chunks;                 // of a row
+    bool stream_once;           // the logits do not stay in L2 anyway
     const float* uniform;       // sampling
     const int64_t* labels;      // statistics
     int64_t ignore_index;
@@ -412,8 +413,10 @@ __device__ __forceinline__ uint64_t share_of(float p, uint64_t S) {
     return target ? target : 1;
 }
 
-// The rows that the finish kernel left, behind it on the stream.
+// The rows that the finish kernel left, behind it on the stream; `filtered`: some
+// row may have a filter.
 template <typename E, bool kSample>
-cudaError_t launch_exact(const FilterArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_exact(const FilterArgs& a, bool filtered, const DeviceInfo& dev,
+                         cudaStream_t stream);
 
 }  // namespace pstat

@@ -33,6 +33,12 @@ constexpr int kLane = kSpan / 32;
 constexpr int kMaxSpans = (int)(kFilterMaxV / kSpan);
 constexpr int kSpansPer = kMaxSpans / kExThreads;
 constexpr int kMaxTeam = 16;   // 16 CTAs are beyond the portable cluster size
+// With kAlone rows or more for every cluster the CTAs take rows alone: what a
+// team saves in a pass it loses again in synchronisation.  Flat rows of
+// V = 151,936 with top_p = 0.9 (us, teams / alone): 16 rows 103 / 248, 64 rows
+// 320 / 259, 192 rows 922 / 348; unfiltered draws: 39 rows 91 / 109, 87 rows
+// 199 / 180.
+constexpr int kAlone = 3;
 static_assert(kBins % kExThreads == 0 && kMaxSpans % kExThreads == 0 && kSpan <= kExThreads, "");
 
 enum Op : uint32_t {
@@ -694,10 +700,8 @@ __global__ void __launch_bounds__(kExThreads, 2)
     grid_wait();
     const int n = *a.left_count;
     if (n == 0) return;
-    // A cluster to a row, or, with more rows than a few for every cluster, a
-    // CTA: what a team saves in a pass it loses again in synchronisation.
     const int clusters = (int)(gridDim.x / cluster.num_blocks());
-    const int size = n >= 4 * clusters ? 1 : (int)cluster.num_blocks();
+    const int size = n >= kAlone * clusters ? 1 : (int)cluster.num_blocks();
     const int rank = size == 1 ? 0 : (int)cluster.block_rank();
     ExactShared& lead = size == 1 ? sm : *cluster.map_shared_rank(&sm, 0);
     uint32_t turn = 0;
@@ -724,14 +728,16 @@ __global__ void __launch_bounds__(kExThreads, 2)
 }  // namespace
 
 template <typename E, bool kSample>
-cudaError_t launch_exact(const FilterArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch_exact(const FilterArgs& a, bool filtered, const DeviceInfo& dev,
+                         cudaStream_t stream) {
     static ContextSeen smem_set, cluster_set;
     const void* fn = reinterpret_cast<const void*>(filter_exact_kernel<E, kSample>);
     cudaError_t e = ensure_smem_optin(fn, (int)sizeof(ExactShared), smem_set);
     if (e == cudaSuccess) e = ensure_large_cluster(fn, cluster_set);
     if (e != cudaSuccess) return e;
-    // Large teams where few rows can be left over.
-    const int most = a.T <= 64 ? kMaxTeam : kMaxTeam / 2;
+    // A row without filters takes one pass, over which synchronisation weighs
+    // more; of many such rows more are worked on at once by smaller teams.
+    const int most = filtered || a.T <= 64 ? kMaxTeam : kMaxTeam / 2;
     int team = 1;
     while (team < most && a.V >= (int64_t)team * 8192) team *= 2;
     int64_t teams = (int64_t)dev.sm_count * 2 / team;
@@ -740,9 +746,13 @@ cudaError_t launch_exact(const FilterArgs& a, const DeviceInfo& dev, cudaStream_
                          sizeof(ExactShared), stream, (unsigned)team, a);
 }
 
-template cudaError_t launch_exact<uint16_t, true>(const FilterArgs&, const DeviceInfo&, cudaStream_t);
-template cudaError_t launch_exact<uint16_t, false>(const FilterArgs&, const DeviceInfo&, cudaStream_t);
-template cudaError_t launch_exact<float, true>(const FilterArgs&, const DeviceInfo&, cudaStream_t);
-template cudaError_t launch_exact<float, false>(const FilterArgs&, const DeviceInfo&, cudaStream_t);
+template cudaError_t launch_exact<uint16_t, true>(const FilterArgs&, bool, const DeviceInfo&,
+                                                cudaStream_t);
+template cudaError_t launch_exact<uint16_t, false>(const FilterArgs&, bool, const DeviceInfo&,
+                                                cudaStream_t);
+template cudaError_t launch_exact<float, true>(const FilterArgs&, bool, const DeviceInfo&,
+                                                cudaStream_t);
+template cudaError_t launch_exact<float, false>(const FilterArgs&, bool, const DeviceInfo&,
+                                                cudaStream_t);
 
 }  // namespace pstat
