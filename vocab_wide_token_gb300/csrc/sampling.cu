@@ -381,9 +381,12 @@ __device__ __forceinline__ void write_kept(const FilterArgs& a, const E* row, co
 // Targets of a nucleus that is measured against the fp32 sum: p S with the
 // error bound taken off and added.
 __device__ __forceinline__ void nucleus_targets(const FinishRow& r, FinishShared& sm) {
-    const double target = (double)r.rs.top_p * (double)r.Sf * (double)(1ull << r.scale);
-    sm.target0 = __double2ull_rd(target * (1.0 - (double)kSumError));
-    sm.target1 = __double2ull_ru(target * (1.0 + (double)kSumError));
+    const uint64_t S = __float2ull_rn(r.Sf * __int_as_float((127 + r.scale) << 23));
+    const uint64_t target = share_of(r.rs.top_p, S);
+    static_assert(kSumError == 1.f / 262144.f, "2^-18");
+    const uint64_t error = (target >> 18) + 2;
+    sm.target0 = target > error ? target - error : 0;
+    sm.target1 = target + error;
 }
 
 // Decides a row from at most kFinThreads candidates.
@@ -447,7 +450,7 @@ __device__ __forceinline__ void finish_few(const FilterArgs& a, const E* row, co
     if (mine && rank == keep - 1) {
         sm.sum = before + w;
         sm.cut = key;
-        if (kSample) sm.draw = __double2ull_rd((double)r.rs.u * (double)(before + w));
+        if (kSample) sm.draw = draw_of(r.rs.u, before + w);
     }
     __syncthreads();
     const uint64_t S = sm.sum;
@@ -554,7 +557,7 @@ __device__ __noinline__ void finish_many(const FilterArgs& a, const E* row, cons
     const bool lowest = r.rs.u == 0.f;
     const Selected s = list_select<kFinThreads>(
         sm.list, sm.cand, sm.weight, n, 0, cut, true, lowest, 1,
-        __double2ull_rd((double)r.rs.u * (double)S) + 1, 0, 0, kGrain<E>);
+        draw_of(r.rs.u, S) + 1, 0, 0, kGrain<E>);
     if (threadIdx.x == 0) write_token<E, kSample>(a, row, r, (uint32_t)s.key, S);
 }
 

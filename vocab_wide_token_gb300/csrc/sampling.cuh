@@ -407,10 +407,31 @@ __device__ __forceinline__ long long entropy_term(unsigned long long key, uint64
     return w ? __float2ll_rn(e * x * 1.7592186e13f) : 0;
 }
 
-// C >= p S in whole numbers; at least 1, so that a token is kept.
+// f S for a float f in [0, 1) and S < 2^62: the whole part, and whether there is
+// a rest.  f = mant 2^-sh; the product is taken in 128 bits (fp64 runs at about
+// two operations per clock and SM here, one conversion costs a thousand cycles).
+__device__ __forceinline__ uint64_t part_of(float f, uint64_t S, bool& rest) {
+    const uint32_t b = __float_as_uint(f), e = b >> 23;
+    const uint64_t mant = (b & 0x7FFFFFu) | (e ? 0x800000u : 0u);
+    const int sh = 150 - (int)(e ? e : 1u);  // in [24, 149]
+    const uint64_t lo = S * mant, hi = __umul64hi(S, mant);
+    if (sh < 64) {
+        rest = (lo & ((1ull << sh) - 1)) != 0;
+        return hi << (64 - sh) | lo >> sh;
+    }
+    rest = lo != 0 || (sh < 128 ? (hi & ((1ull << (sh - 64)) - 1)) != 0 : hi != 0);
+    return sh < 128 ? hi >> (sh - 64) : 0;
+}
+// C >= p S  <=>  C >= share_of(p, S); at least 1, so that a token is kept.
 __device__ __forceinline__ uint64_t share_of(float p, uint64_t S) {
-    const uint64_t target = __double2ull_ru((double)p * (double)S);
-    return target ? target : 1;
+    bool rest;
+    const uint64_t t = part_of(p, S, rest);
+    return max(t + rest, (uint64_t)1);
+}
+// C > u S  <=>  C > draw_of(u, S).
+__device__ __forceinline__ uint64_t draw_of(float u, uint64_t S) {
+    bool rest;
+    return part_of(u, S, rest);
 }
 
 // The rows that the finish kernel left, behind it on the stream; `filtered`: some

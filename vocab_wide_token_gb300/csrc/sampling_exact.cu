@@ -56,19 +56,25 @@ struct Command {
 
 struct ExactShared {
     uint32_t level0[kBins];
-    uint32_t count[kBins];
-    unsigned long long mass[kBins];
+    uint32_t inside[kBins];  // where in the bin they lie, summed, in steps of 2^-11
+    union {
+        struct {
+            uint32_t count[kBins];
+            unsigned long long mass[kBins];
+        };
+        ListShared<kExThreads> list;
+    };
     unsigned long long cand[kCand];
     unsigned long long weight[kCand];
     unsigned long long span[kMaxSpans];
-    ListShared<kExThreads> list;
     float2 table[64];
     unsigned long long scratch[2 * kExWarps];
     unsigned long long sums[3][kExWarps];
     unsigned long long part[kMaxTeam][3];  // the leader's: sums of every CTA
     Command command[2];                    // the leader's, by turns
     uint32_t n_cand, first, lowest, offset;
-    uint32_t bin, n_in, count_before, klo, khi;
+    uint32_t bin, n_in, count_before, klo, khi, edge;
+    float z_min;
     unsigned long long mass_before, shift, wide;
     Selected sel;
 };
@@ -143,7 +149,7 @@ struct Team {
     // ---- passes, by every CTA of the team --------------------------------------
     __device__ __forceinline__ void pass_count() const {
         if (rank) {
-            for (int i = threadIdx.x; i < kBins; i += kExThreads) sm.level0[i] = 0;
+            for (int i = threadIdx.x; i < kBins; i += kExThreads) sm.level0[i] = sm.inside[i] = 0;
             __syncthreads();
         }
         uint32_t n_min = 0, n_finite = 0;
@@ -151,7 +157,10 @@ struct Team {
 #pragma unroll
             for (int e = 0; e < kLane; ++e)
                 if (x[e] > -INFINITY) {
-                    atomicAdd(&sm.level0[bin0(x[e])], 1u);
+                    const int b = bin0(x[e]);
+                    const float in = (M - x[e]) * bin_scale - (float)b;
+                    atomicAdd(&sm.level0[b], 1u);
+                    atomicAdd(&sm.inside[b], (uint32_t)__float2int_rn(fminf(in, 1.f) * 2048.f));
                     n_min += x[e] >= z_min;
                     ++n_finite;
                 }
@@ -159,7 +168,10 @@ struct Team {
         put(n_finite, n_min, 0);
         if (rank)
             for (int i = threadIdx.x; i < kBins; i += kExThreads)
-                if (sm.level0[i]) atomicAdd(&lead.level0[i], sm.level0[i]);
+                if (sm.level0[i]) {
+                    atomicAdd(&lead.level0[i], sm.level0[i]);
+                    atomicAdd(&lead.inside[i], sm.inside[i]);
+                }
     }
 
     __device__ __forceinline__ void pass_weigh(uint32_t klo, uint32_t khi, bool all) const {
@@ -317,7 +329,7 @@ struct Team {
         const Command cmd = {op, lo, hi, arg};
         // what the pass adds to
         if (op == kCount)
-            for (int i = threadIdx.x; i < kBins; i += kExThreads) sm.level0[i] = 0;
+            for (int i = threadIdx.x; i < kBins; i += kExThreads) sm.level0[i] = sm.inside[i] = 0;
         if (op == kNarrow)
             for (int i = threadIdx.x; i < kBins; i += kExThreads) sm.count[i] = 0, sm.mass[i] = 0;
         if (threadIdx.x == 0) {
@@ -363,19 +375,23 @@ struct Team {
         return sm.bin;
     }
 
-    // The last of the level-0 bins [lo, hi] before which the estimated mass is
+    // Around the last of the level-0 bins [lo, hi] before which the estimated mass is
     // below `target`.  A bin's mass is estimated by its count times the weight
-    // of its middle (steps of 1/32 of a binary order: 1.1% of it at most);
-    // `anchor`, if not negative, is a bin before which the mass is known.
-    __device__ uint32_t guess_bin(uint64_t target, int lo, int hi, int anchor, uint64_t known) const {
+    // of its logits' mean (its middle alone is 1.1% off for the few that weigh
+    // most, which made one guess in four miss; the mean 2^-15); `anchor`, if not negative, is a bin before which the mass is known.
+    struct Bins {
+        uint32_t first, last, count_before, n_in;
+    };
+    __device__ Bins guess_bins(uint64_t target, int lo, int hi, int anchor, uint64_t known) const {
         constexpr int kPer = kBins / kExThreads;
         const int b0 = threadIdx.x * kPer;
         const float one = __int_as_float((127 + k) << 23);
         uint64_t n = 0, w = 0, part[kPer];
         for (int i = 0; i < kPer; ++i) {
             n += sm.level0[b0 + i];
-            const float mid = exp2f(-((float)(b0 + i) + 0.5f) * (64.f / kBins));
-            part[i] = (uint64_t)((float)sm.level0[b0 + i] * mid * one);
+            const float count = (float)sm.level0[b0 + i];
+            const float mean = count > 0.f ? (float)sm.inside[b0 + i] / (count * 2048.f) : 0.f;
+            part[i] = (uint64_t)(count * exp2f(-((float)(b0 + i) + mean) * (64.f / kBins)) * one);
             w += part[i];
         }
         uint64_t nb, wb;
@@ -398,23 +414,35 @@ struct Team {
         }
         __syncthreads();
         const uint32_t b = sm.bin;
+        at = wb + sm.shift;
         for (int i = 0; i < kPer; ++i) {
             if ((uint32_t)(b0 + i) == b) {
                 sm.count_before = (uint32_t)nb;
-                sm.n_in = sm.level0[b0 + i];
+                // where in its mass the target is expected: near the start, the end
+                sm.edge = (target - at) * 8 < part[i] ? 1 : (target - at) * 8 > part[i] * 7 ? 2 : 0;
             }
             nb += sm.level0[b0 + i];
+            at += part[i];
         }
         __syncthreads();
-        return b;
+        // There the guess takes the neighbour in, as a miss costs a pass.
+        Bins g = {b, b, sm.count_before, sm.level0[b]};
+        const uint32_t edge = sm.edge;
+        if (edge == 2 && (int)b < hi && g.n_in + sm.level0[b + 1] <= (uint32_t)kCand)
+            g.n_in += sm.level0[++g.last];
+        if (edge == 1 && (int)b > lo && g.n_in + sm.level0[b - 1] <= (uint32_t)kCand) {
+            g.n_in += sm.level0[--g.first];
+            g.count_before -= sm.level0[g.first];
+        }
+        return g;
     }
 
-    // The keys of level-0 bin b, in sm.klo and sm.khi.
-    __device__ void bin_range(uint32_t b) const {
+    // The keys of the level-0 bins [first, last], in sm.klo and sm.khi.
+    __device__ void bin_range(uint32_t first, uint32_t last) const {
         if (threadIdx.x < 2) {
-            // Smallest key whose bin is >= b (thread 0) and > b (thread 1): near
-            // the key of M - b/bin_scale, or wherever a bisection finds it.
-            const int edge = (int)(b + threadIdx.x);
+            // Smallest key whose bin is >= first (thread 0) and > last (thread 1):
+            // near the key of M - edge/bin_scale, or wherever a bisection finds it.
+            const int edge = (int)(threadIdx.x ? last + 1 : first);
             uint32_t lo = desc_key(M), hi = kKeyNegInf;  // answer in [lo, hi]
             const uint32_t near = desc_key(M - (float)edge / bin_scale);
             if (near > lo + 64 && near + 64 < hi) {
@@ -431,7 +459,7 @@ struct Team {
             if (threadIdx.x == 0)
                 sm.klo = lo;
             else
-                sm.khi = b == kBins - 1 ? kKeyNegInf - 1 : lo - 1;
+                sm.khi = last == kBins - 1 ? kKeyNegInf - 1 : lo - 1;
         }
         __syncthreads();
     }
@@ -457,15 +485,6 @@ struct Team {
         __syncthreads();
         return {before, in, before + in + out};
     }
-    // share_of in one thread: fp64 runs at two operations per clock and SM.
-    __device__ uint64_t one_share_of(float p, uint64_t S) const {
-        if (threadIdx.x == 0) sm.wide = share_of(p, S);
-        __syncthreads();
-        const uint64_t t = sm.wide;
-        __syncthreads();
-        return t;
-    }
-
     // The element at which the count reaches `want`, or the mass `target`, in
     // the order of the finite logits, all of which level0 counts.  With `share`
     // the target is that share of the whole mass, which this takes as well;
@@ -474,31 +493,35 @@ struct Team {
     // `ux` its sum of e x.
     __device__ __noinline__ Selected select(bool by_count, uint32_t want, uint64_t target, float share,
                                bool& ties, uint64_t& ux) {
-        uint32_t b = by_count ? pick_bin(sm.level0, nullptr, true, want, 0, 0, 0)
-                              : guess_bin(target, 0, kBins - 1, -1, 0);
-        bin_range(b);
-        uint32_t klo = sm.klo, khi = sm.khi, n_in = sm.n_in, count_before = sm.count_before;
+        Bins g;
+        if (by_count) {
+            const uint32_t b = pick_bin(sm.level0, nullptr, true, want, 0, 0, 0);
+            g = {b, b, sm.count_before, sm.n_in};
+        } else {
+            g = guess_bins(target, 0, kBins - 1, -1, 0);
+        }
+        bin_range(g.first, g.last);
+        uint32_t klo = sm.klo, khi = sm.khi;
         Weighed m = weigh(klo, khi, share > 0.f);
         if (!by_count) {
-            if (share > 0.f) target = one_share_of(share, m.total);
+            if (share > 0.f) target = share_of(share, m.total);
             // A guess that missed narrows the bins that are left, so this ends.
             int lo = 0, hi = kBins - 1;
             while (true) {
-                if (m.before >= target && (int)b > lo)
-                    hi = (int)b - 1;
-                else if (m.before + m.inside < target && (int)b < hi)
-                    lo = (int)b + 1;
+                if (m.before >= target && (int)g.first > lo)
+                    hi = (int)g.first - 1;
+                else if (m.before + m.inside < target && (int)g.last < hi)
+                    lo = (int)g.last + 1;
                 else
                     break;
-                b = guess_bin(target, lo, hi, (int)b, m.before);
-                bin_range(b);
+                g = guess_bins(target, lo, hi, (int)g.first, m.before);
+                bin_range(g.first, g.last);
                 klo = sm.klo;
                 khi = sm.khi;
-                n_in = sm.n_in;
-                count_before = sm.count_before;
                 m = weigh(klo, khi, false);
             }
         }
+        uint32_t n_in = g.n_in, count_before = g.count_before;
         uint64_t mass_before = m.before;
         bool narrowed = false;
         // every round leaves 1/2048 of the keys at most
@@ -605,7 +628,7 @@ struct Team {
             if (rs.cut_p) {
                 if (want < n_finite) {
                     const uint64_t total = select(true, want, 0, 0.f, ties, ux).mass;
-                    sel = select(false, 0, one_share_of(rs.top_p, total), 0.f, ties, ux);
+                    sel = select(false, 0, share_of(rs.top_p, total), 0.f, ties, ux);
                 } else {
                     const float about = rs.top_p * Sf * __int_as_float((127 + k) << 23);
                     sel = select(false, 0, (uint64_t)about, rs.top_p, ties, ux);
@@ -638,7 +661,7 @@ struct Team {
             const uint64_t S = before + mine;
             sm.mass_before = S;
             // C > u S in whole numbers
-            sm.wide = kSample ? __double2ull_rd((double)rs.u * (double)S) : 0;
+            sm.wide = kSample ? draw_of(rs.u, S) : 0;
         }
         if (threadIdx.x == 0) sm.first = 0;
         __syncthreads();
@@ -711,8 +734,14 @@ __global__ void __launch_bounds__(kExThreads, 2)
         const TempScale c = temp_scale(rs.temp);
         const float3 st = fold_records(a.records + t * a.chunks, a.chunks, c.ch, threadIdx.x & 31);
         const float M = st.x + 0.f;
+        float z_min = -INFINITY;
+        if (rs.cut_m) {  // in fp64, so by one thread
+            if (threadIdx.x == 0) sm.z_min = min_p_logit(M, rs);
+            __syncthreads();
+            z_min = sm.z_min;
+        }
         Team<E, kSample> team{sm, lead, static_cast<const E*>(a.logits) + t * a.ld, (int)a.V, rank,
-                              size, turn, rs, M, st.y, min_p_logit(M, rs),
+                              size, turn, rs, M, st.y, z_min,
                               c.ch * ((float)kBins / 64.f), c,
                               fixed_scale(st.y * (1.f + 2.f * kSumError))};
         if (rank == 0)

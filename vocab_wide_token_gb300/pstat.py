@@ -851,13 +851,13 @@ def _grad_list(tensors, out, writes):
     n = len(tensors)
     if dtypes.count(torch.bfloat16) + dtypes.count(torch.float32) != n:
         raise TypeError("tensors must be bfloat16 or float32")
-    words = array.array("q", bytes(32 * n))
-    at = array.array("q", map(T.data_ptr, tensors))
-    sizes = array.array("q", map(T.numel, tensors))
+    bf16 = torch.bfloat16
+    at = list(map(T.data_ptr, tensors))
+    sizes = list(map(T.numel, tensors))
+    words = [0] * (4 * n)
     words[0::4] = at
     words[2::4] = sizes
-    bf16 = torch.bfloat16
-    words[3::4] = array.array("q", [BF16 if d is bf16 else F32 for d in dtypes])
+    words[3::4] = [BF16 if d is bf16 else F32 for d in dtypes]
     outs = tensors
     if out is not None:
         outs = [out] if isinstance(out, torch.Tensor) else list(out)
@@ -866,12 +866,13 @@ def _grad_list(tensors, out, writes):
                 or [o.shape for o in outs] != [x.shape for x in tensors]):
             raise ValueError("out must have one contiguous tensor for each of tensors, of its "
                              f"shape and dtype, on {dev}")
-        at = array.array("q", map(T.data_ptr, outs))
+        at = list(map(T.data_ptr, outs))
     if writes:
         words[1::4] = at
         written = [p for p, k in zip(at, sizes) if k]
         if len(set(written)) != len(written):
             raise ValueError("a tensor may be written once only")
+    words = array.array("q", words)
     return outs, words, dev
 
 
