@@ -303,15 +303,16 @@ def test_undefined_rows_and_bad_values(cuda_lib):
 def test_batch_invariance(cuda_lib, dtype):
     """A row gives the same bits alone, in a small batch and in a large one, at
     any alignment and from call to call."""
-    V = 30011
-    z, g = _rows(300, V, dtype, 12, peak=12.0)
-    u = torch.rand(300, generator=g, device="cuda")
-    y = torch.randint(0, V, (300,), generator=g, device="cuda")
+    V, T = 30011, 700  # more rows than are resident at once: the other finish kernel
+    z, g = _rows(T, V, dtype, 12, peak=12.0)
+    z[::9] = _rows(len(z[::9]), V, dtype, 13)[0]  # flat rows, for the exact path
+    u = torch.rand(T, generator=g, device="cuda")
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
     for s in [(0.9, 0, 1.0, 0.0), (0.9, 0, 0.9, 0.0), (1.0, 40, 1.0, 0.0), (1.0, 0, 1.0, 0.05),
               (1.0, 4000, 0.99, 0.0)]:
         tok, lp = cuda_lib.sample(z, u, *s)
         full = cuda_lib.filtered_forward(z, y, *s)
-        for a, b in ((0, 1), (7, 60), (250, 300)):
+        for a, b in ((0, 1), (7, 60), (250, 300), (600, 700)):
             store = torch.zeros(b - a, V + 5, dtype=dtype, device="cuda")
             store[:, 3:3 + V] = z[a:b]
             for part in (z[a:b], store[:, 3:3 + V]):

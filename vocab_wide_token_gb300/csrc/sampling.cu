@@ -179,9 +179,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 // is a few hundred cycles, where a sort by a block needs 28 synchronised steps.
 // Among more the cut and the draw are selected by histograms (list_select).
 // ---------------------------------------------------------------------------
-constexpr int kFinThreads = 256;
 constexpr int kFinBins = 1024;     // 64 binary orders of e, in steps of 1/16
-constexpr int kFinCand = 2048;
+constexpr int kFinCand = 1024;
 constexpr int kFinGroups = 2048;
 constexpr int kFinAll = 1024;      // columns of a row that are all taken as candidates
 constexpr int kFinShort = 16384;   // columns of a row whose histogram is of its columns
@@ -193,12 +192,14 @@ struct Candidate {
 };
 
 // What a row without filters needs.
+template <int kFinThreads>
 struct DrawShared {
     float prefix[kMaxChunks];
     unsigned long long scratch[2 * (kFinThreads / 32)];
     uint32_t bin, found;
 };
 
+template <int kFinThreads>
 struct FinishShared {
     union {
         struct {
@@ -225,7 +226,7 @@ __device__ __forceinline__ void leave_row(const FilterArgs& a, int64_t t) {
     if (threadIdx.x == 0) a.left[atomicAdd(a.left_count, 1)] = (int)t;
 }
 
-template <typename E, typename Shared>
+template <typename E, int kFinThreads, typename Shared>
 __device__ void finish_greedy(const FilterArgs& a, int64_t t, const E* row, const float4* rec,
                               float M, Shared& sm) {
     constexpr int kChunk = Elem<E>::kChunk;
@@ -247,7 +248,7 @@ __device__ void finish_greedy(const FilterArgs& a, int64_t t, const E* row, cons
     }
 }
 
-template <typename E, typename Shared>
+template <typename E, int kFinThreads, typename Shared>
 __device__ void finish_draw(const FilterArgs& a, int64_t t, const E* row, const float4* rec,
                             float M, float c, const RowSettings& rs, float lnS, Shared& sm) {
     const int lane = threadIdx.x & 31, n = a.chunks;
@@ -281,46 +282,45 @@ __device__ void finish_draw(const FilterArgs& a, int64_t t, const E* row, const 
     __syncthreads();
     const int chunk = (int)sm.bin;
     if (chunk < 0 || chunk >= n) return leave_row(a, t);
+    // Each thread sums its run of columns; the one whose run the target falls
+    // into walks through it again.
     constexpr int kVec = Elem<E>::kVec, kPer = Elem<E>::kChunk / kFinThreads;
     const int col0 = chunk * Elem<E>::kChunk + threadIdx.x * kPer;
-    float z[kPer], sum = 0.f;
-    {
-        int col[kPer / kVec];
-        float x[kPer / kVec][kVec];
+    auto walk = [&](auto each) {
+#pragma unroll 1
+        for (int i = 0; i < kPer; i += 2 * kVec) {
+            const int col[2] = {col0 + i, col0 + i + kVec};
+            float x[2][kVec];
+            load_columns<E, 2>(row, col, (int)a.V, x);
 #pragma unroll
-        for (int v = 0; v < kPer / kVec; ++v) col[v] = col0 + v * kVec;
-        load_columns<E, kPer / kVec>(row, col, (int)a.V, x);
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int v = 0; v < kPer / kVec; ++v)
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) z[v * kVec + e] = x[v][e];
-    }
-    float ex[kPer];
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-        ex[e] = ex2_approx((z[e] - M) * c);
-        sum += ex[e];
-    }
+                for (int e = 0; e < kVec; ++e) each(col[h] + e, x[h][e], ex2_approx((x[h][e] - M) * c));
+        }
+    };
+    float sum = 0.f;
+    walk([&](int, float, float e) { sum += e; });
     float before, unused;
     block_scan<kFinThreads, float>(sm.scratch, sum, 0.f, before, unused);
     float c0 = (chunk ? sm.prefix[chunk - 1] : 0.f) + before;
-    const float room = kSumError * total;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-        const float c1 = c0 + ex[e];
-        if (target - c0 > room && c1 - target > room) {  // one column at most
-            a.token[t] = col0 + e;
-            a.logprob[t] = (z[e] - M) / rs.temp - lnS;
-            sm.found = 1;
-        }
-        c0 = c1;
+    if (c0 <= target && target < c0 + sum) {
+        const float room = kSumError * total;
+        walk([&](int col, float z, float e) {
+            const float c1 = c0 + e;
+            if (target - c0 > room && c1 - target > room) {  // one column at most
+                a.token[t] = col;
+                a.logprob[t] = (z - M) / rs.temp - lnS;
+                sm.found = 1;
+            }
+            c0 = c1;
+        });
     }
     __syncthreads();
     if (!sm.found) leave_row(a, t);
 }
 
 // Calls f(group, maximum) for a row's groups, eight loads ahead.
-template <typename E, typename F>
+template <typename E, int kFinThreads, typename F>
 __device__ __forceinline__ void for_each_group(const E* __restrict__ gm, int groups, F f) {
     constexpr int kAhead = 8;
     for (int i0 = threadIdx.x; i0 < groups; i0 += kAhead * kFinThreads) {
@@ -380,7 +380,8 @@ __device__ __forceinline__ void write_kept(const FilterArgs& a, const E* row, co
 
 // Targets of a nucleus that is measured against the fp32 sum: p S with the
 // error bound taken off and added.
-__device__ __forceinline__ void nucleus_targets(const FinishRow& r, FinishShared& sm) {
+template <int kFinThreads>
+__device__ __forceinline__ void nucleus_targets(const FinishRow& r, FinishShared<kFinThreads>& sm) {
     const uint64_t S = __float2ull_rn(r.Sf * __int_as_float((127 + r.scale) << 23));
     const uint64_t target = share_of(r.rs.top_p, S);
     static_assert(kSumError == 1.f / 262144.f, "2^-18");
@@ -390,9 +391,9 @@ __device__ __forceinline__ void nucleus_targets(const FinishRow& r, FinishShared
 }
 
 // Decides a row from at most kFinThreads candidates.
-template <typename E, bool kSample>
+template <typename E, bool kSample, int kFinThreads>
 __device__ __forceinline__ void finish_few(const FilterArgs& a, const E* row, const FinishRow& r,
-                                           FinishShared& sm) {
+                                           FinishShared<kFinThreads>& sm) {
     const int lane = threadIdx.x & 31, n = r.n;
     // `parts` neighbouring lanes share a candidate, each comparing it with its
     // share of the others.
@@ -476,9 +477,9 @@ __device__ __forceinline__ void finish_few(const FilterArgs& a, const E* row, co
 }
 
 // Decides a row from more candidates, by selections in their list.
-template <typename E, bool kSample>
+template <typename E, bool kSample, int kFinThreads>
 __device__ __noinline__ void finish_many(const FilterArgs& a, const E* row, const FinishRow& r,
-                                         FinishShared& sm) {
+                                         FinishShared<kFinThreads>& sm) {
     const int lane = threadIdx.x & 31, n = r.n;
     uint64_t total = 0;
     int n_hi = 0, n_lo = 0;  // columns that min-p keeps, by both bounds
@@ -563,10 +564,11 @@ __device__ __noinline__ void finish_many(const FilterArgs& a, const E* row, cons
 
 // kFiltered: some row may have a filter; without, the kernel needs neither the
 // registers nor the shared memory of the candidates.
-template <typename E, bool kSample, bool kFiltered>
-__global__ void __launch_bounds__(kFinThreads, kFiltered ? 4 : 6)
+template <typename E, bool kSample, bool kFiltered, int kFinThreads>
+__global__ void __launch_bounds__(kFinThreads, (kFiltered ? 1024 : 1536) / kFinThreads)
     filter_finish_kernel(const __grid_constant__ FilterArgs a) {
-    __shared__ typename std::conditional<kFiltered, FinishShared, DrawShared>::type sm;
+    __shared__ typename std::conditional<kFiltered, FinishShared<kFinThreads>,
+                                         DrawShared<kFinThreads>>::type sm;
     constexpr int kVec = Elem<E>::kVec;
     const int64_t t = blockIdx.x;
     const int V = (int)a.V, lane = threadIdx.x & 31;
@@ -601,12 +603,12 @@ __global__ void __launch_bounds__(kFinThreads, kFiltered ? 4 : 6)
         if (threadIdx.x == 0) write_undefined<kSample>(a, t, PSTAT_DEV_EMPTY_ROW);
         return;
     }
-    if (rs.greedy) return finish_greedy(a, t, row, rec, M, sm);
+    if (rs.greedy) return finish_greedy<E, kFinThreads>(a, t, row, rec, M, sm);
     if (!kFiltered || (!rs.cut_k && !rs.cut_p && !rs.cut_m)) {
         const float lnS = logf(Sf);
         if (kSample) {
             __syncthreads();  // the histogram's zeros share memory with the prefix sums
-            return finish_draw(a, t, row, rec, M, r.c.ch, rs, lnS, sm);
+            return finish_draw<E, kFinThreads>(a, t, row, rec, M, r.c.ch, rs, lnS, sm);
         }
         if (threadIdx.x == 0)
             write_statistics(a, t, row, M, lnS, lnS - kLn2 * (st.z / Sf), rs.temp, 0xFFFFFFFFu,
@@ -650,7 +652,7 @@ __global__ void __launch_bounds__(kFinThreads, kFiltered ? 4 : 6)
                     for (int e = 0; e < kVec; ++e) add(x[h][e]);
             }
         } else {
-            for_each_group(gm, groups, [&](int, float g) { add(g); });
+            for_each_group<E, kFinThreads>(gm, groups, [&](int, float g) { add(g); });
         }
         __syncthreads();
         constexpr int kPer = kFinBins / kFinThreads;
@@ -690,7 +692,7 @@ __global__ void __launch_bounds__(kFinThreads, kFiltered ? 4 : 6)
     if (r.all) {
         n_vec = (V + kVec - 1) / kVec;
     } else {
-        for_each_group(gm, groups, [&](int i, float g) {
+        for_each_group<E, kFinThreads>(gm, groups, [&](int i, float g) {
             if (g > -INFINITY && (M - g) * bin_scale < edge) {
                 const uint32_t at = atomicAdd(&sm.n_group, 1u);
                 if (at < (uint32_t)kFinGroups) sm.group[at] = (uint16_t)i;
@@ -742,9 +744,9 @@ __global__ void __launch_bounds__(kFinThreads, kFiltered ? 4 : 6)
     if (r.n > kFinCand || (rs.cut_p && r.k > r.n && !r.all)) return leave_row(a, t);
     r.scale = fixed_scale(Sf * (1.f + 2.f * kSumError));
     if (r.n <= kFinThreads)
-        finish_few<E, kSample>(a, row, r, sm);
+        finish_few<E, kSample, kFinThreads>(a, row, r, sm);
     else
-        finish_many<E, kSample>(a, row, r, sm);
+        finish_many<E, kSample, kFinThreads>(a, row, r, sm);
 
     }
 }
@@ -779,9 +781,15 @@ cudaError_t launch_filter(FilterArgs a, const DeviceInfo& dev, cudaStream_t stre
     cudaError_t e = kSample || every ? launch_records<E, false>(a, dev, stream)
                                      : launch_records<E, true>(a, dev, stream);
     if (e != cudaSuccess) return e;
-    e = launch_behind(some ? filter_finish_kernel<E, kSample, true>
-                           : filter_finish_kernel<E, kSample, false>,
-                      (unsigned)a.T, kFinThreads, 0, stream, 1, a);
+    // Rows beyond what is resident at once: half the threads to a row, as its time
+    // is mostly latency and registers decide how many rows an SM holds.
+    const bool small = a.T > 4 * dev.sm_count;
+    e = some ? small ? launch_behind(filter_finish_kernel<E, kSample, true, 128>, (unsigned)a.T, 128,
+                                     0, stream, 1, a)
+                     : launch_behind(filter_finish_kernel<E, kSample, true, 256>, (unsigned)a.T, 256,
+                                     0, stream, 1, a)
+             : launch_behind(filter_finish_kernel<E, kSample, false, 256>, (unsigned)a.T, 256, 0,
+                             stream, 1, a);
     // Without filters only a draw can be left over.
     if (e != cudaSuccess || (!some && !kSample)) return e;
     return launch_exact<E, kSample>(a, some, dev, stream);

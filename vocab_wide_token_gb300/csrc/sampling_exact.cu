@@ -666,7 +666,10 @@ struct Team {
         if (threadIdx.x == 0) sm.first = 0;
         __syncthreads();
         const uint64_t S = sm.mass_before, target = sm.wide;
-        const float lnS = fixed_log(S, k);
+        // Without filters ln S is the finish kernel's, so that its bits do not hang
+        // on which of the two decided the row.
+        const bool cut = rs.cut_k || rs.cut_p || rs.cut_m;
+        const float lnS = cut ? fixed_log(S, k) : logf(Sf);
         if (!kSample) {
             if (threadIdx.x == 0) {
                 const float U = (float)(long long)ux * 5.6843419e-14f;  // 2^-44
