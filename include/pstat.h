@@ -497,8 +497,8 @@ PSTAT_API int pstat_grad_norm(const pstat_tensor* tensors, int64_t n_tensors, fl
 
 /* The norm before clipping goes to out_norm.  max_norm >= 0.  When the norm is
  * infinite or NaN the tensors are passed on unscaled (and the bit is set), so
- * that the caller can drop the step.  An `out` may not overlap another
- * tensor of the list. */
+ * that the caller can drop the step.  An `out` that overlaps another `out`, or
+ * a `data` that is not its own, is PSTAT_ERR_PARAM. */
 PSTAT_API int pstat_clip_grad_norm(const pstat_tensor* tensors, int64_t n_tensors, float max_norm,
                                    float* out_norm, void* workspace, size_t ws_bytes,
                                    int* dev_error, pstat_stream_t stream);

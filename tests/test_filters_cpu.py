@@ -189,6 +189,15 @@ def test_grad_argument_checks(lib):
     assert norm(words((0x1002, 0x1002, 10, 0))) == -5 and norm(words((0x1001, 0x1001, 10, 1))) == -5
     assert clip(words(good), -1.0) == -9 and clip(words(good), math.nan) == -9
     assert clip(words((0x1000, 0, 10, 0))) == -1 and clip(words((0x1000, 0x1002, 10, 0))) == -5
+    # outputs that overlap: the same tensor twice, a view into another, an input
+    # of another entry, a shifted copy of its own input
+    assert clip(words(good, good)) == -9
+    assert clip(words((0x1000, 0x1000, 10, 0), (0x1014, 0x1014, 10, 0))) == -9
+    assert clip(words((0x1000, 0x2000, 10, 0), (0x3000, 0x1000, 10, 0))) == -9
+    assert clip(words((0x1000, 0x1004, 10, 0))) == -9
+    # these pass the checks and end at the missing device: inputs may overlap
+    ok = clip(words((0x1000, 0x2000, 10, 0), (0x1000, 0x3000, 10, 0), (0x4000, 0x4000, 0, 0)))
+    assert ok in (-7, -8)
     n = ctypes.c_size_t(0)
     assert lib.pstat_grad_workspace_size(None, 0, ctypes.byref(n)) == 0
     assert lib.pstat_grad_workspace_size(None, 0, None) == -1

@@ -67,6 +67,9 @@ def test_unaligned_and_repeated(cuda_lib):
     # the same tensor twice counts twice in the norm
     twice = cuda_lib.grad_norm([base32, base32])
     assert abs(twice.item() - math.sqrt(2) * _norm([base32])) <= 8 * 2.0**-24 * twice.item()
+    for bad in ([base32, base32], [base32[:100], base32[50:]]):
+        with pytest.raises(cuda_lib.PstatError):
+            cuda_lib.clip_grad_norm(bad, 1.0)
     guard = torch.full((4096,), 5.0, device="cuda")
     cuda_lib.clip_grad_norm([guard[7:4000]], 1.0)
     assert bool((guard[:7] == 5).all()) and bool((guard[4000:] == 5).all())

@@ -65,11 +65,12 @@ __global__ void __launch_bounds__(kFgThreads)
     }
     const float ngK = -g * K;
     const float fill = mode == 1 ? NAN : 0.f;
-    // Column y is kept, so its gradient is g (1 - p_y).
+    // Column y is kept, so its gradient is g (1 - p_y), as -g expm1(ln p_y): near
+    // p_y = 1 the difference itself would be lost.
     auto gradient = [&](float z, int64_t col) {
-        const float e = ex2_approx((z - M) * c);
+        if (col == y) return -g * expm1f((z - M) / temp - rs.y);
         const bool kept = z > tau || (z == tau && col <= last);
-        return col == y ? fmaf(-g, e * K, g) : kept ? e * ngK : 0.f;
+        return kept ? ex2_approx((z - M) * c) * ngK : 0.f;
     };
     auto scalar = [&](int64_t c0, int64_t c1) {
         for (int64_t col = c0 + threadIdx.x; col < c1; col += kFgThreads)

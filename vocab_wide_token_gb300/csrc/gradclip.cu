@@ -2,8 +2,11 @@
 // scaling by min(1, max_norm / norm).
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <memory>
+#include <new>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -249,6 +252,35 @@ int check_tensors(const pstat_tensor* tensors, int64_t n, bool outputs) {
     return PSTAT_OK;
 }
 
+// Whether an output overlaps another output, or another tensor that is read: the
+// blocks that write it would race with those that use it.  (An output that is
+// its own input is in place.)
+struct Interval {
+    uintptr_t from, to;
+    bool out;
+};
+int check_overlap(const pstat_tensor* tensors, int64_t n) {
+    std::unique_ptr<Interval[]> v(new (std::nothrow) Interval[2 * n]);
+    if (!v) return PSTAT_ERR_WORKSPACE;
+    int64_t m = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        const pstat_tensor& t = tensors[i];
+        if (t.n == 0) continue;
+        const uintptr_t bytes = (uintptr_t)t.n * (t.dtype == PSTAT_BF16 ? 2 : 4);
+        const uintptr_t in = reinterpret_cast<uintptr_t>(t.data), out = reinterpret_cast<uintptr_t>(t.out);
+        v[m++] = {out, out + bytes, true};
+        if (in != out) v[m++] = {in, in + bytes, false};
+    }
+    std::sort(v.get(), v.get() + m, [](const Interval& a, const Interval& b) { return a.from < b.from; });
+    uintptr_t end_any = 0, end_out = 0;
+    for (int64_t i = 0; i < m; ++i) {
+        if (v[i].from < (v[i].out ? end_any : end_out)) return PSTAT_ERR_PARAM;
+        end_any = std::max(end_any, v[i].to);
+        if (v[i].out) end_out = std::max(end_out, v[i].to);
+    }
+    return PSTAT_OK;
+}
+
 // Fills the next batch from tensors[i..]; returns how many of them it covers.
 template <int N>
 int64_t fill(GradBatch<N>& g, const pstat_tensor* tensors, int64_t i, int64_t n) {
@@ -318,6 +350,10 @@ int norm_entry(const pstat_tensor* tensors, int64_t n, bool clip, float max_norm
     int rc = check_tensors(tensors, n, clip);
     if (rc != PSTAT_OK) return rc;
     if (clip && !(max_norm >= 0.f)) return PSTAT_ERR_PARAM;
+    if (clip && n > 0) {
+        rc = check_overlap(tensors, n);
+        if (rc != PSTAT_OK) return rc;
+    }
     if (!out_norm) return PSTAT_ERR_NULLPTR;
     size_t need = 0;
     rc = pstat_grad_workspace_size(tensors, n, &need);

@@ -701,7 +701,8 @@ def filter_workspace_size(T: int, V: int, dtype: torch.dtype) -> int:
 @functools.lru_cache(maxsize=256)
 def _plain_filters(temperature, top_k, top_p, min_p):
     """A pstat_filters of numbers alone, by reference (the library only reads it)."""
-    return ctypes.byref(Filters(float(temperature), float(top_p), float(min_p), int(top_k)))
+    return ctypes.byref(Filters(float(temperature), float(top_p), float(min_p),
+                                min(int(top_k), 1 << 62)))
 
 
 def _filters(temperature, top_k, top_p, min_p, T, dev):
@@ -721,7 +722,7 @@ def _filters(temperature, top_k, top_p, min_p, T, dev):
         if isinstance(x, row):
             setattr(f, many, _tensor(x, dtype, (T,), dev, name).data_ptr())
         else:
-            setattr(f, one, int(x) if one == "top_k" else float(x))
+            setattr(f, one, min(int(x), 1 << 62) if one == "top_k" else float(x))
     return ctypes.byref(f)
 
 
@@ -863,15 +864,12 @@ def _grad_list(tensors, out, writes):
         outs = [out] if isinstance(out, torch.Tensor) else list(out)
         if (len(outs) != n or set(map(T.get_device, outs)) != {index}
                 or not all(map(T.is_contiguous, outs)) or list(map(_dtype_of, outs)) != dtypes
-                or [o.shape for o in outs] != [x.shape for x in tensors]):
+                or not all(map(operator.eq, map(T.size, outs), map(T.size, tensors)))):
             raise ValueError("out must have one contiguous tensor for each of tensors, of its "
                              f"shape and dtype, on {dev}")
         at = list(map(T.data_ptr, outs))
     if writes:
         words[1::4] = at
-        written = [p for p, k in zip(at, sizes) if k]
-        if len(set(written)) != len(written):
-            raise ValueError("a tensor may be written once only")
     words = array.array("q", words)
     return outs, words, dev
 
@@ -901,7 +899,8 @@ def clip_grad_norm(tensors, max_norm: float, *, out=None, workspace=None, dev_er
     """Scales a list of gradients by min(1, max_norm / their global L2 norm),
     in place or into the tensors of `out` (same shapes and dtypes).  Returns
     (the norm before scaling, a float32 scalar tensor; the list of the scaled
-    tensors).  A norm that is not finite sets DEV_NONFINITE and scales nothing."""
+    tensors).  A norm that is not finite sets DEV_NONFINITE and scales nothing.
+    Tensors that are written may not overlap (a tensor listed twice, say)."""
     outs, words, dev = _grad_list(tensors, out, True)
     norm = torch.empty((), dtype=torch.float32, device=dev)
     dev_error = _error_flag(dev_error, dev)
