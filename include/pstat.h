@@ -85,7 +85,7 @@ enum {
     PSTAT_ERR_WORKSPACE = -6,   /* workspace NULL or smaller than required */
     PSTAT_ERR_CUDA = -7,        /* a CUDA runtime call or launch failed */
     PSTAT_ERR_UNSUPPORTED = -8, /* the current device is not sm_103 (GB300) */
-    PSTAT_ERR_PARAM = -9        /* a numeric parameter lies outside its range */
+    PSTAT_ERR_PARAM = -9        /* a numeric parameter is out of range, or outputs overlap */
 };
 
 /* Bits OR-ed into *dev_error by the kernels. */
@@ -458,7 +458,8 @@ PSTAT_API int pstat_filtered_forward(const void* logits, pstat_dtype dt, int64_t
  *   rowstats, cut_logit, cut_index  from pstat_filtered_forward on the same
  *                  logits and settings.
  *   temperature    for every row, or `temperatures` [T] where not NULL.
- *   weights, out_dlogits, out_dt, ld_out as pstat_backward.
+ *   weights, out_dlogits, out_dt, ld_out as pstat_backward; out_dlogits may not
+ *   overlap the logits (PSTAT_ERR_PARAM).
  */
 PSTAT_API int pstat_filtered_backward(const void* logits, pstat_dtype dt, int64_t T, int64_t V,
                                       int64_t ld, const int64_t* labels, int64_t ignore_index,

@@ -185,6 +185,12 @@ extern "C" int pstat_filtered_backward(const void* logits, pstat_dtype dt, int64
         !aligned(weights, 4) || !aligned(rowstats, 8) || !aligned(cut_logit, 4) ||
         !aligned(cut_index, 8) || !aligned(temperatures, 4))
         return PSTAT_ERR_ALIGN;
+    // Every block of a row reads the label's logit, so the gradient cannot go
+    // where the logits are.
+    const uintptr_t in = reinterpret_cast<uintptr_t>(logits), out = reinterpret_cast<uintptr_t>(out_dlogits);
+    const uintptr_t in_bytes = (uintptr_t)((T - 1) * ld + V) * (dt == PSTAT_BF16 ? 2 : 4);
+    const uintptr_t out_bytes = (uintptr_t)((T - 1) * ld_out + V) * (out_dt == PSTAT_BF16 ? 2 : 4);
+    if (in < out + out_bytes && out < in + in_bytes) return PSTAT_ERR_PARAM;
     DeviceInfo dev;
     const int rc = device_info(&dev);
     if (rc != PSTAT_OK) return rc;

@@ -155,7 +155,7 @@ const char* pstat_status_string(int code) {
         case PSTAT_ERR_WORKSPACE: return "workspace missing or too small";
         case PSTAT_ERR_CUDA: return "CUDA runtime error";
         case PSTAT_ERR_UNSUPPORTED: return "device is not sm_103 (GB300)";
-        case PSTAT_ERR_PARAM: return "a parameter is outside its range";
+        case PSTAT_ERR_PARAM: return "a parameter is out of range, or outputs overlap";
         default: return "unknown status";
     }
 }

@@ -736,7 +736,9 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, top_k=0
     takes the first maximum; top_k <= 0, top_p = 1 and min_p = 0 filter
     nothing.  The token is the first in index order whose kept mass exceeds
     `uniform` times the whole kept mass.  Returns (token [T] int64, logprob
-    [T] f32); `out` may supply the two.
+    [T] f32); `out` may supply the two, `workspace` a uint8 CUDA tensor of at
+    least ``filter_workspace_size`` bytes, which calls that overlap on the GPU
+    may not share.
     """
     T, V, ld = _rows(logits)
     dev = logits.device
@@ -799,7 +801,8 @@ def filtered_backward(logits: torch.Tensor, labels: torch.Tensor | None,
                       dev_error=None):
     """dlogits = (w / temperature) (onehot(y) - p) with p the softmax over the
     kept columns and 0 elsewhere, from the statistics of ``filtered_forward``
-    with the same settings; a zero row where the label is not kept."""
+    with the same settings; a zero row where the label is not kept.  `out` may
+    not overlap the logits."""
     T, V, ld = _rows(logits)
     dev = logits.device
     dt = _dtype_code(logits)
