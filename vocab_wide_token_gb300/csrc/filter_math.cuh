@@ -226,6 +226,27 @@ __device__ __forceinline__ float warp_max_nan(float m) {
     return r;
 }
 
+// Slot -> registers: lane L takes the 16 neighbouring vectors from 16 L, in an
+// order turned by L so that the lanes of a quarter warp meet no bank twice;
+// vectors past the chunk's end read as -inf.
+template <typename E>
+__device__ __forceinline__ void load_lane_run(const void* buf, int len, int lane,
+                                              uint4 (&q)[kVecPerLane]) {
+    const uint4* v = reinterpret_cast<const uint4*>(buf) + kVecPerLane * lane;
+    constexpr int kVec = Elem<E>::kVec;
+    const int nvec = (len + kVec - 1) / kVec - kVecPerLane * lane;
+    if (len == Elem<E>::kChunk) {
+#pragma unroll
+        for (int j = 0; j < kVecPerLane; ++j) q[j] = v[(j + lane) & (kVecPerLane - 1)];
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVecPerLane; ++j) {
+            const int at = (j + lane) & (kVecPerLane - 1);
+            q[j] = at < nvec ? v[at] : Elem<E>::neg_inf_vec();
+        }
+    }
+}
+
 // Maximum of one lane's vectors: the maximum of its group of columns.
 __device__ __forceinline__ float lane_max(const uint4 (&q)[kVecPerLane], uint16_t*) {
     uint32_t a0 = q[0].x, a1 = q[0].y, a2 = q[0].z, a3 = q[0].w;
