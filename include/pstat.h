@@ -484,7 +484,7 @@ typedef struct {
     const void* data;
     void* out; /* clipping: where the scaled tensor goes, same type; may equal data */
     int64_t n;
-    pstat_dtype dtype;
+    int32_t dtype; /* PSTAT_F32 or PSTAT_BF16 */
 } pstat_tensor;
 
 PSTAT_API int pstat_grad_workspace_size(const pstat_tensor* tensors, int64_t n_tensors,
