@@ -2,7 +2,9 @@
 
 Every ``csrc/*.cu`` file is compiled in parallel to an object under
 ``_build/`` and linked into ``vocab_wide_token_gb300/libpstat.so``.  Only one
-architecture is emitted: ``-gencode arch=compute_103a,code=sm_103a``.
+architecture is emitted: ``-gencode arch=compute_103a,code=sm_103a``.  Next to
+it, ``csrc/binding.cpp`` becomes ``_binding.so``, a CPython module that marshals
+the arguments of the hot calls (host code, over torch's headers).
 """
 from __future__ import annotations
 
@@ -53,12 +55,39 @@ def _compile(src: str, verbose: bool, out_dir: str = BUILD, extra=()) -> str:
     return obj
 
 
+BINDING = os.path.join(PKG, "_binding.so")
+
+
+def _build_binding() -> None:
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden",
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, f"-I{INCLUDE}",
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-L{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False) -> str:
     """Compile and link; returns the path of libpstat.so."""
     os.makedirs(BUILD, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(sources))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(12, len(sources) + 1)) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose), sources))
+        binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cuda_lib = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "lib64")
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs,

@@ -108,6 +108,26 @@ def declare_prototypes(lib: ctypes.CDLL) -> ctypes.CDLL:
 
 declare_prototypes(_lib)
 
+# The well-formed call of the functions below that have one goes through a
+# native module (csrc/binding.cpp): it checks, allocates and calls the library,
+# or answers None, and then the code here serves or refuses the call.
+try:
+    from . import _binding as _native
+
+    _native.bind(*(ctypes.cast(f, _vp).value for f in (
+        _lib.pstat_filter_workspace_size, _lib.pstat_sample, _lib.pstat_filtered_forward,
+        _lib.pstat_filtered_backward, _lib.pstat_grad_workspace_size, _lib.pstat_grad_norm,
+        _lib.pstat_clip_grad_norm)))
+except ImportError:  # not built: every call takes the path below
+    _native = None
+
+
+def _served(got, where: str) -> bool:
+    """Whether the native module served a call; a failed launch raises."""
+    if got.__class__ is int:
+        _check(got, where)
+    return got is not None
+
 F32, BF16 = 0, 1
 OK = 0
 ERR = {-1: "NULLPTR", -2: "SHAPE", -3: "SHARDS", -4: "DTYPE", -5: "ALIGN", -6: "WORKSPACE",
@@ -740,6 +760,10 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, top_k=0
     least ``filter_workspace_size`` bytes, which calls that overlap on the GPU
     may not share.
     """
+    if _native is not None and out is None and workspace is None:
+        got = _native.sample(logits, uniform, temperature, top_k, top_p, min_p, dev_error)
+        if _served(got, "pstat_sample"):
+            return got
     T, V, ld = _rows(logits)
     dev = logits.device
     dt = _dtype_code(logits)
@@ -779,6 +803,11 @@ def filtered_forward(logits: torch.Tensor, labels: torch.Tensor | None, temperat
     cut_index [T] int64): column v is kept when its logit is above cut_logit,
     or equal to it with v <= cut_index.
     """
+    if _native is not None and out is None and workspace is None:
+        got = _native.filtered_forward(logits, labels, temperature, top_k, top_p, min_p,
+                                       ignore_index, dev_error)
+        if _served(got, "pstat_filtered_forward"):
+            return got
     T, V, ld = _rows(logits)
     dev = logits.device
     dt = _dtype_code(logits)
@@ -803,6 +832,11 @@ def filtered_backward(logits: torch.Tensor, labels: torch.Tensor | None,
     kept columns and 0 elsewhere, from the statistics of ``filtered_forward``
     with the same settings; a zero row where the label is not kept.  `out` may
     not overlap the logits."""
+    if _native is not None and out is None and out_dtype is None:
+        got = _native.filtered_backward(logits, labels, weights, rowstats, cut_logit, cut_index,
+                                        temperature, ignore_index, dev_error)
+        if _served(got, "pstat_filtered_backward"):
+            return got
     T, V, ld = _rows(logits)
     dev = logits.device
     dt = _dtype_code(logits)
@@ -888,6 +922,10 @@ def _grad_call(words, workspace, dev):
 def grad_norm(tensors, *, out=None, workspace=None, dev_error=None) -> torch.Tensor:
     """The L2 norm over all elements of a list of gradients (bf16 or fp32, any
     mix of sizes), as a float32 scalar tensor on their device."""
+    if _native is not None and out is None and workspace is None:
+        got = _native.grad_norm(tensors, dev_error)
+        if _served(got, "pstat_grad_norm"):
+            return got
     _, words, dev = _grad_list(tensors, None, False)
     norm = (torch.empty((), dtype=torch.float32, device=dev) if out is None
             else _tensor(out, torch.float32, (), dev, "out"))
@@ -904,6 +942,10 @@ def clip_grad_norm(tensors, max_norm: float, *, out=None, workspace=None, dev_er
     (the norm before scaling, a float32 scalar tensor; the list of the scaled
     tensors).  A norm that is not finite sets DEV_NONFINITE and scales nothing.
     Tensors that are written may not overlap (a tensor listed twice, say)."""
+    if _native is not None and workspace is None:
+        got = _native.clip_grad_norm(tensors, max_norm, out, dev_error)
+        if _served(got, "pstat_clip_grad_norm"):
+            return got, list(tensors if out is None else out)
     outs, words, dev = _grad_list(tensors, out, True)
     norm = torch.empty((), dtype=torch.float32, device=dev)
     dev_error = _error_flag(dev_error, dev)
