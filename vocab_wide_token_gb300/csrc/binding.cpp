@@ -247,7 +247,8 @@ PyObject* filtered_backward(PyObject* const* a, Py_ssize_t n) {
 }
 
 // The tensors of a list or tuple, and where each is written (itself, or `outs`).
-bool take_list(PyObject* list, PyObject* outs, std::vector<pstat_tensor>& v, const at::Tensor** first) {
+bool take_list(PyObject* list, PyObject* outs, bool writes, std::vector<pstat_tensor>& v,
+               const at::Tensor** first) {
     if (!PyList_Check(list) && !PyTuple_Check(list)) return false;
     const Py_ssize_t n = PySequence_Fast_GET_SIZE(list);
     const bool apart = outs != Py_None;
@@ -266,7 +267,7 @@ bool take_list(PyObject* list, PyObject* outs, std::vector<pstat_tensor>& v, con
         if (o != x && (!o->is_cuda() || o->get_device() != x->get_device() || o->scalar_type() != type ||
                        !o->is_contiguous() || o->sizes() != x->sizes()))
             return false;
-        v[(size_t)i] = {x->const_data_ptr(), o->mutable_data_ptr(), x->numel(),
+        v[(size_t)i] = {x->const_data_ptr(), writes ? o->mutable_data_ptr() : nullptr, x->numel(),
                         type == at::kBFloat16 ? PSTAT_BF16 : PSTAT_F32};
     }
     return (*first)->get_device() == c10::cuda::current_device();
@@ -277,7 +278,7 @@ PyObject* norm_of(PyObject* list, PyObject* outs, PyObject* flag, bool clip, flo
     std::vector<pstat_tensor> v;
     const at::Tensor* first = nullptr;
     int* err;
-    if (!take_list(list, outs, v, &first)) Py_RETURN_NONE;
+    if (!take_list(list, outs, clip, v, &first)) Py_RETURN_NONE;
     const at::Tensor like = *first;  // the list may change while the lock is released
     const int device = like.get_device();
     if (!take_flag(flag, device, &err)) Py_RETURN_NONE;

@@ -1,5 +1,6 @@
 // gradclip.cu -- the global L2 norm of a list of gradient tensors and their
 // scaling by min(1, max_norm / norm).
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -11,6 +12,8 @@
 #include "internal.h"
 #include "ptx.cuh"
 
+namespace cg = cooperative_groups;
+
 namespace pstat {
 namespace {
 
@@ -18,6 +21,12 @@ constexpr int kGnThreads = 256;
 constexpr int kGnUnroll = 8;                // 16-byte vectors in flight per thread
 constexpr int64_t kUnitBytes = (int64_t)kGnThreads * kGnUnroll * 16;  // 32 KiB of one tensor
 constexpr int kMaxBlocks = 2048;            // partial sums
+constexpr int kNormCtas = 6;                // CTAs per SM, all resident
+// The scaling holds 8 vectors per thread as well as their addresses: with 6 CTAs it
+// spills (45 us for 110 MB where 4 take 37), and a grid of 6 for 4 resident ones runs
+// one and a half waves (42 us).
+constexpr int kScaleCtas = 4;
+constexpr int kTeam = 16;                   // CTAs of a cluster (beyond the portable 8)
 constexpr int kBatch = 800;                 // tensors of one launch (they travel as its arguments)
 
 struct GradTensor {
@@ -62,12 +71,12 @@ __device__ __noinline__ double wide_squares(const uint4* v, int k, int nv) {
 // Sum of the squares of one thread's vectors of a unit.  In fp32, with one fp64
 // addition for all of them: fp64 runs at about two operations per clock and SM.
 template <bool kBf16>
-__device__ __forceinline__ double unit_squares(const uint4* __restrict__ v, int nv) {
+__device__ __forceinline__ double unit_squares(const uint4* v, int nv) {
     uint4 q[kGnUnroll];
 #pragma unroll
     for (int j = 0; j < kGnUnroll; ++j) {
         const int k = j * kGnThreads + (int)threadIdx.x;
-        q[j] = k < nv ? __ldg(v + k) : make_uint4(0, 0, 0, 0);
+        q[j] = k < nv ? __ldcg(v + k) : make_uint4(0, 0, 0, 0);
     }
     uint64_t s0 = 0, s1 = 0;
     uint32_t any = 0;
@@ -98,141 +107,200 @@ __device__ __forceinline__ double unit_squares(const uint4* __restrict__ v, int 
     return wide_squares<kBf16>(v, (int)threadIdx.x, nv);
 }
 
-// Fixed-order sum of one double per thread; the result is valid in thread 0.
+// Fixed-order sum of one double per thread; the lanes of the first warp get it.
+// Through shared memory: a warp's fp64 addition takes the SM's pipe 16 cycles, and
+// this way a CTA makes 13 of them (with shuffles in every warp, 104: clipping 110 MB
+// took 58 us with those and a square root in every thread, and takes 51).
 __device__ __forceinline__ double block_sum(double v) {
-    __shared__ double warp[kGnThreads / 32];
-#pragma unroll
-    for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
-    if ((threadIdx.x & 31) == 0) warp[threadIdx.x >> 5] = v;
+    __shared__ double all[kGnThreads];
+    all[threadIdx.x] = v;
     __syncthreads();
     double s = 0.0;
-    for (int w = 0; w < kGnThreads / 32; ++w) s += warp[w];
-    __syncthreads();
+    if (threadIdx.x < 32) {
+        for (int w = 0; w < kGnThreads; w += 32) s += all[w + (int)threadIdx.x];
+#pragma unroll
+        for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+    }
     return s;
 }
 
+// Index of the tensor that holds unit u.  Bisected: the records are read one
+// behind another from the launch's arguments, 300 of them in 5 us.
 template <int N>
-__global__ void __launch_bounds__(kGnThreads, 6)
+__device__ __forceinline__ int tensor_of(const GradBatch<N>& g, uint32_t u) {
+    int lo = 0, hi = g.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (g.t[mid].first_unit <= u)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// This thread's share of the squares of unit u, a unit of tensor t.
+__device__ __forceinline__ double square_unit(const GradTensor& t, uint32_t u) {
+    const bool bf16 = t.bf16;
+    const int64_t per = kUnitBytes / (bf16 ? 2 : 4);
+    const int64_t e0 = (int64_t)(u - t.first_unit) * per;
+    const int64_t e1 = min(t.n, e0 + per);
+    const int vec = bf16 ? 8 : 4;
+    int64_t done = e0;
+    double sum = 0.0;
+    if ((reinterpret_cast<uintptr_t>(t.in) & 15u) == 0) {
+        const int nv = (int)((e1 - e0) / vec);
+        const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(t.in) + e0 * (bf16 ? 2 : 4));
+        sum = bf16 ? unit_squares<true>(v, nv) : unit_squares<false>(v, nv);
+        done = e0 + (int64_t)nv * vec;
+    }
+    for (int64_t k = done + threadIdx.x; k < e1; k += kGnThreads) {
+        const double x = elem(t.in, k, bf16);
+        sum = fma(x, x, sum);
+    }
+    return sum;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kGnThreads, kNormCtas)
     square_sums_kernel(const __grid_constant__ GradBatch<N> g, double* __restrict__ partial) {
     grid_launch_dependents();
     const uint32_t u0 = (uint32_t)((uint64_t)g.units * blockIdx.x / gridDim.x);
     const uint32_t u1 = (uint32_t)((uint64_t)g.units * (blockIdx.x + 1) / gridDim.x);
     double sum = 0.0;
-    int i = 0;
+    int i = tensor_of(g, u0);
     for (uint32_t u = u0; u < u1; ++u) {
         while (i + 1 < g.count && g.t[i + 1].first_unit <= u) ++i;
-        const GradTensor& t = g.t[i];
-        const bool bf16 = t.bf16;
-        const int64_t per = kUnitBytes / (bf16 ? 2 : 4);
-        const int64_t e0 = (int64_t)(u - t.first_unit) * per;
-        const int64_t e1 = min(t.n, e0 + per);
-        const int vec = bf16 ? 8 : 4;
-        int64_t done = e0;
-        if ((reinterpret_cast<uintptr_t>(t.in) & 15u) == 0) {
-            const int nv = (int)((e1 - e0) / vec);
-            const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(t.in) + e0 * (bf16 ? 2 : 4));
-            sum += bf16 ? unit_squares<true>(v, nv) : unit_squares<false>(v, nv);
-            done = e0 + (int64_t)nv * vec;
-        }
-        for (int64_t k = done + threadIdx.x; k < e1; k += kGnThreads) {
-            const double x = elem(t.in, k, bf16);
-            sum = fma(x, x, sum);
-        }
+        sum += square_unit(g.t[i], u);
     }
     sum = block_sum(sum);
     if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
 // Every block that needs the norm adds the partial sums up itself, in the same
-// order, so all of them hold the same bits.
-__device__ __forceinline__ double norm_of(const double* partial, int n) {
+// order, so all of them hold the same bits (in the first warp).
+__device__ __forceinline__ double total_of(const double* partial, int n) {
     double s = 0.0;
     for (int i = threadIdx.x; i < n; i += kGnThreads) s += partial[i];
-    return sqrt(block_sum(s));
+    return block_sum(s);
+}
+
+// Norm and error bits, by one thread; returns what the gradients are scaled by.
+__device__ __forceinline__ float finish_norm(double total, float max_norm, bool write, float* out,
+                                             int* dev_error) {
+    const double norm = sqrt(total);
+    const float f = (float)norm;
+    const bool finite = f < INFINITY;
+    if (write) {
+        *out = f;
+        if (!finite && dev_error) atomicOr(dev_error, PSTAT_DEV_NONFINITE);
+    }
+    return finite && norm > (double)max_norm ? (float)((double)max_norm / norm) : 1.f;
 }
 
 __global__ void __launch_bounds__(kGnThreads)
     norm_kernel(const double* __restrict__ partial, int n, float* __restrict__ out,
                 int* __restrict__ dev_error) {
     grid_wait();
-    const float norm = (float)norm_of(partial, n);
-    if (threadIdx.x == 0) {
-        *out = norm;
-        if (!(norm < INFINITY) && dev_error) atomicOr(dev_error, PSTAT_DEV_NONFINITE);
+    const double total = total_of(partial, n);
+    if (threadIdx.x == 0) finish_norm(total, 0.f, true, out, dev_error);
+}
+
+__device__ __forceinline__ void scale_unit(const GradTensor& t, uint32_t u, float factor) {
+    if (factor == 1.f && t.out == t.in) return;
+    const bool bf16 = t.bf16;
+    const int64_t per = kUnitBytes / (bf16 ? 2 : 4);
+    const int64_t e0 = (int64_t)(u - t.first_unit) * per;
+    const int64_t e1 = min(t.n, e0 + per);
+    const int vec = bf16 ? 8 : 4;
+    int64_t done = e0;
+    if (((reinterpret_cast<uintptr_t>(t.in) | reinterpret_cast<uintptr_t>(t.out)) & 15u) == 0) {
+        const int nv = (int)((e1 - e0) / vec);
+        const int64_t off = e0 * (bf16 ? 2 : 4);
+        const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(t.in) + off);
+        uint4* o = reinterpret_cast<uint4*>(static_cast<char*>(t.out) + off);
+        uint4 q[kGnUnroll];
+#pragma unroll
+        for (int j = 0; j < kGnUnroll; ++j) {
+            const int k = j * kGnThreads + (int)threadIdx.x;
+            if (k < nv) q[j] = __ldcs(v + k);
+        }
+#pragma unroll
+        for (int j = 0; j < kGnUnroll; ++j) {
+            const int k = j * kGnThreads + (int)threadIdx.x;
+            if (k >= nv) continue;
+            uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (factor == 1.f) continue;  // passed on bit for bit, NaNs included
+                w[e] = bf16 ? bf2_pack_rn(bf2_lo(w[e]) * factor, bf2_hi(w[e]) * factor)
+                            : __float_as_uint(__uint_as_float(w[e]) * factor);
+            }
+            __stcs(o + k, make_uint4(w[0], w[1], w[2], w[3]));
+        }
+        done = e0 + (int64_t)nv * vec;
+    }
+    for (int64_t k = done + threadIdx.x; k < e1; k += kGnThreads) {
+        if (bf16) {
+            const uint16_t x = static_cast<const uint16_t*>(t.in)[k];
+            static_cast<uint16_t*>(t.out)[k] =
+                factor == 1.f ? x : (uint16_t)(bf2_pack_rn(bf2_lo(x) * factor, 0.f) & 0xFFFFu);
+        } else {
+            const uint32_t x = static_cast<const uint32_t*>(t.in)[k];
+            static_cast<uint32_t*>(t.out)[k] =
+                factor == 1.f ? x : __float_as_uint(__uint_as_float(x) * factor);
+        }
     }
 }
 
 template <int N>
-__global__ void __launch_bounds__(kGnThreads)
+__global__ void __launch_bounds__(kGnThreads, kScaleCtas)
     scale_kernel(const __grid_constant__ GradBatch<N> g, const double* __restrict__ partial, int n,
                  float max_norm, float* __restrict__ out, int* __restrict__ dev_error) {
     __shared__ float s_factor;
-    grid_wait();
-    const double norm = norm_of(partial, n);
-    if (threadIdx.x == 0) {
-        const float f = (float)norm;
-        const bool finite = f < INFINITY;
-        s_factor = finite && norm > (double)max_norm ? (float)((double)max_norm / norm) : 1.f;
-        if (blockIdx.x == 0) {
-            *out = f;
-            if (!finite && dev_error) atomicOr(dev_error, PSTAT_DEV_NONFINITE);
-        }
-    }
-    __syncthreads();
-    const float factor = s_factor;
     const uint32_t u0 = (uint32_t)((uint64_t)g.units * blockIdx.x / gridDim.x);
     const uint32_t u1 = (uint32_t)((uint64_t)g.units * (blockIdx.x + 1) / gridDim.x);
+    int i = tensor_of(g, u1 - 1);
+    grid_wait();
+    const double total = total_of(partial, n);
+    if (threadIdx.x == 0) s_factor = finish_norm(total, max_norm, blockIdx.x == 0, out, dev_error);
+    __syncthreads();
+    const float factor = s_factor;
     // Backwards: what the norm read last is still in L2.
-    int i = g.count - 1;
     for (uint32_t u = u1; u-- > u0;) {
         while (i > 0 && g.t[i].first_unit > u) --i;
-        const GradTensor& t = g.t[i];
-        if (factor == 1.f && t.out == t.in) continue;
-        const bool bf16 = t.bf16;
-        const int64_t per = kUnitBytes / (bf16 ? 2 : 4);
-        const int64_t e0 = (int64_t)(u - t.first_unit) * per;
-        const int64_t e1 = min(t.n, e0 + per);
-        const int vec = bf16 ? 8 : 4;
-        int64_t done = e0;
-        if (((reinterpret_cast<uintptr_t>(t.in) | reinterpret_cast<uintptr_t>(t.out)) & 15u) == 0) {
-            const int nv = (int)((e1 - e0) / vec);
-            const int64_t off = e0 * (bf16 ? 2 : 4);
-            const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(t.in) + off);
-            uint4* o = reinterpret_cast<uint4*>(static_cast<char*>(t.out) + off);
-            uint4 q[kGnUnroll];
-#pragma unroll
-            for (int j = 0; j < kGnUnroll; ++j) {
-                const int k = j * kGnThreads + (int)threadIdx.x;
-                if (k < nv) q[j] = __ldcs(v + k);
-            }
-#pragma unroll
-            for (int j = 0; j < kGnUnroll; ++j) {
-                const int k = j * kGnThreads + (int)threadIdx.x;
-                if (k >= nv) continue;
-                uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (factor == 1.f) continue;  // passed on bit for bit, NaNs included
-                    w[e] = bf16 ? bf2_pack_rn(bf2_lo(w[e]) * factor, bf2_hi(w[e]) * factor)
-                                : __float_as_uint(__uint_as_float(w[e]) * factor);
-                }
-                __stcs(o + k, make_uint4(w[0], w[1], w[2], w[3]));
-            }
-            done = e0 + (int64_t)nv * vec;
-        }
-        for (int64_t k = done + threadIdx.x; k < e1; k += kGnThreads) {
-            if (bf16) {
-                const uint16_t x = static_cast<const uint16_t*>(t.in)[k];
-                static_cast<uint16_t*>(t.out)[k] =
-                    factor == 1.f ? x
-                                  : (uint16_t)(bf2_pack_rn(bf2_lo(x) * factor, 0.f) & 0xFFFFu);
-            } else {
-                const uint32_t x = static_cast<const uint32_t*>(t.in)[k];
-                static_cast<uint32_t*>(t.out)[k] =
-                    factor == 1.f ? x : __float_as_uint(__uint_as_float(x) * factor);
-            }
-        }
+        scale_unit(g.t[i], u, factor);
     }
+}
+
+// At most kTeam units: the norm and the scaling in one launch, by a cluster of
+// one CTA per unit, whose CTAs hand each other their sums through shared memory.
+// 16 units: norm 4.8 us against 5.5 by two launches, clipping 5.6 against 7.7 (and a
+// launch less on the host, 2 us).  With two units per CTA the two launches win (32
+// units: 8.0 against 5.5).
+template <int N>
+__global__ void __launch_bounds__(kGnThreads)
+    few_units_kernel(const __grid_constant__ GradBatch<N> g, bool clip, float max_norm,
+                     float* __restrict__ out, int* __restrict__ dev_error) {
+    __shared__ double parts[kTeam];
+    __shared__ float s_factor;
+    const cg::cluster_group team = cg::this_cluster();
+    const uint32_t rank = team.block_rank(), size = team.num_blocks();
+    team.barrier_arrive();  // before a CTA's memory is written it has to have started
+    grid_wait();
+    const GradTensor& t = g.t[tensor_of(g, rank)];
+    const double sum = block_sum(square_unit(t, rank));
+    team.barrier_wait();
+    if (threadIdx.x < size) *team.map_shared_rank(&parts[rank], threadIdx.x) = sum;
+    team.sync();
+    if (threadIdx.x == 0) {
+        double s = 0.0;
+        for (uint32_t r = 0; r < size; ++r) s += parts[r];
+        s_factor = finish_norm(s, max_norm, rank == 0, out, dev_error);
+    }
+    if (!clip) return;
+    __syncthreads();
+    scale_unit(t, rank, s_factor);
 }
 
 int check_tensors(const pstat_tensor* tensors, int64_t n, bool outputs) {
@@ -300,8 +368,8 @@ int64_t fill(GradBatch<N>& g, const pstat_tensor* tensors, int64_t i, int64_t n)
     return j - i;
 }
 
-int blocks_for(uint32_t units, const DeviceInfo& dev) {
-    const uint32_t most = (uint32_t)(dev.sm_count * 6 < kMaxBlocks ? dev.sm_count * 6 : kMaxBlocks);
+int blocks_for(uint32_t units, int per_sm, const DeviceInfo& dev) {
+    const uint32_t most = (uint32_t)(dev.sm_count * per_sm < kMaxBlocks ? dev.sm_count * per_sm : kMaxBlocks);
     return (int)(units < most ? units : most);
 }
 
@@ -316,7 +384,15 @@ int run_norm(const pstat_tensor* tensors, int64_t n, bool clip, float max_norm, 
     for (int64_t i = 0; i < n;) {
         i += fill(g, tensors, i, n);
         if (g.units == 0) continue;
-        const int blocks = blocks_for(g.units, dev);
+        if (n_partial == 0 && i == n && g.units <= (uint32_t)kTeam) {
+            static ContextSeen cluster_set;
+            if (ensure_large_cluster((const void*)few_units_kernel<N>, cluster_set) != cudaSuccess ||
+                launch_behind(few_units_kernel<N>, g.units, kGnThreads, 0, st, g.units, g, clip,
+                              max_norm, out_norm, dev_error) != cudaSuccess)
+                return PSTAT_ERR_CUDA;
+            return PSTAT_OK;
+        }
+        const int blocks = blocks_for(g.units, kNormCtas, dev);
         if (n_partial + blocks > max_partials) return PSTAT_ERR_WORKSPACE;
         square_sums_kernel<N><<<blocks, kGnThreads, 0, st>>>(g, partial + n_partial);
         n_partial += blocks;
@@ -329,7 +405,7 @@ int run_norm(const pstat_tensor* tensors, int64_t n, bool clip, float max_norm, 
         for (int64_t i = 0; i < n;) {
             i += fill(g, tensors, i, n);
             if (g.units == 0) continue;
-            if (launch_behind(scale_kernel<N>, (unsigned)blocks_for(g.units, dev), kGnThreads, 0, st,
+            if (launch_behind(scale_kernel<N>, (unsigned)blocks_for(g.units, kScaleCtas, dev), kGnThreads, 0, st,
                               1, g, (const double*)partial, n_partial, max_norm, out_norm,
                               dev_error) != cudaSuccess)
                 return PSTAT_ERR_CUDA;
