@@ -170,8 +170,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 // <= b are sure or likely to hold all kept ones: of the group maxima (top-k: k
 // maxima, so at least k columns; top-p: their maxima alone hold the mass), of
 // the columns themselves in a row short enough to be read twice at little
-// cost, or simply the bin of min-p's threshold.  Only the groups whose maximum
-// lies in those bins are read again.  What is found has exact weights; a
+// cost, or simply the bin of min-p's threshold.  Of a longer row only the groups
+// whose maximum lies in those bins are read again.  What is found has exact weights; a
 // nucleus is measured against the fp32 sum with its error bound (against an
 // exact one after top-k), and the row is left to the exact kernel where the
 // bound does not decide or the columns do not suffice.
@@ -184,7 +184,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 constexpr int kFinBins = 1024;     // 64 binary orders of e, in steps of 1/16
 constexpr int kFinCand = 1024;
 constexpr int kFinGroups = 2048;
-constexpr int kFinAll = 1024;      // columns of a row that are all taken as candidates
 constexpr int kFinShort = 16384;   // columns of a row whose histogram is of its columns
 constexpr int kMaxChunks = (int)(kFilterMaxV / PSTAT_CHUNK_F32);
 
@@ -228,21 +227,36 @@ __device__ __forceinline__ void leave_row(const FilterArgs& a, int64_t t) {
     if (threadIdx.x == 0) a.left[atomicAdd(a.left_count, 1)] = (int)t;
 }
 
+// Calls f(group, maximum) for a row's groups, eight loads ahead.
+template <typename E, int kFinThreads, typename F>
+__device__ __forceinline__ void for_each_group(const E* __restrict__ gm, int groups, F f) {
+    constexpr int kAhead = 8;
+    for (int i0 = threadIdx.x; i0 < groups; i0 += kAhead * kFinThreads) {
+        E g[kAhead];
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h)
+            g[h] = i0 + h * kFinThreads < groups ? gm[i0 + h * kFinThreads] : Elem<E>::neg_inf();
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h)
+            if (i0 + h * kFinThreads < groups) f(i0 + h * kFinThreads, Elem<E>::to_float(g[h]));
+    }
+}
+
+// The first group with the row's maximum, and its first column there.
 template <typename E, int kFinThreads, typename Shared>
-__device__ void finish_greedy(const FilterArgs& a, int64_t t, const E* row, const float4* rec,
-                              float M, Shared& sm) {
-    constexpr int kChunk = Elem<E>::kChunk;
+__device__ void finish_greedy(const FilterArgs& a, int64_t t, const E* row, const E* gm, float M,
+                              Shared& sm) {
+    constexpr int kGroup = kVecPerLane * Elem<E>::kVec;
+    static_assert(kGroup <= kFinThreads, "a thread per column of a group");
     if (threadIdx.x == 0) sm.bin = sm.found = 0xFFFFFFFFu;
     __syncthreads();
-    for (int i = threadIdx.x; i < a.chunks; i += kFinThreads)
-        if (rec[i].x == M) atomicMin(&sm.bin, (uint32_t)i);
+    for_each_group<E, kFinThreads>(gm, a.chunks * 32, [&](int i, float g) {
+        if (g == M) atomicMin(&sm.bin, (uint32_t)i);
+    });
     __syncthreads();
-    const int c0 = (int)sm.bin * kChunk, c1 = min((int)a.V, c0 + kChunk);
-    for (int col = c0 + threadIdx.x; col < c1; col += kFinThreads)
-        if (Elem<E>::to_float(row[col]) == M) {
-            atomicMin(&sm.found, (uint32_t)col);
-            break;
-        }
+    const uint32_t col = sm.bin * kGroup + threadIdx.x;
+    if (threadIdx.x < kGroup && col < (uint32_t)a.V && Elem<E>::to_float(row[col]) == M)
+        atomicMin(&sm.found, col);
     __syncthreads();
     if (threadIdx.x == 0) {
         a.token[t] = (int64_t)sm.found;
@@ -319,21 +333,6 @@ __device__ void finish_draw(const FilterArgs& a, int64_t t, const E* row, const 
     }
     __syncthreads();
     if (!sm.found) leave_row(a, t);
-}
-
-// Calls f(group, maximum) for a row's groups, eight loads ahead.
-template <typename E, int kFinThreads, typename F>
-__device__ __forceinline__ void for_each_group(const E* __restrict__ gm, int groups, F f) {
-    constexpr int kAhead = 8;
-    for (int i0 = threadIdx.x; i0 < groups; i0 += kAhead * kFinThreads) {
-        E g[kAhead];
-#pragma unroll
-        for (int h = 0; h < kAhead; ++h)
-            g[h] = i0 + h * kFinThreads < groups ? gm[i0 + h * kFinThreads] : Elem<E>::neg_inf();
-#pragma unroll
-        for (int h = 0; h < kAhead; ++h)
-            if (i0 + h * kFinThreads < groups) f(i0 + h * kFinThreads, Elem<E>::to_float(g[h]));
-    }
 }
 
 // ln(min_p) t + M with the bounds of its fp32 error: the product of a logarithm
@@ -605,7 +604,8 @@ __global__ void __launch_bounds__(kFinThreads, (kFiltered ? 1024 : 1536) / kFinT
         if (threadIdx.x == 0) write_undefined<kSample>(a, t, PSTAT_DEV_EMPTY_ROW);
         return;
     }
-    if (rs.greedy) return finish_greedy<E, kFinThreads>(a, t, row, rec, M, sm);
+    const E* gm = static_cast<const E*>(a.group_max) + t * a.chunks * 32;
+    if (rs.greedy) return finish_greedy<E, kFinThreads>(a, t, row, gm, M, sm);
     if (!kFiltered || (!rs.cut_k && !rs.cut_p && !rs.cut_m)) {
         const float lnS = logf(Sf);
         if (kSample) {
@@ -621,18 +621,18 @@ __global__ void __launch_bounds__(kFinThreads, (kFiltered ? 1024 : 1536) / kFinT
 
     r.k = rs.cut_k ? (int)rs.top_k : 0;
     r.mp = min_p_bounds(M, rs);
-    r.all = V <= kFinAll;
+    const bool short_row = V <= kFinShort;
+    r.all = V <= kFinThreads;
     const float bin_scale = r.c.ch * ((float)kFinBins / 64.f);
     const float ch = r.c.ch;
     auto bin_of = [&](float z) { return min(kFinBins - 1, __float2int_rd((M - z) * bin_scale)); };
-    const E* gm = static_cast<const E*>(a.group_max) + t * a.chunks * 32;
     const int groups = a.chunks * 32;
     const int bin_m = rs.cut_m ? bin_of(r.mp.lo) : kFinBins;
     // Columns up to this bin are gathered; the last bin is open.
-    int b = kFinBins;
+    int b = kFinBins, n_finite = V;
     __syncthreads();
     if (!r.all && (rs.cut_k || rs.cut_p)) {
-        const bool by_mass = rs.cut_p && !rs.cut_k, short_row = V <= kFinShort;
+        const bool by_mass = rs.cut_p && !rs.cut_k;
         constexpr float kUnit = 131072.f;  // 2^17: of all groups together below 2^32
         auto add = [&](float z) {
             if (z == -INFINITY) return;
@@ -678,20 +678,26 @@ __global__ void __launch_bounds__(kFinThreads, (kFiltered ? 1024 : 1536) / kFinT
             cb = c1;
             mb = m1;
         }
+        if (threadIdx.x == kFinThreads - 1) sm.found = cb;
         __syncthreads();
         b = (int)sm.bin;
+        n_finite = short_row ? (int)sm.found : V;
     }
     // top-p after top-k needs the whole top-k mass, so min-p may not shorten it
     if (!r.all) {
         if (!(rs.cut_k && rs.cut_p)) b = min(b, bin_m);
-        if (b >= kFinBins - 1) return leave_row(a, t);
+        if (b >= kFinBins - 1) {
+            if (n_finite > kFinCand) return leave_row(a, t);
+            r.all = true;
+        }
     }
     r.all_min = rs.cut_m && b >= bin_m;
 
     // ---- gather.  bin_of(z) <= b  <=>  (M - z) bin_scale < b + 1
     const float edge = r.all ? INFINITY : (float)(b + 1);
-    int n_vec;  // vectors of kVec columns to look through
-    if (r.all) {
+    const bool direct = r.all || short_row;  // every column, from L1 by now
+    int n_vec;                               // vectors of kVec columns to look through
+    if (direct) {
         n_vec = (V + kVec - 1) / kVec;
     } else {
         for_each_group<E, kFinThreads>(gm, groups, [&](int i, float g) {
@@ -714,7 +720,7 @@ __global__ void __launch_bounds__(kFinThreads, (kFiltered ? 1024 : 1536) / kFinT
 #pragma unroll
         for (int h = 0; h < kAhead; ++h) {
             const int i = i0 + h * kFinThreads;
-            if (r.all) {
+            if (direct) {
                 col[h] = i * kVec;
             } else {
                 const int g = sm.group[min(i, n_vec - 1) / kVecPerLane], j = i % kVecPerLane;
