@@ -499,3 +499,40 @@ def test_rollout_scoring_and_update_together(cuda_lib):
     assert abs(norm.item() - before) <= 2.0**-23 * before
     after = cuda_lib.grad_norm([clipped]).item()
     assert abs(after - 0.5 * before) <= 2.0**-8 * before
+
+
+@pytest.mark.parametrize("dtype,out_dtype", [(BF16, BF16), (F32, F32), (F32, BF16)])
+@pytest.mark.parametrize("V", [1, 7, 15, 16, 17, 40, 2047, 2049, 4095, 4097, 12301])
+def test_any_alignment(cuda_lib, dtype, out_dtype, V):
+    """Rows at every offset from a 16-byte boundary, even and odd strides, inside
+    memory full of NaN: the bits of an aligned copy's results, and nothing
+    written beside the gradient."""
+    T = 3
+    g = torch.Generator(device="cuda").manual_seed(V)
+    y = torch.randint(V, (T,), generator=g, device="cuda")
+    u = torch.rand(T, generator=g, device="cuda")
+    w = torch.randn(T, generator=g, device="cuda")
+    z0 = (3 * torch.randn(T, V, generator=g, device="cuda")).to(dtype)
+    even = (V + 15) // 8 * 8
+    base = torch.empty(T, even, device="cuda", dtype=dtype)[:, :V].copy_(z0)
+
+    def results(z, out):
+        got = []
+        for s in ((1.0, 0, 1.0, 0.0), (0.7, 9, 0.9, 0.0)):
+            got += cuda_lib.sample(z, u, *s)
+            st = cuda_lib.filtered_forward(z, y, *s)
+            grad = cuda_lib.filtered_backward(z, y, w, *st[2:], s[0], out=out)
+            got += [*st, grad.clone()]
+        return got
+
+    want = results(base, torch.empty(T, even, device="cuda", dtype=out_dtype)[:, :V])
+    for off in range(8):
+        for pad, out_off, out_pad in ((0, 0, 0), (1, off, 1), (8, 8 - off, 3), (5, 1, 8)):
+            mem = torch.full((off + T * (V + pad) + 16,), math.nan, device="cuda", dtype=dtype)
+            z = mem.as_strided((T, V), (V + pad, 1), off).copy_(z0)
+            store = torch.full((out_off + T * (V + out_pad) + 16,), 7.0, device="cuda", dtype=out_dtype)
+            out = store.as_strided((T, V), (V + out_pad, 1), out_off)
+            for i, (a, b) in enumerate(zip(results(z, out), want, strict=True)):
+                assert torch.equal(a, b), (off, pad, out_off, out_pad, i)
+            out.fill_(7.0)
+            assert bool((store == 7.0).all()), (off, pad, out_off, out_pad)

@@ -247,6 +247,36 @@ __device__ __forceinline__ void load_lane_run(const void* buf, int len, int lane
     }
 }
 
+// The 16 bytes from byte `shift` (below 16, a multiple of 2) of two vectors.
+__device__ __forceinline__ uint4 shift_vectors(const uint4& lo, const uint4& hi, uint32_t shift) {
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (shift & 8)
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    if (shift & 4)
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    if (shift & 2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// load_lane_run of a chunk that starts `shift` bytes into the slot; the same
+// vectors in the same places, so the same bits come out of them.
+template <typename E>
+__device__ __forceinline__ void load_lane_run_shifted(const void* buf, uint32_t shift, int len,
+                                                      int lane, uint4 (&q)[kVecPerLane]) {
+    const uint4* v = reinterpret_cast<const uint4*>(buf) + kVecPerLane * lane;
+    constexpr int kVec = Elem<E>::kVec;
+    const int nvec = (len + kVec - 1) / kVec - kVecPerLane * lane;
+#pragma unroll
+    for (int j = 0; j < kVecPerLane; ++j) {
+        const int at = (j + lane) & (kVecPerLane - 1);
+        q[j] = at < nvec ? shift_vectors(v[at], v[at + 1], shift) : Elem<E>::neg_inf_vec();
+    }
+}
+
 // Maximum of one lane's vectors: the maximum of its group of columns.
 __device__ __forceinline__ float lane_max(const uint4 (&q)[kVecPerLane], uint16_t*) {
     uint32_t a0 = q[0].x, a1 = q[0].y, a2 = q[0].z, a3 = q[0].w;

@@ -30,16 +30,22 @@ namespace {
 // group that is read again is one run of memory (with the vectors L, L + 32, ...
 // of the chunk statistics it is 16 half-used sectors, and drawing 1024 rows
 // with top-k 50 spent 42 us on them).
+// A chunk need not start or end on 16 bytes (odd vocabularies and strides): its
+// aligned middle is copied to the place in the slot that has the same offset from
+// a boundary, up to seven columns at either end are loaded by the lanes when the
+// copy is issued, and the slot is read through a shift.
 // ---------------------------------------------------------------------------
+constexpr int kRecordSlot = kSlotBytes + 32;  // the offset, and the rest of the last vector
+
 template <typename E, bool kU>
 __global__ void __launch_bounds__(kWarps * 32, 1)
     filter_records_kernel(const __grid_constant__ FilterArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int lane = threadIdx.x & 31;
-    uint8_t* slots = smem + (size_t)warp * kStages * kSlotBytes;
+    uint8_t* slots = smem + (size_t)warp * kStages * kRecordSlot;
     uint64_t* bars =
-        reinterpret_cast<uint64_t*>(smem + (size_t)warps * kStages * kSlotBytes) + warp * kStages;
+        reinterpret_cast<uint64_t*>(smem + (size_t)warps * kStages * kRecordSlot) + warp * kStages;
     constexpr int kChunk = Elem<E>::kChunk;
     const E* logits = static_cast<const E*>(a.logits);
     E* group_max = static_cast<E*>(a.group_max);
@@ -51,7 +57,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const int64_t gw = (int64_t)blockIdx.x * warps + warp;
     const int64_t nw = (int64_t)gridDim.x * warps;
     const int64_t i0 = n_items * gw / nw, i1 = n_items * (gw + 1) / nw;
-    const int64_t n = i1 - i0;
+    const int n = (int)(i1 - i0);
     if (n <= 0) return;
     if (lane == 0) {
         for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 1);
@@ -70,20 +76,48 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             ++it.t;
         }
     };
-    auto locate = [&](const Item& it, const E*& src, int& len) -> bool {
-        const int start = it.g * kChunk;
-        len = min(kChunk, V - start);
-        src = logits + it.t * a.ld + start;
-        return ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) &&
-               ((((size_t)len * sizeof(E)) & 15u) == 0);
-    };
-    auto issue = [&](const Item& it, int slot) {
+    struct Span {
         const E* src;
         int len;
-        if (locate(it, src, len) && lane == 0) {
-            const uint32_t bytes = (uint32_t)len * (uint32_t)sizeof(E);
-            mbar_arrive_expect_tx(&bars[slot], bytes);
-            bulk_g2s_hint(slots + (size_t)slot * kSlotBytes, src, bytes, &bars[slot], policy);
+        uint32_t shift;  // of the start from a 16-byte boundary
+        int head;        // columns before the next one
+        uint32_t bytes;  // from there, to be copied
+        // Lanes 0 to 7 have the columns before the copied ones, 8 to 15 those
+        // behind them, 16 to 23 fill the last vector; -1: none.
+        __device__ int edge(int lane) const {
+            constexpr int kVec = Elem<E>::kVec;
+            if (lane < 8) return lane < head ? lane : -1;
+            const int col = lane < 16 ? head + (int)(bytes / sizeof(E)) + lane - 8 : len + lane - 16;
+            return col < (lane < 16 ? len : lane < 24 ? (len + kVec - 1) / kVec * kVec : 0) ? col : -1;
+        }
+        __device__ bool ragged() const { return shift || (len * sizeof(E)) % 16; }
+    };
+    auto locate = [&](const Item& it) {
+        Span p;
+        const int start = it.g * kChunk;
+        p.len = min(kChunk, V - start);
+        p.src = logits + it.t * a.ld + start;
+        p.shift = (uint32_t)(reinterpret_cast<uintptr_t>(p.src) & 15u);
+        p.head = p.shift ? min(p.len, (int)((16 - p.shift) / sizeof(E))) : 0;
+        p.bytes = (uint32_t)((p.len - p.head) * (int)sizeof(E)) & ~15u;
+        return p;
+    };
+    static_assert(kStages == 2, "one register of edge columns for each slot");
+    E edge0 = Elem<E>::neg_inf(), edge1 = edge0;
+    auto issue = [&](const Item& it, int slot) {
+        const Span p = locate(it);
+        if (p.bytes && lane == 0) {
+            mbar_arrive_expect_tx(&bars[slot], p.bytes);
+            bulk_g2s_hint(slots + (size_t)slot * kRecordSlot + p.shift + p.head * sizeof(E),
+                          p.src + p.head, p.bytes, &bars[slot], policy);
+        }
+        if (p.ragged()) {
+            const int col = p.edge(lane);
+            const E x = col >= 0 && col < p.len ? p.src[col] : Elem<E>::neg_inf();
+            if (slot == 0)
+                edge0 = x;
+            else
+                edge1 = x;
         }
     };
     auto scale_of = [&](int64_t t) {
@@ -93,21 +127,20 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
     Item cur = {i0 / chunks, (int)(i0 % chunks)};
     Item ahead = cur;
-    const int64_t prologue = n < kStages ? n : kStages;
-    for (int64_t j = 0; j < prologue; ++j) {
-        issue(ahead, (int)j);
+    const int prologue = n < kStages ? n : kStages;
+    for (int j = 0; j < prologue; ++j) {
+        issue(ahead, j);
         next_item(ahead);
     }
     uint32_t phase = 0;
-    int64_t j = 0;
+    int j = 0;
     bool timed_out = false;
     float c = scale_of(cur.t);
     for (; j < n; ++j) {
-        const int slot = (int)(j % kStages);
-        E* buf = reinterpret_cast<E*>(slots + (size_t)slot * kSlotBytes);
-        const E* src;
-        int len;
-        if (locate(cur, src, len)) {
+        const int slot = j % kStages;
+        uint8_t* buf = slots + (size_t)slot * kRecordSlot;
+        const Span p = locate(cur);
+        if (p.bytes) {
             bool ok = mbar_wait_bounded(&bars[slot], (phase >> slot) & 1u, kWaitLimitNs);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) {
@@ -115,14 +148,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 break;
             }
             phase ^= 1u << slot;
-        } else {
-            constexpr int kVec = Elem<E>::kVec;
-            const int padded = (len + kVec - 1) / kVec * kVec;
-            for (int k = lane; k < padded; k += 32) buf[k] = (k < len) ? src[k] : Elem<E>::neg_inf();
-            __syncwarp();
         }
         uint4 q[kVecPerLane];
-        load_lane_run<E>(buf, len, lane, q);
+        if (p.ragged()) {
+            const int col = p.edge(lane);
+            if (col >= 0)
+                *reinterpret_cast<E*>(buf + p.shift + col * sizeof(E)) = slot == 0 ? edge0 : edge1;
+            __syncwarp();
+        }
+        if (p.shift)
+            load_lane_run_shifted<E>(buf, p.shift, p.len, lane, q);
+        else
+            load_lane_run<E>(buf, p.len, lane, q);
         __syncwarp();
         fence_proxy_async_smem();  // our reads of the slot precede the next bulk write into it
         if (j + kStages < n) {
@@ -142,14 +179,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         if (lane == 0 && a.dev_error) atomicOr(a.dev_error, PSTAT_DEV_TIMEOUT);
         // The rows this warp leaves unfinished are undefined; copies still in
         // flight into this CTA's shared memory are drained before it ends.
-        for (int64_t k = j; k < n; ++k)
+        for (int k = j; k < n; ++k)
             if (lane == 0) a.records[i0 + k] = make_float4(NAN, 0.f, 0.f, 0.f);
-        const int64_t last = (j + kStages < n) ? j + kStages : n;
-        for (int64_t k = j; k < last; ++k) {
-            const int slot = (int)(k % kStages);
-            const E* src;
-            int len;
-            if (locate(cur, src, len)) {
+        const int last = (j + kStages < n) ? j + kStages : n;
+        for (int k = j; k < last; ++k) {
+            const int slot = k % kStages;
+            if (locate(cur).bytes) {
                 mbar_wait_bounded(&bars[slot], (phase >> slot) & 1u, kWaitLimitNs);
                 phase ^= 1u << slot;
             }
@@ -764,7 +799,7 @@ cudaError_t launch_records(const FilterArgs& a, const DeviceInfo& dev, cudaStrea
     static ContextSeen configured;
     const cudaError_t e =
         ensure_smem_optin(reinterpret_cast<const void*>(filter_records_kernel<E, kU>),
-                          (int)chunk_stats_smem_bytes(), configured);
+                          kWarps * kStages * (int)(kRecordSlot + sizeof(uint64_t)), configured);
     if (e != cudaSuccess) return e;
     // Few items are spread over as many SMs as there are, one warp each at first.
     const int64_t items = a.T * a.chunks;
@@ -773,7 +808,7 @@ cudaError_t launch_records(const FilterArgs& a, const DeviceInfo& dev, cudaStrea
     int64_t grid = (items + warps - 1) / warps;
     grid = grid < dev.sm_count ? grid : dev.sm_count;
     filter_records_kernel<E, kU><<<(unsigned)grid, (unsigned)warps * 32,
-                                   (size_t)warps * kStages * (kSlotBytes + sizeof(uint64_t)),
+                                   (size_t)warps * kStages * (kRecordSlot + sizeof(uint64_t)),
                                    stream>>>(a);
     return cudaGetLastError();
 }
