@@ -12,8 +12,10 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // Gradient: dz_v = (w/t)(1[v = y] - kept_v e_v/S), elementwise, one read and
-// one write of a row: bound by HBM.  Each thread keeps kU 8-column groups in
-// flight as raw 16-byte vectors.  A group without a logit of at least tau (all
+// one write of a row: bound by HBM.  Each thread keeps kAhead groups of columns in
+// flight as raw 16-byte vectors; a group is one 16-byte vector of the gradient
+// (of two, 32 bytes apart between lanes, 512 x 151,936 fp32 zeros took 73 us, and
+// take 47 us).  A group without a logit of at least tau (all
 // but a few, once a filter cuts) is written as zeros without an exponential.
 // A row is taken from the first column whose gradient is on 16 bytes.  Where its
 // logit is not (kShift: odd strides or vocabularies), the groups are shifted out
@@ -21,6 +23,21 @@ namespace {
 // 151,937 bf16 columns out of a stride of 151,944 took 89 us column by column.
 // ---------------------------------------------------------------------------
 constexpr int kFgThreads = 256;
+
+// Groups that a thread has in flight (2048 x 151,936 bf16 with a nucleus: 3 groups
+// 207 us, 4 201, 5 213, 6 248: registers), and how often: few blocks leave a tail,
+// many repeat the row's set-up (1024 rows of fp32: 1 192 us, 2 180, 4 184; 2048 of
+// bf16: 2 214, 4 201, 10 199, but 64 rows 10.2, 9.7 and 14.4).
+constexpr int kAhead = 4;
+template <typename Eout>
+constexpr int kBlockCols = kFgThreads * kAhead * (16 / (int)sizeof(Eout)) * (sizeof(Eout) == 2 ? 4 : 2);
+
+__device__ __forceinline__ void store_group(uint16_t* p, const float (&g)[8]) {
+    Store8<uint16_t>::run(p, g);
+}
+__device__ __forceinline__ void store_group(float* p, const float (&g)[4]) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(g[0], g[1], g[2], g[3]));
+}
 
 template <typename Ein, typename Eout, bool kShift>
 __global__ void __launch_bounds__(kFgThreads)
@@ -79,31 +96,31 @@ __global__ void __launch_bounds__(kFgThreads)
             zout[col] = out_cast(mode == 2 ? gradient(Elem<Ein>::to_float(zin[col]), col) : fill, zout);
     };
 
-    constexpr int kVecs = (int)sizeof(Ein) / 2;  // 16-byte vectors per group
+    constexpr int kCols = 16 / (int)sizeof(Eout);           // columns of a group
+    constexpr int kVecs = kCols * (int)sizeof(Ein) / 16;  // vectors of logits of a group
     const int out_off = (int)((reinterpret_cast<uintptr_t>(zout) & 15u) / sizeof(Eout));
-    int64_t head = out_off ? 16 / (int)sizeof(Eout) - out_off : 0;
+    int64_t head = out_off ? kCols - out_off : 0;
     uint32_t shift = 0;
     int64_t behind = 0;  // columns that the last group's vectors hold behind it
     if (kShift) {
         shift = (uint32_t)(reinterpret_cast<uintptr_t>(zin + head) & 15u);
-        if (head * sizeof(Ein) < shift) head += 8;
+        if (head * sizeof(Ein) < shift) head += kCols;
         if (shift) behind = (16 - shift) / sizeof(Ein);
     }
     if (head + behind > V) return scalar(V * seg / segs, V * (seg + 1) / segs);
-    const int64_t groups = (V - head - behind) >> 3;
+    const int64_t groups = (V - head - behind) / kCols;
     const int64_t g0 = groups * seg / segs, g1 = groups * (seg + 1) / segs;
     if (seg == 0) scalar(0, head);
-    if (seg == segs - 1) scalar(head + (groups << 3), V);
+    if (seg == segs - 1) scalar(head + groups * kCols, V);
     const uint4* vin =
         reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(zin + head) - shift);
     Eout* vout = zout + head;
 
-    constexpr int kU = kShift ? 4 : kVecs == 1 ? 6 : 4;
     constexpr int kLoads = kVecs + (kShift ? 1 : 0);
-    for (int64_t base = g0; base < g1; base += (int64_t)kFgThreads * kU) {
-        uint4 raw[kU][kLoads];
+    for (int64_t base = g0; base < g1; base += (int64_t)kFgThreads * kAhead) {
+        uint4 raw[kAhead][kLoads];
 #pragma unroll
-        for (int k = 0; k < kU; ++k) {
+        for (int k = 0; k < kAhead; ++k) {
             const int64_t i = base + k * kFgThreads + threadIdx.x;
             if (i < g1 && mode == 2) {
                 const uint4* src = vin + i * kVecs;
@@ -113,14 +130,14 @@ __global__ void __launch_bounds__(kFgThreads)
             }
         }
 #pragma unroll
-        for (int k = 0; k < kU; ++k) {
+        for (int k = 0; k < kAhead; ++k) {
             const int64_t i = base + k * kFgThreads + threadIdx.x;
             if (i >= g1) continue;
-            float o[8];
+            float o[kCols];
             bool any = false;
-            float x[8];
+            float x[kCols];
             if (mode == 2) {
-                constexpr int kPer = 8 / kVecs;
+                constexpr int kPer = kCols / kVecs;
 #pragma unroll
                 for (int h = 0; h < kVecs; ++h) {
                     float part[kPer];
@@ -132,22 +149,22 @@ __global__ void __launch_bounds__(kFgThreads)
                     for (int e = 0; e < kPer; ++e) x[h * kPer + e] = part[e];
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) any |= x[e] >= tau;
+                for (int e = 0; e < kCols; ++e) any |= x[e] >= tau;
             }
             if (any) {
-                const int64_t col = head + (i << 3);
+                const int64_t col = head + i * kCols;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = ex2_approx((x[e] - M) * c) * ngK;
+                for (int e = 0; e < kCols; ++e) o[e] = ex2_approx((x[e] - M) * c) * ngK;
                 // the few groups that the cut or the label falls into
-                if (tau > -INFINITY || (y >= col && y < col + 8)) {
+                if (tau > -INFINITY || (y >= col && y < col + kCols)) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = gradient(x[e], col + e);
+                    for (int e = 0; e < kCols; ++e) o[e] = gradient(x[e], col + e);
                 }
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = fill;
+                for (int e = 0; e < kCols; ++e) o[e] = fill;
             }
-            Store8<Eout>::run(vout + (i << 3), o);
+            store_group(vout + i * kCols, o);
         }
     }
 }
@@ -159,8 +176,6 @@ cudaError_t launch_filtered_backward(const void* logits, int64_t T, int64_t V, i
                                      const float* cut_logit, const int64_t* cut_index,
                                      float temperature, const float* temperatures, void* out,
                                      int64_t ld_out, int* dev_error, cudaStream_t stream) {
-    int64_t segs = V / 32768;
-    if (segs < 1) segs = 1;
     // Whether the first column whose gradient is on 16 bytes has its logit there as
     // well, in every row: a boundary of either comes round within 8 rows.
     bool shift = false;
@@ -170,6 +185,7 @@ cudaError_t launch_filtered_backward(const void* logits, int64_t T, int64_t V, i
         const uintptr_t head = ((16 - (zout & 15u)) & 15u) / sizeof(Eout);
         shift |= ((zin + head * sizeof(Ein)) & 15u) != 0;
     }
+    const int64_t segs = (V + kBlockCols<Eout> - 1) / kBlockCols<Eout>;
     const auto kernel = shift ? filtered_backward_kernel<Ein, Eout, true>
                               : filtered_backward_kernel<Ein, Eout, false>;
     kernel<<<(unsigned)(T * segs), kFgThreads, 0, stream>>>(
