@@ -9,7 +9,7 @@
 // the logits in 2048 bins of M - z, one weighs every column exactly, by spans
 // of the index order, and collects the columns of the bin that the cut is
 // expected in.  A cluster barrier takes 1 to 2 thousand cycles and a pass over
-// 151,936 columns by 16 CTAs some 15 thousand, so decisions that only the leader
+// 151,936 columns by ten CTAs some 15 thousand, so decisions that only the leader
 // needs stay with it.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -32,13 +32,17 @@ constexpr int kSpan = 256;     // columns of one span of the index order, a warp
 constexpr int kLane = kSpan / 32;
 constexpr int kMaxSpans = (int)(kFilterMaxV / kSpan);
 constexpr int kSpansPer = kMaxSpans / kExThreads;
-constexpr int kMaxTeam = 16;   // 16 CTAs are beyond the portable cluster size
+// One CTA per SM: with two the CTAs of a few rows crowd on half of the SMs, and
+// the registers do not suffice for the weights (8 flat rows of V = 151,936 with
+// top_p = 0.9: 61 us, with one 46).  Ten CTAs a team, as two such teams fill the 20
+// SMs of a processing cluster, where two of eight leave four idle (16 clusters of
+// ten or thirty of five are resident, 14 of eight).
+constexpr int kMaxTeam = 10;
 // With kAlone rows or more for every cluster the CTAs take rows alone: what a
 // team saves in a pass it loses again in synchronisation.  Flat rows of
-// V = 151,936 with top_p = 0.9 (us, teams / alone): 16 rows 103 / 248, 64 rows
-// 320 / 259, 192 rows 922 / 348; unfiltered draws: 39 rows 91 / 109, 87 rows
-// 199 / 180.
-constexpr int kAlone = 3;
+// V = 151,936 with top_p = 0.9, all by teams or all alone: 12 rows 46 / 150 us,
+// 32 rows 148 / 148.
+constexpr int kAlone = 2;
 static_assert(kBins % kExThreads == 0 && kMaxSpans % kExThreads == 0 && kSpan <= kExThreads, "");
 
 enum Op : uint32_t {
@@ -179,7 +183,7 @@ struct Team {
             if (threadIdx.x == 0) sm.n_cand = 0;
             __syncthreads();
         }
-        uint64_t outside = 0, inside = 0, ux = 0;
+        uint64_t total = 0, inside = 0, ux = 0;
         each_span([&](int s, int col, const float (&x)[kLane]) {
             bool any = all;
 #pragma unroll
@@ -187,20 +191,21 @@ struct Team {
             uint64_t before = 0;
             uint32_t hits = 0;
             if (__any_sync(0xFFFFFFFFu, any)) {
-                uint64_t w[kLane];
 #pragma unroll
-                for (int e = 0; e < kLane; e += 2)
-                    fixed_weights(x[e], x[e + 1], M, c, k, sm.table, w[e], w[e + 1]);
+                for (int e = 0; e < kLane; e += 2) {
+                    uint64_t w[2];
+                    fixed_weights(x[e], x[e + 1], M, c, k, sm.table, w[0], w[1]);
 #pragma unroll
-                for (int e = 0; e < kLane; ++e) {
-                    const uint32_t dk = desc_key(x[e]);
-                    before += dk < klo ? w[e] : 0;
-                    outside += dk > khi ? w[e] : 0;
-                    const bool in = dk >= klo && dk <= khi;
-                    inside += in ? w[e] : 0;
-                    hits |= (uint32_t)in << e;
-                    if (!kSample && dk < klo)
-                        ux += (uint64_t)entropy_term((unsigned long long)dk << 32, w[e], M, rs.temp, k);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t dk = desc_key(x[e + h]);
+                        total += w[h];
+                        before += dk < klo ? w[h] : 0;
+                        const bool in = dk >= klo && dk <= khi;
+                        inside += in ? w[h] : 0;
+                        hits |= (uint32_t)in << (e + h);
+                        if (!kSample && dk < klo)
+                            ux += (uint64_t)entropy_term((unsigned long long)dk << 32, w[h], M, rs.temp, k);
+                    }
                 }
                 before = warp_sum(before);
             }
@@ -216,7 +221,7 @@ struct Team {
                     }
             }
         });
-        put(inside, outside, ux);
+        put(inside, total, ux);
         if (rank) {  // the leader's own candidates are in place
             if (threadIdx.x == 0) sm.offset = atomicAdd(&lead.n_cand, sm.n_cand);
             __syncthreads();
@@ -267,17 +272,19 @@ struct Team {
     __device__ __forceinline__ void pass_spans(uint32_t cut_key, uint32_t cut_index) const {
         uint64_t ux = 0;
         each_span([&](int s, int col, const float (&x)[kLane]) {
-            uint64_t sum = 0, w[kLane];
+            uint64_t sum = 0;
 #pragma unroll
-            for (int e = 0; e < kLane; e += 2)
-                fixed_weights(x[e], x[e + 1], M, c, k, sm.table, w[e], w[e + 1]);
+            for (int e = 0; e < kLane; e += 2) {
+                uint64_t w[2];
+                fixed_weights(x[e], x[e + 1], M, c, k, sm.table, w[0], w[1]);
 #pragma unroll
-            for (int e = 0; e < kLane; ++e) {
-                const bool kept = is_kept(x[e], col + e, cut_key, cut_index);
-                sum += kept ? w[e] : 0;
-                if (!kSample && kept)
-                    ux += (uint64_t)entropy_term((unsigned long long)desc_key(x[e]) << 32, w[e], M,
-                                                 rs.temp, k);
+                for (int h = 0; h < 2; ++h) {
+                    const bool kept = is_kept(x[e + h], col + e + h, cut_key, cut_index);
+                    sum += kept ? w[h] : 0;
+                    if (!kSample && kept)
+                        ux += (uint64_t)entropy_term((unsigned long long)desc_key(x[e + h]) << 32, w[h],
+                                                     M, rs.temp, k);
+                }
             }
             sum = warp_sum(sum);
             if ((threadIdx.x & 31) == 0) lead.span[s] = sum;
@@ -481,9 +488,9 @@ struct Team {
         __syncthreads();
         const int lane = threadIdx.x & 31;
         before = warp_sum(lane < kExWarps ? sm.scratch[lane] : 0);
-        const uint64_t in = get(0), out = get(1);
+        const uint64_t in = get(0), total = get(1);
         __syncthreads();
-        return {before, in, before + in + out};
+        return {before, in, total};
     }
     // The element at which the count reaches `want`, or the mass `target`, in
     // the order of the finite logits, all of which level0 counts.  With `share`
@@ -716,7 +723,7 @@ struct Team {
 };
 
 template <typename E, bool kSample>
-__global__ void __launch_bounds__(kExThreads, 2)
+__global__ void __launch_bounds__(kExThreads, 1)
     filter_exact_kernel(const __grid_constant__ FilterArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     ExactShared& sm = *reinterpret_cast<ExactShared*>(smem_raw);
@@ -768,11 +775,12 @@ cudaError_t launch_exact(const FilterArgs& a, bool filtered, const DeviceInfo& d
     if (e == cudaSuccess) e = ensure_large_cluster(fn, cluster_set);
     if (e != cudaSuccess) return e;
     // A row without filters takes one pass, over which synchronisation weighs
-    // more; of many such rows more are worked on at once by smaller teams.
+    // more; of many such rows more are worked on at once by smaller teams (28 of
+    // 2048 rows: 25 us, by teams of ten 33).
     const int most = filtered || a.T <= 64 ? kMaxTeam : kMaxTeam / 2;
-    int team = 1;
-    while (team < most && a.V >= (int64_t)team * 8192) team *= 2;
-    int64_t teams = (int64_t)dev.sm_count * 2 / team;
+    const int64_t want = (a.V + 8191) / 8192;
+    const int team = (int)(want < most ? want : most);
+    int64_t teams = dev.sm_count / team;
     if (teams > a.T) teams = a.T;
     return launch_behind(filter_exact_kernel<E, kSample>, (unsigned)(teams * team), kExThreads,
                          sizeof(ExactShared), stream, (unsigned)team, a);
