@@ -113,17 +113,34 @@ struct Team {
     __device__ __forceinline__ void each_span(F f) const {
         constexpr int kVec = Elem<E>::kVec, kVecs = kLane / kVec;
         const int lane = threadIdx.x & 31, warps = size * kExWarps;
-        for (int s = rank * kExWarps + ((int)threadIdx.x >> 5); s * kSpan < V; s += warps) {
-            int col[kVecs];
-            float part[kVecs][kVec], x[kLane];
+        const bool even = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
+        auto fetch = [&](int s, uint4 (&raw)[kVecs]) {
 #pragma unroll
-            for (int h = 0; h < kVecs; ++h) col[h] = s * kSpan + lane * kLane + h * kVec;
-            load_columns<E, kVecs>(row, col, V, part);
+            for (int h = 0; h < kVecs; ++h) {
+                const int col = s * kSpan + lane * kLane + h * kVec;
+                if (even && col + kVec <= V) raw[h] = __ldg(reinterpret_cast<const uint4*>(row + col));
+            }
+        };
+        int s = rank * kExWarps + ((int)threadIdx.x >> 5);
+        uint4 next[kVecs];
+        fetch(s, next);
+        for (; s * kSpan < V; s += warps) {
+            const int col0 = s * kSpan + lane * kLane;
+            float x[kLane];
 #pragma unroll
-            for (int h = 0; h < kVecs; ++h)
+            for (int h = 0; h < kVecs; ++h) {
+                float part[kVec];
+                RowReader<E>::unpack(next[h], part);
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) x[h * kVec + e] = part[h][e];
-            f(s, col[0], x);
+                for (int e = 0; e < kVec; ++e) x[h * kVec + e] = part[e];
+            }
+            fetch(s + warps, next);
+            if (!even || col0 + kLane > V) {
+#pragma unroll
+                for (int e = 0; e < kLane; ++e)
+                    x[e] = col0 + e < V ? Elem<E>::to_float(row[col0 + e]) : -INFINITY;
+            }
+            f(s, col0, x);
         }
     }
 
