@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 // Up to one candidate per thread, every thread finds the rank and the mass
 // before its own by comparing with all others: for the usual 50 to 100 that
 // is a few hundred cycles, where a sort by a block needs 28 synchronised steps.
-// Among more the cut and the draw are selected by histograms (list_select).
+// More are sorted.
 // ---------------------------------------------------------------------------
 constexpr int kFinBins = 1024;     // 64 binary orders of e, in steps of 1/16
 constexpr int kFinCand = 1024;
@@ -243,7 +243,6 @@ struct FinishShared {
             uint32_t mass[kFinBins];
         } hist;
         Candidate pair[kFinThreads];
-        ListShared<kFinThreads> list;
         float prefix[kMaxChunks];
     };
     unsigned long long cand[kFinCand];
@@ -512,90 +511,130 @@ __device__ __forceinline__ void finish_few(const FilterArgs& a, const E* row, co
         write_token<E, kSample>(a, row, r, col, S);
 }
 
-// Decides a row from more candidates, by selections in their list.
+// Sorts n <= kFinCand keys; the places up to the next power of two, which it
+// returns, are filled with the largest.  Bitonic: pairs up to 32 apart stay with a
+// warp, so most steps need no barrier of the block.
+template <int kFinThreads>
+__device__ __noinline__ int block_sort(unsigned long long* key, int n) {
+    int size = 64;
+    while (size < n) size *= 2;
+    for (int i = n + (int)threadIdx.x; i < size; i += kFinThreads) key[i] = ~0ull;
+    __syncthreads();
+    for (int run = 2; run <= size; run *= 2)
+        for (int stride = run / 2; stride > 0; stride /= 2) {
+            if (stride >= 32 && run > 64) __syncthreads();  // after a pair further apart, or before
+            for (int p = threadIdx.x; p < size / 2; p += kFinThreads) {
+                const int i = 2 * p - (p & (stride - 1));
+                const unsigned long long x = key[i], y = key[i + stride];
+                if ((x > y) == ((i & run) == 0)) {
+                    key[i] = y;
+                    key[i + stride] = x;
+                }
+            }
+            __syncwarp();
+        }
+    __syncthreads();
+    return size;
+}
+
+// Decides a row from more candidates: sorted, their ranks are their places and
+// the mass before each is a prefix sum; the kept ones are sorted again by index
+// for the draw.
 template <typename E, bool kSample, int kFinThreads>
 __device__ __noinline__ void finish_many(const FilterArgs& a, const E* row, const FinishRow& r,
                                          FinishShared<kFinThreads>& sm) {
+    constexpr int kMost = kFinCand / kFinThreads;
     const int lane = threadIdx.x & 31, n = r.n;
-    uint64_t total = 0;
-    int n_hi = 0, n_lo = 0;  // columns that min-p keeps, by both bounds
-    for (int i = threadIdx.x; i < n; i += kFinThreads) {
-        const float z = key_logit((uint32_t)(sm.cand[i] >> 32));
-        const uint64_t w = fixed_weight(z, r.M, r.c, r.scale, sm.table);
+    // neighbours, so many to a thread
+    const int per = (block_sort<kFinThreads>(sm.cand, n) + kFinThreads - 1) / kFinThreads;
+    const int i0 = (int)threadIdx.x * per;
+    uint64_t sum = 0, before, unused;
+    for (int i = i0; i < i0 + per; ++i) {
+        const uint64_t w =
+            i < n ? fixed_weight(key_logit((uint32_t)(sm.cand[i] >> 32)), r.M, r.c, r.scale, sm.table)
+                  : 0;
         sm.weight[i] = w;
-        total += w;
-        n_hi += z >= r.mp.hi;
-        n_lo += z >= r.mp.lo;
+        sum += w;
     }
-    total = warp_sum(total);
-    n_hi = __reduce_add_sync(0xFFFFFFFFu, n_hi);
-    n_lo = __reduce_add_sync(0xFFFFFFFFu, n_lo);
-    if (lane == 0) {
-        add_wide(&sm.total, total);
-        atomicAdd(&sm.keep0, (uint32_t)n_hi);
-        atomicAdd(&sm.keep1, (uint32_t)n_lo);
+    block_scan<kFinThreads, uint64_t>(sm.scratch, sum, 0, before, unused);
+    const bool whole = r.k > 0 || r.all;  // the whole mass is among the candidates'
+    const int most_k = r.k > 0 && r.k < n ? r.k : n;
+    if (r.rs.cut_p && !whole && threadIdx.x == 0) nucleus_targets(r, sm);
+    uint64_t at = before;
+    for (int i = i0; i < i0 + per; ++i) {
+        at += sm.weight[i];
+        if (i == n - 1) sm.total = at;
+        if (r.rs.cut_p && whole && i == most_k - 1) sm.target0 = sm.target1 = share_of(r.rs.top_p, at);
     }
-    if (threadIdx.x == 0) nucleus_targets(r, sm);
     __syncthreads();
-    total = sm.total;
-    n_hi = (int)sm.keep0;
-    n_lo = (int)sm.keep1;
-    auto select = [&](bool by_count, uint32_t want, uint64_t target) {
-        return list_select<kFinThreads>(sm.list, sm.cand, sm.weight, n, 0, ~0ull, false, by_count,
-                                        want, target, 0, 0, kGrain<E>);
-    };
-    const bool whole = r.k > 0 || r.all;
-    int keep = n + 1;  // n + 1: all of these, and perhaps more
-    Selected end = {0, 0, 0};
-    if (r.k > 0 && r.k <= n) {
-        keep = r.k;
-        end = select(true, (uint32_t)r.k, 0);
+    // How many pass every filter, by the narrow and by the wide bounds.
+    int keep = 0, most = 0;
+    at = before;
+    for (int i = i0; i < i0 + per && i < most_k; ++i) {
+        const float z = key_logit((uint32_t)(sm.cand[i] >> 32));
+        keep += (!r.rs.cut_m || z >= r.mp.hi) && (!r.rs.cut_p || at < sm.target0);
+        most += (!r.rs.cut_m || z >= r.mp.lo) && (!r.rs.cut_p || at < sm.target1);
+        at += sm.weight[i];
     }
-    if (r.rs.cut_p) {
-        uint64_t t0 = sm.target0, t1 = sm.target1;
-        if (whole) {
-            t0 = t1 = share_of(r.rs.top_p, keep <= n ? end.mass : total);
+    keep = __reduce_add_sync(0xFFFFFFFFu, keep);
+    most = __reduce_add_sync(0xFFFFFFFFu, most);
+    if (lane == 0) {
+        atomicAdd(&sm.keep0, (uint32_t)keep);
+        atomicAdd(&sm.keep1, (uint32_t)most);
+    }
+    __syncthreads();
+    keep = (int)sm.keep0;
+    most = (int)sm.keep1;
+    // All candidates kept: then a filter must end here, or there are no others.
+    const bool ends = keep < n || r.all || (r.k > 0 && r.k <= n) || r.all_min ||
+                      (r.rs.cut_p && sm.total >= sm.target1);
+    if (keep == 0 || keep != most || !ends) return leave_row(a, r.t);
+    at = before;
+    uint64_t ux = 0;
+    unsigned long long by_index[kMost];
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+        const int i = i0 + j;
+        by_index[j] = ~0ull;
+        if (j >= per || i >= keep) continue;
+        const unsigned long long key = sm.cand[i];
+        const uint64_t w = sm.weight[i];
+        at += w;
+        if (!kSample) ux += (uint64_t)entropy_term(key, w, r.M, r.rs.temp, r.scale);
+        if (i == keep - 1) {
+            sm.sum = at;
+            sm.cut = key;
+            if (kSample) sm.draw = draw_of(r.rs.u, at);
         }
-        if (t0 == 0) return leave_row(a, r.t);
-        if (total >= t0) {
-            const Selected s = select(false, 0, t0);
-            if (s.mass < t1) {
-                // between the bounds, unless min-p ends before it
-                if (!(r.rs.cut_m && n_lo < (int)s.rank)) return leave_row(a, r.t);
-            } else if ((int)s.rank < keep) {
-                keep = (int)s.rank;
-                end = s;
-            }
-        }
+        by_index[j] = key << 32 | (uint32_t)i;
     }
-    if (r.rs.cut_m && n_hi < keep && n_hi != n_lo) return leave_row(a, r.t);
-    if (r.rs.cut_m && n_lo < keep && (n_lo < n || r.all_min || r.all)) {
-        keep = n_lo;
-        end = select(true, (uint32_t)keep, 0);
-    }
-    if (keep > n && r.all) {
-        keep = n;
-        end = select(true, (uint32_t)n, 0);
-    }
-    if (keep > n || keep == 0 || (int)end.rank != keep) return leave_row(a, r.t);
-    const uint64_t S = end.mass;
-    const unsigned long long cut = end.key;
     if (!kSample) {
-        long long ux = 0;
-        for (int i = threadIdx.x; i < n; i += kFinThreads)
-            if (sm.cand[i] <= cut)
-                ux += entropy_term(sm.cand[i], sm.weight[i], r.M, r.rs.temp, r.scale);
-        ux = (long long)warp_sum((uint64_t)ux);
-        if (lane == 0 && ux) add_wide(&sm.ux, (uint64_t)ux);
+        ux = warp_sum(ux);
+        if (lane == 0 && ux) add_wide(&sm.ux, ux);
         __syncthreads();
-        if (threadIdx.x == 0) write_kept(a, row, r, cut, S, (long long)sm.ux);
+        if (threadIdx.x == 0) write_kept(a, row, r, sm.cut, sm.sum, (long long)sm.ux);
         return;
     }
-    const bool lowest = r.rs.u == 0.f;
-    const Selected s = list_select<kFinThreads>(
-        sm.list, sm.cand, sm.weight, n, 0, cut, true, lowest, 1,
-        draw_of(r.rs.u, S) + 1, 0, 0, kGrain<E>);
-    if (threadIdx.x == 0) write_token<E, kSample>(a, row, r, (uint32_t)s.key, S);
+    // The draw: the kept columns in index order.  u = 0 takes the first of
+    // them, however small its weight.
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kMost; ++j)
+        if (j < per && i0 + j < keep) sm.cand[i0 + j] = by_index[j];
+    __syncthreads();
+    const int draws = (block_sort<kFinThreads>(sm.cand, keep) + kFinThreads - 1) / kFinThreads;
+    const int d0 = (int)threadIdx.x * draws;
+    sum = 0;
+    for (int i = d0; i < d0 + draws && i < keep; ++i) sum += sm.weight[(uint32_t)sm.cand[i]];
+    block_scan<kFinThreads, uint64_t>(sm.scratch, sum, 0, before, unused);
+    const uint64_t target = sm.draw, S = sm.sum;
+    at = before;
+    for (int i = d0; i < d0 + draws && i < keep; ++i) {
+        const uint64_t w = sm.weight[(uint32_t)sm.cand[i]];
+        if (r.rs.u == 0.f ? i == 0 : (at <= target && at + w > target))
+            write_token<E, kSample>(a, row, r, (uint32_t)(sm.cand[i] >> 32), S);
+        at += w;
+    }
 }
 
 // kFiltered: some row may have a filter; without, the kernel needs neither the
