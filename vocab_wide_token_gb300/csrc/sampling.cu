@@ -211,15 +211,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 // exact one after top-k), and the row is left to the exact kernel where the
 // bound does not decide or the columns do not suffice.
 //
-// Up to one candidate per thread, every thread finds the rank and the mass
-// before its own by comparing with all others: for the usual 50 to 100 that
-// is a few hundred cycles, where a sort by a block needs 28 synchronised steps.
-// More are sorted.
+// Of up to 256 candidates every thread finds the rank and the mass before its own
+// by comparing with all others: for the usual 50 to 100 that is a few hundred
+// cycles, where a sort by a block needs 28 steps.  More are sorted.
 // ---------------------------------------------------------------------------
 constexpr int kFinBins = 1024;     // 64 binary orders of e, in steps of 1/16
 constexpr int kFinCand = 1024;
 constexpr int kFinGroups = 2048;
 constexpr int kFinShort = 16384;   // columns of a row whose histogram is of its columns
+// Candidates that are compared all with all, one to a thread (1000 by 1024 threads
+// take 110 us).
+template <int kFinThreads>
+constexpr int kFinFew = kFinThreads < 256 ? kFinThreads : 256;
 constexpr int kMaxChunks = (int)(kFilterMaxV / PSTAT_CHUNK_F32);
 
 struct Candidate {
@@ -242,7 +245,7 @@ struct FinishShared {
             uint32_t count[kFinBins];
             uint32_t mass[kFinBins];
         } hist;
-        Candidate pair[kFinThreads];
+        Candidate pair[kFinFew<kFinThreads>];
         float prefix[kMaxChunks];
     };
     unsigned long long cand[kFinCand];
@@ -334,16 +337,21 @@ __device__ void finish_draw(const FilterArgs& a, int64_t t, const E* row, const 
     if (chunk < 0 || chunk >= n) return leave_row(a, t);
     // Each thread sums its run of columns; the one whose run the target falls
     // into walks through it again.
-    constexpr int kVec = Elem<E>::kVec, kPer = Elem<E>::kChunk / kFinThreads;
-    const int col0 = chunk * Elem<E>::kChunk + threadIdx.x * kPer;
+    constexpr int kVec = Elem<E>::kVec, kChunk = Elem<E>::kChunk;
+    constexpr int kPer = kChunk / kFinThreads < kVec ? kVec : kChunk / kFinThreads;
+    constexpr int kAhead = kPer / kVec < 2 ? kPer / kVec : 2;
+    static_assert(kPer % (kAhead * kVec) == 0, "whole vectors to a thread");
+    const int own = (int)threadIdx.x * kPer, col0 = own < kChunk ? chunk * kChunk + own : (int)a.V;
     auto walk = [&](auto each) {
 #pragma unroll 1
-        for (int i = 0; i < kPer; i += 2 * kVec) {
-            const int col[2] = {col0 + i, col0 + i + kVec};
-            float x[2][kVec];
-            load_columns<E, 2>(row, col, (int)a.V, x);
+        for (int i = 0; i < kPer; i += kAhead * kVec) {
+            int col[kAhead];
+            float x[kAhead][kVec];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < kAhead; ++h) col[h] = col0 + i + h * kVec;
+            load_columns<E, kAhead>(row, col, (int)a.V, x);
+#pragma unroll
+            for (int h = 0; h < kAhead; ++h)
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) each(col[h] + e, x[h][e], ex2_approx((x[h][e] - M) * c));
         }
@@ -425,14 +433,17 @@ __device__ __forceinline__ void nucleus_targets(const FinishRow& r, FinishShared
     sm.target1 = target + error;
 }
 
-// Decides a row from at most kFinThreads candidates.
+// Decides a row from at most kFinFew candidates.
 template <typename E, bool kSample, int kFinThreads>
 __device__ __forceinline__ void finish_few(const FilterArgs& a, const E* row, const FinishRow& r,
                                            FinishShared<kFinThreads>& sm) {
     const int lane = threadIdx.x & 31, n = r.n;
     // `parts` neighbouring lanes share a candidate, each comparing it with its
     // share of the others.
-    const int parts = n <= kFinThreads / 4 ? 4 : n <= kFinThreads / 2 ? 2 : 1;
+    const int parts = n <= kFinThreads / 8   ? 8
+                      : n <= kFinThreads / 4 ? 4
+                      : n <= kFinThreads / 2 ? 2
+                                             : 1;
     const int item = (int)threadIdx.x / parts, part = (int)threadIdx.x % parts;
     // (number, mass) of the candidates that `less` accepts
     auto count_before = [&](auto less, int& number, uint64_t& mass) {
@@ -696,7 +707,7 @@ __global__ void __launch_bounds__(kFinThreads, (kFiltered ? 1024 : 1536) / kFinT
     r.k = rs.cut_k ? (int)rs.top_k : 0;
     r.mp = min_p_bounds(M, rs);
     const bool short_row = V <= kFinShort;
-    r.all = V <= kFinThreads;
+    r.all = V <= kFinFew<kFinThreads>;
     const float bin_scale = r.c.ch * ((float)kFinBins / 64.f);
     const float ch = r.c.ch;
     auto bin_of = [&](float z) { return min(kFinBins - 1, __float2int_rd((M - z) * bin_scale)); };
@@ -825,7 +836,7 @@ __global__ void __launch_bounds__(kFinThreads, (kFiltered ? 1024 : 1536) / kFinT
     r.n = (int)sm.n_cand;
     if (r.n > kFinCand || (rs.cut_p && r.k > r.n && !r.all)) return leave_row(a, t);
     r.scale = fixed_scale(Sf * (1.f + 2.f * kSumError));
-    if (r.n <= kFinThreads)
+    if (r.n <= kFinFew<kFinThreads>)
         finish_few<E, kSample, kFinThreads>(a, row, r, sm);
     else
         finish_many<E, kSample, kFinThreads>(a, row, r, sm);
@@ -863,15 +874,19 @@ cudaError_t launch_filter(FilterArgs a, const DeviceInfo& dev, cudaStream_t stre
     cudaError_t e = kSample || every ? launch_records<E, false>(a, dev, stream)
                                      : launch_records<E, true>(a, dev, stream);
     if (e != cudaSuccess) return e;
-    // Rows beyond what is resident at once: half the threads to a row, as its time
-    // is mostly latency and registers decide how many rows an SM holds.
-    const bool small = a.T > 4 * dev.sm_count;
-    e = some ? small ? launch_behind(filter_finish_kernel<E, kSample, true, 128>, (unsigned)a.T, 128,
-                                     0, stream, 1, a)
-                     : launch_behind(filter_finish_kernel<E, kSample, true, 256>, (unsigned)a.T, 256,
-                                     0, stream, 1, a)
-             : launch_behind(filter_finish_kernel<E, kSample, false, 256>, (unsigned)a.T, 256, 0,
-                             stream, 1, a);
+    // A row's time is mostly latency, so rows that are all resident at once get as
+    // many threads as that leaves each; beyond, registers decide how many an SM holds.
+    // 64 rows of V = 151,936, half of them with top-k 200: 256 threads 33 us, 512 25,
+    // 1024 23, but then one row with top-k 50 takes 12 us in place of 11.
+    const unsigned T = (unsigned)a.T;
+    if (!some)
+        e = launch_behind(filter_finish_kernel<E, kSample, false, 256>, T, 256, 0, stream, 1, a);
+    else if (a.T <= 2 * dev.sm_count)
+        e = launch_behind(filter_finish_kernel<E, kSample, true, 512>, T, 512, 0, stream, 1, a);
+    else if (a.T <= 4 * dev.sm_count)
+        e = launch_behind(filter_finish_kernel<E, kSample, true, 256>, T, 256, 0, stream, 1, a);
+    else
+        e = launch_behind(filter_finish_kernel<E, kSample, true, 128>, T, 128, 0, stream, 1, a);
     // Without filters only a draw can be left over.
     if (e != cudaSuccess || (!some && !kSample)) return e;
     return launch_exact<E, kSample>(a, some, dev, stream);
