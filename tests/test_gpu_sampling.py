@@ -536,3 +536,30 @@ def test_any_alignment(cuda_lib, dtype, out_dtype, V):
                 assert torch.equal(a, b), (off, pad, out_off, out_pad, i)
             out.fill_(7.0)
             assert bool((store == 7.0).all()), (off, pad, out_off, out_pad)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [128, 129, 256, 257, 511, 1024, 1025, 4000, 16384, 16385, 40000])
+def test_candidate_counts(cuda_lib, dtype, V):
+    """From a handful of candidates to more than a block lists, few and many
+    finite logits: against the oracle, and with the bits of larger batches,
+    which other numbers of threads finish."""
+    z, g = _rows(5, V, dtype, V)
+    z[1] = _rows(1, V, dtype, V + 1, mask=0.97)[0]
+    z[2] = _rows(1, V, dtype, V + 2, std=0.2)[0]
+    z[3] = _rows(1, V, dtype, V + 3, mask=0.6)[0]
+    u = torch.rand(5, generator=g, device="cuda")
+    u[4] = 0.0
+    y = z.float().argmax(1)
+    w = torch.ones(5, device="cuda")
+    for s in (dict(k=129), dict(k=255, p=0.97), dict(k=300), dict(k=700, p=0.999), dict(k=1023),
+              dict(k=1030, m=1e-4), dict(p=0.5), dict(p=0.9), dict(m=0.003), dict(p=0.999, m=0.001)):
+        tok, lp = _check_sample(cuda_lib, z, u, what=(V, s), **s)
+        stats = _check_train(cuda_lib, z, y, w, what=(V, s), **s)[:5]
+        a = (1.0, s.get("k", 0), s.get("p", 1.0), s.get("m", 0.0))
+        for n in (62, 124):  # 310 and 620 rows
+            many = z.repeat(n, 1)
+            tok2, lp2 = cuda_lib.sample(many, u.repeat(n), *a)
+            assert torch.equal(tok2, tok.repeat(n)) and torch.equal(lp2, lp.repeat(n)), (V, s)
+            for x, x2 in zip(stats, cuda_lib.filtered_forward(many, y.repeat(n), *a)):
+                assert torch.equal(x2, x.repeat(n, *[1] * (x.dim() - 1))), (V, s)

@@ -799,6 +799,7 @@ cudaError_t launch_exact(const FilterArgs& a, bool filtered, const DeviceInfo& d
     const int team = (int)(want < most ? want : most);
     int64_t teams = dev.sm_count / team;
     if (teams > a.T) teams = a.T;
+    if (teams < 1) teams = 1;
     return launch_behind(filter_exact_kernel<E, kSample>, (unsigned)(teams * team), kExThreads,
                          sizeof(ExactShared), stream, (unsigned)team, a);
 }
