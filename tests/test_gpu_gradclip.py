@@ -137,3 +137,42 @@ def test_graph_and_lmhead_gradients(cuda_lib):
         want = _norm([dh, dW])
         assert abs(norm.item() - want) <= 5 * 2.0**-24 * want
         assert abs(_norm(outs) - min(0.1, want)) <= 8 * 2.0**-24
+
+
+@pytest.mark.parametrize("units", [1, 2, 15, 16, 17, 40])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_one_launch_and_two(cuda_lib, dtype, units):
+    """Lists on either side of 16 units of 32 KB, aligned or not, among empty
+    tensors: norm, scaling, tiny and huge values, a NaN passed on."""
+    per = 32768 // (2 if dtype == BF16 else 4)
+    err = cuda_lib.new_error_flag("cuda:0")
+    for off, scale in ((0, 1.0), (1, 1.0), (0, 1e-30), (3, 1e25)):
+        store = _list([units * per + 8], units, (dtype,), scale)[0]
+        whole = store[off:off + units * per - 5]
+        cut = whole.numel() // 2 // per * per
+        for xs in ([whole], [whole[:cut], whole[:0], whole[cut:]], [whole[:0]] * 40 + [whole]):
+            want = _norm(xs)
+            err.zero_()
+            got = cuda_lib.grad_norm(xs, dev_error=err)
+            assert abs(got.item() - want) <= 5 * 2.0**-24 * want + 2.0**-149
+            limit = float(np.float32(want * 0.5))
+            outs = [torch.empty_like(x) for x in xs]
+            norm, _ = cuda_lib.clip_grad_norm(xs, limit, out=outs, dev_error=err)
+            assert torch.equal(norm, got) and err.item() == 0
+            step = 2.0**-8 if dtype == BF16 else 2.0**-24
+            for x, o in zip(xs, outs):
+                exact = x.double() * (limit / want if want > limit else 1.0)
+                tiny = 2.0**-133 if dtype == BF16 else 2.0**-149  # subnormal results
+                # the factor carries the norm's error and two roundings
+                assert bool(((o.double() - exact).abs()
+                             <= (step + 8 * 2.0**-24) * exact.abs() + tiny).all())
+            own = [x.clone() for x in xs]
+            cuda_lib.clip_grad_norm(own, limit)
+            assert all(torch.equal(a, b) for a, b in zip(own, outs))
+        keep = store.clone()
+        whole[-1] = math.nan
+        keep[off + units * per - 6] = math.nan
+        norm, _ = cuda_lib.clip_grad_norm([whole], 1e-3, dev_error=err)
+        assert math.isnan(norm.item()) and err.item() == cuda_lib.DEV_NONFINITE
+        bits = torch.int16 if dtype == BF16 else torch.int32
+        assert torch.equal(store.view(bits), keep.view(bits))
