@@ -54,6 +54,6 @@ def test_refusals_are_those_of_the_functions():
 
 
 def test_a_failed_launch_raises():
-    assert pstat._served((1,), "x") and not pstat._served(None, "x")
+    assert pstat._launched((1,), "x") == (1,)
     with pytest.raises(pstat.PstatError, match="pstat_sample"):
-        pstat._served(-7, "pstat_sample")
+        pstat._launched(-7, "pstat_sample")

@@ -13,13 +13,14 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
 #include <exception>
+#include <optional>
 #include <vector>
 
 #include "pstat.h"
@@ -118,8 +119,9 @@ bool take_index(PyObject* o, int64_t* v) {
     return !over;
 }
 
+// Straight to the allocator: through torch's dispatcher an output takes 0.5 us more.
 at::Tensor empty(const at::Tensor& like, at::IntArrayRef size, at::ScalarType type) {
-    return at::empty(size, at::TensorOptions().device(like.device()).dtype(type));
+    return at::detail::empty_cuda(size, type, like.device(), std::nullopt);
 }
 pstat_stream_t stream_of(int device) {
     return reinterpret_cast<pstat_stream_t>(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());

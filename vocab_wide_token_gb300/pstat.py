@@ -122,12 +122,6 @@ except ImportError:  # not built: every call takes the path below
     _native = None
 
 
-def _served(got, where: str) -> bool:
-    """Whether the native module served a call; a failed launch raises."""
-    if got.__class__ is int:
-        _check(got, where)
-    return got is not None
-
 F32, BF16 = 0, 1
 OK = 0
 ERR = {-1: "NULLPTR", -2: "SHAPE", -3: "SHARDS", -4: "DTYPE", -5: "ALIGN", -6: "WORKSPACE",
@@ -148,6 +142,13 @@ class PstatError(RuntimeError):
 def _check(code: int, where: str) -> None:
     if code != OK:
         raise PstatError(code, where)
+
+
+def _launched(got, where: str):
+    """The native module's result; a status in its place is a failed launch's."""
+    if got.__class__ is int:
+        _check(got, where)
+    return got
 
 
 def _call(dev, where: str, fn, *args) -> None:
@@ -762,8 +763,8 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, top_k=0
     """
     if _native is not None and out is None and workspace is None:
         got = _native.sample(logits, uniform, temperature, top_k, top_p, min_p, dev_error)
-        if _served(got, "pstat_sample"):
-            return got
+        if got is not None:
+            return _launched(got, "pstat_sample")
     T, V, ld = _rows(logits)
     dev = logits.device
     dt = _dtype_code(logits)
@@ -806,8 +807,8 @@ def filtered_forward(logits: torch.Tensor, labels: torch.Tensor | None, temperat
     if _native is not None and out is None and workspace is None:
         got = _native.filtered_forward(logits, labels, temperature, top_k, top_p, min_p,
                                        ignore_index, dev_error)
-        if _served(got, "pstat_filtered_forward"):
-            return got
+        if got is not None:
+            return _launched(got, "pstat_filtered_forward")
     T, V, ld = _rows(logits)
     dev = logits.device
     dt = _dtype_code(logits)
@@ -835,8 +836,8 @@ def filtered_backward(logits: torch.Tensor, labels: torch.Tensor | None,
     if _native is not None and out is None and out_dtype is None:
         got = _native.filtered_backward(logits, labels, weights, rowstats, cut_logit, cut_index,
                                         temperature, ignore_index, dev_error)
-        if _served(got, "pstat_filtered_backward"):
-            return got
+        if got is not None:
+            return _launched(got, "pstat_filtered_backward")
     T, V, ld = _rows(logits)
     dev = logits.device
     dt = _dtype_code(logits)
@@ -924,8 +925,8 @@ def grad_norm(tensors, *, out=None, workspace=None, dev_error=None) -> torch.Ten
     mix of sizes), as a float32 scalar tensor on their device."""
     if _native is not None and out is None and workspace is None:
         got = _native.grad_norm(tensors, dev_error)
-        if _served(got, "pstat_grad_norm"):
-            return got
+        if got is not None:
+            return _launched(got, "pstat_grad_norm")
     _, words, dev = _grad_list(tensors, None, False)
     norm = (torch.empty((), dtype=torch.float32, device=dev) if out is None
             else _tensor(out, torch.float32, (), dev, "out"))
@@ -944,7 +945,8 @@ def clip_grad_norm(tensors, max_norm: float, *, out=None, workspace=None, dev_er
     Tensors that are written may not overlap (a tensor listed twice, say)."""
     if _native is not None and workspace is None:
         got = _native.clip_grad_norm(tensors, max_norm, out, dev_error)
-        if _served(got, "pstat_clip_grad_norm"):
+        if got is not None:
+            _launched(got, "pstat_clip_grad_norm")
             return got, list(tensors if out is None else out)
     outs, words, dev = _grad_list(tensors, out, True)
     norm = torch.empty((), dtype=torch.float32, device=dev)
