@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(kFgThreads)
                              const int64_t* __restrict__ cut_index, float temperature,
                              const float* __restrict__ temperatures, Eout* __restrict__ out,
                              int64_t ld_out, int segs, int* __restrict__ dev_error) {
+    grid_wait();
     const int64_t t = blockIdx.x / segs;
     const int seg = (int)(blockIdx.x - t * segs);
     const Ein* zin = logits + t * ld;
@@ -188,11 +189,10 @@ cudaError_t launch_filtered_backward(const void* logits, int64_t T, int64_t V, i
     const int64_t segs = (V + kBlockCols<Eout> - 1) / kBlockCols<Eout>;
     const auto kernel = shift ? filtered_backward_kernel<Ein, Eout, true>
                               : filtered_backward_kernel<Ein, Eout, false>;
-    kernel<<<(unsigned)(T * segs), kFgThreads, 0, stream>>>(
-        static_cast<const Ein*>(logits), V, ld, labels, ignore_index, weights,
-        reinterpret_cast<const float2*>(rowstats), cut_logit, cut_index, temperature, temperatures,
-        static_cast<Eout*>(out), ld_out, (int)segs, dev_error);
-    return cudaGetLastError();
+    return launch_behind(kernel, (unsigned)(T * segs), kFgThreads, 0, stream, 1,
+                         static_cast<const Ein*>(logits), V, ld, labels, ignore_index, weights,
+                         reinterpret_cast<const float2*>(rowstats), cut_logit, cut_index, temperature,
+                         temperatures, static_cast<Eout*>(out), ld_out, (int)segs, dev_error);
 }
 
 }  // namespace

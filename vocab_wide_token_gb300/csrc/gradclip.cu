@@ -166,6 +166,7 @@ __device__ __forceinline__ double square_unit(const GradTensor& t, uint32_t u) {
 template <int N>
 __global__ void __launch_bounds__(kGnThreads, kNormCtas)
     square_sums_kernel(const __grid_constant__ GradBatch<N> g, double* __restrict__ partial) {
+    grid_wait();
     grid_launch_dependents();
     const uint32_t u0 = (uint32_t)((uint64_t)g.units * blockIdx.x / gridDim.x);
     const uint32_t u1 = (uint32_t)((uint64_t)g.units * (blockIdx.x + 1) / gridDim.x);
@@ -396,7 +397,9 @@ int run_norm(const pstat_tensor* tensors, int64_t n, bool clip, float max_norm, 
         }
         const int blocks = blocks_for(g.units, kNormCtas, dev);
         if (n_partial + blocks > max_partials) return PSTAT_ERR_WORKSPACE;
-        square_sums_kernel<N><<<blocks, kGnThreads, 0, st>>>(g, partial + n_partial);
+        if (launch_behind(square_sums_kernel<N>, (unsigned)blocks, kGnThreads, 0, st, 1, g,
+                          partial + n_partial) != cudaSuccess)
+            return PSTAT_ERR_CUDA;
         n_partial += blocks;
     }
     if (!clip || n_partial == 0) {

@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const E* logits = static_cast<const E*>(a.logits);
     E* group_max = static_cast<E*>(a.group_max);
     const int V = (int)a.V, chunks = a.chunks;
+    grid_wait();  // the logits may be the previous kernel's, and so may the workspace
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.left_count = 0;
     grid_launch_dependents();
 
@@ -860,10 +861,8 @@ cudaError_t launch_records(const FilterArgs& a, const DeviceInfo& dev, cudaStrea
     warps = warps < kWarps ? warps : kWarps;
     int64_t grid = (items + warps - 1) / warps;
     grid = grid < dev.sm_count ? grid : dev.sm_count;
-    filter_records_kernel<E, kU><<<(unsigned)grid, (unsigned)warps * 32,
-                                   (size_t)warps * kStages * (kRecordSlot + sizeof(uint64_t)),
-                                   stream>>>(a);
-    return cudaGetLastError();
+    return launch_behind(filter_records_kernel<E, kU>, (unsigned)grid, (unsigned)warps * 32,
+                         (size_t)warps * kStages * (kRecordSlot + sizeof(uint64_t)), stream, 1, a);
 }
 
 template <typename E, bool kSample>
