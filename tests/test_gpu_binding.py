@@ -138,3 +138,68 @@ def test_another_stream_and_a_graph(both):
     graph.replay()
     torch.cuda.synchronize()
     same(got, want)
+
+
+@pytest.mark.parametrize("before", ["nothing", "kernel", "copy", "memset", "join", "join of copies"])
+def test_captured_behind(cuda_lib, before):
+    """Captured calls behind whatever comes before them: what is written there is
+    what they read, replay after replay."""
+    T, V = 6, 5000
+    src = [torch.randn(T, V, device=DEV), torch.rand(T, device=DEV)]
+    z, u = torch.empty(T, V, device=DEV), torch.empty(T, device=DEV)
+    y = torch.arange(T, device=DEV)
+    w = torch.empty(T, device=DEV)
+    side = torch.cuda.Stream()
+
+    def feed():
+        main = torch.cuda.current_stream()
+        if before == "kernel":
+            torch.mul(src[1], 1.0, out=u)
+            w.fill_(1.0)
+            torch.mul(src[0], 2.0, out=z)
+        elif before == "copy":
+            u.copy_(src[1])
+            w.fill_(1.0)
+            z.copy_(src[0])
+        elif before == "memset":
+            u.copy_(src[1])
+            z.copy_(src[0])
+            w.zero_()
+        else:
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                z.copy_(src[0]) if before.endswith("copies") else torch.mul(src[0], 2.0, out=z)
+            w.fill_(1.0)
+            u.copy_(src[1]) if before.endswith("copies") else torch.mul(src[1], 1.0, out=u)
+            main.wait_stream(side)
+
+    def calls():
+        if before != "nothing":
+            feed()
+        got = list(pstat.sample(z, u, 0.9, 40, 0.9))
+        if before != "nothing":
+            feed()
+        st = pstat.filtered_forward(z, y, 0.9, 40, 0.9)
+        if before != "nothing":
+            feed()
+        got += [*st, pstat.filtered_backward(z, y, w, *st[2:], 0.9)]
+        if before != "nothing":
+            feed()
+        big = [z, z[:1].reshape(-1), z.reshape(-1)[:7]] * 8
+        return got + [pstat.grad_norm(big), pstat.grad_norm([z])]
+
+    if before == "nothing":
+        z.copy_(src[0]), u.copy_(src[1]), w.fill_(1.0)
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = calls()
+    for _ in range(3):
+        for x in src:
+            x.copy_(torch.rand_like(x) if x.dim() == 1 else torch.randn_like(x))
+        if before == "nothing":
+            z.copy_(src[0]), u.copy_(src[1])
+        graph.replay()
+        torch.cuda.synchronize()
+        same(got, calls())

@@ -159,7 +159,14 @@ PyObject* guarded(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* pack(std::vector<at::Tensor>& v) {
     PyObject* t = PyTuple_New((Py_ssize_t)v.size());
     if (!t) return nullptr;
-    for (size_t i = 0; i < v.size(); ++i) PyTuple_SET_ITEM(t, (Py_ssize_t)i, THPVariable_Wrap(std::move(v[i])));
+    for (size_t i = 0; i < v.size(); ++i) {
+        PyObject* o = THPVariable_Wrap(std::move(v[i]));
+        if (!o) {
+            Py_DECREF(t);
+            return nullptr;
+        }
+        PyTuple_SET_ITEM(t, (Py_ssize_t)i, o);
+    }
     return t;
 }
 
