@@ -18,6 +18,9 @@ The label's own element, (w/t)(1 - p), inherits the absolute error of ln S: p
 changes by p d(ln S).  A row without filters has ln S from fp32 sums, which near
 S = 1 lie 2^-23 apart, off by half of that in each of the chunk's sum, the fold
 and the logarithm: 4 x 2^-23 (w/t) is added there.
+Exponentials and products below the least normal number, 2^-126, are flushed to
+0: an element (w/t) e/S with S >= 1 may be off by 2^-126 (w/t) for the one and
+2^-126 for the other.
 """
 import math
 
@@ -109,8 +112,10 @@ def _check_train(lib, z, y, w, t=1.0, k=0, p=1.0, m=0.0, out_dtype=None, what=""
             big += abs(ref["logprob"])
             assert abs(lp[i].item() - ref["logprob"]) <= tol + 8 * big * 2.0**-24, (what, i)
         grads.append(oflt.backward(zi, int(y[i]), w[i].item(), *a, IGN))
+        # below 2^-126 a weight and its product with w/t are taken as 0
+        room[i] = 2.0**-126 * (1 + abs(w[i].item()) / _at(t, i))
         if y[i] != IGN:
-            room[i, int(y[i])] = 4 * 2.0**-23 * abs(w[i].item()) / _at(t, i)
+            room[i, int(y[i])] += 4 * 2.0**-23 * abs(w[i].item()) / _at(t, i)
     _grad_close(g, np.stack(grads), room, what)
     return lp, ent, rs, tau, idx, g
 
@@ -563,3 +568,21 @@ def test_candidate_counts(cuda_lib, dtype, V):
             assert torch.equal(tok2, tok.repeat(n)) and torch.equal(lp2, lp.repeat(n)), (V, s)
             for x, x2 in zip(stats, cuda_lib.filtered_forward(many, y.repeat(n), *a)):
                 assert torch.equal(x2, x.repeat(n, *[1] * (x.dim() - 1))), (V, s)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("t", [0.3, 0.1, 0.03, 0.004])
+def test_low_temperatures(cuda_lib, dtype, t):
+    """top-k far below the maximum: tokens of weights from 2^-64 down to none are
+    still counted, kept and, at u = 0, drawn."""
+    for V in (2318, 20011, 60000):
+        z, g = _rows(6, V, dtype, V, peak=12.0)
+        z[3] = _rows(1, V, dtype, V + 1, peak=40.0)[0]
+        u = torch.rand(6, generator=g, device="cuda")
+        u[5] = 0.0
+        w = torch.ones(6, device="cuda")
+        y = z.float().topk(60, dim=1).indices[:, [0, 1, 7, 30, 49, 59]].diagonal().contiguous()
+        for s in (dict(k=50), dict(k=200, p=0.95), dict(k=50, p=0.8, m=0.05), dict(k=200, m=1e-30),
+                  dict(k=7, p=0.999999), dict(p=0.95), dict(m=1e-37)):
+            _check_sample(cuda_lib, z, u, t=t, what=(V, s), **s)
+            _check_train(cuda_lib, z, y, w, t=t, what=(V, s), **s)

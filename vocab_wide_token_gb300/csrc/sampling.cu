@@ -219,7 +219,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 // Bound by latency (records, maxima, columns, ranks, each behind the last): 7 us for
 // one row of V = 151,936 with top-k 50, 30 us for 2048 rows with a nucleus.
 // ---------------------------------------------------------------------------
-constexpr int kFinBins = 1024;     // 64 binary orders of e, in steps of 1/16
+// Bins of M - z: 48 binary orders of e in steps of 1/16, then 510 in steps of 2 (at
+// temperature 0.25 the 50th largest of 151,936 logits can be 2^-70 of the first:
+// such rows took 95 us by way of the exact kernel, and take 18).
+constexpr int kFinBins = 1024;
+constexpr int kFineBins = 768;
+constexpr float kBinsPerOrder = 16.f, kBinsPerStep = 32.f;
 constexpr int kFinCand = 1024;
 constexpr int kFinGroups = 2048;
 constexpr int kFinShort = 16384;   // columns of a row whose histogram is of its columns
@@ -527,27 +532,59 @@ __device__ __forceinline__ void finish_few(const FilterArgs& a, const E* row, co
 }
 
 // Sorts n <= kFinCand keys; the places up to the next power of two, which it
-// returns, are filled with the largest.  Bitonic: pairs up to 32 apart stay with a
-// warp, so most steps need no barrier of the block.
+// returns, are filled with the largest.  Bitonic, element t + r kFinThreads in
+// register r of thread t: a pair is in one thread, in one warp (most steps), or met
+// through shared memory.
 template <int kFinThreads>
 __device__ __noinline__ int block_sort(unsigned long long* key, int n) {
+    constexpr int kRegs = kFinCand / kFinThreads;
+    const int t = (int)threadIdx.x;
     int size = 64;
     while (size < n) size *= 2;
-    for (int i = n + (int)threadIdx.x; i < size; i += kFinThreads) key[i] = ~0ull;
-    __syncthreads();
+    unsigned long long v[kRegs];
+#pragma unroll
+    for (int r = 0; r < kRegs; ++r) v[r] = t + r * kFinThreads < n ? key[t + r * kFinThreads] : ~0ull;
+    // This thread's element of the pair whose other element is `other`.
+    auto meet = [&](int r, int run, int stride, unsigned long long other) {
+        const bool low = !(t & stride), up = !((t + r * kFinThreads) & run);
+        if ((other < v[r]) == (low == up)) v[r] = other;
+    };
+#pragma unroll 1
     for (int run = 2; run <= size; run *= 2)
+#pragma unroll 1
         for (int stride = run / 2; stride > 0; stride /= 2) {
-            if (stride >= 32 && run > 64) __syncthreads();  // after a pair further apart, or before
-            for (int p = threadIdx.x; p < size / 2; p += kFinThreads) {
-                const int i = 2 * p - (p & (stride - 1));
-                const unsigned long long x = key[i], y = key[i + stride];
-                if ((x > y) == ((i & run) == 0)) {
-                    key[i] = y;
-                    key[i + stride] = x;
-                }
+            if (stride >= kFinThreads) {
+#pragma unroll
+                for (int d = 1; d < kRegs; d *= 2)
+                    if (stride == d * kFinThreads)
+#pragma unroll
+                        for (int r = 0; r < kRegs; ++r)
+                            if (!(r & d) && ((v[r | d] < v[r]) == !((r * kFinThreads) & run))) {
+                                const unsigned long long x = v[r];
+                                v[r] = v[r | d];
+                                v[r | d] = x;
+                            }
+            } else if (stride >= 32) {
+                __syncthreads();
+#pragma unroll
+                for (int r = 0; r < kRegs; ++r)
+                    if (r * kFinThreads < size) key[t + r * kFinThreads] = v[r];
+                __syncthreads();
+#pragma unroll
+                for (int r = 0; r < kRegs; ++r)
+                    if (r * kFinThreads < size)
+                        meet(r, run, stride, key[(t ^ stride) + r * kFinThreads]);
+            } else {
+#pragma unroll
+                for (int r = 0; r < kRegs; ++r)
+                    if (r * kFinThreads < size)
+                        meet(r, run, stride, __shfl_xor_sync(0xFFFFFFFFu, v[r], stride));
             }
-            __syncwarp();
         }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kRegs; ++r)
+        if (r * kFinThreads < size) key[t + r * kFinThreads] = v[r];
     __syncthreads();
     return size;
 }
@@ -712,9 +749,15 @@ __global__ void __launch_bounds__(kFinThreads, (kFiltered ? 1024 : 1536) / kFinT
     r.mp = min_p_bounds(M, rs);
     const bool short_row = V <= kFinShort;
     r.all = V <= kFinFew<kFinThreads>;
-    const float bin_scale = r.c.ch * ((float)kFinBins / 64.f);
+    const float bin_scale = r.c.ch * kBinsPerOrder;
     const float ch = r.c.ch;
-    auto bin_of = [&](float z) { return min(kFinBins - 1, __float2int_rd((M - z) * bin_scale)); };
+    auto bin_of = [&](float z) {
+        const float y = (M - z) * bin_scale;
+        if (y < (float)kFineBins) return __float2int_rd(y);
+        // exact: both are multiples of the last place of y
+        return kFineBins + min(kFinBins - 1 - kFineBins,
+                               __float2int_rd((y - (float)kFineBins) * (1.f / kBinsPerStep)));
+    };
     const int groups = a.chunks * 32;
     const int bin_m = rs.cut_m ? bin_of(r.mp.lo) : kFinBins;
     // Columns up to this bin are gathered; the last bin is open.
@@ -782,8 +825,10 @@ __global__ void __launch_bounds__(kFinThreads, (kFiltered ? 1024 : 1536) / kFinT
     }
     r.all_min = rs.cut_m && b >= bin_m;
 
-    // ---- gather.  bin_of(z) <= b  <=>  (M - z) bin_scale < b + 1
-    const float edge = r.all ? INFINITY : (float)(b + 1);
+    // ---- gather.  bin_of(z) <= b  <=>  (M - z) bin_scale < edge
+    const float edge = r.all          ? INFINITY
+                       : b < kFineBins ? (float)(b + 1)
+                                       : (float)kFineBins + (float)(b + 1 - kFineBins) * kBinsPerStep;
     const bool direct = r.all || short_row;  // every column, from L1 by now
     int n_vec;                               // vectors of kVec columns to look through
     if (direct) {
