@@ -391,7 +391,7 @@ constexpr float kSumError = 1.f / 262144.f;
 
 // The row's (M, S, U base 2) from its records, by one warp, every lane alike;
 // NaN M where a record is bad, -inf where every logit is masked.
-__device__ __forceinline__ float3 fold_records(const float4* __restrict__ rec, int n, float c,
+__device__ __forceinline__ float3 fold_records(const float4* rec, int n, float c,
                                                int lane) {
     // The usual rows have at most 64 chunks: both of a lane's records are loaded
     // before either is used.

@@ -41,15 +41,19 @@ __device__ __forceinline__ void store_group(float* p, const float (&g)[4]) {
 
 template <typename Ein, typename Eout, bool kShift>
 __global__ void __launch_bounds__(kFgThreads)
-    filtered_backward_kernel(const Ein* __restrict__ logits, int64_t V, int64_t ld,
-                             const int64_t* __restrict__ labels, int64_t ignore_index,
-                             const float* __restrict__ weights,
-                             const float2* __restrict__ rowstats,
-                             const float* __restrict__ cut_logit,
-                             const int64_t* __restrict__ cut_index, float temperature,
-                             const float* __restrict__ temperatures, Eout* __restrict__ out,
-                             int64_t ld_out, int segs, int* __restrict__ dev_error) {
+    filtered_backward_kernel(const Ein* logits, int64_t V, int64_t ld, const int64_t* labels,
+                             int64_t ignore_index, const float* weights, const float2* rowstats,
+                             const float* cut_logit, const int64_t* cut_index, float temperature,
+                             const float* temperatures, Eout* out, int64_t ld_out, int segs,
+                             int* dev_error) {
     grid_wait();
+    logits = after_wait(logits);
+    labels = after_wait(labels);
+    weights = after_wait(weights);
+    rowstats = after_wait(rowstats);  // the finish kernel before this one may just have written them
+    cut_logit = after_wait(cut_logit);
+    cut_index = after_wait(cut_index);
+    temperatures = after_wait(temperatures);
     const int64_t t = blockIdx.x / segs;
     const int seg = (int)(blockIdx.x - t * segs);
     const Ein* zin = logits + t * ld;

@@ -144,20 +144,21 @@ __device__ __forceinline__ int tensor_of(const GradBatch<N>& g, uint32_t u) {
 // This thread's share of the squares of unit u, a unit of tensor t.
 __device__ __forceinline__ double square_unit(const GradTensor& t, uint32_t u) {
     const bool bf16 = t.bf16;
+    const void* in = after_wait(t.in);
     const int64_t per = kUnitBytes / (bf16 ? 2 : 4);
     const int64_t e0 = (int64_t)(u - t.first_unit) * per;
     const int64_t e1 = min(t.n, e0 + per);
     const int vec = bf16 ? 8 : 4;
     int64_t done = e0;
     double sum = 0.0;
-    if ((reinterpret_cast<uintptr_t>(t.in) & 15u) == 0) {
+    if ((reinterpret_cast<uintptr_t>(in) & 15u) == 0) {
         const int nv = (int)((e1 - e0) / vec);
-        const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(t.in) + e0 * (bf16 ? 2 : 4));
+        const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(in) + e0 * (bf16 ? 2 : 4));
         sum = bf16 ? unit_squares<true>(v, nv) : unit_squares<false>(v, nv);
         done = e0 + (int64_t)nv * vec;
     }
     for (int64_t k = done + threadIdx.x; k < e1; k += kGnThreads) {
-        const double x = elem(t.in, k, bf16);
+        const double x = elem(in, k, bf16);
         sum = fma(x, x, sum);
     }
     return sum;
@@ -165,7 +166,7 @@ __device__ __forceinline__ double square_unit(const GradTensor& t, uint32_t u) {
 
 template <int N>
 __global__ void __launch_bounds__(kGnThreads, kNormCtas)
-    square_sums_kernel(const __grid_constant__ GradBatch<N> g, double* __restrict__ partial) {
+    square_sums_kernel(const __grid_constant__ GradBatch<N> g, double* partial) {
     grid_wait();
     grid_launch_dependents();
     const uint32_t u0 = (uint32_t)((uint64_t)g.units * blockIdx.x / gridDim.x);
@@ -202,26 +203,28 @@ __device__ __forceinline__ float finish_norm(double total, float max_norm, bool 
 }
 
 __global__ void __launch_bounds__(kGnThreads)
-    norm_kernel(const double* __restrict__ partial, int n, float* __restrict__ out,
-                int* __restrict__ dev_error) {
+    norm_kernel(const double* partial, int n, float* out, int* dev_error) {
     grid_wait();
+    partial = after_wait(partial);
     const double total = total_of(partial, n);
     if (threadIdx.x == 0) finish_norm(total, 0.f, true, out, dev_error);
 }
 
 __device__ __forceinline__ void scale_unit(const GradTensor& t, uint32_t u, float factor) {
-    if (factor == 1.f && t.out == t.in) return;
+    const void* in = after_wait(t.in);
+    void* out = t.out;
+    if (factor == 1.f && out == in) return;
     const bool bf16 = t.bf16;
     const int64_t per = kUnitBytes / (bf16 ? 2 : 4);
     const int64_t e0 = (int64_t)(u - t.first_unit) * per;
     const int64_t e1 = min(t.n, e0 + per);
     const int vec = bf16 ? 8 : 4;
     int64_t done = e0;
-    if (((reinterpret_cast<uintptr_t>(t.in) | reinterpret_cast<uintptr_t>(t.out)) & 15u) == 0) {
+    if (((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0) {
         const int nv = (int)((e1 - e0) / vec);
         const int64_t off = e0 * (bf16 ? 2 : 4);
-        const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(t.in) + off);
-        uint4* o = reinterpret_cast<uint4*>(static_cast<char*>(t.out) + off);
+        const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(in) + off);
+        uint4* o = reinterpret_cast<uint4*>(static_cast<char*>(out) + off);
         uint4 q[kGnUnroll];
 #pragma unroll
         for (int j = 0; j < kGnUnroll; ++j) {
@@ -245,12 +248,12 @@ __device__ __forceinline__ void scale_unit(const GradTensor& t, uint32_t u, floa
     }
     for (int64_t k = done + threadIdx.x; k < e1; k += kGnThreads) {
         if (bf16) {
-            const uint16_t x = static_cast<const uint16_t*>(t.in)[k];
-            static_cast<uint16_t*>(t.out)[k] =
+            const uint16_t x = static_cast<const uint16_t*>(in)[k];
+            static_cast<uint16_t*>(out)[k] =
                 factor == 1.f ? x : (uint16_t)(bf2_pack_rn(bf2_lo(x) * factor, 0.f) & 0xFFFFu);
         } else {
-            const uint32_t x = static_cast<const uint32_t*>(t.in)[k];
-            static_cast<uint32_t*>(t.out)[k] =
+            const uint32_t x = static_cast<const uint32_t*>(in)[k];
+            static_cast<uint32_t*>(out)[k] =
                 factor == 1.f ? x : __float_as_uint(__uint_as_float(x) * factor);
         }
     }
@@ -258,13 +261,14 @@ __device__ __forceinline__ void scale_unit(const GradTensor& t, uint32_t u, floa
 
 template <int N>
 __global__ void __launch_bounds__(kGnThreads, kScaleCtas)
-    scale_kernel(const __grid_constant__ GradBatch<N> g, const double* __restrict__ partial, int n,
-                 float max_norm, float* __restrict__ out, int* __restrict__ dev_error) {
+    scale_kernel(const __grid_constant__ GradBatch<N> g, const double* partial, int n,
+                 float max_norm, float* out, int* dev_error) {
     __shared__ float s_factor;
     const uint32_t u0 = (uint32_t)((uint64_t)g.units * blockIdx.x / gridDim.x);
     const uint32_t u1 = (uint32_t)((uint64_t)g.units * (blockIdx.x + 1) / gridDim.x);
     int i = tensor_of(g, u1 - 1);
     grid_wait();
+    partial = after_wait(partial);
     const double total = total_of(partial, n);
     if (threadIdx.x == 0) s_factor = finish_norm(total, max_norm, blockIdx.x == 0, out, dev_error);
     __syncthreads();
@@ -284,7 +288,7 @@ __global__ void __launch_bounds__(kGnThreads, kScaleCtas)
 template <int N>
 __global__ void __launch_bounds__(kGnThreads)
     few_units_kernel(const __grid_constant__ GradBatch<N> g, bool clip, float max_norm,
-                     float* __restrict__ out, int* __restrict__ dev_error) {
+                     float* out, int* dev_error) {
     __shared__ double parts[kTeam];
     __shared__ float s_factor;
     const cg::cluster_group team = cg::this_cluster();

@@ -72,7 +72,11 @@ cudaError_t ensure_large_cluster(const void* func, ContextSeen& seen);
 
 // Launches `kernel` behind the stream's previous kernel by programmatic
 // dependent launch: its blocks may start early and call grid_wait() before they
-// touch anything that kernel writes.  `cluster` > 1 groups the blocks.
+// touch anything that kernel writes.  What that kernel may have written is not
+// constant while this one lives, so it is read neither through `const __restrict__`
+// parameters nor by __ldg: such loads may pass the wait, or a cache that is not
+// kept coherent.  Pointers are taken through after_wait().  `cluster` > 1 groups the
+// blocks.
 template <typename... P, typename... A>
 cudaError_t launch_behind(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
                           cudaStream_t stream, unsigned cluster, const A&... args) {

@@ -106,6 +106,14 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 __device__ __forceinline__ void grid_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// The same pointer, made anew behind a grid_wait(): no load through it, of whatever
+// kind, can be moved before the wait or be taken for one of constant memory.
+template <typename T>
+__device__ __forceinline__ T* after_wait(T* p) {
+    uint64_t a = reinterpret_cast<uint64_t>(p);
+    asm volatile("" : "+l"(a)::"memory");
+    return reinterpret_cast<T*>(a);
+}
 
 // ---- packed f32x2 arithmetic (sm_100+) --------------------------------------
 __device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {

@@ -275,7 +275,7 @@ __device__ __forceinline__ void leave_row(const FilterArgs& a, int64_t t) {
 
 // Calls f(group, maximum) for a row's groups, eight loads ahead.
 template <typename E, int kFinThreads, typename F>
-__device__ __forceinline__ void for_each_group(const E* __restrict__ gm, int groups, F f) {
+__device__ __forceinline__ void for_each_group(const E* gm, int groups, F f) {
     constexpr int kAhead = 8;
     for (int i0 = threadIdx.x; i0 < groups; i0 += kAhead * kFinThreads) {
         E g[kAhead];

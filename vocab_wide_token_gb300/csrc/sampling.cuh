@@ -143,7 +143,9 @@ struct RowReader<float> {
 };
 
 // Reads N times kVec columns from col[h] (multiples of kVec) of a row, all loads
-// before the first use; columns past V read as -inf.
+// before the first use; columns past V read as -inf.  The logits are constant while
+// the finish and the exact kernel live (the records kernel, whose blocks all wait
+// before they let these start, comes between them and whatever wrote the logits).
 template <typename E, int N>
 __device__ __forceinline__ void load_columns(const E* row, const int (&col)[N], int V,
                                              float (&x)[N][Elem<E>::kVec]) {
