@@ -255,19 +255,19 @@ PyObject* filtered_backward(PyObject* const* a, Py_ssize_t n) {
     return THPVariable_Wrap(std::move(out));
 }
 
-// The tensors of a list or tuple, and where each is written (itself, or `outs`).
-bool take_list(PyObject* list, PyObject* outs, bool writes, std::vector<pstat_tensor>& v,
-               const at::Tensor** first) {
-    if (!PyList_Check(list) && !PyTuple_Check(list)) return false;
-    const Py_ssize_t n = PySequence_Fast_GET_SIZE(list);
+// The tensors of a tuple, and where each is written (itself, or `outs`).  No list is
+// taken: the call goes on without the interpreter lock, and another thread could
+// empty a list meanwhile and free what the launch uses.  A tuple keeps its tensors.
+bool take_tuple(PyObject* list, PyObject* outs, bool writes, std::vector<pstat_tensor>& v,
+                const at::Tensor** first) {
+    if (!PyTuple_Check(list)) return false;
+    const Py_ssize_t n = PyTuple_GET_SIZE(list);
     const bool apart = outs != Py_None;
-    if (n == 0 || (apart && ((!PyList_Check(outs) && !PyTuple_Check(outs)) ||
-                             PySequence_Fast_GET_SIZE(outs) != n)))
-        return false;
+    if (n == 0 || (apart && (!PyTuple_Check(outs) || PyTuple_GET_SIZE(outs) != n))) return false;
     v.resize((size_t)n);
     for (Py_ssize_t i = 0; i < n; ++i) {
-        const at::Tensor* x = tensor(PySequence_Fast_GET_ITEM(list, i));
-        const at::Tensor* o = apart ? tensor(PySequence_Fast_GET_ITEM(outs, i)) : x;
+        const at::Tensor* x = tensor(PyTuple_GET_ITEM(list, i));
+        const at::Tensor* o = apart ? tensor(PyTuple_GET_ITEM(outs, i)) : x;
         if (!x || !o || !x->defined() || !o->defined() || !x->is_cuda() || !x->is_contiguous()) return false;
         if (i == 0) *first = x;
         const at::ScalarType type = x->scalar_type();
@@ -287,8 +287,8 @@ PyObject* norm_of(PyObject* list, PyObject* outs, PyObject* flag, bool clip, flo
     std::vector<pstat_tensor> v;
     const at::Tensor* first = nullptr;
     int* err;
-    if (!take_list(list, outs, clip, v, &first)) Py_RETURN_NONE;
-    const at::Tensor like = *first;  // the list may change while the lock is released
+    if (!take_tuple(list, outs, clip, v, &first)) Py_RETURN_NONE;
+    const at::Tensor& like = *first;
     const int device = like.get_device();
     if (!take_flag(flag, device, &err)) Py_RETURN_NONE;
     at::Tensor norm;

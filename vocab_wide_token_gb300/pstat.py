@@ -869,6 +869,12 @@ def filtered_backward(logits: torch.Tensor, labels: torch.Tensor | None,
 _dtype_of = operator.attrgetter("dtype")
 
 
+def _held(tensors):
+    """A list as a tuple, which keeps its tensors while the native module works
+    on their addresses without the interpreter lock."""
+    return tuple(tensors) if isinstance(tensors, list) else tensors
+
+
 def _grad_list(tensors, out, writes):
     """(the outputs, the pstat_tensor array, the device) of a list of tensors
     that must be contiguous, bf16 or fp32, on one CUDA device.  A list of
@@ -923,6 +929,7 @@ def _grad_call(words, workspace, dev):
 def grad_norm(tensors, *, out=None, workspace=None, dev_error=None) -> torch.Tensor:
     """The L2 norm over all elements of a list of gradients (bf16 or fp32, any
     mix of sizes), as a float32 scalar tensor on their device."""
+    tensors = _held(tensors)
     if _native is not None and out is None and workspace is None:
         got = _native.grad_norm(tensors, dev_error)
         if got is not None:
@@ -943,6 +950,7 @@ def clip_grad_norm(tensors, max_norm: float, *, out=None, workspace=None, dev_er
     (the norm before scaling, a float32 scalar tensor; the list of the scaled
     tensors).  A norm that is not finite sets DEV_NONFINITE and scales nothing.
     Tensors that are written may not overlap (a tensor listed twice, say)."""
+    tensors, out = _held(tensors), _held(out)
     if _native is not None and workspace is None:
         got = _native.clip_grad_norm(tensors, max_norm, out, dev_error)
         if got is not None:
