@@ -189,8 +189,17 @@ __device__ __forceinline__ double total_of(const double* partial, int n) {
     return block_sum(s);
 }
 
-// Norm and error bits, by one thread; returns what the gradients are scaled by.
-__device__ __forceinline__ float finish_norm(double total, float max_norm, bool write, float* out,
+// What gradients are scaled by: factor, then rest, a power of two that is 1 unless
+// max_norm / norm lies below the normal numbers.  There (max_norm < 4) the factor is
+// 2^125 times as large, so that it keeps its 24 bits and no product overflows; an
+// element of 1e37 clipped by a factor of 1e-45 is still a normal number.
+struct Scale {
+    float factor, rest;
+    __device__ float operator()(float x) const { return x * factor * rest; }
+};
+
+// Norm and error bits, by one thread.
+__device__ __forceinline__ Scale finish_norm(double total, float max_norm, bool write, float* out,
                                              int* dev_error) {
     const double norm = sqrt(total);
     const float f = (float)norm;
@@ -199,7 +208,9 @@ __device__ __forceinline__ float finish_norm(double total, float max_norm, bool 
         *out = f;
         if (!finite && dev_error) atomicOr(dev_error, PSTAT_DEV_NONFINITE);
     }
-    return finite && norm > (double)max_norm ? (float)((double)max_norm / norm) : 1.f;
+    if (!finite || norm <= (double)max_norm) return {1.f, 1.f};
+    const double ratio = (double)max_norm / norm;
+    return ratio < 0x1p-126 ? Scale{(float)(ratio * 0x1p125), 0x1p-125f} : Scale{(float)ratio, 1.f};
 }
 
 __global__ void __launch_bounds__(kGnThreads)
@@ -210,10 +221,11 @@ __global__ void __launch_bounds__(kGnThreads)
     if (threadIdx.x == 0) finish_norm(total, 0.f, true, out, dev_error);
 }
 
-__device__ __forceinline__ void scale_unit(const GradTensor& t, uint32_t u, float factor) {
+__device__ __forceinline__ void scale_unit(const GradTensor& t, uint32_t u, const Scale scale) {
     const void* in = after_wait(t.in);
     void* out = t.out;
-    if (factor == 1.f && out == in) return;
+    const bool same = scale.factor == 1.f && scale.rest == 1.f;
+    if (same && out == in) return;
     const bool bf16 = t.bf16;
     const int64_t per = kUnitBytes / (bf16 ? 2 : 4);
     const int64_t e0 = (int64_t)(u - t.first_unit) * per;
@@ -238,9 +250,9 @@ __device__ __forceinline__ void scale_unit(const GradTensor& t, uint32_t u, floa
             uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                if (factor == 1.f) continue;  // passed on bit for bit, NaNs included
-                w[e] = bf16 ? bf2_pack_rn(bf2_lo(w[e]) * factor, bf2_hi(w[e]) * factor)
-                            : __float_as_uint(__uint_as_float(w[e]) * factor);
+                if (same) continue;  // passed on bit for bit, NaNs included
+                w[e] = bf16 ? bf2_pack_rn(scale(bf2_lo(w[e])), scale(bf2_hi(w[e])))
+                            : __float_as_uint(scale(__uint_as_float(w[e])));
             }
             __stcs(o + k, make_uint4(w[0], w[1], w[2], w[3]));
         }
@@ -250,11 +262,11 @@ __device__ __forceinline__ void scale_unit(const GradTensor& t, uint32_t u, floa
         if (bf16) {
             const uint16_t x = static_cast<const uint16_t*>(in)[k];
             static_cast<uint16_t*>(out)[k] =
-                factor == 1.f ? x : (uint16_t)(bf2_pack_rn(bf2_lo(x) * factor, 0.f) & 0xFFFFu);
+                same ? x : (uint16_t)(bf2_pack_rn(scale(bf2_lo(x)), 0.f) & 0xFFFFu);
         } else {
             const uint32_t x = static_cast<const uint32_t*>(in)[k];
             static_cast<uint32_t*>(out)[k] =
-                factor == 1.f ? x : __float_as_uint(__uint_as_float(x) * factor);
+                same ? x : __float_as_uint(scale(__uint_as_float(x)));
         }
     }
 }
@@ -263,20 +275,20 @@ template <int N>
 __global__ void __launch_bounds__(kGnThreads, kScaleCtas)
     scale_kernel(const __grid_constant__ GradBatch<N> g, const double* partial, int n,
                  float max_norm, float* out, int* dev_error) {
-    __shared__ float s_factor;
+    __shared__ Scale s_scale;
     const uint32_t u0 = (uint32_t)((uint64_t)g.units * blockIdx.x / gridDim.x);
     const uint32_t u1 = (uint32_t)((uint64_t)g.units * (blockIdx.x + 1) / gridDim.x);
     int i = tensor_of(g, u1 - 1);
     grid_wait();
     partial = after_wait(partial);
     const double total = total_of(partial, n);
-    if (threadIdx.x == 0) s_factor = finish_norm(total, max_norm, blockIdx.x == 0, out, dev_error);
+    if (threadIdx.x == 0) s_scale = finish_norm(total, max_norm, blockIdx.x == 0, out, dev_error);
     __syncthreads();
-    const float factor = s_factor;
+    const Scale scale = s_scale;
     // Backwards: what the norm read last is still in L2.
     for (uint32_t u = u1; u-- > u0;) {
         while (i > 0 && g.t[i].first_unit > u) --i;
-        scale_unit(g.t[i], u, factor);
+        scale_unit(g.t[i], u, scale);
     }
 }
 
@@ -290,7 +302,7 @@ __global__ void __launch_bounds__(kGnThreads)
     few_units_kernel(const __grid_constant__ GradBatch<N> g, bool clip, float max_norm,
                      float* out, int* dev_error) {
     __shared__ double parts[kTeam];
-    __shared__ float s_factor;
+    __shared__ Scale s_scale;
     const cg::cluster_group team = cg::this_cluster();
     const uint32_t rank = team.block_rank(), size = team.num_blocks();
     team.barrier_arrive();  // before a CTA's memory is written it has to have started
@@ -303,11 +315,11 @@ __global__ void __launch_bounds__(kGnThreads)
     if (threadIdx.x == 0) {
         double s = 0.0;
         for (uint32_t r = 0; r < size; ++r) s += parts[r];
-        s_factor = finish_norm(s, max_norm, rank == 0, out, dev_error);
+        s_scale = finish_norm(s, max_norm, rank == 0, out, dev_error);
     }
     if (!clip) return;
     __syncthreads();
-    scale_unit(t, rank, s_factor);
+    scale_unit(t, rank, s_scale);
 }
 
 int check_tensors(const pstat_tensor* tensors, int64_t n, bool outputs) {
