@@ -476,8 +476,9 @@ PSTAT_API int pstat_filtered_backward(const void* logits, pstat_dtype dt, int64_
  * The list is a HOST array; each entry names `n` contiguous elements on the
  * device.  Tensors may differ in type and size, be empty, and start at any
  * element; at most PSTAT_GRAD_MAX_ELEMENTS each.  Squares are summed without
- * overflow or underflow, in an order fixed by the sizes: the same list gives
- * the same bits.  An empty list has norm 0.
+ * overflow or underflow, in an order fixed by the sizes and types and by the
+ * device's number of SMs: the same values give the same bits, wherever the
+ * tensors lie.  An empty list has norm 0.
  */
 #define PSTAT_GRAD_MAX_ELEMENTS ((int64_t)1 << 40)
 typedef struct {
