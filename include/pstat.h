@@ -478,7 +478,8 @@ PSTAT_API int pstat_filtered_backward(const void* logits, pstat_dtype dt, int64_
  * element; at most PSTAT_GRAD_MAX_ELEMENTS each.  Squares are summed without
  * overflow or underflow, in an order fixed by the sizes and types and by the
  * device's number of SMs: the same values give the same bits, wherever the
- * tensors lie.  An empty list has norm 0.
+ * tensors lie.  The norm is within 10 x 2^-24 of the exact one.  An empty list
+ * has norm 0.
  */
 #define PSTAT_GRAD_MAX_ELEMENTS ((int64_t)1 << 40)
 typedef struct {

@@ -115,6 +115,9 @@ __device__ __forceinline__ void add_squares(const uint4& q, uint64_t& s0, uint64
 // Vectors off 16 bytes are put together from their elements and added in the same
 // order, so a tensor's bits do not depend on where it starts.  100 million elements:
 // bf16 34 us, at an odd offset 52; fp32 61 and 78.
+// The sum of up to 32 fp32 (64 bf16) squares in four fp32 sums is off by at most 10 (17:
+// bf16 squares are exact, 15 of 16 additions round, and two join the sums) roundings of
+// 2^-24, the norm by half of that and its own rounding: 6 x 2^-24, 9.5 x 2^-24 with bf16.
 template <bool kBf16>
 __device__ __forceinline__ double unit_squares(const void* v, int nv) {
     uint64_t s0 = 0, s1 = 0;
