@@ -304,6 +304,13 @@ PyObject* norm_of(PyObject* list, PyObject* outs, PyObject* flag, bool clip, flo
                                     ws.mutable_data_ptr(), bytes, err, stream_of(device));
     });
     if (rc != PSTAT_OK) return refuse(rc);
+    if (clip) {  // an in-place change, for autograd to notice (inference tensors have no count)
+        PyObject* written = outs == Py_None ? list : outs;
+        for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(written); ++i) {
+            const at::Tensor* x = tensor(PyTuple_GET_ITEM(written, i));
+            if (!x->is_inference()) x->unsafeGetTensorImpl()->bump_version();
+        }
+    }
     return THPVariable_Wrap(std::move(norm));
 }
 PyObject* grad_norm(PyObject* const* a, Py_ssize_t n) {

@@ -288,6 +288,15 @@ def _workspace(ws, need, dev):
     return ws
 
 
+def _written(*tensors) -> None:
+    """Counts the call as an in-place change of the caller's tensors, so that
+    autograd notices when one that it saved was overwritten (inference tensors
+    have no such count)."""
+    for x in tensors:
+        if not x.is_inference():
+            torch.autograd.graph.increment_version(x)
+
+
 def workspace_size(T: int, V: int, dtype: torch.dtype, shard_bounds=None) -> int:
     n = ctypes.c_size_t(0)
     arr, ns = _bounds(shard_bounds, V)
@@ -781,6 +790,8 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, top_k=0
     _call(dev, "pstat_sample", _lib.pstat_sample,
           _ptr(logits), dt, T, V, ld, _ptr(u), f, _ptr(token), _ptr(lp),
           _ptr(workspace), workspace.numel(), _ptr(dev_error), _stream(dev))
+    if out is not None:
+        _written(token, lp)
     return token, lp
 
 
@@ -821,6 +832,8 @@ def filtered_forward(logits: torch.Tensor, labels: torch.Tensor | None, temperat
           _ptr(logits), dt, T, V, ld, _ptr(lab), int(ignore_index), f, _ptr(lp),
           _ptr(ent), _ptr(rs), _ptr(tau), _ptr(index), _ptr(workspace), workspace.numel(),
           _ptr(dev_error), _stream(dev))
+    if out is not None:
+        _written(lp, ent, rs, tau, index)
     return lp, ent, rs, tau, index
 
 
@@ -843,6 +856,7 @@ def filtered_backward(logits: torch.Tensor, labels: torch.Tensor | None,
     dt = _dtype_code(logits)
     lab = _labels(labels, T, dev)
     out_dtype = out_dtype or logits.dtype
+    given = out is not None
     if out is None:
         out = torch.empty(T, V, dtype=out_dtype, device=dev)
     ld_out = _matrix_output(out, T, V, dev, "out")
@@ -861,6 +875,8 @@ def filtered_backward(logits: torch.Tensor, labels: torch.Tensor | None,
           _ptr(tau), _ptr(index), 1.0 if row_t else float(temperature),
           _ptr(temperature) if row_t else None, _ptr(out),
           _dtype_code(out), ld_out, _ptr(dev_error), _stream(dev))
+    if given:
+        _written(out)
     return out
 
 
@@ -941,6 +957,8 @@ def grad_norm(tensors, *, out=None, workspace=None, dev_error=None) -> torch.Ten
     at, n, workspace = _grad_call(words, workspace, dev)
     _call(dev, "pstat_grad_norm", _lib.pstat_grad_norm,
           at, n, _ptr(norm), _ptr(workspace), workspace.numel(), _ptr(dev_error), _stream(dev))
+    if out is not None:
+        _written(norm)
     return norm
 
 
@@ -963,6 +981,7 @@ def clip_grad_norm(tensors, max_norm: float, *, out=None, workspace=None, dev_er
     _call(dev, "pstat_clip_grad_norm", _lib.pstat_clip_grad_norm,
           at, n, float(max_norm), _ptr(norm), _ptr(workspace), workspace.numel(),
           _ptr(dev_error), _stream(dev))
+    _written(*outs)
     return norm, outs
 
 
