@@ -1058,8 +1058,23 @@ def lmhead_policy_stats(hidden, W, labels, ignore_index: int = -100):
     return LmheadPolicyStats.apply(hidden, W, labels, ignore_index)
 
 
+class _FilteredGradient(torch.autograd.Function):
+    """filtered_backward as a function of the logits and the logprob's gradient,
+    whose own derivative does not exist here: where a graph of it is asked for,
+    differentiating that raises, in place of taking it for a constant."""
+
+    @staticmethod
+    def forward(ctx, grad_lp, logits, labels, rs, tau, index, temperature, ignore_index):
+        return filtered_backward(logits, labels, grad_lp.float().contiguous(), rs, tau, index,
+                                 temperature, ignore_index)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("filtered_policy_stats has no second derivative")
+
+
 class FilteredPolicyStats(torch.autograd.Function):
-    """logprob (differentiable) and entropy (a no-grad metric) of every row
+    """logprob (differentiable, once) and entropy (a no-grad metric) of every row
     under its tempered, truncated softmax; the kept set is held fixed."""
 
     @staticmethod
@@ -1076,8 +1091,8 @@ class FilteredPolicyStats(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad_lp, grad_ent):
         logits, labels, rs, tau, index, row_t = ctx.saved_tensors
-        g = filtered_backward(logits, labels, grad_lp.float().contiguous(), rs, tau, index,
-                              ctx.temperature if row_t is None else row_t, ctx.ignore_index)
+        g = _FilteredGradient.apply(grad_lp, logits, labels, rs, tau, index,
+                                    ctx.temperature if row_t is None else row_t, ctx.ignore_index)
         return g, None, None, None, None, None, None
 
 
