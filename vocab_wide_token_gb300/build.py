@@ -4,7 +4,9 @@ Every ``csrc/*.cu`` file is compiled in parallel to an object under
 ``_build/`` and linked into ``vocab_wide_token_gb300/libpstat.so``.  Only one
 architecture is emitted: ``-gencode arch=compute_103a,code=sm_103a``.  Next to
 it, ``csrc/binding.cpp`` becomes ``_binding.so``, a CPython module that marshals
-the arguments of the hot calls (host code, over torch's headers).
+the arguments of the hot calls (host code, over torch's headers).  Where that
+module cannot be compiled a warning says so, and every call takes its path in
+Python.
 """
 from __future__ import annotations
 
@@ -14,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -88,7 +91,15 @@ def build(verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(12, len(sources) + 1)) as ex:
         binding = ex.submit(_build_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose), sources))
-        binding.result()
+        try:
+            binding.result()
+        except (RuntimeError, OSError, ImportError) as e:
+            # pstat.py serves every call without it; one of an earlier build may
+            # not fit this library or this torch
+            if os.path.exists(BINDING):
+                os.remove(BINDING)
+            warnings.warn(f"_binding.so is not built, calls are marshalled in Python: {e}",
+                          RuntimeWarning, stacklevel=2)
     tmp = LIB + f".tmp{os.getpid()}"
     cuda_lib = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "lib64")
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs,
