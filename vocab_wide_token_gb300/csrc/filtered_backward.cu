@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kFgThreads)
     const float ngK = -g * K;
     const float fill = mode == 1 ? NAN : 0.f;
     // Column y is kept, so its gradient is g (1 - p_y), as -g expm1(ln p_y): near
-    // p_y = 1 the difference itself would be lost.
+    // p_y = 1 the difference itself would be lost (ln S keeps the precision of S - 1).
     auto gradient = [&](float z, int64_t col) {
         if (col == y) return -g * expm1f((z - M) / temp - rs.y);
         const bool kept = z > tau || (z == tau && col <= last);

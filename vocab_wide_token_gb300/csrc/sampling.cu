@@ -733,7 +733,8 @@ __global__ void __launch_bounds__(kFinThreads, (kFiltered ? 1024 : 1536) / kFinT
     const E* gm = static_cast<const E*>(a.group_max) + t * a.chunks * 32;
     if (rs.greedy) return finish_greedy<E, kFinThreads>(a, t, row, gm, M, sm);
     if (!kFiltered || (!rs.cut_k && !rs.cut_p && !rs.cut_m)) {
-        const float lnS = logf(Sf);
+        const float lnS = unfiltered_log<E, kFinThreads>(row, rec, a.chunks, V, M, Sf, r.c.ch,
+                                                         reinterpret_cast<float*>(sm.scratch));
         if (kSample) {
             __syncthreads();  // the histogram's zeros share memory with the prefix sums
             return finish_draw<E, kFinThreads>(a, t, row, rec, M, r.c.ch, rs, lnS, sm);

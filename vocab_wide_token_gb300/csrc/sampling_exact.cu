@@ -693,7 +693,10 @@ struct Team {
         // Without filters ln S is the finish kernel's, so that its bits do not hang
         // on which of the two decided the row.
         const bool cut = rs.cut_k || rs.cut_p || rs.cut_m;
-        const float lnS = cut ? fixed_log(S, k) : logf(Sf);
+        const float lnS = cut ? fixed_log(S, k)
+                              : unfiltered_log<E, kExThreads>(row, a.records + t * a.chunks, a.chunks, V,
+                                                              M, Sf, c.ch,
+                                                              reinterpret_cast<float*>(sm.scratch));
         if (!kSample) {
             if (threadIdx.x == 0) {
                 const float U = (float)(long long)ux * 5.6843419e-14f;  // 2^-44
