@@ -385,8 +385,9 @@ PSTAT_API int pstat_lmhead_backward(const void* hidden, const void* W, int64_t T
  * The kept set is the shortest of the three.  Its last token is the cut
  * (tau, i): v is kept when z_v > tau, or z_v == tau and v <= i.  With no
  * filter the cut is (-inf, V - 1).
- * Which tokens are kept and drawn is decided as in exact arithmetic (fixed-
- * point weights of about 46 bits, integer sums), ties by the lowest index.
+ * Which tokens are kept and drawn is decided by fixed-point weights, each within
+ * 2^-45 + 2^-44.5 |x_v| of its e_v (relative), and exact integer sums of them;
+ * ties by the lowest index.
  * The results of a row depend on its own values and settings only: they are
  * bit-identical in any batch.
  * A row with a NaN or +inf logit, or without a finite one, has no
