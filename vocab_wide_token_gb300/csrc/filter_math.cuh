@@ -98,13 +98,13 @@ __device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ uint64_t f2_neg(uint64_t v) { return v ^ 0x8000000080000000ull; }
 
-// round(2^k e^((z - M)/t)) of two logits, k <= 60; 0 where that is far below 1.  With y = (M - z) log2(e)/t in double-float
-// arithmetic, write y = j/64 + r, |r| <= 2^-7 (plus the low part); then 2^-y =
-// 2^-(j/64) 2^-r: the first factor from the table and a power of two, the
-// second from e^-s = 1 - s + s^2/2 - s^3/6 + s^4/24 - s^5/120, s = r ln 2 <=
-// 2^-7.5, whose next term s^6/720 is below 2^-54.  The first two terms are
-// carried in double-float, the others (below 2^-24) in fp32.  z = M gives 2^k
-// exactly.  (A table-driven exponential, as in Tang, ACM TOMS 15, 1989.)
+// round(2^k e^((z - M)/t)) of two logits, k <= 60; 0 where that is far below 1.
+// With y = (M - z) log2(e)/t in double-float arithmetic, write y = j/64 + r, |r| <=
+// 2^-7 (plus the low part); then 2^-y = 2^-(j/64) 2^-r: the first factor from the
+// table and a power of two, the second from e^-s = 1 - s + s^2/2 - s^3/6 + s^4/24 -
+// s^5/120, s = r ln 2 <= 2^-7.5, whose next term s^6/720 is below 2^-54.  The first
+// two terms are carried in double-float, the others (below 2^-24) in fp32.  z = M
+// gives 2^k exactly.  (A table-driven exponential, as in Tang, ACM TOMS 15, 1989.)
 // Before the rounding to whole numbers the relative error is at most 2^-45 (the terms
 // in fp32 and the low word's roundings) + 2^-44.5 |x|: y is off by 10.5 x 2^-48 of itself,
 // from the scale's low part and from four roundings of its own.  Measured, at

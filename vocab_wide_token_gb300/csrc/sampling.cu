@@ -216,8 +216,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 // Of up to 256 candidates every thread finds the rank and the mass before its own
 // by comparing with all others: for the usual 50 to 100 that is a few hundred
 // cycles, where a sort by a block needs 28 steps.  More are sorted.
-// Bound by latency (records, maxima, columns, ranks, each behind the last): 7 us for
-// one row of V = 151,936 with top-k 50, 30 us for 2048 rows with a nucleus.
+// Bound by latency (records, maxima, columns, ranks, each behind the last): 7 us of a
+// call's 11 for one row of V = 151,936 with top-k 50, 30 us for 2048 rows with a nucleus.
 // ---------------------------------------------------------------------------
 // Bins of M - z: 48 binary orders of e in steps of 1/16, then 510 in steps of 2 (at
 // temperature 0.25 the 50th largest of 151,936 logits can be 2^-70 of the first:

@@ -419,7 +419,7 @@ __device__ __noinline__ Selected list_select(ListShared<kThreads>& ls,
         }
     }
     __syncthreads();
-    // Two (four, in a CTA of 512) neighbouring lanes share a member.
+    // Neighbouring lanes (four, in the exact kernel's CTA of 512) share a member.
     constexpr int kParts = kThreads / kListMembers;
     const int m = min((int)ls.n_member, kListMembers);
     const int item = (int)threadIdx.x / kParts;

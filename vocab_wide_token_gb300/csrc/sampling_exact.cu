@@ -34,14 +34,14 @@ constexpr int kMaxSpans = (int)(kFilterMaxV / kSpan);
 constexpr int kSpansPer = kMaxSpans / kExThreads;
 // One CTA per SM: with two the CTAs of a few rows crowd on half of the SMs, and
 // the registers do not suffice for the weights (8 flat rows of V = 151,936 with
-// top_p = 0.9: 61 us, with one 46).  Ten CTAs a team, as two such teams fill the 20
+// top_p = 0.9: 61 us a call, with one 43).  Ten CTAs a team, as two such teams fill the 20
 // SMs of a processing cluster, where two of eight leave four idle (16 clusters of
 // ten or thirty of five are resident, 14 of eight).
 constexpr int kMaxTeam = 10;
 // With kAlone rows or more for every cluster the CTAs take rows alone: what a
 // team saves in a pass it loses again in synchronisation.  Flat rows of
-// V = 151,936 with top_p = 0.9, all by teams or all alone: 12 rows 46 / 150 us,
-// 32 rows 148 / 148.
+// V = 151,936 with top_p = 0.9, a call with all by teams or all alone: 12 rows 44 /
+// 150 us, 32 rows 148 / 148.
 constexpr int kAlone = 2;
 static_assert(kBins % kExThreads == 0 && kMaxSpans % kExThreads == 0 && kSpan <= kExThreads, "");
 

@@ -943,8 +943,8 @@ def _grad_call(words, workspace, dev):
 
 
 def grad_norm(tensors, *, out=None, workspace=None, dev_error=None) -> torch.Tensor:
-    """The L2 norm over all elements of a list of gradients (bf16 or fp32, any
-    mix of sizes), as a float32 scalar tensor on their device."""
+    """The L2 norm over all elements of a list of contiguous gradients (bf16 or
+    fp32, any mix of sizes), as a float32 scalar tensor on their device."""
     tensors = _held(tensors)
     if _native is not None and out is None and workspace is None:
         got = _native.grad_norm(tensors, dev_error)
@@ -963,8 +963,8 @@ def grad_norm(tensors, *, out=None, workspace=None, dev_error=None) -> torch.Ten
 
 
 def clip_grad_norm(tensors, max_norm: float, *, out=None, workspace=None, dev_error=None):
-    """Scales a list of gradients by min(1, max_norm / their global L2 norm),
-    in place or into the tensors of `out` (same shapes and dtypes).  Returns
+    """Scales a list of contiguous gradients by min(1, max_norm / their global L2
+    norm), in place or into the tensors of `out` (same shapes and dtypes).  Returns
     (the norm before scaling, a float32 scalar tensor; the list of the scaled
     tensors).  A norm that is not finite sets DEV_NONFINITE and scales nothing.
     Tensors that are written may not overlap (a tensor listed twice, say)."""
