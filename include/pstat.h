@@ -508,6 +508,71 @@ PSTAT_API int pstat_clip_grad_norm(const pstat_tensor* tensors, int64_t n_tensor
                                    int* dev_error, pstat_stream_t stream);
 
 /*
+ * An AdamW step over a list of tensors:
+ *   g' = f g,  f = min(1, max_norm / norm) (1 where norm is NULL)
+ *   m  = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2
+ *   p  = p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+ * in fp32, with m and v as products and sums that are each rounded once (no fused
+ * multiply-add).  A norm that is infinite or NaN sets PSTAT_DEV_NONFINITE, and
+ * nothing is changed.
+ *
+ * Moments of 32 bits are float[n].  Moments of 8 bits are uint8[n + ceil(n / 128)]:
+ * n codes, then one byte for each block of 128 of them, the exponent field E of the
+ * block's largest magnitude as an fp32 number.  With base = max(8 (E - d), 0), code c
+ * > 0 stands for the fp32 number whose bits are (c + base) << 20 (three bits of
+ * mantissa), 0 for zero; m has d = 14, codes to 126, NaN 127, and the sign in bit 7;
+ * v has d = 30, codes to 254 and NaN 255.  All zeros is a fresh state.
+ * What is held in fewer than 32 bits (8-bit moments, bf16 parameters) is rounded
+ * up with the probability of its distance from the number below, by a hash of
+ * (seed, place of the tensor in the list, element), where `random` is set: the
+ * same call gives the same bits.  Otherwise it is rounded to nearest (8-bit moments:
+ * halves away from zero); then an 8-bit v follows only gradients that move it by
+ * a sixteenth.  An 8-bit v above zero stays above zero.
+ *   param, exp_avg, exp_avg_sq  read and written; they may overlap nothing else of
+ *                   the call (PSTAT_ERR_PARAM).
+ *   lr_at, step_at, seed_at     device values that take the place of lr, step and
+ *                   seed where not NULL, so that a captured step can be replayed.
+ *                   step >= 1 (t above); one on the device is not checked.
+ */
+#define PSTAT_ADAMW_MAX_TENSORS ((int64_t)1 << 28)
+typedef struct {
+    void* param;
+    const void* grad;
+    void* exp_avg;
+    void* exp_avg_sq;
+    int64_t n;
+    int32_t param_dtype; /* PSTAT_F32 or PSTAT_BF16, each on its own */
+    int32_t grad_dtype;
+    int32_t bits; /* of the moments: 32 or 8 */
+    int32_t reserved;
+} pstat_adamw_tensor;
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay; /* lr, eps, wd >= 0; 0 <= beta < 1 */
+    int64_t step;
+    const float* lr_at;
+    const int64_t* step_at;
+    const int64_t* seed_at;
+    const float* norm; /* device, as pstat_grad_norm leaves it, or NULL */
+    uint64_t seed;
+    float max_norm; /* >= 0, used with norm */
+    int32_t random;
+} pstat_adamw_options;
+
+PSTAT_API int pstat_adamw_step(const pstat_adamw_tensor* tensors, int64_t n_tensors,
+                               const pstat_adamw_options* options, int* dev_error,
+                               pstat_stream_t stream);
+
+/* The values that 8-bit moments stand for, as float[n] each. */
+typedef struct {
+    const void* exp_avg;
+    const void* exp_avg_sq;
+    float* out_avg;
+    float* out_avg_sq;
+    int64_t n;
+} pstat_adamw_moment;
+PSTAT_API int pstat_adamw_moments(const pstat_adamw_moment* list, int64_t n, pstat_stream_t stream);
+
+/*
  * Self-test of the bounded waits.  Every kernel of this library waits on its
  * mbarriers for at most a fixed time (2 s); a wait that runs out sets
  * PSTAT_DEV_TIMEOUT in *dev_error and the kernel winds down instead of

@@ -38,6 +38,14 @@ class Filters(ctypes.Structure):
                 ("top_ks", _vp), ("top_ps", _vp), ("min_ps", _vp)]
 
 
+class AdamwOptions(ctypes.Structure):
+    """pstat_adamw_options of include/pstat.h."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", _i64),
+                ("lr_at", _vp), ("step_at", _vp), ("seed_at", _vp), ("norm", _vp),
+                ("seed", ctypes.c_uint64), ("max_norm", ctypes.c_float), ("random", _i32)]
+
+
 def declare_prototypes(lib: ctypes.CDLL) -> ctypes.CDLL:
     """Set the argument and result types of every entry point of
     include/pstat.h on a loaded copy of the library (ctypes would otherwise
@@ -99,6 +107,10 @@ def declare_prototypes(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.pstat_grad_norm.restype = _i32
     lib.pstat_clip_grad_norm.argtypes = [_vp, _i64, ctypes.c_float, _vp, _vp, _sz, _vp, _vp]
     lib.pstat_clip_grad_norm.restype = _i32
+    lib.pstat_adamw_step.argtypes = [_vp, _i64, _vp, _vp, _vp]
+    lib.pstat_adamw_step.restype = _i32
+    lib.pstat_adamw_moments.argtypes = [_vp, _i64, _vp]
+    lib.pstat_adamw_moments.restype = _i32
     lib.pstat_noalloc_scratch_bytes.argtypes = []
     lib.pstat_noalloc_scratch_bytes.restype = _sz
     lib.pstat_selftest_wait_timeout.argtypes = [ctypes.c_uint64, _vp, _vp]
@@ -983,6 +995,165 @@ def clip_grad_norm(tensors, max_norm: float, *, out=None, workspace=None, dev_er
           _ptr(dev_error), _stream(dev))
     _written(*outs)
     return norm, outs
+
+
+# ---- the optimiser's step ------------------------------------------------------------
+
+ADAMW_BLOCK = 128  # elements of an 8-bit moment that share an exponent (include/pstat.h)
+
+
+def adamw_state(param: torch.Tensor, bits: int = 32):
+    """Fresh moments (exp_avg, exp_avg_sq) of a parameter: float32 of its shape, or for
+    ``bits=8`` uint8 of n + ceil(n / 128), the codes of its n elements and an exponent
+    for each block of 128."""
+    if not param.is_cuda:
+        raise ValueError("param must be a CUDA tensor (no CPU path exists)")
+    if bits == 32:
+        return (torch.zeros(param.shape, dtype=torch.float32, device=param.device),
+                torch.zeros(param.shape, dtype=torch.float32, device=param.device))
+    if bits != 8:
+        raise ValueError("bits must be 32 or 8")
+    n = param.numel()
+    size = n + -(-n // ADAMW_BLOCK)
+    return (torch.zeros(size, dtype=torch.uint8, device=param.device),
+            torch.zeros(size, dtype=torch.uint8, device=param.device))
+
+
+def _one_device(tensors, name):
+    index = tensors[0].get_device()
+    if index < 0 or set(map(torch.Tensor.get_device, tensors)) != {index}:
+        raise ValueError(f"{name} must be on one CUDA device (no CPU path exists)")
+    if not all(map(torch.Tensor.is_contiguous, tensors)):
+        raise ValueError(f"{name} must be contiguous")
+    return tensors[0].device
+
+
+def _types(tensors, name):
+    dtypes = list(map(_dtype_of, tensors))
+    if dtypes.count(torch.bfloat16) + dtypes.count(torch.float32) != len(dtypes):
+        raise TypeError(f"{name} must be bfloat16 or float32")
+    return dtypes
+
+
+def _tensor_list(x):
+    return [x] if isinstance(x, torch.Tensor) else list(x)
+
+
+def _moment_bits(moments, sizes, name):
+    """32 or 8 for each moment, by its type; its size has to be its parameter's."""
+    bits = []
+    for x, n in zip(moments, sizes):
+        if x.dtype == torch.float32 and x.numel() == n:
+            bits.append(32)
+        elif x.dtype == torch.uint8 and x.numel() == n + -(-n // ADAMW_BLOCK):
+            bits.append(8)
+        else:
+            raise ValueError(f"{name} must be float32 with the parameter's {n} elements, or uint8 "
+                             f"with {n + -(-n // ADAMW_BLOCK)}, got {x.dtype} with {x.numel()}")
+    return bits
+
+
+def _scalar_at(x, dtype, dev, name):
+    """(address or None, number) of a setting that is a number or a scalar tensor."""
+    if isinstance(x, torch.Tensor):
+        if x.dtype != dtype or x.numel() != 1 or x.device != dev:
+            raise ValueError(f"{name} must be a number or a {dtype} tensor of one element on {dev}")
+        return x.data_ptr(), 0
+    return None, x
+
+
+def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999), eps=1e-8,
+               weight_decay=0.01, *, norm=None, max_norm=None, seed=None, dev_error=None):
+    """One AdamW step over a list of contiguous tensors, in place:
+
+        g' = g min(1, max_norm / norm)         (g without norm and max_norm)
+        m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2
+        p = p (1 - lr wd) - lr / (1 - b1^step) m / (sqrt(v) / sqrt(1 - b2^step) + eps)
+
+    Parameters and gradients are bf16 or float32 each; the moments come from
+    ``adamw_state``, of 32 or 8 bits, both alike.  `step` counts from 1.  `norm` is
+    ``grad_norm``'s scalar tensor: with it the gradients are clipped on the way, and
+    one that is not finite sets DEV_NONFINITE and changes nothing.  `step`, `lr` and
+    `seed` may be one-element tensors (int64, float32, int64) that a captured step
+    reads at each replay.
+
+    What is held in fewer than 32 bits is rounded to nearest; with a `seed`, up or
+    down with the probability of the distance, by a hash of seed, tensor and
+    element.  8-bit moments want one, another at each step: rounded to nearest,
+    exp_avg_sq follows only gradients that move it by a sixteenth.  Returns the
+    list of the parameters.
+    """
+    params, grads = _tensor_list(params), _tensor_list(grads)
+    ms, vs = _tensor_list(exp_avgs), _tensor_list(exp_avg_sqs)
+    n = len(params)
+    if n == 0 or len(grads) != n or len(ms) != n or len(vs) != n:
+        raise ValueError("params, grads, exp_avgs and exp_avg_sqs must be lists of one length, "
+                         "not empty")
+    dev = _one_device(params + grads + ms + vs, "params, grads, exp_avgs and exp_avg_sqs")
+    p_types, g_types = _types(params, "params"), _types(grads, "grads")
+    sizes = list(map(torch.Tensor.numel, params))
+    if list(map(torch.Tensor.size, grads)) != list(map(torch.Tensor.size, params)):
+        raise ValueError("grads must have the shapes of params")
+    bits = _moment_bits(ms, sizes, "exp_avgs")
+    if _moment_bits(vs, sizes, "exp_avg_sqs") != bits:
+        raise ValueError("exp_avgs and exp_avg_sqs must have the same types")
+    if (norm is None) != (max_norm is None):
+        raise ValueError("norm and max_norm go together")
+    if norm is not None:
+        norm = _tensor(norm, torch.float32, (), dev, "norm")
+    lr_at, lr = _scalar_at(lr, torch.float32, dev, "lr")
+    step_at, step = _scalar_at(step, torch.int64, dev, "step")
+    seed_at, number = _scalar_at(0 if seed is None else seed, torch.int64, dev, "seed")
+    dev_error = _error_flag(dev_error, dev)
+    o = AdamwOptions(float(lr), float(betas[0]), float(betas[1]), float(eps), float(weight_decay),
+                     int(step), lr_at, step_at, seed_at, _ptr(norm), int(number) & (1 << 64) - 1,
+                     0.0 if max_norm is None else float(max_norm), seed is not None)
+    words = [0] * (7 * n)
+    for k, tensors in enumerate((params, grads, ms, vs)):
+        words[k::7] = map(torch.Tensor.data_ptr, tensors)
+    words[4::7] = sizes
+    bf16 = torch.bfloat16
+    words[5::7] = [(BF16 if a is bf16 else F32) | (BF16 if b is bf16 else F32) << 32
+                   for a, b in zip(p_types, g_types)]
+    words[6::7] = bits
+    words = array.array("q", words)
+    _call(dev, "pstat_adamw_step", _lib.pstat_adamw_step,
+          words.buffer_info()[0], n, ctypes.byref(o), _ptr(dev_error), _stream(dev))
+    _written(*params, *ms, *vs)
+    return params
+
+
+def adamw_moments(exp_avgs, exp_avg_sqs, params, *, out=None):
+    """The values that 8-bit moments stand for: (exp_avg's, exp_avg_sq's), lists of
+    float32 tensors of the parameters' shapes.  `out` may supply the two lists."""
+    ms, vs, params = _tensor_list(exp_avgs), _tensor_list(exp_avg_sqs), _tensor_list(params)
+    n = len(params)
+    if n == 0 or len(ms) != n or len(vs) != n:
+        raise ValueError("exp_avgs, exp_avg_sqs and params must be lists of one length, not empty")
+    dev = _one_device(ms + vs, "exp_avgs and exp_avg_sqs")
+    sizes = list(map(torch.Tensor.numel, params))
+    if set(_moment_bits(ms, sizes, "exp_avgs") + _moment_bits(vs, sizes, "exp_avg_sqs")) != {8}:
+        raise ValueError("exp_avgs and exp_avg_sqs must be uint8 (8-bit moments)")
+    if out is None:
+        outs = [[torch.empty(p.shape, dtype=torch.float32, device=dev) for p in params]
+                for _ in range(2)]
+    else:
+        outs = [_tensor_list(out[0]), _tensor_list(out[1])]
+        for x in outs:
+            if len(x) != n:
+                raise ValueError("out must have a tensor for each parameter in either list")
+            for o, p in zip(x, params):
+                _tensor(o, torch.float32, p.shape, dev, "out")
+    words = [0] * (5 * n)
+    for k, tensors in enumerate((ms, vs, *outs)):
+        words[k::5] = map(torch.Tensor.data_ptr, tensors)
+    words[4::5] = sizes
+    words = array.array("q", words)
+    _call(dev, "pstat_adamw_moments", _lib.pstat_adamw_moments, words.buffer_info()[0], n,
+          _stream(dev))
+    if out is not None:
+        _written(*outs[0], *outs[1])
+    return outs[0], outs[1]
 
 
 def selftest_wait_timeout(device, limit_ns: int = 10_000_000) -> int:
