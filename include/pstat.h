@@ -93,7 +93,7 @@ enum {
 #define PSTAT_DEV_EMPTY_ROW 0x2 /* every logit of a row is -inf: softmax undefined */
 #define PSTAT_DEV_TIMEOUT 0x4   /* a bounded wait on an asynchronous copy gave up */
 #define PSTAT_DEV_RANGE 0x8     /* lm_head backward: a value exceeds the fp16 range (65504) */
-#define PSTAT_DEV_BAD_PARAM 0x10 /* a row's temperature, top_p, min_p or uniform is out of range */
+#define PSTAT_DEV_BAD_PARAM 0x10 /* a row's temperature, top_p, min_p, uniform or parent is out of range */
 #define PSTAT_DEV_NONFINITE 0x20 /* the gradient norm is infinite or NaN */
 
 #define PSTAT_MAX_SHARDS 64
@@ -571,6 +571,53 @@ typedef struct {
     int64_t n;
 } pstat_adamw_moment;
 PSTAT_API int pstat_adamw_moments(const pstat_adamw_moment* list, int64_t n, pstat_stream_t stream);
+
+/*
+ * Beam search: the best n continuations of each of B searches with `beams` beams.
+ * Beam k of search b has the row z = logits[b beams + k] and the score s = scores[b,
+ * k]; its continuation by token v scores s + z_v - M - ln S.  Of the beams x V
+ * continuations the n best, in descending order; equal ones by the lowest (k, v).
+ * Scores are compared as they are in exact arithmetic, to 2^-40 of the larger of
+ * |score| and 1; what comes out is within 6e-6 + 2^-24 |score| of the score.  A score of -inf, and a row whose logits are all -inf, is a
+ * beam without continuations; places that none is left for get score -inf, parent
+ * and token -1.  A score of NaN or +inf, or a row with a NaN or +inf logit (of a
+ * beam with a finite score), leaves its search undefined: PSTAT_DEV_EMPTY_ROW, scores
+ * NaN, parents and tokens -1.
+ *   logits      [B beams, ld] of dtype `dt`, V <= PSTAT_FILTER_MAX_V; ld 0: one row for
+ *               all beams.
+ *   scores      [B, beams] float.
+ *   n           at most PSTAT_BEAM_MAX_N; beams at most PSTAT_BEAM_MAX.
+ *   out_score   [B, n] float, out_parent (k) and out_token (v) [B, n] int64.
+ *   workspace   16-byte aligned, at least pstat_beam_workspace_size(...) bytes.
+ */
+#define PSTAT_BEAM_MAX 64
+#define PSTAT_BEAM_MAX_N 128
+PSTAT_API int pstat_beam_workspace_size(int64_t B, int64_t beams, int64_t V, pstat_dtype dt,
+                                        size_t* bytes);
+PSTAT_API int pstat_beam_select(const void* logits, pstat_dtype dt, int64_t B, int64_t beams,
+                                int64_t V, int64_t ld, const float* scores, int64_t n,
+                                float* out_score, int64_t* out_parent, int64_t* out_token,
+                                void* workspace, size_t ws_bytes, int* dev_error,
+                                pstat_stream_t stream);
+
+/*
+ * Reordering of the beams' states: row b out_beams + i of every output becomes row
+ * b beams + parents[b, i] of its input.  A row consists of `segments` runs of
+ * seg_bytes bytes; all strides are in bytes.  In place (out == data for all states,
+ * equal strides, beams == out_beams) rows of beams that are their own parent are not
+ * touched.  An output may overlap nothing else of the call but, in place, its own
+ * input (PSTAT_ERR_PARAM).  A parent of -1 leaves its row as it was, and so does one
+ * outside [0, beams), which sets PSTAT_DEV_BAD_PARAM.
+ */
+typedef struct {
+    const void* data;
+    void* out;
+    int64_t row_stride, out_row_stride;
+    int64_t segments, seg_stride, out_seg_stride, seg_bytes;
+} pstat_beam_state;
+PSTAT_API int pstat_beam_reorder(const pstat_beam_state* states, int64_t n_states,
+                                 const int64_t* parents, int64_t B, int64_t beams,
+                                 int64_t out_beams, int* dev_error, pstat_stream_t stream);
 
 /*
  * Self-test of the bounded waits.  Every kernel of this library waits on its

@@ -940,6 +940,17 @@ cudaError_t launch_filter(FilterArgs a, const DeviceInfo& dev, cudaStream_t stre
     return launch_exact<E, kSample>(a, some, dev, stream);
 }
 
+}  // namespace
+
+cudaError_t launch_row_records(FilterArgs a, pstat_dtype dt, const DeviceInfo& dev,
+                               cudaStream_t stream) {
+    a.stream_once = a.T * a.V * (dt == PSTAT_BF16 ? 2 : 4) > dev.l2_bytes / 2;
+    return dt == PSTAT_BF16 ? launch_records<uint16_t, false>(a, dev, stream)
+                            : launch_records<float, false>(a, dev, stream);
+}
+
+namespace {
+
 struct FilterWorkspace {
     size_t group_max, left_count, left, total;  // records first
 };

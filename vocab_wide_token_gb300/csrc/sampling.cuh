@@ -494,6 +494,11 @@ __device__ __forceinline__ uint64_t draw_of(float u, uint64_t S) {
     return part_of(u, S, rest);
 }
 
+// The records and group maxima of all rows, at the temperature of `a` (sampling.cu).
+// stream_once is set here.
+cudaError_t launch_row_records(FilterArgs a, pstat_dtype dt, const DeviceInfo& dev,
+                               cudaStream_t stream);
+
 // The rows that the finish kernel left, behind it on the stream; `filtered`: some
 // row may have a filter.
 template <typename E, bool kSample>

@@ -111,6 +111,13 @@ def declare_prototypes(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.pstat_adamw_step.restype = _i32
     lib.pstat_adamw_moments.argtypes = [_vp, _i64, _vp]
     lib.pstat_adamw_moments.restype = _i32
+    lib.pstat_beam_workspace_size.argtypes = [_i64, _i64, _i64, _i32, ctypes.POINTER(_sz)]
+    lib.pstat_beam_workspace_size.restype = _i32
+    lib.pstat_beam_select.argtypes = [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp,
+                                      _vp, _sz, _vp, _vp]
+    lib.pstat_beam_select.restype = _i32
+    lib.pstat_beam_reorder.argtypes = [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp]
+    lib.pstat_beam_reorder.restype = _i32
     lib.pstat_noalloc_scratch_bytes.argtypes = []
     lib.pstat_noalloc_scratch_bytes.restype = _sz
     lib.pstat_selftest_wait_timeout.argtypes = [ctypes.c_uint64, _vp, _vp]
@@ -1154,6 +1161,140 @@ def adamw_moments(exp_avgs, exp_avg_sqs, params, *, out=None):
     if out is not None:
         _written(*outs[0], *outs[1])
     return outs[0], outs[1]
+
+
+# ---- beam search ----------------------------------------------------------------------
+
+BEAM_MAX, BEAM_MAX_N = 64, 128
+
+
+def beam_workspace_size(B: int, beams: int, V: int, dtype: torch.dtype) -> int:
+    """Bytes of workspace of ``beam_select`` on B searches of `beams` rows of V logits."""
+    need = ctypes.c_size_t(0)
+    code = BF16 if dtype == torch.bfloat16 else F32
+    _check(_lib.pstat_beam_workspace_size(B, beams, V, code, ctypes.byref(need)),
+           "pstat_beam_workspace_size")
+    return int(need.value)
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int, *, out=None, workspace=None,
+                dev_error=None):
+    """The n best continuations of every search, over its beams and the vocabulary.
+
+    `scores` is float32 [B, beams], the sum of the log-probabilities of each beam so
+    far (-inf for one without continuations: all but one at the first step, say);
+    `logits` holds the beams' rows, [B * beams, V].  Continuation (k, v) scores
+    scores[b, k] + log softmax(row)[v].  Returns (score [B, n] f32, parent [B, n] int64:
+    k, token [B, n] int64: v), best first, equal ones by the lowest (k, v), and
+    (-inf, -1, -1) where no continuation is left.  Which ones they are is decided as in
+    exact arithmetic.  With n twice the beams, as many go on as there were beams even
+    when all others end.  `out` may supply the three tensors, `workspace` a uint8
+    CUDA tensor of at least ``beam_workspace_size`` bytes, which calls that overlap
+    on the GPU may not share.
+    """
+    T, V, ld = _rows(logits)
+    dev = logits.device
+    dt = _dtype_code(logits)
+    if not isinstance(scores, torch.Tensor) or scores.dim() != 2 or scores.numel() != T:
+        raise ValueError("scores must be [B, beams] with one for each row of logits")
+    B, beams = scores.shape
+    scores = _tensor(scores, torch.float32, (B, beams), dev, "scores")
+    n = int(n)
+    if not 1 <= n <= BEAM_MAX_N:
+        raise ValueError(f"n must be 1 to {BEAM_MAX_N}")
+    if out is None:
+        best = torch.empty(B, n, dtype=torch.float32, device=dev)
+        parent = torch.empty(B, n, dtype=torch.int64, device=dev)
+        token = torch.empty(B, n, dtype=torch.int64, device=dev)
+    else:
+        best = _tensor(out[0], torch.float32, (B, n), dev, "out[0] (score)")
+        parent = _tensor(out[1], torch.int64, (B, n), dev, "out[1] (parent)")
+        token = _tensor(out[2], torch.int64, (B, n), dev, "out[2] (token)")
+    dev_error = _error_flag(dev_error, dev)
+    workspace = _workspace(workspace, beam_workspace_size(B, beams, V, logits.dtype), dev)
+    _call(dev, "pstat_beam_select", _lib.pstat_beam_select,
+          _ptr(logits), dt, B, beams, V, ld, _ptr(scores), n, _ptr(best), _ptr(parent), _ptr(token),
+          _ptr(workspace), workspace.numel(), _ptr(dev_error), _stream(dev))
+    if out is not None:
+        _written(best, parent, token)
+    return best, parent, token
+
+
+def _runs(x: torch.Tensor, o: torch.Tensor):
+    """The rows x[i] and o[i] as evenly spaced runs of bytes: a list of (offset in x and
+    in o, segments, stride in x and in o, bytes of a run), more than one where the
+    runs of a row are not evenly spaced as a whole."""
+    size = x.element_size()
+    dims = [(n, a, b) for n, a, b in zip(x.shape[1:], x.stride()[1:], o.stride()[1:]) if n != 1]
+    run = 1
+    while dims and dims[-1][1] == run and dims[-1][2] == run:
+        run *= dims.pop()[0]
+    if not dims:
+        return [(0, 0, 1, run * size, run * size, run * size)]
+    segments, a, b = dims.pop()
+    while dims and dims[-1][1] == segments * a and dims[-1][2] == segments * b:
+        segments *= dims.pop()[0]
+    parts = [(0, 0)]
+    for n, oa, ob in dims:
+        if len(parts) * n > 1024:
+            raise ValueError("the rows of a state consist of too many runs that are not evenly "
+                             "spaced: make it contiguous")
+        parts = [(i + k * oa, j + k * ob) for i, j in parts for k in range(n)]
+    return [(i * size, j * size, segments, a * size, b * size, run * size) for i, j in parts]
+
+
+def beam_reorder(states, parents: torch.Tensor, *, out=None, dev_error=None):
+    """Lets the beams' states follow them: row b * beams' + i of every result is row b *
+    beams + parents[b, i] of the state, parents [B, beams'] int64 as ``beam_select``
+    returns them (or the chosen of them).
+
+    `states` is a list of strided tensors of any type with B * beams rows, such as views
+    of a cache (``cache[:, :, :length]``).  `out`
+    may supply the results; the states themselves, for as many beams as before,
+    are reordered in place, and rows of beams that stay are not touched.  A parent of
+    -1 leaves its row as it was.  Returns the list of the results.
+    """
+    states = _tensor_list(states)
+    if not states:
+        raise ValueError("states must not be empty")
+    index = states[0].get_device()
+    if index < 0 or set(map(torch.Tensor.get_device, states)) != {index}:
+        raise ValueError("states must be on one CUDA device (no CPU path exists)")
+    dev = states[0].device
+    if not isinstance(parents, torch.Tensor) or parents.dim() != 2:
+        raise ValueError("parents must be int64 [B, beams]")
+    B, out_beams = parents.shape
+    parents = _tensor(parents, torch.int64, (B, out_beams), dev, "parents")
+    rows = {x.shape[0] if x.dim() else -1 for x in states}
+    if len(rows) != 1 or B == 0 or min(rows) < 0 or min(rows) % B:
+        raise ValueError("states must have B * beams rows each")
+    beams = min(rows) // B
+    given = out is not None
+    outs = _tensor_list(out) if given else [
+        torch.empty((B * out_beams, *x.shape[1:]), dtype=x.dtype, device=dev) for x in states]
+    if len(outs) != len(states):
+        raise ValueError("out must have a tensor for each state")
+    words = []
+    for x, o in zip(states, outs):
+        if o is not x and (o.dtype != x.dtype or o.device != dev
+                           or tuple(o.shape) != (B * out_beams, *x.shape[1:])):
+            raise ValueError(f"out must have {x.dtype} tensors of {B * out_beams} such rows on {dev}")
+        if x.layout != torch.strided or x.is_conj() or x.is_neg() or o.is_conj() or o.is_neg():
+            raise ValueError("states must be plain strided tensors")
+        if x.numel() == 0 or o.numel() == 0:
+            continue
+        size = x.element_size()
+        for i, j, segments, a, b, seg_bytes in _runs(x, o):
+            words += [x.data_ptr() + i, o.data_ptr() + j, x.stride(0) * size, o.stride(0) * size,
+                      segments, a, b, seg_bytes]
+    words = array.array("q", words)
+    if len(words):
+        _call(dev, "pstat_beam_reorder", _lib.pstat_beam_reorder,
+              words.buffer_info()[0], len(words) // 8, _ptr(parents), B, beams, out_beams,
+              _ptr(_error_flag(dev_error, dev)), _stream(dev))
+    if given:
+        _written(*outs)
+    return outs
 
 
 def selftest_wait_timeout(device, limit_ns: int = 10_000_000) -> int:
