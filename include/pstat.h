@@ -94,7 +94,7 @@ enum {
 #define PSTAT_DEV_TIMEOUT 0x4   /* a bounded wait on an asynchronous copy gave up */
 #define PSTAT_DEV_RANGE 0x8     /* lm_head backward: a value exceeds the fp16 range (65504) */
 #define PSTAT_DEV_BAD_PARAM 0x10 /* a row's temperature, top_p, min_p, uniform or parent is out of range */
-#define PSTAT_DEV_NONFINITE 0x20 /* the gradient norm is infinite or NaN */
+#define PSTAT_DEV_NONFINITE 0x20 /* the gradient norm, or an element to be quantised, is infinite or NaN */
 
 #define PSTAT_MAX_SHARDS 64
 #define PSTAT_CHUNK_BF16 4096 /* chunk length in elements for bf16 logits */
@@ -571,6 +571,42 @@ typedef struct {
     int64_t n;
 } pstat_adamw_moment;
 PSTAT_API int pstat_adamw_moments(const pstat_adamw_moment* list, int64_t n, pstat_stream_t stream);
+
+/*
+ * Matrices in 8-bit floating point (e4m3: 4 bits of exponent, 3 of mantissa, largest
+ * 448, no infinity) with one scale for each run of 128 columns, of one row or
+ * of 128 rows.
+ *   scale = the least power of two s with max|x| <= 448 s over the block (at least
+ *           2^-126; 1 for a block of zeros),  q = x / s, rounded to nearest even.
+ * The division is exact, so q s is off by one rounding of 2^-4 relative.  A block
+ * with an infinity or NaN gets scale NaN and codes 0 (PSTAT_DEV_NONFINITE).
+ *   x        [T, ld] dtype `dt`, any alignment of its elements.
+ *   rows     rows that share a scale: 1 or 128.
+ *   out_q    [T, K] e4m3, rows of K bytes.
+ *   out_scale  float, that of row block i and column block j at
+ *            out_scale[i * scale_row + j * scale_col]; ceil(T / rows) by
+ *            ceil(K / 128).
+ */
+PSTAT_API int pstat_fp8_quantize(const void* x, pstat_dtype dt, int64_t T, int64_t K, int64_t ld,
+                                 int rows, void* out_q, float* out_scale, int64_t scale_row,
+                                 int64_t scale_col, int* dev_error, pstat_stream_t stream);
+
+/*
+ * Logits of an 8-bit head: out[t, v] = sum_j S[v / 128, j] s[t, j] (sum over column
+ * block j of q[t, k] W[v, k]).  The inner sums run on the tensor cores with fp32
+ * accumulators, the outer one in fp32, blocks in ascending order: a row's results
+ * depend on its own codes and scales only, they are bit-identical in any batch.
+ *   q        [T, K] e4m3 with scales s as pstat_fp8_quantize lays them out (rows 1);
+ *            scale_row 1 is the quick order.
+ *   W        [V, K] e4m3, W_scale [ceil(V / 128), ceil(K / 128)] row-major: any
+ *            scales, powers of two or not.
+ *   q and W 16-byte aligned, K a multiple of 16.
+ *   out      [T, ld_out] of out_dt.
+ */
+PSTAT_API int pstat_fp8_logits(const void* q, const float* q_scale, int64_t scale_row,
+                               int64_t scale_col, const void* W, const float* W_scale, int64_t T,
+                               int64_t V, int64_t K, void* out, pstat_dtype out_dt, int64_t ld_out,
+                               int* dev_error, pstat_stream_t stream);
 
 /*
  * Beam search: the best n continuations of each of B searches with `beams` beams.

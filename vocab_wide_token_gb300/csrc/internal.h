@@ -97,6 +97,11 @@ cudaError_t launch_behind(void (*kernel)(P...), unsigned grid, unsigned block, s
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Row-major matrix [rows, cols] of 1-byte elements (row pitch in bytes, a multiple of
+// 16) -> tensor map (a CUtensorMap) with boxes of [box_rows, 128] in the 128-byte swizzle;
+// elements outside read as 0 (lmhead.cu).
+bool make_byte_map(void* map, const void* ptr, int64_t rows, int64_t cols, int64_t pitch, int box_rows);
+
 // Kernel launchers (stats_kernels.cu).  They assume validated arguments.
 cudaError_t launch_chunk_stats(const void* logits, pstat_dtype dt, int64_t T, int64_t ld,
                                const ShardPlan& plan, float4* chunk_stats, int* dev_error,

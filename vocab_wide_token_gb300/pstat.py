@@ -111,6 +111,12 @@ def declare_prototypes(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.pstat_adamw_step.restype = _i32
     lib.pstat_adamw_moments.argtypes = [_vp, _i64, _vp]
     lib.pstat_adamw_moments.restype = _i32
+    lib.pstat_fp8_quantize.argtypes = [_vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _i64, _i64, _vp,
+                                       _vp]
+    lib.pstat_fp8_quantize.restype = _i32
+    lib.pstat_fp8_logits.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i32,
+                                     _i64, _vp, _vp]
+    lib.pstat_fp8_logits.restype = _i32
     lib.pstat_beam_workspace_size.argtypes = [_i64, _i64, _i64, _i32, ctypes.POINTER(_sz)]
     lib.pstat_beam_workspace_size.restype = _i32
     lib.pstat_beam_select.argtypes = [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp,
@@ -1161,6 +1167,84 @@ def adamw_moments(exp_avgs, exp_avg_sqs, params, *, out=None):
     if out is not None:
         _written(*outs[0], *outs[1])
     return outs[0], outs[1]
+
+
+# ---- the head in 8 bits -----------------------------------------------------------------
+
+FP8_BLOCK = 128  # columns (and rows of a weight) that share a scale
+
+
+def fp8_quantize(x: torch.Tensor, rows: int = 1, *, out=None, dev_error=None):
+    """A matrix [T, K] (bf16 or float32, rows contiguous) in 8-bit floating point with a scale
+    for each run of 128 columns of one row (``rows=1``, activations) or of 128 rows (``rows=128``,
+    a weight).
+
+    A scale is the least power of two that brings the block's largest magnitude to 448
+    or less, and the codes are x / scale rounded to nearest even.  Returns (codes
+    float8_e4m3fn [T, K], scales float32 [ceil(T / rows), ceil(K / 128)]; those of single
+    rows lie column by column, as ``fp8_logits`` reads them).  A block with an
+    infinity or NaN gets scale NaN and sets DEV_NONFINITE.  `out` may supply the two.
+    """
+    T, K, ld = _rows(x)
+    dev = x.device
+    dt = _dtype_code(x)
+    if rows not in (1, FP8_BLOCK):
+        raise ValueError(f"rows must be 1 or {FP8_BLOCK}")
+    shape = (-(-T // rows), -(-K // FP8_BLOCK))
+    if out is None:
+        q = torch.empty(T, K, dtype=torch.float8_e4m3fn, device=dev)
+        scale = (torch.empty(shape, dtype=torch.float32, device=dev) if rows != 1 else
+                 torch.empty(shape[::-1], dtype=torch.float32, device=dev).t())
+    else:
+        q = _tensor(out[0], torch.float8_e4m3fn, (T, K), dev, "out[0] (codes)")
+        scale = out[1]
+        if (not isinstance(scale, torch.Tensor) or scale.dtype != torch.float32
+                or tuple(scale.shape) != shape or scale.device != dev
+                or not (scale.is_contiguous() or scale.t().is_contiguous())):
+            raise ValueError(f"out[1] (scales) must be a float32 tensor of shape {shape} on {dev}, "
+                             "contiguous by rows or by columns")
+    dev_error = _error_flag(dev_error, dev)
+    _call(dev, "pstat_fp8_quantize", _lib.pstat_fp8_quantize,
+          _ptr(x), dt, T, K, ld, rows, _ptr(q), _ptr(scale), scale.stride(0), scale.stride(1),
+          _ptr(dev_error), _stream(dev))
+    if out is not None:
+        _written(q, scale)
+    return q, scale
+
+
+def fp8_logits(q: torch.Tensor, q_scale: torch.Tensor, W: torch.Tensor, W_scale: torch.Tensor,
+               out_dtype: torch.dtype = torch.bfloat16, *, out=None, dev_error=None):
+    """The logits [T, V] of an 8-bit head: hidden states as ``fp8_quantize(hidden)`` gives
+    them times the rows of a weight W [V, K] with scales [ceil(V / 128), ceil(K / 128)], as
+    ``fp8_quantize(W, 128)`` gives them or with any others.  K is a multiple of 16.  A
+    row's logits are the same bits in any batch.  `out` may supply the result (bf16 or
+    float32, rows contiguous)."""
+    for x, name in ((q, "q"), (W, "W")):
+        if (not isinstance(x, torch.Tensor) or x.dtype != torch.float8_e4m3fn or x.dim() != 2
+                or not x.is_cuda or not x.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous float8_e4m3fn CUDA matrix")
+    (T, K), V, dev = q.shape, W.shape[0], q.device
+    if W.shape[1] != K or W.device != dev:
+        raise ValueError("W must have q's columns and device")
+    blocks = -(-K // FP8_BLOCK)
+    if (not isinstance(q_scale, torch.Tensor) or q_scale.dtype != torch.float32
+            or tuple(q_scale.shape) != (T, blocks) or q_scale.device != dev):
+        raise ValueError(f"q_scale must be a float32 tensor of shape {(T, blocks)} on {dev}")
+    W_scale = _tensor(W_scale, torch.float32, (-(-V // FP8_BLOCK), blocks), dev, "W_scale")
+    if out is None:
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError("out_dtype must be bfloat16 or float32")
+        got = torch.empty(T, V, dtype=out_dtype, device=dev)
+    else:
+        got = out
+    ld_out = _matrix_output(got, T, V, dev, "out")
+    dev_error = _error_flag(dev_error, dev)
+    _call(dev, "pstat_fp8_logits", _lib.pstat_fp8_logits,
+          _ptr(q), _ptr(q_scale), q_scale.stride(0), q_scale.stride(1), _ptr(W), _ptr(W_scale), T, V,
+          K, _ptr(got), _dtype_code(got), ld_out, _ptr(dev_error), _stream(dev))
+    if out is not None:
+        _written(got)
+    return got
 
 
 # ---- beam search ----------------------------------------------------------------------
