@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -145,26 +146,36 @@ __global__ void __launch_bounds__(kQuThreads)
 
 // ---------------------------------------------------------------------------
 // Logits.  out[t, v] = sum_j f_j sum_k q[t, k] W[v, k], f_j = S[v / 128, j] s[t, j], j the blocks
-// of 128 columns k.  128 rows of W are the tensor cores' M, tokens their N, so that few
-// tokens cost few columns, a head's row block has one scale, and lanes, which hold rows
-// of W, write neighbouring logits.  Each block's product goes to a tensor-memory
-// accumulator of its own, from where the epilogue adds it, times its scales, to sums in
-// registers; blocks in ascending order and one CTA to a tile, so that a logit's bits
-// depend on its row alone and not on the tile that it falls in.
+// of 128 columns k.  Each block's product goes to a tensor-memory accumulator of its own,
+// from where the epilogue adds it, times its scales, to sums in registers; blocks in
+// ascending order and one CTA to a tile, so that a logit's bits depend on its row alone
+// and not on the tile that it falls in.
 //   warp 0    copies tiles of W and q into a ring of stages (TMA, 128-byte swizzle)
-//   warp 1    issues tcgen05.mma (M 128, N up to 256, K 32), four to a block
-//   warps 2.. a thread adds up one row of W for a part of the tokens
+//   warp 1    issues tcgen05.mma (M 128, K 32), four to a block
+//   warps 2.. a thread adds up one lane of the accumulator for up to 64 columns
+// Two shapes of tile:
+//   up to 128 tokens  128 rows of W are M, the tokens N (16, 32, 64 or 128): few tokens cost
+//              few columns.  Bound by the one pass over W.
+//   beyond     128 tokens are M, 256 rows of W N.  A thread's factor is one number to a
+//              block, where with tokens as columns it is one for each column, read
+//              from shared memory.  Bound by the tensor cores and the epilogue that
+//              keeps up with them: 128 x 256 sums every 512 cycles.
+// The epilogue's loads from tensor memory take their time whatever their size, so many
+// warps with few columns each take turns: with 8 warps of 128 columns 2048 x 40,000
+// logits ran at a tenth of the tensor cores' rate.
 // All waits are bounded; on a timeout the CTA drains what is in flight and ends.
 // ---------------------------------------------------------------------------
 constexpr uint64_t kF8WaitNs = 2000000000ull;
-constexpr int kF8Rows = 128;  // of W in a tile
+constexpr int kF8M = 128;
 
 template <int kN>
 struct F8Tile {
-    static constexpr int kEpiWarps = kN >= 128 ? 8 : 4;
-    static constexpr int kCols = kN / (kEpiWarps / 4);  // of a warp
-    static constexpr int kThreads = 64 + 32 * kEpiWarps;
-    static constexpr uint32_t kABytes = kF8Rows * kF8Block;
+    static constexpr bool kTokenLanes = kN == 256;
+    static constexpr int kCols = kTokenLanes ? 64 : kN < 32 ? kN : 32;  // of an epilogue warp
+    static constexpr int kEpiWarps = 4 * (kN / kCols);
+    static constexpr int kFirstEpi = kTokenLanes ? 4 : 2;  // a warpgroup, for setmaxnreg
+    static constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
+    static constexpr uint32_t kABytes = kF8M * kF8Block;
     static constexpr uint32_t kBBytes = kN * kF8Block;
     static constexpr int kStages = kN == 256 ? 4 : kN == 128 ? 6 : kN == 64 ? 8 : kN == 32 ? 10 : 11;
     static constexpr int kBufs = kN == 256 ? 2 : 4;  // accumulators
@@ -172,7 +183,7 @@ struct F8Tile {
     static constexpr uint32_t kA = 0;
     static constexpr uint32_t kB = kA + kStages * kABytes;
     static constexpr uint32_t kScale = kB + kStages * kBBytes;  // [warps][2][kCols] floats
-    static constexpr uint32_t kBars = kScale + kEpiWarps * 2 * kCols * 4;
+    static constexpr uint32_t kBars = kScale + (kTokenLanes ? 0 : kEpiWarps * 2 * kCols * 4);
     static constexpr uint32_t kNumBars = 2 * kStages + 2 * kBufs + 1;
     static constexpr uint32_t kSlot = kBars + kNumBars * 8;
     static constexpr uint32_t kBytes = kSlot + 16 + 1024;  // + alignment slack
@@ -180,18 +191,57 @@ struct F8Tile {
 };
 
 struct F8Args {
-    CUtensorMap W, q;
+    CUtensorMap lanes, columns;  // the operands that are M and N
     const float* W_scale;
     const float* q_scale;
     int64_t scale_row, scale_col;
-    int64_t T, V, ld_out;
+    int64_t ld_out;
     void* out;
-    int blocks;      // of columns
-    int tokens;      // of a tile: its N, a multiple of 16 for each epilogue warp
-    int t_tiles;
-    int64_t tiles;
+    int T, V;
+    int blocks;      // of 128 along K
+    int row_blocks;  // of W_scale
+    int t_tiles;     // tiles along the tokens, the quick index
+    uint32_t tiles;
+    bool vector;     // rows of logits start on 16 bytes
     int* dev_error;
 };
+
+// Registers of the wide tile's threads: launched with kLaunchRegs each, the first warpgroup
+// keeps few and the epilogue takes more, its 64 sums, two loads in flight and the rest.
+constexpr int kLaunchRegs = 96, kRoleRegs = 24, kEpiRegs = 112;
+static_assert(128 * kRoleRegs + 512 * kEpiRegs <= 640 * kLaunchRegs, "the split fits what was launched");
+
+template <typename O>
+__device__ __forceinline__ void put(O* out, float x) {
+    if constexpr (sizeof(O) == 4)
+        *out = x;
+    else
+        *out = (uint16_t)(bf2_pack_rn(x, 0.f) & 0xFFFFu);
+}
+
+// One row on; opaque, so that the addresses of all rows are not formed at once, at two
+// registers each.
+template <typename O>
+__device__ __forceinline__ O* next_row(O* at, int64_t ld) {
+    return after_wait(at + ld);
+}
+
+// 16 registers of 32 lanes: in either half of the lanes, the 16 x 16 values lane by register
+// turned to register by lane.
+__device__ __forceinline__ void transpose16(float (&x)[16], int lane) {
+#pragma unroll
+    for (int d = 8; d; d /= 2)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (i & d) continue;
+            const bool high = (lane & d) != 0;
+            const float got = __shfl_xor_sync(0xFFFFFFFFu, high ? x[i] : x[i + d], d);
+            if (high)
+                x[i] = got;
+            else
+                x[i + d] = got;
+        }
+}
 
 template <int kN, typename O>
 __global__ void __launch_bounds__(F8Tile<kN>::kThreads, 1)
@@ -218,8 +268,8 @@ __global__ void __launch_bounds__(F8Tile<kN>::kThreads, 1)
         }
         mbar_init(drain, 1);
         fence_mbar_init();
-        prefetch_tensormap(&a.W);
-        prefetch_tensormap(&a.q);
+        prefetch_tensormap(&a.lanes);
+        prefetch_tensormap(&a.columns);
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, C::kTmemCols);
@@ -232,23 +282,27 @@ __global__ void __launch_bounds__(F8Tile<kN>::kThreads, 1)
     bool failed = false;
     grid_wait();
 
+    if (warp < C::kFirstEpi) {
+    if (C::kTokenLanes) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
     if (warp == 0) {
         if (lane == 0) {
             const uint64_t pol_w = a.t_tiles == 1 ? policy_evict_first() : policy_evict_normal();
             const uint64_t pol_q = policy_evict_last();
-            const uint32_t bytes = C::kABytes + (uint32_t)a.tokens * kF8Block;
             uint32_t it = 0;
-            for (int64_t u = blockIdx.x; u < a.tiles && !failed; u += gridDim.x) {
-                const int v0 = (int)(u / a.t_tiles) * kF8Rows, t0 = (int)(u % a.t_tiles) * a.tokens;
+            for (uint32_t u = blockIdx.x; u < a.tiles && !failed; u += gridDim.x) {
+                const int tt = (int)(u % (uint32_t)a.t_tiles), vt = (int)(u / (uint32_t)a.t_tiles);
+                const int m0 = (C::kTokenLanes ? tt : vt) * kF8M, n0 = (C::kTokenLanes ? vt : tt) * kN;
                 for (int j = 0; j < a.blocks; ++j, ++it) {
                     const int s = it % C::kStages;
                     if (!mbar_wait_bounded(&empty[s], ((it / C::kStages) & 1u) ^ 1u, kF8WaitNs)) {
                         failed = true;
                         break;
                     }
-                    mbar_arrive_expect_tx(&full[s], bytes);
-                    tma_load_2d(smem + C::kA + s * C::kABytes, &a.W, j * kF8Block, v0, &full[s], pol_w);
-                    tma_load_2d(smem + C::kB + s * C::kBBytes, &a.q, j * kF8Block, t0, &full[s], pol_q);
+                    mbar_arrive_expect_tx(&full[s], C::kABytes + C::kBBytes);
+                    tma_load_2d(smem + C::kA + s * C::kABytes, &a.lanes, j * kF8Block, m0, &full[s],
+                                C::kTokenLanes ? pol_q : pol_w);
+                    tma_load_2d(smem + C::kB + s * C::kBBytes, &a.columns, j * kF8Block, n0, &full[s],
+                                C::kTokenLanes ? pol_w : pol_q);
                 }
             }
             // every copy has landed before the CTA ends
@@ -259,9 +313,9 @@ __global__ void __launch_bounds__(F8Tile<kN>::kThreads, 1)
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            const uint32_t idesc = idesc_e4m3_f32(kF8Rows, a.tokens);
+            constexpr uint32_t idesc = idesc_e4m3_f32(kF8M, kN);
             uint32_t it = 0;
-            for (int64_t u = blockIdx.x; u < a.tiles && !failed; u += gridDim.x) {
+            for (uint32_t u = blockIdx.x; u < a.tiles && !failed; u += gridDim.x) {
                 for (int j = 0; j < a.blocks; ++j, ++it) {
                     const uint32_t b = it % C::kBufs;
                     const int s = it % C::kStages;
@@ -284,89 +338,141 @@ __global__ void __launch_bounds__(F8Tile<kN>::kThreads, 1)
             umma_commit(drain);
             if (!mbar_wait_bounded(drain, 0, kF8WaitNs)) failed = true;
         }
+    }
     } else {
-        constexpr int kMine = (C::kCols + 31) / 32;  // scales of a lane
-        const int e = warp - 2, quarter = warp & 3, part = e / 4;
-        const int cols = a.tokens / (C::kEpiWarps / 4);  // of this warp, a multiple of 16
-        const int c0 = part * cols;
+        if (C::kTokenLanes) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+        constexpr int kCols = C::kCols;
+        const int e = warp - C::kFirstEpi, quarter = warp & 3, part = e / 4;
+        const int c0 = part * kCols;
         const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
-        float* scales = reinterpret_cast<float*>(smem + C::kScale) + e * 2 * C::kCols;
+        float* scales = reinterpret_cast<float*>(smem + C::kScale) + e * 2 * kCols;
         const float* W_scale = after_wait(a.W_scale);
         const float* q_scale = after_wait(a.q_scale);
+        // After a timeout no wait is made and nothing is written, but the sums run to their
+        // end: a way out of their loop would cost every sum a register of its own.
+        auto wait_full = [&](uint32_t i) {
+            if (!failed) {
+                const bool ok = mbar_wait_bounded(&tfull[i % C::kBufs], (i / C::kBufs) & 1u, kF8WaitNs);
+                failed = !__all_sync(0xFFFFFFFFu, ok);
+            }
+            tc_fence_after_sync();
+        };
         uint32_t it = 0;
-        for (int64_t u = blockIdx.x; u < a.tiles && !failed; u += gridDim.x) {
-            const int64_t vb = u / a.t_tiles, t0 = u % a.t_tiles * a.tokens + c0;
-            float next[kMine], next_w = W_scale[vb * a.blocks];
-            auto fetch = [&](int j) {
+        for (uint32_t u = blockIdx.x; u < a.tiles && !failed; u += gridDim.x) {
+            const int tt = (int)(u % (uint32_t)a.t_tiles), vt = (int)(u / (uint32_t)a.t_tiles);
+            // tokens: of this lane, or of this warp's columns (a lane fetches one column's)
+            const int t = C::kTokenLanes ? tt * kF8M + quarter * 32 + lane : tt * kN + c0 + lane;
+            const int v = C::kTokenLanes ? vt * kN + c0 : vt * kF8M + quarter * 32 + lane;
+            const bool mine = t < a.T && (C::kTokenLanes || lane < kCols);
+            const float* qs = q_scale + (mine ? t * a.scale_row : 0);
+            const int vb = C::kTokenLanes ? min(v / kF8Block, a.row_blocks - 1) : vt;
+            const float* ws = W_scale + (int64_t)vb * a.blocks;
+            float next = (mine ? qs[0] : 0.f), next_w = ws[0];
+            uint64_t acc[kCols / 2];
 #pragma unroll
-                for (int i = 0; i < kMine; ++i) {
-                    const int64_t t = t0 + lane + 32 * i;
-                    next[i] = lane + 32 * i < cols && t < a.T ? q_scale[t * a.scale_row + j * a.scale_col] : 0.f;
-                }
-                next_w = W_scale[vb * a.blocks + j];
-            };
-            fetch(0);
-            uint64_t acc[C::kCols / 2];
-#pragma unroll
-            for (int i = 0; i < C::kCols / 2; ++i) acc[i] = 0;
-            for (int j = 0; j < a.blocks; ++j, ++it) {
-                float* f = scales + (j & 1) * C::kCols;
-#pragma unroll
-                for (int i = 0; i < kMine; ++i)
-                    if (lane + 32 * i < C::kCols) f[lane + 32 * i] = __fmul_rn(next[i], next_w);
-                if (j + 1 < a.blocks) fetch(j + 1);
-                __syncwarp();
-                const uint32_t b = it % C::kBufs;
-                bool ok = mbar_wait_bounded(&tfull[b], (it / C::kBufs) & 1u, kF8WaitNs);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) {
-                    failed = true;
-                    break;
-                }
-                tc_fence_after_sync();
-                uint32_t r[2][16];
-                tmem_ld16(taddr + b * kN, r[0]);
-#pragma unroll
-                for (int c = 0; c < C::kCols / 16; ++c) {
-                    if (c * 16 >= cols) break;
-                    tmem_ld_wait();
-                    if (c + 1 < C::kCols / 16 && (c + 1) * 16 < cols)
-                        tmem_ld16(taddr + b * kN + (c + 1) * 16, r[(c + 1) & 1]);
-                    else {
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&tempty[b]);
+            for (int i = 0; i < kCols / 2; ++i) acc[i] = 0;
+            if constexpr (C::kTokenLanes) {
+#pragma unroll 1
+                for (int j = 0; j < a.blocks; ++j, ++it) {
+                    const float f = __fmul_rn(next, next_w);
+                    const uint64_t ff = f2_pack(f, f);
+                    if (j + 1 < a.blocks) {
+                        qs += a.scale_col;
+                        next = mine ? *qs : 0.f;
+                        next_w = *++ws;
                     }
+                    const uint32_t b = it % C::kBufs;
+                    wait_full(it);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 s = *reinterpret_cast<const float4*>(f + c * 16 + i);
-                        const uint32_t(&x)[16] = r[c & 1];
-                        uint64_t& y0 = acc[c * 8 + i / 2];
-                        uint64_t& y1 = acc[c * 8 + i / 2 + 1];
-                        y0 = f2_fma(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), f2_pack(s.x, s.y), y0);
-                        y1 = f2_fma(f2_pack(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
-                                    f2_pack(s.z, s.w), y1);
+                    for (int c = 0; c < kCols / 32; ++c) {
+                        uint32_t r[32];
+                        tmem_load(taddr + b * kN + c * 32, r);
+                        tmem_ld_wait();
+                        if (c == kCols / 32 - 1) {
+                            tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&tempty[b]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            uint64_t& y = acc[(c * 32 + i) / 2];
+                            y = f2_fma(f2_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), ff, y);
+                        }
+                    }
+                }
+            } else {
+                for (int j = 0; j < a.blocks; ++j, ++it) {
+                    float* fs = scales + (j & 1) * kCols;
+                    if (lane < kCols) fs[lane] = __fmul_rn(next, next_w);
+                    if (j + 1 < a.blocks) {
+                        qs += a.scale_col;
+                        next = mine ? *qs : 0.f;
+                        next_w = *++ws;
+                    }
+                    const uint32_t b = it % C::kBufs;
+                    wait_full(it);  // and the scales are written
+                    uint32_t r[kCols];
+                    tmem_load(taddr + b * kN, r);
+                    tmem_ld_wait();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&tempty[b]);
+#pragma unroll
+                    for (int i = 0; i < kCols; i += 4) {
+                        const float4 s = *reinterpret_cast<const float4*>(fs + i);
+                        uint64_t &y0 = acc[i / 2], &y1 = acc[i / 2 + 1];
+                        y0 = f2_fma(f2_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2_pack(s.x, s.y), y0);
+                        y1 = f2_fma(f2_pack(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), f2_pack(s.z, s.w),
+                                    y1);
                     }
                 }
             }
             if (failed) break;
-            const int64_t v = vb * kF8Rows + quarter * 32 + lane;
-            if (v < a.V) {
-                O* out = static_cast<O*>(a.out) + v;
+            O* out = static_cast<O*>(a.out);
+            if constexpr (!C::kTokenLanes) {
+                // lanes write neighbouring logits of one token after another
+                const int n = min(kCols, a.T - (tt * kN + c0));
+                if (v < a.V) {
+                    O* at = out + (int64_t)(tt * kN + c0) * a.ld_out + v;
 #pragma unroll
-                for (int i = 0; i < C::kCols / 2; ++i) {
-                    float x, y;
-                    f2_unpack(acc[i], x, y);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int c = 2 * i + h;
-                        if (c >= cols || t0 + c >= a.T) continue;
-                        const float z = h ? y : x;
-                        if constexpr (sizeof(O) == 4)
-                            out[(t0 + c) * a.ld_out] = z;
-                        else
-                            out[(t0 + c) * a.ld_out] = (uint16_t)(bf2_pack_rn(z, 0.f) & 0xFFFFu);
+                    for (int i = 0; i < kCols; ++i, at = next_row(at, a.ld_out)) {
+                        float x, y;
+                        f2_unpack(acc[i / 2], x, y);
+                        if (i < n) put(at, i & 1 ? y : x);
                     }
+                }
+            } else if (a.vector && v + kCols <= a.V) {
+                // a lane writes its token's logits, 16 bytes at a time
+                constexpr int kVec = 16 / sizeof(O);
+                uint4* row = reinterpret_cast<uint4*>(out + t * a.ld_out + v);
+                if (t < a.T) {
+#pragma unroll
+                    for (int i = 0; i < kCols / kVec; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            float x, y;
+                            f2_unpack(acc[(i * kVec + h * (kVec / 4)) / 2], x, y);
+                            w[h] = kVec == 8 ? bf2_pack_rn(x, y) : __float_as_uint(h & 1 ? y : x);
+                        }
+                        row[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            } else {
+                // rows at any alignment: turned, so that lanes write neighbouring logits
+#pragma unroll
+                for (int c = 0; c < kCols / 16; ++c) {
+                    float x[16];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f2_unpack(acc[c * 8 + i], x[2 * i], x[2 * i + 1]);
+                    transpose16(x, lane);
+                    const int col = v + c * 16 + (lane & 15);
+                    const int t0 = tt * kF8M + quarter * 32 + (lane & 16);
+                    O* at = out + (int64_t)t0 * a.ld_out + col;
+                    const int n = col < a.V ? min(16, a.T - t0) : 0;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i, at = next_row(at, a.ld_out))
+                        if (i < n) put(at, x[i]);
                 }
             }
         }
@@ -381,29 +487,42 @@ __global__ void __launch_bounds__(F8Tile<kN>::kThreads, 1)
 }
 
 template <int kN, typename O>
-cudaError_t launch_logits(F8Args a, const void* q, int64_t K, const DeviceInfo& dev, cudaStream_t st) {
+cudaError_t launch_logits(F8Args a, const void* q, const void* W, int64_t K, const DeviceInfo& dev, cudaStream_t st) {
     using C = F8Tile<kN>;
     static ContextSeen configured;
     const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(fp8_logits_kernel<kN, O>), (int)C::kBytes,
                                             configured);
     if (e != cudaSuccess) return e;
-    // Tiles of equal width, as narrow as covers the tokens.
-    a.t_tiles = (int)((a.T + kN - 1) / kN);
-    const int step = 16 * (C::kEpiWarps / 4);
-    a.tokens = (int)((a.T + a.t_tiles - 1) / a.t_tiles + step - 1) / step * step;
-    a.tiles = (a.V + kF8Rows - 1) / kF8Rows * a.t_tiles;
-    if (!make_byte_map(&a.q, q, a.T, K, K, a.tokens)) return cudaErrorInvalidValue;
+    if (C::kTokenLanes) {  // a warp that asks for registers that are not there waits for ever
+        static std::atomic<int> regs{0};
+        if (!regs) {
+            cudaFuncAttributes attr;
+            const cudaError_t f = cudaFuncGetAttributes(&attr, fp8_logits_kernel<kN, O>);
+            if (f != cudaSuccess) return f;
+            regs = attr.numRegs;
+        }
+        if (regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+    }
+    const int64_t t_tile = C::kTokenLanes ? kF8M : kN, v_tile = C::kTokenLanes ? kN : kF8M;
+    a.t_tiles = (int)((a.T + t_tile - 1) / t_tile);
+    const int64_t tiles = (a.V + v_tile - 1) / v_tile * a.t_tiles;
+    if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+    a.tiles = (uint32_t)tiles;
+    if (!make_byte_map(C::kTokenLanes ? &a.lanes : &a.columns, q, a.T, K, K, (int)t_tile) ||
+        !make_byte_map(C::kTokenLanes ? &a.columns : &a.lanes, W, a.V, K, K, (int)v_tile))
+        return cudaErrorInvalidValue;
     const int64_t grid = a.tiles < dev.sm_count ? a.tiles : dev.sm_count;
     return launch_behind(fp8_logits_kernel<kN, O>, (unsigned)grid, C::kThreads, C::kBytes, st, 1, a);
 }
 
 template <typename O>
-cudaError_t launch_logits_of(const F8Args& a, const void* q, int64_t K, const DeviceInfo& dev, cudaStream_t st) {
-    if (a.T <= 16) return launch_logits<16, O>(a, q, K, dev, st);
-    if (a.T <= 32) return launch_logits<32, O>(a, q, K, dev, st);
-    if (a.T <= 64) return launch_logits<64, O>(a, q, K, dev, st);
-    if (a.T <= 128) return launch_logits<128, O>(a, q, K, dev, st);
-    return launch_logits<256, O>(a, q, K, dev, st);
+cudaError_t launch_logits_of(const F8Args& a, const void* q, const void* W, int64_t K, const DeviceInfo& dev,
+                             cudaStream_t st) {
+    if (a.T <= 16) return launch_logits<16, O>(a, q, W, K, dev, st);
+    if (a.T <= 32) return launch_logits<32, O>(a, q, W, K, dev, st);
+    if (a.T <= 64) return launch_logits<64, O>(a, q, W, K, dev, st);
+    if (a.T <= 128) return launch_logits<128, O>(a, q, W, K, dev, st);
+    return launch_logits<256, O>(a, q, W, K, dev, st);
 }
 
 bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -462,16 +581,17 @@ int pstat_fp8_logits(const void* q, const float* q_scale, int64_t scale_row, int
     a.q_scale = q_scale;
     a.scale_row = scale_row;
     a.scale_col = scale_col;
-    a.T = T;
-    a.V = V;
+    a.T = (int)T;
+    a.V = (int)V;
     a.ld_out = ld_out;
     a.out = out;
     a.blocks = (int)((K + kF8Block - 1) / kF8Block);
+    a.row_blocks = (int)((V + kF8Block - 1) / kF8Block);
+    a.vector = aligned_to(out, 16) && ld_out % (out_dt == PSTAT_BF16 ? 8 : 4) == 0;
     a.dev_error = dev_error;
-    if (!make_byte_map(&a.W, W, V, K, K, kF8Rows)) return PSTAT_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = out_dt == PSTAT_BF16 ? launch_logits_of<uint16_t>(a, q, K, dev, st)
-                                               : launch_logits_of<float>(a, q, K, dev, st);
+    const cudaError_t e = out_dt == PSTAT_BF16 ? launch_logits_of<uint16_t>(a, q, W, K, dev, st)
+                                               : launch_logits_of<float>(a, q, W, K, dev, st);
     return e == cudaSuccess ? PSTAT_OK : PSTAT_ERR_CUDA;
 }
 
