@@ -69,6 +69,17 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
     }
 }
 
+// The same, giving up after `cycles` of the SM's clock.  For waits on a kernel's critical path:
+// a read of the global timer takes as long as hundreds of instructions.
+__device__ __forceinline__ bool mbar_wait_cycles(uint64_t* bar, uint32_t parity, long long cycles) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (clock64() - t0 > cycles) return false;
+    }
+}
+
 // ---- bulk asynchronous copy (global -> shared), completion on an mbarrier --
 // Both addresses must be 16-byte aligned and `bytes` a multiple of 16.  The L2
 // cache policy comes from createpolicy: evict-first for data streamed once,
