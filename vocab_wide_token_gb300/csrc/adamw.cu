@@ -28,6 +28,7 @@
 #include <cstdint>
 #include <memory>
 #include <new>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -38,7 +39,7 @@ namespace {
 constexpr int kAdThreads = 256;
 constexpr int kAdBlock = 128;                   // elements that share an exponent: a warp's
 constexpr int kAdUnit = 4096;                   // elements of one tensor, a CTA's turn
-constexpr int kAdCtas = 2;                      // per SM
+constexpr int kAdCtas = 2, kAdCtasDrawn = 4;                      // per SM
 constexpr int kAdBatch = 600;                   // tensors of one launch (they travel as its arguments)
 constexpr int kDepthM = 14, kDepthV = 30;       // binary orders below a block's largest
 
@@ -49,7 +50,7 @@ struct AdTensor {
     void* v;
     int64_t n;
     uint32_t first_unit;
-    uint32_t kind;  // bit 0: bf16 parameter, 1: bf16 gradient, 2: 8-bit moments; from bit 3: place in the list
+    uint32_t place;  // in the list
 };
 template <int N>
 struct AdBatch {
@@ -77,6 +78,7 @@ struct AdScalars {
     float b1, c1, b2, c2, eps, factor, decay, size, root;
     uint32_t seed_key;
     bool skip;
+    bool tiny_eps;  // the root's small values weigh against eps
 };
 
 // 32 bits that are as good as random, from a counter under a key: two rounds of
@@ -114,6 +116,7 @@ __device__ AdScalars scalars_of(const AdOptions& o) {
         const double t = (double)(o.step_at ? *after_wait(o.step_at) : o.step);
         corrections(lr, o.weight_decay, o.beta1, o.beta2, t, s.decay, s.size, s.root);
     }
+    s.tiny_eps = !(s.eps >= 0x1p-60f);
     s.factor = 1.f;
     s.skip = false;
     if (o.norm) {
@@ -126,15 +129,12 @@ __device__ AdScalars scalars_of(const AdOptions& o) {
     return s;
 }
 
-// Four neighbouring elements of one lane, or four that are 32 apart.
-__device__ __forceinline__ void load4(const void* at, int64_t i, bool bf16, float (&x)[4]) {
-    if (bf16) {
-        const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(at) + i);
-        x[0] = bf2_lo(q.x), x[1] = bf2_hi(q.x), x[2] = bf2_lo(q.y), x[3] = bf2_hi(q.y);
-    } else {
-        const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(at) + i);
-        x[0] = q.x, x[1] = q.y, x[2] = q.z, x[3] = q.w;
-    }
+__device__ __forceinline__ void unpack4(const uint2& q, float (&x)[4]) {
+    x[0] = bf2_lo(q.x), x[1] = bf2_hi(q.x), x[2] = bf2_lo(q.y), x[3] = bf2_hi(q.y);
+}
+__device__ __forceinline__ void unpack4(const uint4& q, float (&x)[4]) {
+    x[0] = __uint_as_float(q.x), x[1] = __uint_as_float(q.y);
+    x[2] = __uint_as_float(q.z), x[3] = __uint_as_float(q.w);
 }
 __device__ __forceinline__ float load1(const void* at, int64_t i, bool bf16) {
     return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(at)[i] << 16)
@@ -181,166 +181,309 @@ __device__ __forceinline__ void moments(float g, const AdScalars& s, float& m, f
     m = __fadd_rn(__fmul_rn(m, s.b1), __fmul_rn(x, s.c1));
     v = __fadd_rn(__fmul_rn(v, s.b2), __fmul_rn(__fmul_rn(x, x), s.c2));
 }
-__device__ __forceinline__ float approx_sqrt(float x) {
-    float y;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // The root and the quotient are approximations of 2^-22: the step they give is a small
-// part of the parameter, or all of one that was zero.
+// part of the parameter, or all of one that was zero.  Where eps is at least 2^-60, a root below
+// 2^-63 does not count beside it, and the divisor is a normal number.
 __device__ __forceinline__ float updated(float p, float m, float v, const AdScalars& s) {
-    const float step = __fdividef(m, fmaf(approx_sqrt(v), s.root, s.eps));
+    float root, step;
+    if (s.tiny_eps) {
+        asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v));
+        step = __fdividef(m, fmaf(root, s.root, s.eps));
+    } else {
+        asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(v));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(step) : "f"(fmaf(root, s.root, s.eps)));
+        step *= m;
+    }
     return fmaf(-s.size, step, p * s.decay);
 }
-__device__ __forceinline__ uint16_t to_bf16(float x, uint32_t draw, bool random) {
-    if (random && x == x) return (uint16_t)((__float_as_uint(x) + draw) >> 16);
-    return (uint16_t)(bf2_pack_rn(x, 0.f) & 0xFFFFu);
+// Two parameters to bf16; the draws' upper 16 bits are used.  kAny: they may be NaN.
+template <bool kRandom, bool kAny>
+__device__ __forceinline__ uint32_t to_bf16(float x, float y, uint32_t draw_x, uint32_t draw_y) {
+    if (!kRandom) return bf2_pack_rn(x, y);
+    uint32_t a = __float_as_uint(x) + (draw_x >> 16), b = __float_as_uint(y) + (draw_y >> 16);
+    if (kAny && x != x) a = 0x7FC00000u;
+    if (kAny && y != y) b = 0x7FC00000u;
+    return __byte_perm(a, b, 0x7632);
 }
 
-// One warp's blocks of 128 elements of a unit, kRows of them at a time.
-template <bool kBf16P, bool kBf16G, bool kSmall>
-__device__ __forceinline__ void step_unit(const AdTensor& t, uint32_t u, const AdScalars& s, bool random) {
-    constexpr int kRows = kSmall ? 4 : 2;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const void* g = after_wait(t.g);
-    void* p = t.p;
-    const int64_t n = t.n;
-    uint8_t* m8 = static_cast<uint8_t*>(t.m);
-    uint8_t* v8 = static_cast<uint8_t*>(t.v);
-    float* m32 = static_cast<float*>(t.m);
-    float* v32 = static_cast<float*>(t.v);
-    const uint32_t key = mix32(s.seed_key ^ (t.kind >> 3), 0xDAA66D2Bu);
-    const uint32_t key_p = key ^ 0xA54FF53Au;
-    const bool aligned = ((reinterpret_cast<uintptr_t>(p) & (kBf16P ? 7u : 15u)) |
-                          (reinterpret_cast<uintptr_t>(g) & (kBf16G ? 7u : 15u)) |
-                          ((reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v)) &
-                           (kSmall ? 3u : 15u))) == 0;
-    const int64_t b0 = (int64_t)(u - t.first_unit) * (kAdUnit / kAdBlock);
-#pragma unroll 1
-    for (int r = warp * kRows; r < kAdUnit / kAdBlock; r += kAdThreads / 32 * kRows) {
-        if ((b0 + r) * kAdBlock >= n) break;
-        float xp[kRows][4], xg[kRows][4], xm[kRows][4], xv[kRows][4];
-        uint32_t cm[kRows], cv[kRows];
-        uint8_t em[kRows], ev[kRows];
-        const bool whole = aligned && (b0 + r + kRows) * kAdBlock <= n;
-        const int stride = whole ? 1 : 32;
-        const int first = whole ? 4 * lane : lane;
+// One tensor's addresses and keys, for the blocks of a unit.
+struct AdView {
+    void* p;
+    const void* g;
+    void* m;
+    void* v;
+    int64_t n;
+    uint32_t key, key_p;
+};
+__device__ __forceinline__ uint32_t draw_of(const AdView& t, int64_t k) {
+    return mix32((uint32_t)k, t.key + (uint32_t)(k >> 32) * 0x9E3779B9u);
+}
+
+// A block of 128 elements by a warp, whatever its alignment, size and values: element
+// 128 b + 32 e + lane is a lane's e-th.
+template <bool kBf16P, bool kBf16G, bool kSmall, bool kRandom>
+__device__ __noinline__ void step_block(const AdView t, const AdScalars* shared, int64_t b) {
+    const int lane = threadIdx.x & 31;
+    const AdScalars s = *shared;
+    uint8_t *m8 = static_cast<uint8_t*>(t.m), *v8 = static_cast<uint8_t*>(t.v);
+    float *m32 = static_cast<float*>(t.m), *v32 = static_cast<float*>(t.v);
+    int bm = 0, bv = 0;
+    if (kSmall) {
+        bm = code_base(m8[t.n + b], kDepthM);
+        bv = code_base(v8[t.n + b], kDepthV);
+    }
+    float xp[4], xm[4], xv[4];
+    uint32_t top_m = 0, top_v = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int64_t k = b * kAdBlock + 32 * e + lane;
+        const bool in = k < t.n;
+        xp[e] = in ? load1(t.p, k, kBf16P) : 0.f;
+        const float xg = in ? load1(t.g, k, kBf16G) : 0.f;
+        if (kSmall) {
+            xm[e] = decode_m(in ? m8[k] : 0u, bm);
+            xv[e] = decode_v(in ? v8[k] : 0u, bv);
+        } else {
+            xm[e] = in ? m32[k] : 0.f;
+            xv[e] = in ? v32[k] : 0.f;
+        }
+        moments(xg, s, xm[e], xv[e]);
+        xp[e] = updated(xp[e], xm[e], xv[e], s);
+        top_m = max(top_m, finite_bits(xm[e]));
+        top_v = max(top_v, finite_bits(xv[e]));
+    }
+    if (kSmall) {
+        top_m = __reduce_max_sync(0xFFFFFFFFu, top_m) >> 23;
+        top_v = __reduce_max_sync(0xFFFFFFFFu, top_v) >> 23;
+        bm = code_base(top_m, kDepthM);
+        bv = code_base(top_v, kDepthV);
+        __syncwarp();  // every lane has read the old exponents
+        if (lane == 0) {
+            m8[t.n + b] = (uint8_t)top_m;
+            v8[t.n + b] = (uint8_t)top_v;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int64_t k = b * kAdBlock + 32 * e + lane;
+        if (k >= t.n) continue;
+        const uint32_t h = kRandom ? draw_of(t, k) : 0x80008000u;  // nearest: half a step
+        if (kBf16P)
+            static_cast<uint16_t*>(t.p)[k] =
+                (uint16_t)(to_bf16<kRandom, true>(xp[e], 0.f, kRandom ? mix32(h, t.key_p) : 0u, 0u) & 0xFFFFu);
+        else
+            static_cast<float*>(t.p)[k] = xp[e];
+        if (kSmall) {
+            const uint32_t low = kRandom ? 8u : 0u;
+            m8[k] = (uint8_t)encode_m(xm[e], bm, h >> 16 << 4 | low);
+            v8[k] = (uint8_t)encode_v(xv[e], bv, (h & 0xFFFFu) << 4 | low);
+        } else {
+            m32[k] = xm[e];
+            v32[k] = xv[e];
+        }
+    }
+}
+
+// The step of a normal eps (see updated): a divisor of a normal number.
+__device__ __forceinline__ float updated_fast(float p, float m, float v, const AdScalars& s) {
+    float root, step;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(v));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(step) : "f"(fmaf(root, s.root, s.eps)));
+    return fmaf(-s.size, step * m, p * s.decay);
+}
+
+// kRows whole blocks whose tensors start on the vectors' sizes: element 128 b + 4 lane + e is a
+// lane's e-th.  All loads come before the first use.  What is rare in a block takes a branch
+// of its own that the warp goes through together: codes of zero or NaN, values below the
+// least code; and infinities and NaN among the results leave the block to step_block.
+//   decoding   bits = (code << 20) + (base << 20)
+//   encoding   the code is bits 20.. of bits + draw - (base << 20), which 16 times as large
+//              is the upper byte
+// 93 instructions an element with drawn roundings (18 for two hashes), 58 without; 96 and 75
+// with a select for every such case.
+template <bool kBf16P, bool kBf16G, bool kSmall, int kRows>
+struct AdRaw {
+    using P = typename std::conditional<kBf16P, uint2, uint4>::type;
+    using G = typename std::conditional<kBf16G, uint2, uint4>::type;
+    P rp[kRows];
+    G rg[kRows];
+    uint4 rm[kSmall ? 1 : kRows], rv[kSmall ? 1 : kRows];
+    uint32_t cm[kRows], cv[kRows], em[kRows], ev[kRows];
+
+    __device__ __forceinline__ void load(const AdView& t, int64_t b) {
+        const int lane = threadIdx.x & 31;
+        const uint8_t *m8 = static_cast<const uint8_t*>(t.m), *v8 = static_cast<const uint8_t*>(t.v);
 #pragma unroll
         for (int j = 0; j < kRows; ++j) {
-            const int64_t i = (b0 + r + j) * kAdBlock + first;
-            if (whole) {
-                load4(p, i, kBf16P, xp[j]);
-                load4(g, i, kBf16G, xg[j]);
-                if (kSmall) {
-                    cm[j] = *reinterpret_cast<const uint32_t*>(m8 + i);
-                    cv[j] = *reinterpret_cast<const uint32_t*>(v8 + i);
-                } else {
-                    load4(m32, i, false, xm[j]);
-                    load4(v32, i, false, xv[j]);
-                }
-            } else {
-                cm[j] = cv[j] = 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int64_t k = i + e * 32;
-                    const bool in = k < n;
-                    xp[j][e] = in ? load1(p, k, kBf16P) : 0.f;
-                    xg[j][e] = in ? load1(g, k, kBf16G) : 0.f;
-                    if (kSmall) {
-                        cm[j] |= in ? (uint32_t)m8[k] << (8 * e) : 0u;
-                        cv[j] |= in ? (uint32_t)v8[k] << (8 * e) : 0u;
-                    } else {
-                        xm[j][e] = in ? m32[k] : 0.f;
-                        xv[j][e] = in ? v32[k] : 0.f;
-                    }
-                }
-            }
+            const int64_t i = (b + j) * kAdBlock + 4 * lane;
+            rp[j] = *reinterpret_cast<const P*>(static_cast<const char*>(t.p) + i * (kBf16P ? 2 : 4));
+            rg[j] = *reinterpret_cast<const G*>(static_cast<const char*>(t.g) + i * (kBf16G ? 2 : 4));
             if (kSmall) {
-                const bool in = (b0 + r + j) * kAdBlock < n;
-                em[j] = in ? m8[n + b0 + r + j] : 0;
-                ev[j] = in ? v8[n + b0 + r + j] : 0;
+                cm[j] = *reinterpret_cast<const uint32_t*>(m8 + i);
+                cv[j] = *reinterpret_cast<const uint32_t*>(v8 + i);
+                em[j] = m8[t.n + b + j];
+                ev[j] = v8[t.n + b + j];
+            } else {
+                rm[j] = *reinterpret_cast<const uint4*>(static_cast<const float*>(t.m) + i);
+                rv[j] = *reinterpret_cast<const uint4*>(static_cast<const float*>(t.v) + i);
             }
         }
+    }
+};
+template <bool kBf16P, bool kBf16G, bool kSmall, bool kRandom, int kRows>
+__device__ __forceinline__ void step_blocks(const AdRaw<kBf16P, kBf16G, kSmall, kRows>& raw, const AdView& t,
+                                            const AdScalars& s, const AdScalars* shared, int64_t b) {
+    const int lane = threadIdx.x & 31;
+    uint8_t *m8 = static_cast<uint8_t*>(t.m), *v8 = static_cast<uint8_t*>(t.v);
+    float *m32 = static_cast<float*>(t.m), *v32 = static_cast<float*>(t.v);
 #pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-            const int64_t i = (b0 + r + j) * kAdBlock + first;
-            if (kSmall) {
-                const int bm = code_base(em[j], kDepthM), bv = code_base(ev[j], kDepthV);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    xm[j][e] = decode_m(cm[j] >> (8 * e) & 255u, bm);
-                    xv[j][e] = decode_v(cv[j] >> (8 * e) & 255u, bv);
-                }
-            }
-            uint32_t top_m = 0, top_v = 0;
-            uint32_t h[4];
+    for (int j = 0; j < kRows; ++j) {
+        const int64_t i = (b + j) * kAdBlock + 4 * lane;
+        float xp[4], xg[4], xm[4], xv[4];
+        unpack4(raw.rp[j], xp);
+        unpack4(raw.rg[j], xg);
+        if (kSmall) {
+            const int bm = code_base(raw.em[j], kDepthM), bv = code_base(raw.ev[j], kDepthV);
+            const uint32_t w = raw.cm[j] & 0x7F7F7F7Fu;
+            // a byte of 127 (m) or 255 (v), and a byte of 0
+            const bool nan = ((w + 0x01010101u) | ((~raw.cv[j] - 0x01010101u) & raw.cv[j])) & 0x80808080u;
+            const bool zero = ((w - 0x01010101u) | ((raw.cv[j] - 0x01010101u) & ~raw.cv[j])) & 0x80808080u;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                moments(xg[j][e], s, xm[j][e], xv[j][e]);
-                xp[j][e] = updated(xp[j][e], xm[j][e], xv[j][e], s);
-                if (kSmall) {
-                    top_m = max(top_m, finite_bits(xm[j][e]));
-                    top_v = max(top_v, finite_bits(xv[j][e]));
-                }
-                const int64_t k = i + e * stride;
-                h[e] = 0x80008000u;
-                if (random && (kSmall || kBf16P))
-                    h[e] = mix32((uint32_t)k, key + (uint32_t)(k >> 32) * 0x9E3779B9u);
+                const uint32_t a = __byte_perm(w, 0, 0x4440 + e), c = __byte_perm(raw.cv[j], 0, 0x4440 + e);
+                const uint32_t sign = (raw.cm[j] << (24 - 8 * e)) & 0x80000000u;
+                xm[e] = __uint_as_float(a * 0x100000u + ((uint32_t)bm << 20) | sign);
+                xv[e] = __uint_as_float(c * 0x100000u + ((uint32_t)bv << 20));
             }
-            uint32_t out_m = 0, out_v = 0;
-            if (kSmall) {
-                top_m = __reduce_max_sync(0xFFFFFFFFu, top_m) >> 23;
-                top_v = __reduce_max_sync(0xFFFFFFFFu, top_v) >> 23;
-                const int bm = code_base(top_m, kDepthM), bv = code_base(top_v, kDepthV);
-                const uint32_t low = random ? 8u : 0u;  // nearest: half a step
+            if (__any_sync(0xFFFFFFFFu, nan)) {
+                step_block<kBf16P, kBf16G, true, kRandom>(t, shared, b + j);
+                continue;
+            }
+            if (__any_sync(0xFFFFFFFFu, zero)) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    out_m |= encode_m(xm[j][e], bm, h[e] >> 16 << 4 | low) << (8 * e);
-                    out_v |= encode_v(xv[j][e], bv, (h[e] & 0xFFFFu) << 4 | low) << (8 * e);
-                }
-                if (lane == 0 && (b0 + r + j) * kAdBlock < n) {
-                    m8[n + b0 + r + j] = (uint8_t)top_m;
-                    v8[n + b0 + r + j] = (uint8_t)top_v;
+                    if (!(w & 0xFFu << (8 * e))) xm[e] = __uint_as_float(__float_as_uint(xm[e]) & 0x80000000u);
+                    if (!(raw.cv[j] & 0xFFu << (8 * e))) xv[e] = 0.f;
                 }
             }
-            uint16_t q[4];
-            if (kBf16P) {
+        } else {
+            unpack4(raw.rm[kSmall ? 0 : j], xm);
+            unpack4(raw.rv[kSmall ? 0 : j], xv);
+        }
+        const uint32_t key = t.key + (uint32_t)(i >> 32) * 0x9E3779B9u;
+        uint32_t am[4], av[4], h[4];
+        float lost = 0.f;  // a NaN where a parameter is not finite
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    q[e] = to_bf16(xp[j][e], random ? mix32(h[e], key_p) >> 16 : 0u, random);
+        for (int e = 0; e < 4; ++e) {
+            moments(xg[e], s, xm[e], xv[e]);
+            am[e] = __float_as_uint(xm[e]) & 0x7FFFFFFFu;
+            av[e] = __float_as_uint(xv[e]);  // no less than +0, or a NaN, which may have a sign
+            xp[e] = kSmall ? updated_fast(xp[e], xm[e], xv[e], s) : updated(xp[e], xm[e], xv[e], s);
+            if (kSmall && kBf16P && kRandom) lost = fmaf(xp[e], 0.f, lost);
+            h[e] = kRandom && (kSmall || kBf16P) ? mix32((uint32_t)i + e, key) : 0u;
+        }
+        uint32_t out_m = 0, out_v = 0, top_m = 0, top_v = 0;
+        if (kSmall) {
+            top_m = __reduce_max_sync(0xFFFFFFFFu, max(max(am[0], am[1]), max(am[2], am[3])));
+            top_v = __reduce_max_sync(0xFFFFFFFFu, max(max(av[0], av[1]), max(av[2], av[3])));
+            if (top_m >= 0x7F800000u || top_v >= 0x7F800000u || __any_sync(0xFFFFFFFFu, lost != lost)) {
+                step_block<kBf16P, kBf16G, true, kRandom>(t, shared, b + j);
+                continue;
             }
-            if (whole) {
-                if (kBf16P)
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
-                        make_uint2(q[0] | (uint32_t)q[1] << 16, q[2] | (uint32_t)q[3] << 16);
-                else
-                    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) =
-                        make_float4(xp[j][0], xp[j][1], xp[j][2], xp[j][3]);
-                if (kSmall) {
-                    *reinterpret_cast<uint32_t*>(m8 + i) = out_m;
-                    *reinterpret_cast<uint32_t*>(v8 + i) = out_v;
-                } else {
-                    *reinterpret_cast<float4*>(m32 + i) = make_float4(xm[j][0], xm[j][1], xm[j][2], xm[j][3]);
-                    *reinterpret_cast<float4*>(v32 + i) = make_float4(xv[j][0], xv[j][1], xv[j][2], xv[j][3]);
-                }
-            } else {
+            top_m >>= 23;
+            top_v >>= 23;
+            const uint32_t Bm = (uint32_t)code_base(top_m, kDepthM) << 20;
+            const uint32_t Bv = (uint32_t)code_base(top_v, kDepthV) << 20;
+            const uint32_t half = kRandom ? 8u : 0x80000u;
+            uint32_t ym[4], yv[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // a draw is 16 bits, times 16, and a half of that
+                ym[e] = am[e] * 16u + (half - Bm) * 16u + (kRandom ? __byte_perm(h[e], 0, 0x4324) : 0u);
+                yv[e] = av[e] * 16u + (half - Bv) * 16u + (kRandom ? __byte_perm(h[e], 0, 0x4104) : 0u);
+                ym[e] |= __float_as_uint(xm[e]) & 0x80000000u;
+            }
+            const uint32_t least_m = Bm + (1u << 20), least_v = Bv + (1u << 20);
+            if (__any_sync(0xFFFFFFFFu, min(min(am[0], am[1]), min(am[2], am[3])) < least_m ||
+                                            min(min(av[0], av[1]), min(av[2], av[3])) < least_v)) {
+                const float unit = __uint_as_float(least_m) * 0x1p-20f;  // as encode_m has it: a power of two
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int64_t k = i + e * 32;
-                    if (k >= n) continue;
-                    if (kBf16P)
-                        static_cast<uint16_t*>(p)[k] = q[e];
-                    else
-                        static_cast<float*>(p)[k] = xp[j][e];
-                    if (kSmall) {
-                        m8[k] = (uint8_t)(out_m >> (8 * e));
-                        v8[k] = (uint8_t)(out_v >> (8 * e));
-                    } else {
-                        m32[k] = xm[j][e];
-                        v32[k] = xv[j][e];
-                    }
+                    const uint32_t draw = kRandom ? (h[e] >> 12 & 0xFFFF0u) | 8u : 0x80000u;
+                    if (am[e] < least_m)
+                        ym[e] = (__float_as_uint(xm[e]) & 0x80000000u) |
+                                (fabsf(xm[e]) > unit * (float)draw ? 1u << 24 : 0u);
+                    if (av[e] < least_v) yv[e] = av[e] ? 1u << 24 : 0u;
                 }
             }
+            out_m = __byte_perm(__byte_perm(ym[0], ym[1], 0x0073), __byte_perm(ym[2], ym[3], 0x0073), 0x5410);
+            out_v = __byte_perm(__byte_perm(yv[0], yv[1], 0x0073), __byte_perm(yv[2], yv[3], 0x0073), 0x5410);
+        }
+        if (kBf16P) {
+            uint32_t d[4] = {};
+            if (kRandom) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[e] = mix32(h[e], t.key_p);
+            }
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(t.p) + i) =
+                make_uint2(to_bf16<kRandom, !kSmall>(xp[0], xp[1], d[0], d[1]),
+                           to_bf16<kRandom, !kSmall>(xp[2], xp[3], d[2], d[3]));
+        } else {
+            *reinterpret_cast<float4*>(static_cast<float*>(t.p) + i) = make_float4(xp[0], xp[1], xp[2], xp[3]);
+        }
+        if (kSmall) {
+            *reinterpret_cast<uint32_t*>(m8 + i) = out_m;
+            *reinterpret_cast<uint32_t*>(v8 + i) = out_v;
+            if (lane == 0) {
+                m8[t.n + b + j] = (uint8_t)top_m;
+                v8[t.n + b + j] = (uint8_t)top_v;
+            }
+        } else {
+            *reinterpret_cast<float4*>(m32 + i) = make_float4(xm[0], xm[1], xm[2], xm[3]);
+            *reinterpret_cast<float4*>(v32 + i) = make_float4(xv[0], xv[1], xv[2], xv[3]);
+        }
+    }
+}
+
+// One warp's blocks of units [u0, u1) of a tensor.  Rounded to nearest, the 8-bit forms load the
+// next blocks before they work on these: 60 million bf16 elements in 172 us, 207 without.  With
+// draws the code is as long again, and twice in a loop it no longer fits the instruction
+// cache: 237 us, and 222 with four CTAs on an SM that load what they work on.
+template <bool kBf16P, bool kBf16G, bool kSmall, bool kRandom>
+__device__ __forceinline__ void step_units(const AdTensor& at, uint32_t u0, uint32_t u1, const AdScalars& s,
+                                           const AdScalars* shared) {
+    constexpr int kRows = kSmall ? 4 : 2, kPerUnit = kAdUnit / kAdBlock;
+    constexpr bool kAhead = kSmall && !kRandom;
+    AdView t = {at.p, after_wait(at.g), at.m, at.v, at.n, mix32(s.seed_key ^ at.place, 0xDAA66D2Bu), 0};
+    t.key_p = t.key ^ 0xA54FF53Au;
+    const bool quick = ((reinterpret_cast<uintptr_t>(t.p) & (kBf16P ? 7u : 15u)) |
+                        (reinterpret_cast<uintptr_t>(t.g) & (kBf16G ? 7u : 15u)) |
+                        ((reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v)) &
+                         (kSmall ? 3u : 15u))) == 0 &&
+                       !(kSmall && s.tiny_eps);
+    // A warp's turns: kRows neighbouring blocks every kAdThreads / 32 * kRows of them.
+    constexpr int kTurn = kAdThreads / 32 * kRows;
+    static_assert(kPerUnit % kTurn == 0, "");
+    const int64_t first = (int64_t)(u0 - at.first_unit) * kPerUnit + (threadIdx.x >> 5) * kRows;
+    const int64_t blocks = min((t.n + kAdBlock - 1) / kAdBlock, (int64_t)(u1 - at.first_unit) * kPerUnit);
+    const int64_t whole = quick ? t.n / kAdBlock - kRows : -1;  // last start of kRows whole blocks
+    AdRaw<kBf16P, kBf16G, kSmall, kRows> raw[kAhead ? 2 : 1];
+    if (kAhead && first < blocks && first <= whole) raw[0].load(t, first);
+#pragma unroll 1
+    for (int64_t b = first; b < blocks; b += (kAhead ? 2 : 1) * kTurn) {
+#pragma unroll
+        for (int half = 0; half < (kAhead ? 2 : 1); ++half) {
+            const int64_t c = b + half * kTurn, next = c + kTurn;
+            if (c >= blocks) break;
+            if (c > whole) {
+                for (int64_t k = c; k < min(c + kRows, blocks); ++k)
+                    step_block<kBf16P, kBf16G, kSmall, kRandom>(t, shared, k);
+                continue;
+            }
+            if (!kAhead)
+                raw[0].load(t, c);
+            else if (next < blocks && next <= whole)
+                raw[half ^ 1].load(t, next);
+            step_blocks<kBf16P, kBf16G, kSmall, kRandom, kRows>(raw[half], t, s, shared, c);
         }
     }
 }
@@ -358,8 +501,9 @@ __device__ __forceinline__ int ad_tensor_of(const AdBatch<N>& g, uint32_t u) {
     return lo;
 }
 
-template <int N>
-__global__ void __launch_bounds__(kAdThreads, kAdCtas)
+// One kind of tensors to a launch, so that each has the registers that it needs.
+template <int N, bool kBf16P, bool kBf16G, bool kSmall, bool kRandom>
+__global__ void __launch_bounds__(kAdThreads, kSmall && kRandom ? kAdCtasDrawn : kAdCtas)
     adamw_kernel(const __grid_constant__ AdBatch<N> b, const __grid_constant__ AdOptions o) {
     __shared__ AdScalars shared;
     const uint32_t u0 = (uint32_t)((uint64_t)b.units * blockIdx.x / gridDim.x);
@@ -373,20 +517,10 @@ __global__ void __launch_bounds__(kAdThreads, kAdCtas)
     __syncthreads();
     const AdScalars s = shared;
     if (s.skip) return;
-    for (uint32_t u = u0; u < u1; ++u) {
-        while (i + 1 < b.count && b.t[i + 1].first_unit <= u) ++i;
-        const AdTensor& t = b.t[i];
-        const bool random = o.random != 0;
-        switch (t.kind & 7u) {
-            case 0: step_unit<false, false, false>(t, u, s, random); break;
-            case 1: step_unit<true, false, false>(t, u, s, random); break;
-            case 2: step_unit<false, true, false>(t, u, s, random); break;
-            case 3: step_unit<true, true, false>(t, u, s, random); break;
-            case 4: step_unit<false, false, true>(t, u, s, random); break;
-            case 5: step_unit<true, false, true>(t, u, s, random); break;
-            case 6: step_unit<false, true, true>(t, u, s, random); break;
-            default: step_unit<true, true, true>(t, u, s, random); break;
-        }
+    for (uint32_t u = u0; u < u1; ++i) {
+        const uint32_t end = i + 1 < b.count ? min(u1, b.t[i + 1].first_unit) : u1;
+        step_units<kBf16P, kBf16G, kSmall, kRandom>(b.t[i], u, end, s, &shared);
+        u = end;
     }
 }
 
@@ -408,22 +542,32 @@ __global__ void __launch_bounds__(kAdThreads) adamw_moments_kernel(const __grid_
         const bool aligned = ((reinterpret_cast<uintptr_t>(om) | reinterpret_cast<uintptr_t>(ov)) & 15u) == 0 &&
                              ((reinterpret_cast<uintptr_t>(m) | reinterpret_cast<uintptr_t>(v)) & 3u) == 0;
         const int64_t b0 = (int64_t)(u - t.first_unit) * (kAdUnit / kAdBlock);
+        constexpr int kRows = kAdUnit / kAdBlock / (kAdThreads / 32);  // blocks of a warp
+        const int64_t k0 = b0 + warp * kRows;
+        if (aligned && (k0 + kRows) * kAdBlock <= t.n) {
+            uint32_t cm[kRows], cv[kRows], em[kRows], ev[kRows];
 #pragma unroll
-        for (int r = 0; r < kAdUnit / kAdBlock / (kAdThreads / 32); ++r) {
-            const int64_t k = b0 + r * (kAdThreads / 32) + warp, e0 = k * kAdBlock;
-            if (e0 >= t.n) break;
-            const int bm = code_base(m[t.n + k], kDepthM), bv = code_base(v[t.n + k], kDepthV);
-            if (aligned && e0 + kAdBlock <= t.n) {
-                const uint32_t cm = *reinterpret_cast<const uint32_t*>(m + e0 + 4 * lane);
-                const uint32_t cv = *reinterpret_cast<const uint32_t*>(v + e0 + 4 * lane);
-                *reinterpret_cast<float4*>(om + e0 + 4 * lane) =
-                    make_float4(decode_m(cm & 255u, bm), decode_m(cm >> 8 & 255u, bm),
-                                decode_m(cm >> 16 & 255u, bm), decode_m(cm >> 24, bm));
-                *reinterpret_cast<float4*>(ov + e0 + 4 * lane) =
-                    make_float4(decode_v(cv & 255u, bv), decode_v(cv >> 8 & 255u, bv),
-                                decode_v(cv >> 16 & 255u, bv), decode_v(cv >> 24, bv));
-            } else {
-                for (int64_t e = e0 + lane; e < min(t.n, e0 + kAdBlock); e += 32) {
+            for (int r = 0; r < kRows; ++r) {
+                cm[r] = *reinterpret_cast<const uint32_t*>(m + (k0 + r) * kAdBlock + 4 * lane);
+                cv[r] = *reinterpret_cast<const uint32_t*>(v + (k0 + r) * kAdBlock + 4 * lane);
+                em[r] = m[t.n + k0 + r];
+                ev[r] = v[t.n + k0 + r];
+            }
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const int bm = code_base(em[r], kDepthM), bv = code_base(ev[r], kDepthV);
+                const int64_t e0 = (k0 + r) * kAdBlock + 4 * lane;
+                *reinterpret_cast<float4*>(om + e0) =
+                    make_float4(decode_m(cm[r] & 255u, bm), decode_m(cm[r] >> 8 & 255u, bm),
+                                decode_m(cm[r] >> 16 & 255u, bm), decode_m(cm[r] >> 24, bm));
+                *reinterpret_cast<float4*>(ov + e0) =
+                    make_float4(decode_v(cv[r] & 255u, bv), decode_v(cv[r] >> 8 & 255u, bv),
+                                decode_v(cv[r] >> 16 & 255u, bv), decode_v(cv[r] >> 24, bv));
+            }
+        } else {
+            for (int64_t k = k0; k < k0 + kRows && k * kAdBlock < t.n; ++k) {
+                const int bm = code_base(m[t.n + k], kDepthM), bv = code_base(v[t.n + k], kDepthV);
+                for (int64_t e = k * kAdBlock + lane; e < min(t.n, (k + 1) * kAdBlock); e += 32) {
                     om[e] = decode_m(m[e], bm);
                     ov[e] = decode_v(v[e], bv);
                 }
@@ -514,14 +658,20 @@ bool add_tensor(AdBatch<N>& b, uint64_t& units, const AdTensor& t) {
     return true;
 }
 
-unsigned grid_of(uint32_t units, const DeviceInfo& dev) {
-    const uint32_t most = (uint32_t)dev.sm_count * kAdCtas;
+unsigned grid_of(uint32_t units, int per_sm, const DeviceInfo& dev) {
+    const uint32_t most = (uint32_t)dev.sm_count * per_sm;
     return units < most ? units : most;
 }
 
-template <int N>
-int run_adamw(const pstat_adamw_tensor* tensors, int64_t n, const AdOptions& o, const DeviceInfo& dev,
-              cudaStream_t st) {
+// Bit 0: bf16 parameter, 1: bf16 gradient, 2: 8-bit moments.
+uint32_t kind_of(const pstat_adamw_tensor& t) {
+    return (t.param_dtype == PSTAT_BF16 ? 1u : 0u) | (t.grad_dtype == PSTAT_BF16 ? 2u : 0u) | (t.bits == 8 ? 4u : 0u);
+}
+
+template <int N, uint32_t kKind, bool kRandom>
+int run_kind(const pstat_adamw_tensor* tensors, int64_t n, const AdOptions& o, const DeviceInfo& dev,
+             cudaStream_t st) {
+    constexpr bool kSmall = (kKind & 4u) != 0;
     AdBatch<N> b;
     for (int64_t i = 0; i < n;) {
         b.count = 0;
@@ -529,14 +679,44 @@ int run_adamw(const pstat_adamw_tensor* tensors, int64_t n, const AdOptions& o, 
         uint64_t units = 0;
         for (; i < n; ++i) {
             const pstat_adamw_tensor& t = tensors[i];
-            if (t.n == 0) continue;
-            const uint32_t kind = (t.param_dtype == PSTAT_BF16 ? 1u : 0u) | (t.grad_dtype == PSTAT_BF16 ? 2u : 0u) |
-                                  (t.bits == 8 ? 4u : 0u) | (uint32_t)i << 3;
-            if (!add_tensor(b, units, {t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.n, 0u, kind})) break;
+            if (t.n == 0 || kind_of(t) != kKind) continue;
+            if (!add_tensor(b, units, {t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.n, 0u, (uint32_t)i})) break;
         }
-        if (b.count &&
-            launch_behind(adamw_kernel<N>, grid_of(b.units, dev), kAdThreads, 0, st, 1, b, o) != cudaSuccess)
+        if (b.count && launch_behind(adamw_kernel<N, (kKind & 1u) != 0, (kKind & 2u) != 0, kSmall, kRandom>,
+                                     grid_of(b.units, kSmall && kRandom ? kAdCtasDrawn : kAdCtas, dev), kAdThreads, 0, st, 1, b,
+                                     o) != cudaSuccess)
             return PSTAT_ERR_CUDA;
+    }
+    return PSTAT_OK;
+}
+
+template <int N>
+int run_adamw(const pstat_adamw_tensor* tensors, int64_t n, const AdOptions& o, const DeviceInfo& dev,
+              cudaStream_t st) {
+    uint32_t present = 0;
+    for (int64_t i = 0; i < n; ++i)
+        if (tensors[i].n) present |= 1u << kind_of(tensors[i]);
+    for (uint32_t kind = 0; kind < 8; ++kind) {
+        if (!(present >> kind & 1u)) continue;
+        int rc = PSTAT_OK;
+        // draws are for what is held in fewer than 32 bits
+        switch (kind | (o.random && (kind & 5u) ? 8u : 0u)) {
+            case 0: rc = run_kind<N, 0, false>(tensors, n, o, dev, st); break;
+            case 1: rc = run_kind<N, 1, false>(tensors, n, o, dev, st); break;
+            case 2: rc = run_kind<N, 2, false>(tensors, n, o, dev, st); break;
+            case 3: rc = run_kind<N, 3, false>(tensors, n, o, dev, st); break;
+            case 4: rc = run_kind<N, 4, false>(tensors, n, o, dev, st); break;
+            case 5: rc = run_kind<N, 5, false>(tensors, n, o, dev, st); break;
+            case 6: rc = run_kind<N, 6, false>(tensors, n, o, dev, st); break;
+            case 7: rc = run_kind<N, 7, false>(tensors, n, o, dev, st); break;
+            case 9: rc = run_kind<N, 1, true>(tensors, n, o, dev, st); break;
+            case 11: rc = run_kind<N, 3, true>(tensors, n, o, dev, st); break;
+            case 12: rc = run_kind<N, 4, true>(tensors, n, o, dev, st); break;
+            case 13: rc = run_kind<N, 5, true>(tensors, n, o, dev, st); break;
+            case 14: rc = run_kind<N, 6, true>(tensors, n, o, dev, st); break;
+            default: rc = run_kind<N, 7, true>(tensors, n, o, dev, st); break;
+        }
+        if (rc != PSTAT_OK) return rc;
     }
     return PSTAT_OK;
 }
@@ -552,11 +732,11 @@ int run_moments(const pstat_adamw_moment* list, int64_t n, const DeviceInfo& dev
             const pstat_adamw_moment& t = list[i];
             if (t.n == 0) continue;
             if (!add_tensor(b, units, {t.out_avg, t.out_avg_sq, const_cast<void*>(t.exp_avg),
-                                       const_cast<void*>(t.exp_avg_sq), t.n, 0u, 0u}))
+                                       const_cast<void*>(t.exp_avg_sq), t.n, 0u, (uint32_t)i}))
                 break;
         }
         if (b.count &&
-            launch_behind(adamw_moments_kernel<N>, grid_of(b.units, dev), kAdThreads, 0, st, 1, b) != cudaSuccess)
+            launch_behind(adamw_moments_kernel<N>, grid_of(b.units, 8, dev), kAdThreads, 0, st, 1, b) != cudaSuccess)
             return PSTAT_ERR_CUDA;
     }
     return PSTAT_OK;
