@@ -27,30 +27,18 @@ constexpr int kF8Block = 128;
 constexpr int kQuThreads = 256;
 constexpr int kQuRows = 64;  // rows of a CTA where each has its own scale
 
-template <typename E>
-__device__ __forceinline__ void load8(const E* row, int64_t col, int64_t K, bool vector, float (&x)[8]);
-template <>
-__device__ __forceinline__ void load8(const uint16_t* row, int64_t col, int64_t K, bool vector, float (&x)[8]) {
-    if (vector && col + 8 <= K) {
-        const uint4 q = *reinterpret_cast<const uint4*>(row + col);
-        x[0] = bf2_lo(q.x), x[1] = bf2_hi(q.x), x[2] = bf2_lo(q.y), x[3] = bf2_hi(q.y);
-        x[4] = bf2_lo(q.z), x[5] = bf2_hi(q.z), x[6] = bf2_lo(q.w), x[7] = bf2_hi(q.w);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = col + i < K ? __uint_as_float((uint32_t)row[col + i] << 16) : 0.f;
-    }
+// 8 neighbouring columns, from an address on 16 bytes.
+__device__ __forceinline__ void load8(const uint16_t* at, float (&x)[8]) {
+    const uint4 q = *reinterpret_cast<const uint4*>(at);
+    x[0] = bf2_lo(q.x), x[1] = bf2_hi(q.x), x[2] = bf2_lo(q.y), x[3] = bf2_hi(q.y);
+    x[4] = bf2_lo(q.z), x[5] = bf2_hi(q.z), x[6] = bf2_lo(q.w), x[7] = bf2_hi(q.w);
 }
-template <>
-__device__ __forceinline__ void load8(const float* row, int64_t col, int64_t K, bool vector, float (&x)[8]) {
-    if (vector && col + 8 <= K) {
-        const float4 a = *reinterpret_cast<const float4*>(row + col);
-        const float4 b = *reinterpret_cast<const float4*>(row + col + 4);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = col + i < K ? row[col + i] : 0.f;
-    }
+__device__ __forceinline__ void load8(const float* at, float (&x)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(at)[0], b = reinterpret_cast<const float4*>(at)[1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
+__device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+__device__ __forceinline__ float widen(float x) { return x; }
 
 // The exponent field of a block's scale from the bits of its largest magnitude; 0 for
 // a block that is not finite.
@@ -100,10 +88,21 @@ __global__ void __launch_bounds__(kQuThreads)
     const bool in_vec = ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)(ld * (int64_t)sizeof(E))) & 15u) == 0;
     const bool out_vec = ((reinterpret_cast<uintptr_t>(q) | (uintptr_t)K) & 7u) == 0;
     float v[kIter][8];
+    // One way for all rows of the CTA: a test between two loads would keep the second waiting.
+    if (in_vec && (cb + 1) * (int64_t)kF8Block <= K && (rb + 1) * (int64_t)(kIter * 16) <= T) {
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) {
-        const int64_t r = r0 + 16 * i;
-        load8<E>(x + (r < T ? r : 0) * ld, r < T ? col : K, K, in_vec, v[i]);
+        for (int i = 0; i < kIter; ++i) load8(x + (r0 + 16 * i) * ld + col, v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+            const int64_t r = r0 + 16 * i;
+            const E* at = x + r * ld + col;
+            if (in_vec && r < T && col + 8 <= K)
+                load8(at, v[i]);
+            else
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[i][e] = r < T && col + e < K ? widen(at[e]) : 0.f;
+        }
     }
     uint32_t top[kIter];
 #pragma unroll
