@@ -1,5 +1,6 @@
-// binding.cpp -- argument marshalling of the sampling, filtered-statistics and
-// gradient-clipping entry points, as a CPython module over torch's tensors.
+// binding.cpp -- argument marshalling of the sampling, filtered-statistics,
+// gradient-clipping, optimiser, 8-bit head and beam search entry points, as a CPython
+// module over torch's tensors.
 //
 // The same marshalling as in pstat.py costs 12 to 20 us of a call there, as much
 // as the kernels of a decode step take, and 0.35 us per tensor of a gradient
@@ -36,6 +37,13 @@ struct Library {
     decltype(&pstat_grad_workspace_size) grad_workspace_size;
     decltype(&pstat_grad_norm) grad_norm;
     decltype(&pstat_clip_grad_norm) clip_grad_norm;
+    decltype(&pstat_adamw_step) adamw_step;
+    decltype(&pstat_adamw_moments) adamw_moments;
+    decltype(&pstat_fp8_quantize) fp8_quantize;
+    decltype(&pstat_fp8_logits) fp8_logits;
+    decltype(&pstat_beam_workspace_size) beam_workspace_size;
+    decltype(&pstat_beam_select) beam_select;
+    decltype(&pstat_beam_reorder) beam_reorder;
 } lib = {};
 
 const at::Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
@@ -327,6 +335,282 @@ PyObject* clip_grad_norm(PyObject* const* a, Py_ssize_t n) {
     return norm_of(a[0], a[2], a[3], true, (float)limit);
 }
 
+// ---- the optimiser's step ------------------------------------------------------------
+
+// An in-place change, for autograd to notice (inference tensors have no count).
+void count_written(PyObject* tuple) {
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(tuple); ++i) {
+        const at::Tensor* x = tensor(PyTuple_GET_ITEM(tuple, i));
+        if (!x->is_inference()) x->unsafeGetTensorImpl()->bump_version();
+    }
+}
+bool take_number(PyObject* o, double* v) {
+    if (!PyFloat_Check(o) && !PyLong_Check(o)) return false;
+    *v = PyFloat_AsDouble(o);
+    if (*v == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        return false;
+    }
+    return true;
+}
+// A contiguous tensor on `device`, of one of two types.
+const at::Tensor* take_one(PyObject* o, int device, at::ScalarType a, at::ScalarType b) {
+    const at::Tensor* t = tensor(o);
+    if (!t || !t->defined() || !t->is_cuda() || t->get_device() != device || !t->is_contiguous() ||
+        (t->scalar_type() != a && t->scalar_type() != b))
+        return nullptr;
+    return t;
+}
+int dtype_of(const at::Tensor* t) { return t->scalar_type() == at::kBFloat16 ? PSTAT_BF16 : PSTAT_F32; }
+constexpr int64_t kAdamwBlock = 128;
+int64_t codes_of(int64_t n) { return n + (n + kAdamwBlock - 1) / kAdamwBlock; }
+// Tuples of one length, not empty.
+bool take_tuples(PyObject* const* a, int count, Py_ssize_t* n) {
+    for (int i = 0; i < count; ++i)
+        if (!PyTuple_Check(a[i]) || PyTuple_GET_SIZE(a[i]) != PyTuple_GET_SIZE(a[0])) return false;
+    *n = PyTuple_GET_SIZE(a[0]);
+    return *n > 0;
+}
+
+// adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, beta1, beta2, eps, weight_decay, norm,
+//            max_norm, seed, dev_error): True.  Step, lr and seed as numbers.
+PyObject* adamw_step(PyObject* const* a, Py_ssize_t argc) {
+    Py_ssize_t n;
+    if (argc != 14 || !take_tuples(a, 4, &n)) Py_RETURN_NONE;
+    const int device = c10::cuda::current_device();
+    pstat_adamw_options o = {};
+    double max_norm = 0.0;
+    int64_t seed = 0;
+    int* err;
+    if (!take_index(a[4], &o.step) || !take_number(a[5], &o.lr) || !take_number(a[6], &o.beta1) ||
+        !take_number(a[7], &o.beta2) || !take_number(a[8], &o.eps) || !take_number(a[9], &o.weight_decay) ||
+        !take_flag(a[13], device, &err) || (a[10] == Py_None) != (a[11] == Py_None))
+        Py_RETURN_NONE;
+    if (a[10] != Py_None) {
+        const at::Tensor* norm = take_one(a[10], device, at::kFloat, at::kFloat);
+        if (!norm || norm->dim() != 0 || !take_number(a[11], &max_norm)) Py_RETURN_NONE;
+        o.norm = norm->const_data_ptr<float>();
+        o.max_norm = (float)max_norm;
+    }
+    if (a[12] != Py_None) {
+        if (!take_index(a[12], &seed)) Py_RETURN_NONE;
+        o.seed = (uint64_t)seed;
+        o.random = 1;
+    }
+    std::vector<pstat_adamw_tensor> v((size_t)n);
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        const at::Tensor* p = take_one(PyTuple_GET_ITEM(a[0], i), device, at::kBFloat16, at::kFloat);
+        const at::Tensor* g = take_one(PyTuple_GET_ITEM(a[1], i), device, at::kBFloat16, at::kFloat);
+        const at::Tensor* m = take_one(PyTuple_GET_ITEM(a[2], i), device, at::kFloat, at::kByte);
+        const at::Tensor* s = take_one(PyTuple_GET_ITEM(a[3], i), device, at::kFloat, at::kByte);
+        if (!p || !g || !m || !s || g->sizes() != p->sizes() || m->scalar_type() != s->scalar_type()) Py_RETURN_NONE;
+        const bool small = m->scalar_type() == at::kByte;
+        const int64_t size = p->numel(), want = small ? codes_of(size) : size;
+        if (m->numel() != want || s->numel() != want) Py_RETURN_NONE;
+        v[(size_t)i] = {p->mutable_data_ptr(), g->const_data_ptr(), m->mutable_data_ptr(), s->mutable_data_ptr(),
+                        size, dtype_of(p), dtype_of(g), small ? 8 : 32, 0};
+    }
+    const int rc = run([&] { return lib.adamw_step(v.data(), (int64_t)n, &o, err, stream_of(device)); });
+    if (rc != PSTAT_OK) return refuse(rc);
+    count_written(a[0]);
+    count_written(a[2]);
+    count_written(a[3]);
+    Py_RETURN_TRUE;
+}
+
+// adamw_moments(exp_avgs, exp_avg_sqs, params, out_avgs, out_avg_sqs): True.
+PyObject* adamw_moments(PyObject* const* a, Py_ssize_t argc) {
+    Py_ssize_t n;
+    if (argc != 5 || !take_tuples(a, 5, &n)) Py_RETURN_NONE;
+    const int device = c10::cuda::current_device();
+    std::vector<pstat_adamw_moment> v((size_t)n);
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        const at::Tensor* p = tensor(PyTuple_GET_ITEM(a[2], i));
+        const at::Tensor* m = take_one(PyTuple_GET_ITEM(a[0], i), device, at::kByte, at::kByte);
+        const at::Tensor* s = take_one(PyTuple_GET_ITEM(a[1], i), device, at::kByte, at::kByte);
+        const at::Tensor* om = take_one(PyTuple_GET_ITEM(a[3], i), device, at::kFloat, at::kFloat);
+        const at::Tensor* os = take_one(PyTuple_GET_ITEM(a[4], i), device, at::kFloat, at::kFloat);
+        if (!p || !p->defined() || !m || !s || !om || !os || om->sizes() != p->sizes() || os->sizes() != p->sizes() ||
+            m->numel() != codes_of(p->numel()) || s->numel() != codes_of(p->numel()))
+            Py_RETURN_NONE;
+        v[(size_t)i] = {m->const_data_ptr(), s->const_data_ptr(), om->mutable_data_ptr<float>(),
+                        os->mutable_data_ptr<float>(), p->numel()};
+    }
+    const int rc = run([&] { return lib.adamw_moments(v.data(), (int64_t)n, stream_of(device)); });
+    if (rc != PSTAT_OK) return refuse(rc);
+    count_written(a[3]);
+    count_written(a[4]);
+    Py_RETURN_TRUE;
+}
+
+// ---- the head in 8 bits ----------------------------------------------------------------
+
+constexpr int64_t kFp8Block = 128;
+int64_t blocks_of(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
+
+// fp8_quantize(x, rows, dev_error): (codes, scales)
+PyObject* fp8_quantize(PyObject* const* a, Py_ssize_t argc) {
+    Logits l;
+    int64_t rows;
+    int* err;
+    if (argc != 3 || !take_logits(a[0], l) || !take_index(a[1], &rows) || (rows != 1 && rows != kFp8Block) ||
+        !take_flag(a[2], l.device, &err))
+        Py_RETURN_NONE;
+    std::vector<at::Tensor> out(2);
+    const int rc = run([&] {
+        const int64_t r = (l.T + rows - 1) / rows, c = blocks_of(l.V);
+        out[0] = empty(*l.t, {l.T, l.V}, at::kFloat8_e4m3fn);
+        out[1] = rows != 1 ? empty(*l.t, {r, c}, at::kFloat) : empty(*l.t, {c, r}, at::kFloat).t();
+        return lib.fp8_quantize(l.t->const_data_ptr(), l.dt, l.T, l.V, l.ld, (int)rows, out[0].mutable_data_ptr(),
+                                out[1].mutable_data_ptr<float>(), out[1].stride(0), out[1].stride(1), err,
+                                stream_of(l.device));
+    });
+    if (rc != PSTAT_OK) return refuse(rc);
+    return pack(out);
+}
+
+// fp8_logits(q, q_scale, W, W_scale, bf16, dev_error): logits
+PyObject* fp8_logits(PyObject* const* a, Py_ssize_t argc) {
+    if (argc != 6 || !PyBool_Check(a[4])) Py_RETURN_NONE;
+    const int device = c10::cuda::current_device();
+    const at::Tensor* q = take_one(a[0], device, at::kFloat8_e4m3fn, at::kFloat8_e4m3fn);
+    const at::Tensor* W = take_one(a[2], device, at::kFloat8_e4m3fn, at::kFloat8_e4m3fn);
+    const at::Tensor* Ws = take_one(a[3], device, at::kFloat, at::kFloat);
+    const at::Tensor* qs = tensor(a[1]);
+    int* err;
+    if (!q || !W || !Ws || !qs || !qs->defined() || !qs->is_cuda() || qs->get_device() != device ||
+        qs->scalar_type() != at::kFloat || q->dim() != 2 || W->dim() != 2 || qs->dim() != 2 || Ws->dim() != 2 ||
+        !take_flag(a[5], device, &err))
+        Py_RETURN_NONE;
+    const int64_t T = q->size(0), K = q->size(1), V = W->size(0), c = blocks_of(K);
+    if (W->size(1) != K || qs->size(0) != T || qs->size(1) != c || Ws->size(0) != blocks_of(V) || Ws->size(1) != c)
+        Py_RETURN_NONE;
+    const bool bf16 = a[4] == Py_True;
+    at::Tensor out;
+    const int rc = run([&] {
+        out = empty(*q, {T, V}, bf16 ? at::kBFloat16 : at::kFloat);
+        return lib.fp8_logits(q->const_data_ptr(), qs->const_data_ptr<float>(), qs->stride(0), qs->stride(1),
+                              W->const_data_ptr(), Ws->const_data_ptr<float>(), T, V, K, out.mutable_data_ptr(),
+                              bf16 ? PSTAT_BF16 : PSTAT_F32, V, err, stream_of(device));
+    });
+    if (rc != PSTAT_OK) return refuse(rc);
+    return THPVariable_Wrap(std::move(out));
+}
+
+// ---- beam search ------------------------------------------------------------------------
+
+// beam_select(logits, scores, n, dev_error): (score, parent, token)
+PyObject* beam_select(PyObject* const* a, Py_ssize_t argc) {
+    Logits l;
+    int64_t n;
+    int* err;
+    if (argc != 4 || !take_logits(a[0], l) || !take_index(a[2], &n) || n < 1 || n > PSTAT_BEAM_MAX_N ||
+        !take_flag(a[3], l.device, &err))
+        Py_RETURN_NONE;
+    const at::Tensor* scores = take_one(a[1], l.device, at::kFloat, at::kFloat);
+    if (!scores || scores->dim() != 2 || scores->numel() != l.T) Py_RETURN_NONE;
+    const int64_t B = scores->size(0), beams = scores->size(1);
+    std::vector<at::Tensor> out(3);
+    const int rc = run([&] {
+        size_t bytes = 0;
+        const int fit = lib.beam_workspace_size(B, beams, l.V, l.dt, &bytes);
+        if (fit != PSTAT_OK) return fit;
+        out[0] = empty(*l.t, {B, n}, at::kFloat);
+        out[1] = empty(*l.t, {B, n}, at::kLong);
+        out[2] = empty(*l.t, {B, n}, at::kLong);
+        at::Tensor ws = empty(*l.t, {(int64_t)bytes}, at::kByte);
+        return lib.beam_select(l.t->const_data_ptr(), l.dt, B, beams, l.V, l.ld, scores->const_data_ptr<float>(), n,
+                               out[0].mutable_data_ptr<float>(), out[1].mutable_data_ptr<int64_t>(),
+                               out[2].mutable_data_ptr<int64_t>(), ws.mutable_data_ptr(), bytes, err,
+                               stream_of(l.device));
+    });
+    if (rc != PSTAT_OK) return refuse(rc);
+    return pack(out);
+}
+
+// A row of `x` and of `o` as evenly spaced runs; false where it takes more than one set.
+bool take_runs(const at::Tensor& x, const at::Tensor& o, pstat_beam_state* s) {
+    const int64_t size = (int64_t)x.element_size();
+    int64_t d = x.dim() - 1, run_size = 1;
+    for (; d > 0; --d) {
+        if (x.size(d) == 1) continue;
+        if (x.stride(d) != run_size || o.stride(d) != run_size) break;
+        run_size *= x.size(d);
+    }
+    int64_t segments = 1, sx = run_size, so = run_size;
+    bool any = false;
+    for (; d > 0; --d) {
+        if (x.size(d) == 1) continue;
+        if (!any) {
+            segments = x.size(d);
+            sx = x.stride(d);
+            so = o.stride(d);
+            any = true;
+        } else if (x.stride(d) == segments * sx && o.stride(d) == segments * so) {
+            segments *= x.size(d);
+        } else {
+            return false;
+        }
+    }
+    *s = {x.const_data_ptr(), const_cast<void*>(o.const_data_ptr()), x.stride(0) * size, o.stride(0) * size, segments,
+          sx * size, so * size, run_size * size};
+    return true;
+}
+
+// beam_reorder(states, parents, outs or None, dev_error): True, or the new tensors
+PyObject* beam_reorder(PyObject* const* a, Py_ssize_t argc) {
+    if (argc != 4 || !PyTuple_Check(a[0]) || PyTuple_GET_SIZE(a[0]) == 0) Py_RETURN_NONE;
+    const bool given = a[2] != Py_None;
+    const Py_ssize_t n = PyTuple_GET_SIZE(a[0]);
+    if (given && (!PyTuple_Check(a[2]) || PyTuple_GET_SIZE(a[2]) != n)) Py_RETURN_NONE;
+    const int device = c10::cuda::current_device();
+    const at::Tensor* parents = take_one(a[1], device, at::kLong, at::kLong);
+    int* err;
+    if (!parents || parents->dim() != 2 || parents->size(0) == 0 || !take_flag(a[3], device, &err)) Py_RETURN_NONE;
+    const int64_t B = parents->size(0), out_beams = parents->size(1);
+    std::vector<at::Tensor> made(given ? 0 : (size_t)n);
+    std::vector<const at::Tensor*> xs((size_t)n), os((size_t)n);
+    int64_t rows = -1;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        const at::Tensor* x = tensor(PyTuple_GET_ITEM(a[0], i));
+        const at::Tensor* o = given ? tensor(PyTuple_GET_ITEM(a[2], i)) : nullptr;
+        if (!x || !x->defined() || !x->is_cuda() || x->layout() != at::kStrided || x->get_device() != device ||
+            x->dim() < 1 || x->is_conj() || x->is_neg() || x->numel() == 0 || (i > 0 && x->size(0) != rows))
+            Py_RETURN_NONE;
+        rows = x->size(0);
+        if (given) {
+            if (!o || !o->defined() || !o->is_cuda() || o->layout() != at::kStrided || o->get_device() != device ||
+                o->scalar_type() != x->scalar_type() || o->dim() != x->dim() || o->size(0) != B * out_beams ||
+                o->sizes().slice(1) != x->sizes().slice(1) || o->is_conj() || o->is_neg())
+                Py_RETURN_NONE;
+            os[(size_t)i] = o;
+        }
+        xs[(size_t)i] = x;
+    }
+    if (rows % B) Py_RETURN_NONE;
+    bool taken = true;
+    const int rc = run([&] {
+        std::vector<pstat_beam_state> v((size_t)n);
+        for (size_t i = 0; i < (size_t)n; ++i) {
+            if (!given) {
+                std::vector<int64_t> shape(xs[i]->sizes().begin(), xs[i]->sizes().end());
+                shape[0] = B * out_beams;
+                made[i] = empty(*xs[i], shape, xs[i]->scalar_type());
+                os[i] = &made[i];
+            }
+            taken = taken && take_runs(*xs[i], *os[i], &v[i]);
+        }
+        if (!taken) return (int)PSTAT_OK;
+        return lib.beam_reorder(v.data(), (int64_t)n, parents->const_data_ptr<int64_t>(), B, rows / B, out_beams, err,
+                                stream_of(device));
+    });
+    if (rc != PSTAT_OK) return refuse(rc);
+    if (!taken) Py_RETURN_NONE;
+    if (!given) return pack(made);
+    count_written(a[2]);
+    Py_RETURN_TRUE;
+}
+
 // bind(addresses): the library's functions, in the order of Library.
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
     void* p[7];
@@ -351,9 +635,35 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
+// bind_more(addresses): those from adamw_step on.
+PyObject* bind_more(PyObject* const* a, Py_ssize_t n) {
+    void* p[7];
+    if (n != 7) {
+        PyErr_SetString(PyExc_TypeError, "seven addresses expected");
+        return nullptr;
+    }
+    for (int i = 0; i < 7; ++i) {
+        p[i] = PyLong_AsVoidPtr(a[i]);
+        if (!p[i]) {
+            if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "an address is null");
+            return nullptr;
+        }
+    }
+    lib.adamw_step = reinterpret_cast<decltype(lib.adamw_step)>(p[0]);
+    lib.adamw_moments = reinterpret_cast<decltype(lib.adamw_moments)>(p[1]);
+    lib.fp8_quantize = reinterpret_cast<decltype(lib.fp8_quantize)>(p[2]);
+    lib.fp8_logits = reinterpret_cast<decltype(lib.fp8_logits)>(p[3]);
+    lib.beam_workspace_size = reinterpret_cast<decltype(lib.beam_workspace_size)>(p[4]);
+    lib.beam_select = reinterpret_cast<decltype(lib.beam_select)>(p[5]);
+    lib.beam_reorder = reinterpret_cast<decltype(lib.beam_reorder)>(p[6]);
+    Py_RETURN_NONE;
+}
+
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<name>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(bind),      FAST(sample),         FAST(filtered_forward), FAST(filtered_backward),
-                         FAST(grad_norm), FAST(clip_grad_norm), {nullptr, nullptr, 0, nullptr}};
+                         FAST(grad_norm), FAST(clip_grad_norm), FAST(bind_more),    FAST(adamw_step),
+                         FAST(adamw_moments), FAST(fp8_quantize), FAST(fp8_logits), FAST(beam_select),
+                         FAST(beam_reorder), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -143,6 +143,10 @@ try:
         _lib.pstat_filter_workspace_size, _lib.pstat_sample, _lib.pstat_filtered_forward,
         _lib.pstat_filtered_backward, _lib.pstat_grad_workspace_size, _lib.pstat_grad_norm,
         _lib.pstat_clip_grad_norm)))
+    _native.bind_more(*(ctypes.cast(f, _vp).value for f in (
+        _lib.pstat_adamw_step, _lib.pstat_adamw_moments, _lib.pstat_fp8_quantize,
+        _lib.pstat_fp8_logits, _lib.pstat_beam_workspace_size, _lib.pstat_beam_select,
+        _lib.pstat_beam_reorder)))
 except ImportError:  # not built: every call takes the path below
     _native = None
 
@@ -1098,6 +1102,13 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999
     """
     params, grads = _tensor_list(params), _tensor_list(grads)
     ms, vs = _tensor_list(exp_avgs), _tensor_list(exp_avg_sqs)
+    if _native is not None:
+        got = _native.adamw_step(tuple(params), tuple(grads), tuple(ms), tuple(vs), step, lr,
+                                 betas[0], betas[1], eps, weight_decay, norm, max_norm, seed,
+                                 dev_error)
+        if got is not None:
+            _launched(got, "pstat_adamw_step")
+            return params
     n = len(params)
     if n == 0 or len(grads) != n or len(ms) != n or len(vs) != n:
         raise ValueError("params, grads, exp_avgs and exp_avg_sqs must be lists of one length, "
@@ -1140,6 +1151,13 @@ def adamw_moments(exp_avgs, exp_avg_sqs, params, *, out=None):
     """The values that 8-bit moments stand for: (exp_avg's, exp_avg_sq's), lists of
     float32 tensors of the parameters' shapes.  `out` may supply the two lists."""
     ms, vs, params = _tensor_list(exp_avgs), _tensor_list(exp_avg_sqs), _tensor_list(params)
+    if _native is not None and out is not None:
+        outs = _tensor_list(out[0]), _tensor_list(out[1])
+        got = _native.adamw_moments(tuple(ms), tuple(vs), tuple(params), tuple(outs[0]),
+                                    tuple(outs[1]))
+        if got is not None:
+            _launched(got, "pstat_adamw_moments")
+            return outs
     n = len(params)
     if n == 0 or len(ms) != n or len(vs) != n:
         raise ValueError("exp_avgs, exp_avg_sqs and params must be lists of one length, not empty")
@@ -1185,6 +1203,10 @@ def fp8_quantize(x: torch.Tensor, rows: int = 1, *, out=None, dev_error=None):
     rows lie column by column, as ``fp8_logits`` reads them).  A block with an
     infinity or NaN gets scale NaN and sets DEV_NONFINITE.  `out` may supply the two.
     """
+    if _native is not None and out is None:
+        got = _native.fp8_quantize(x, rows, dev_error)
+        if got is not None:
+            return _launched(got, "pstat_fp8_quantize")
     T, K, ld = _rows(x)
     dev = x.device
     dt = _dtype_code(x)
@@ -1219,6 +1241,11 @@ def fp8_logits(q: torch.Tensor, q_scale: torch.Tensor, W: torch.Tensor, W_scale:
     ``fp8_quantize(W, 128)`` gives them or with any others.  K is a multiple of 16.  A
     row's logits are the same bits in any batch.  `out` may supply the result (bf16 or
     float32, rows contiguous)."""
+    if (_native is not None and out is None
+            and (out_dtype is torch.bfloat16 or out_dtype is torch.float32)):
+        got = _native.fp8_logits(q, q_scale, W, W_scale, out_dtype is torch.bfloat16, dev_error)
+        if got is not None:
+            return _launched(got, "pstat_fp8_logits")
     for x, name in ((q, "q"), (W, "W")):
         if (not isinstance(x, torch.Tensor) or x.dtype != torch.float8_e4m3fn or x.dim() != 2
                 or not x.is_cuda or not x.is_contiguous()):
@@ -1276,6 +1303,10 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int, *, out=None,
     CUDA tensor of at least ``beam_workspace_size`` bytes, which calls that overlap
     on the GPU may not share.
     """
+    if _native is not None and out is None and workspace is None:
+        got = _native.beam_select(logits, scores, n, dev_error)
+        if got is not None:
+            return _launched(got, "pstat_beam_select")
     T, V, ld = _rows(logits)
     dev = logits.device
     dt = _dtype_code(logits)
@@ -1339,6 +1370,12 @@ def beam_reorder(states, parents: torch.Tensor, *, out=None, dev_error=None):
     -1 leaves its row as it was.  Returns the list of the results.
     """
     states = _tensor_list(states)
+    if _native is not None:
+        outs = None if out is None else tuple(_tensor_list(out))
+        got = _native.beam_reorder(tuple(states), parents, outs, dev_error)
+        if got is not None:
+            _launched(got, "pstat_beam_reorder")
+            return list(got if outs is None else outs)
     if not states:
         raise ValueError("states must not be empty")
     index = states[0].get_device()
