@@ -20,7 +20,9 @@
 // closer than that, in or at the end of the list, the S of both beams is summed anew from
 // exact weights (2^-40, filter_math.cuh), and the choice is made again; scores of one beam
 // differ by its logits alone and need none.
-// Bound by the records, hence by HBM, for a batch of searches; by latency for one.
+// Bound by the records, hence by HBM, for a batch of searches (64 of 16 beams over 151,936
+// bf16 columns: 65 us, 311 MB at 4.8 TB/s, of which the records are 48 us); by latency for
+// one (4 beams: 15 us, the records 5).
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -31,9 +33,7 @@
 namespace pstat {
 namespace {
 
-constexpr int kBmThreads = 1024;
-constexpr int kBmKeep = PSTAT_BEAM_MAX_N;            // places of the list that is carried along
-constexpr int kBmNew = kBmThreads - kBmKeep;         // candidates of one round of sorting
+constexpr int kBmKeep = PSTAT_BEAM_MAX_N;  // places of the list that is carried along
 // Error of c_k: kSumError of S, and logf's of 1 ulp of at most ln 2^20 (2^-20).
 constexpr float kBmError = 0x1.8p-18f;
 static_assert(kBmError >= kSumError + 0x1p-20f, "");
@@ -89,18 +89,21 @@ __device__ __forceinline__ float pair_gap(uint64_t a, uint64_t b) {
     return (x.hi - y.hi) + (x.lo - y.lo);
 }
 
+template <int kThreads>
 struct BeamShared {
+    static constexpr int kNew = kThreads - kBmKeep;  // candidates of one round of sorting
     Pair c[PSTAT_BEAM_MAX];
     float M[PSTAT_BEAM_MAX], S[PSTAT_BEAM_MAX];
-    uint64_t key[kBmThreads];
-    uint32_t at[kBmThreads];
+    uint64_t key[kThreads];
+    uint32_t at[kThreads];
     Entry list[kBmKeep];       // what the last selection kept, best first
-    uint64_t cand_key[kBmNew];
-    uint32_t cand_at[kBmNew];
+    uint32_t picked[kBmKeep];  // places of it
+    uint64_t cand_key[kNew];
+    uint32_t cand_at[kNew];
     int n_cand;
     int bad;
     unsigned long long doubtful;  // beams to be summed anew
-    unsigned long long sum[kBmThreads / 32];
+    unsigned long long sum[kThreads / 32];
     float2 table[64];
 };
 
@@ -121,15 +124,20 @@ __device__ __forceinline__ void warp_sort(Entry& e, int lane) {
         for (int m = size / 2; m; m /= 2) exchange(e, m, size == 32 || (lane & size) == 0, lane);
 }
 
-// The best `n` of one entry from every thread, in order, in sm.list.  Up to 32: sorted
+// The best `n` of the first `count` threads' entries, in order, in sm.list.  Up to 32: sorted
 // warps whose lists of 32 are merged, two by two; beyond, all are sorted.
-__device__ __noinline__ void keep_best(BeamShared& sm, Entry e, int n) {
+template <int kThreads>
+__device__ __noinline__ void keep_best(BeamShared<kThreads>& sm, Entry e, int n, int count) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    warp_sort(e, lane);
+    int warps = 1;
+    while (warps * 32 < count) warps *= 2;
+    if (warp < warps) warp_sort(e, lane);
     if (n <= 32) {
-        sm.key[threadIdx.x] = e.key;
-        sm.at[threadIdx.x] = e.at;
-        for (int left = kBmThreads / 64; left; left /= 2) {
+        if (warp < warps) {
+            sm.key[threadIdx.x] = e.key;
+            sm.at[threadIdx.x] = e.at;
+        }
+        for (int left = warps / 2; left; left /= 2) {
             __syncthreads();
             Entry a = {0, 0};
             if (warp < left) {
@@ -146,14 +154,13 @@ __device__ __noinline__ void keep_best(BeamShared& sm, Entry e, int n) {
                 sm.at[32 * warp + lane] = a.at;
             }
         }
-        __syncthreads();
     } else {
         // Sorted warps alternate in direction from here on, as a bitonic sort wants them.
-        if (warp & 1) {
+        const int total = warps * 32;
+        if ((warp & 1) && warp < warps)
             e = {__shfl_sync(0xFFFFFFFFu, e.key, 31 - lane), __shfl_sync(0xFFFFFFFFu, e.at, 31 - lane)};
-        }
-        for (int size = 64; size <= kBmThreads; size *= 2) {
-            const bool up = size == kBmThreads || (threadIdx.x & size) == 0;
+        for (int size = 64; size <= total; size *= 2) {
+            const bool up = size == total || (threadIdx.x & size) == 0;
             for (int m = size / 2; m >= 32; m /= 2) {
                 __syncthreads();
                 sm.key[threadIdx.x] = e.key;
@@ -163,77 +170,83 @@ __device__ __noinline__ void keep_best(BeamShared& sm, Entry e, int n) {
                 const Entry o = {sm.key[j], sm.at[j]};
                 if (before(o, e) == (((threadIdx.x & m) == 0) == up)) e = o;
             }
+            if (warp < warps)
 #pragma unroll
-            for (int m = 16; m; m /= 2) exchange(e, m, up, lane);
+                for (int m = 16; m; m /= 2) exchange(e, m, up, lane);
         }
         __syncthreads();
         sm.key[threadIdx.x] = e.key;
         sm.at[threadIdx.x] = e.at;
-        __syncthreads();
     }
-    if (threadIdx.x < kBmKeep)
-        sm.list[threadIdx.x] = (int)threadIdx.x < n ? Entry{sm.key[threadIdx.x], sm.at[threadIdx.x]}
-                                                    : Entry{0, 0xFFFFFFFFu};
+    __syncthreads();
+    if (threadIdx.x < kBmKeep) {
+        const bool in = (int)threadIdx.x < n && (int)threadIdx.x < warps * 32;
+        const Entry got = in ? Entry{sm.key[threadIdx.x], sm.at[threadIdx.x]} : Entry{0, 0xFFFFFFFFu};
+        sm.list[threadIdx.x] = got;
+        sm.picked[threadIdx.x] = got.key ? got.at : 0xFFFFFFFFu;
+    }
     __syncthreads();
 }
 
 // The best n of `count` candidates in sm.list.  `visit(emit)` calls emit(entry, i) for
 // all of them that this thread owns, i being the candidate's number; those that are not
 // below `least` are gathered, and sorted at once where there is room, else by rounds.
-template <typename Visit>
-__device__ __forceinline__ void select_best(BeamShared& sm, int n, int count, uint64_t least, Visit visit) {
+template <int kThreads, typename Visit>
+__device__ __forceinline__ void select_best(BeamShared<kThreads>& sm, int n, int count, uint64_t least, Visit visit) {
+    constexpr int kNew = BeamShared<kThreads>::kNew;
     if (threadIdx.x == 0) sm.n_cand = 0;
     __syncthreads();
     const uint64_t floor = max(least, (uint64_t)1);
     visit([&](const Entry& e, int) {
         if (e.key < floor) return;
         const int at = atomicAdd(&sm.n_cand, 1);
-        if (at < kBmNew) {
+        if (at < kNew) {
             sm.cand_key[at] = e.key;
             sm.cand_at[at] = e.at;
         }
     });
     __syncthreads();
     const int found = sm.n_cand;
-    __syncthreads();
-    if (found <= kBmNew) {
+    if (found <= kNew) {
         Entry e = {0, 0xFFFFFFFFu};
         if ((int)threadIdx.x < found) e = {sm.cand_key[threadIdx.x], sm.cand_at[threadIdx.x]};
-        keep_best(sm, e, n);
+        keep_best(sm, e, n, found);
         return;
     }
-    if (threadIdx.x < kBmKeep) sm.list[threadIdx.x] = {0, 0xFFFFFFFFu};
-    for (int i0 = 0; i0 < count; i0 += kBmNew) {
+    // What `visit` reads of the list before (sm.picked) has to last through the rounds.
+    Entry kept = {0, 0xFFFFFFFFu};
+    const uint32_t picked = threadIdx.x < kBmKeep ? sm.picked[threadIdx.x] : 0u;
+    for (int i0 = 0; i0 < count; i0 += kNew) {
         __syncthreads();
-        if (threadIdx.x < kBmNew) sm.cand_key[threadIdx.x] = 0;
+        if (threadIdx.x < kBmKeep) sm.picked[threadIdx.x] = picked;
+        if ((int)threadIdx.x < kNew) sm.cand_key[threadIdx.x] = 0;
         __syncthreads();
         visit([&](const Entry& e, int i) {
-            if (i >= i0 && i < i0 + kBmNew) {
+            if (i >= i0 && i < i0 + kNew) {
                 sm.cand_key[i - i0] = e.key;
                 sm.cand_at[i - i0] = e.at;
             }
         });
         __syncthreads();
-        Entry e = {0, 0xFFFFFFFFu};
-        if (threadIdx.x >= kBmNew)
-            e = sm.list[threadIdx.x - kBmNew];
-        else if (sm.cand_key[threadIdx.x])
-            e = {sm.cand_key[threadIdx.x], sm.cand_at[threadIdx.x]};
-        __syncthreads();
-        keep_best(sm, e, n);
+        Entry e = kept;
+        if ((int)threadIdx.x < kNew)
+            e = sm.cand_key[threadIdx.x] ? Entry{sm.cand_key[threadIdx.x], sm.cand_at[threadIdx.x]}
+                                         : Entry{0, 0xFFFFFFFFu};
+        keep_best(sm, e, n, kThreads);
+        if ((int)threadIdx.x >= kNew) kept = sm.list[threadIdx.x - kNew];
     }
 }
 
 // ln S of a beam's row from exact weights: every thread of the CTA.
-template <typename E>
-__device__ __noinline__ void sum_anew(BeamShared& sm, const BeamArgs& a, int64_t t, int k, float score) {
+template <typename E, int kThreads>
+__device__ __noinline__ void sum_anew(BeamShared<kThreads>& sm, const BeamArgs& a, int64_t t, int k, float score) {
     const E* row = static_cast<const E*>(a.f.logits) + t * a.f.ld;
     const float M = sm.M[k];
     const int scale = fixed_scale(sm.S[k] * (1.f + 2.f * kSumError));
     const TempScale one = temp_scale(1.f);
     constexpr int kVec = Elem<E>::kVec;
     unsigned long long sum = 0;
-    for (int c = (int)threadIdx.x * kVec; c < (int)a.f.V; c += kBmThreads * kVec) {
+    for (int c = (int)threadIdx.x * kVec; c < (int)a.f.V; c += kThreads * kVec) {
         const int col[1] = {c};
         float x[1][kVec];
         load_columns<E, 1>(row, col, (int)a.f.V, x);
@@ -249,7 +262,7 @@ __device__ __noinline__ void sum_anew(BeamShared& sm, const BeamArgs& a, int64_t
     __syncthreads();
     if (threadIdx.x == 0) {
         sum = 0;
-        for (int w = 0; w < kBmThreads / 32; ++w) sum += sm.sum[w];
+        for (int w = 0; w < kThreads / 32; ++w) sum += sm.sum[w];
         const double lnS = log((double)sum) - scale * 0.69314718055994530942;
         const float hi = (float)lnS;
         Pair c = pair_sum(pair_sum({score, 0.f}, -M), -hi);
@@ -259,10 +272,11 @@ __device__ __noinline__ void sum_anew(BeamShared& sm, const BeamArgs& a, int64_t
     __syncthreads();
 }
 
-template <typename E>
-__global__ void __launch_bounds__(kBmThreads, 1) beam_finish_kernel(const __grid_constant__ BeamArgs a) {
+template <typename E, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) beam_finish_kernel(const __grid_constant__ BeamArgs a) {
     extern __shared__ __align__(16) uint8_t raw[];
-    BeamShared& sm = *reinterpret_cast<BeamShared*>(raw);
+    using Shared = BeamShared<kThreads>;
+    Shared& sm = *reinterpret_cast<Shared*>(raw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int beams = a.beams, n = a.n, V = (int)a.f.V, chunks = a.f.chunks;
     constexpr int kVec = Elem<E>::kVec;
@@ -277,7 +291,7 @@ __global__ void __launch_bounds__(kBmThreads, 1) beam_finish_kernel(const __grid
     const E* maxima = static_cast<const E*>(after_wait(a.f.group_max)) + t0 * chunks * 32;
     const E* logits = static_cast<const E*>(a.f.logits) + t0 * a.f.ld;
 
-    for (int k = warp; k < beams; k += kBmThreads / 32) {
+    for (int k = warp; k < beams; k += kThreads / 32) {
         const float s = scores[k];
         const float3 r = fold_records(records + (int64_t)k * chunks, chunks, kLog2e, lane);
         if (lane == 0) {
@@ -312,7 +326,7 @@ __global__ void __launch_bounds__(kBmThreads, 1) beam_finish_kernel(const __grid
 
     const int groups = chunks * 32;  // of a row
     const int total = beams * groups;
-    const int run = ((total + kBmThreads - 1) / kBmThreads + 7) / 8 * 8;
+    const int run = ((total + kThreads - 1) / kThreads + 7) / 8 * 8;
     // The maxima of 8 groups from g, a multiple of 8: of one row, whose groups are a
     // multiple of 32.
     auto load8 = [&](int g, float (&x)[8]) {
@@ -327,67 +341,69 @@ __global__ void __launch_bounds__(kBmThreads, 1) beam_finish_kernel(const __grid
             x[4] = y[0], x[5] = y[1], x[6] = y[2], x[7] = y[3];
         }
     };
+    const int g0 = min(total, (int)threadIdx.x * run), g1 = min(total, g0 + run), k0 = g0 / groups;
+    // Calls f(maxima, their first group, beam) for this thread's run.
+    auto each_of_run = [&](auto f) {
+        int k = k0;
+        for (int g = g0; g < g1; g += 8) {
+            float x[8];
+            load8(g, x);
+            k += g >= (k + 1) * groups;
+            f(x, g, k);
+        }
+    };
+    constexpr int kVecs = kGroup / kVec;
+    // Calls f(columns' logits, their first column, beam, candidate number) for this thread's
+    // share of the picked groups.
+    auto each_of_groups = [&](auto f) {
+        for (int i = threadIdx.x; i < n * kVecs; i += kThreads) {
+            const uint32_t g = sm.picked[i / kVecs];
+            if (g == 0xFFFFFFFFu) continue;
+            const int k = (int)g / groups;
+            const int col[1] = {((int)g - k * groups) * kGroup + i % kVecs * kVec};
+            if (col[0] >= V) continue;
+            float x[1][kVec];
+            load_columns<E, 1>(logits + (int64_t)k * a.f.ld, col, V, x);
+            f(x[0], col[0], k, kVec * i);
+        }
+    };
     unsigned long long exact = 0;  // beams that were summed anew
     while (true) {
-        {
-            Entry e = {0, 0xFFFFFFFFu};
-            const int g1 = min(total, ((int)threadIdx.x + 1) * run);
-            for (int g = (int)threadIdx.x * run; g < g1; g += 8) {
+        Entry mine = {0, 0xFFFFFFFFu};
+        each_of_run([&](const float(&x)[8], int, int k) {
+            const float m = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
+                                  fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+            const uint64_t key = score_key(sm.c[k], m);
+            if (key > mine.key) mine = {key, threadIdx.x};
+        });
+        keep_best(sm, mine, n, kThreads);
+        // groups of those runs
+        const int eights = run / 8;
+        select_best(sm, n, n * run, sm.list[n - 1].key, [&](auto emit) {
+            for (int i = threadIdx.x; i < n * eights; i += kThreads) {
+                const uint32_t r = sm.picked[i / eights];
+                const int g = r == 0xFFFFFFFFu ? total : (int)r * run + i % eights * 8;
+                if (g >= total) continue;
                 float x[8];
                 load8(g, x);
-                const float m = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
-                                      fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-                const uint64_t key = score_key(sm.c[g / groups], m);
-                if (key > e.key) e = {key, threadIdx.x};
+                const Pair c = sm.c[g / groups];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) emit(Entry{score_key(c, x[q]), (uint32_t)(g + q)}, 8 * i + q);
             }
-            keep_best(sm, e, n);
-        }
-        // groups of those runs
-        {
-            const uint64_t least = sm.list[n - 1].key;
-            __shared__ uint32_t runs[kBmKeep];
-            if ((int)threadIdx.x < n) runs[threadIdx.x] = sm.list[threadIdx.x].key ? sm.list[threadIdx.x].at : 0xFFFFFFFFu;
-            __syncthreads();
-            const int eights = run / 8;
-            select_best(sm, n, n * run, least, [&](auto emit) {
-                for (int i = threadIdx.x; i < n * eights; i += kBmThreads) {
-                    const uint32_t r = runs[i / eights];
-                    const int g = r == 0xFFFFFFFFu ? total : (int)r * run + i % eights * 8;
-                    if (g >= total) continue;
-                    float x[8];
-                    load8(g, x);
-                    const Pair c = sm.c[g / groups];
+        });
+        // columns of those groups, whose list is wanted again below
+        const uint32_t picked = threadIdx.x < kBmKeep ? sm.picked[threadIdx.x] : 0u;
+        select_best(sm, n, n * kGroup, sm.list[n - 1].key, [&](auto emit) {
+            each_of_groups([&](const float(&x)[kVec], int col, int k, int i) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) emit(Entry{score_key(c, x[q]), (uint32_t)(g + q)}, 8 * i + q);
-                }
+                for (int q = 0; q < kVec; ++q)
+                    emit(Entry{score_key(sm.c[k], x[q]), (uint32_t)(k * V + col + q)}, i + q);
             });
-        }
-        // columns of those groups
-        __shared__ uint32_t picked[kBmKeep];
-        {
-            const uint64_t least = sm.list[n - 1].key;
-            if ((int)threadIdx.x < n)
-                picked[threadIdx.x] = sm.list[threadIdx.x].key ? sm.list[threadIdx.x].at : 0xFFFFFFFFu;
-            __syncthreads();
-            constexpr int kVecs = kGroup / kVec;
-            select_best(sm, n, n * kGroup, least, [&](auto emit) {
-                for (int i = threadIdx.x; i < n * kVecs; i += kBmThreads) {
-                    const uint32_t g = picked[i / kVecs];
-                    if (g == 0xFFFFFFFFu) continue;
-                    const int k = (int)g / groups;
-                    const int col[1] = {((int)g - k * groups) * kGroup + i % kVecs * kVec};
-                    if (col[0] >= V) continue;
-                    float x[1][kVec];
-                    load_columns<E, 1>(logits + (int64_t)k * a.f.ld, col, V, x);
-#pragma unroll
-                    for (int q = 0; q < kVec; ++q)
-                        emit(Entry{score_key(sm.c[k], x[0][q]), (uint32_t)(k * V + col[0] + q)}, kVec * i + q);
-                }
-            });
-        }
+        });
         if (beams == 1) break;
         // Beams whose sums' errors could change the list.
         if (threadIdx.x == 0) sm.doubtful = 0;
+        if (threadIdx.x < kBmKeep) sm.picked[threadIdx.x] = picked;
         __syncthreads();
         const uint64_t last = sm.list[n - 1].key;  // 0: every continuation is in the list
         constexpr float kTol = 2.f * kBmError;
@@ -407,27 +423,15 @@ __global__ void __launch_bounds__(kBmThreads, 1) beam_finish_kernel(const __grid
             auto outside = [&](uint64_t key, int row) {
                 if (key && key <= last && pair_gap(last, key) <= kTol) doubt(border, row);
             };
-            const int g1 = min(total, ((int)threadIdx.x + 1) * run);
-            for (int g = (int)threadIdx.x * run; g < g1; g += 8) {
-                float x[8];
-                load8(g, x);
-                const int k = g / groups;
-                const Pair c = sm.c[k];
+            if (mine.key && (mine.key >= last || pair_gap(last, mine.key) <= kTol))
+                each_of_run([&](const float(&x)[8], int, int k) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) outside(score_key(c, x[q]), k);
-            }
-            constexpr int kVecs = kGroup / kVec;
-            for (int i = threadIdx.x; i < n * kVecs; i += kBmThreads) {
-                const uint32_t g = picked[i / kVecs];
-                if (g == 0xFFFFFFFFu) continue;
-                const int k = (int)g / groups;
-                const int col[1] = {((int)g - k * groups) * kGroup + i % kVecs * kVec};
-                if (col[0] >= V) continue;
-                float x[1][kVec];
-                load_columns<E, 1>(logits + (int64_t)k * a.f.ld, col, V, x);
+                    for (int q = 0; q < 8; ++q) outside(score_key(sm.c[k], x[q]), k);
+                });
+            each_of_groups([&](const float(&x)[kVec], int, int k, int) {
 #pragma unroll
-                for (int q = 0; q < kVec; ++q) outside(score_key(sm.c[k], x[0][q]), k);
-            }
+                for (int q = 0; q < kVec; ++q) outside(score_key(sm.c[k], x[q]), k);
+            });
         }
         __syncthreads();
         const unsigned long long rows = sm.doubtful;
@@ -466,13 +470,23 @@ int check_beams(pstat_dtype dt, int64_t B, int64_t beams, int64_t V) {
     return PSTAT_OK;
 }
 
-template <typename E>
+template <typename E, int kThreads>
 cudaError_t launch_finish(const BeamArgs& a, unsigned B, cudaStream_t st) {
     static ContextSeen configured;
-    const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(beam_finish_kernel<E>),
-                                            (int)sizeof(BeamShared), configured);
+    const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(beam_finish_kernel<E, kThreads>),
+                                            (int)sizeof(BeamShared<kThreads>), configured);
     if (e != cudaSuccess) return e;
-    return launch_behind(beam_finish_kernel<E>, B, kBmThreads, sizeof(BeamShared), st, 1, a);
+    return launch_behind(beam_finish_kernel<E, kThreads>, B, kThreads, sizeof(BeamShared<kThreads>), st, 1, a);
+}
+
+// A search's time is latency: sorting the threads' best takes longer with more of them,
+// reading the maxima with fewer.  Where 256 threads have 8 maxima each at most (and the
+// list leaves room for its candidates) they take 13.0 us a call against 15.1 with 1024 (33
+// searches, 3 beams of 10,007); with 64 searches of 8 beams of 152,064 it is 48 against 39.
+template <typename E>
+cudaError_t launch_finish_of(const BeamArgs& a, unsigned B, cudaStream_t st) {
+    if (a.n <= 32 && (int64_t)a.beams * a.f.chunks * 32 <= 256 * 8) return launch_finish<E, 256>(a, B, st);
+    return launch_finish<E, 1024>(a, B, st);
 }
 
 }  // namespace
@@ -530,7 +544,8 @@ int pstat_beam_select(const void* logits, pstat_dtype dt, int64_t B, int64_t bea
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = launch_row_records(a.f, dt, dev, st);
     if (e != cudaSuccess) return PSTAT_ERR_CUDA;
-    e = dt == PSTAT_BF16 ? launch_finish<uint16_t>(a, (unsigned)B, st) : launch_finish<float>(a, (unsigned)B, st);
+    e = dt == PSTAT_BF16 ? launch_finish_of<uint16_t>(a, (unsigned)B, st)
+                         : launch_finish_of<float>(a, (unsigned)B, st);
     return e == cudaSuccess ? PSTAT_OK : PSTAT_ERR_CUDA;
 }
 
