@@ -585,7 +585,8 @@ PSTAT_API int pstat_adamw_moments(const pstat_adamw_moment* list, int64_t n, pst
  *   out_q    [T, K] e4m3, rows of K bytes.
  *   out_scale  float, that of row block i and column block j at
  *            out_scale[i * scale_row + j * scale_col]; ceil(T / rows) by
- *            ceil(K / 128).
+ *            ceil(K / 128), each in a place of its own (PSTAT_ERR_SHAPE).
+ * Outputs that overlap one another or x are refused (PSTAT_ERR_PARAM).
  */
 PSTAT_API int pstat_fp8_quantize(const void* x, pstat_dtype dt, int64_t T, int64_t K, int64_t ld,
                                  int rows, void* out_q, float* out_scale, int64_t scale_row,
@@ -601,7 +602,7 @@ PSTAT_API int pstat_fp8_quantize(const void* x, pstat_dtype dt, int64_t T, int64
  *   W        [V, K] e4m3, W_scale [ceil(V / 128), ceil(K / 128)] row-major: any
  *            scales, powers of two or not.
  *   q and W 16-byte aligned, K a multiple of 16.
- *   out      [T, ld_out] of out_dt.
+ *   out      [T, ld_out] of out_dt; one that overlaps an input is refused (PSTAT_ERR_PARAM).
  */
 PSTAT_API int pstat_fp8_logits(const void* q, const float* q_scale, int64_t scale_row,
                                int64_t scale_col, const void* W, const float* W_scale, int64_t T,
@@ -614,9 +615,9 @@ PSTAT_API int pstat_fp8_logits(const void* q, const float* q_scale, int64_t scal
  * k]; its continuation by token v scores s + z_v - M - ln S.  Of the beams x V
  * continuations the n best, in descending order; equal ones by the lowest (k, v).
  * Scores are compared as they are in exact arithmetic, to 2^-40 of the larger of
- * |score| and 1; what comes out is within 6e-6 + 2^-24 |score| of the score.  A score of -inf, and a row whose logits are all -inf, is a
- * beam without continuations; places that none is left for get score -inf, parent
- * and token -1.  A score of NaN or +inf, or a row with a NaN or +inf logit (of a
+ * |score| and 1; what comes out is within 6e-6 + 2^-24 |score| of the score.  A score of
+ * -inf, and a row whose logits are all -inf, is a beam without continuations; places
+ * that none is left for get score -inf, parent and token -1.  A score of NaN or +inf, or a row with a NaN or +inf logit (of a
  * beam with a finite score), leaves its search undefined: PSTAT_DEV_EMPTY_ROW, scores
  * NaN, parents and tokens -1.
  *   logits      [B beams, ld] of dtype `dt`, V <= PSTAT_FILTER_MAX_V; ld 0: one row for
@@ -625,6 +626,8 @@ PSTAT_API int pstat_fp8_logits(const void* q, const float* q_scale, int64_t scal
  *   n           at most PSTAT_BEAM_MAX_N; beams at most PSTAT_BEAM_MAX.
  *   out_score   [B, n] float, out_parent (k) and out_token (v) [B, n] int64.
  *   workspace   16-byte aligned, at least pstat_beam_workspace_size(...) bytes.
+ * Outputs and workspace may overlap nothing else of the call (PSTAT_ERR_PARAM) but, for
+ * n == beams, out_score == scores.
  */
 #define PSTAT_BEAM_MAX 64
 #define PSTAT_BEAM_MAX_N 128

@@ -83,7 +83,9 @@ struct AdScalars {
 
 // 32 bits that are as good as random, from a counter under a key: two rounds of
 // multiplications by odd constants (the fractions of the roots of 2 and 3) and shifts,
-// with the key before and between them.
+// with the key before and between them.  Each half is even over counters, keys and
+// neighbours, so that a moment's mean is kept; the halves of one word (the draws of an
+// element's two moments) depend on one another: a bit agrees in 36 to 64 of a hundred.
 __device__ __forceinline__ uint32_t mix32(uint32_t x, uint32_t key) {
     x ^= key;
     x ^= x >> 16;

@@ -519,6 +519,22 @@ int pstat_beam_select(const void* logits, pstat_dtype dt, int64_t B, int64_t bea
     const BeamWorkspace w = beam_workspace(B * beams, V, dt);
     if (!workspace || ws_bytes < w.total) return PSTAT_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return PSTAT_ERR_ALIGN;
+    // A search's scores are read by the CTA that writes its results, before it writes them.
+    const bool in_place = out_score == scores && n == beams;
+    const struct {
+        const void* p;
+        int64_t bytes;
+        bool written;
+    } range[] = {{workspace, (int64_t)w.total, true},
+                 {out_score, B * n * 4, true},
+                 {out_parent, B * n * 8, true},
+                 {out_token, B * n * 8, true},
+                 {logits, extent_bytes(B * beams, ld, V, dt == PSTAT_BF16 ? 2 : 4), false},
+                 {scores, in_place ? 0 : B * beams * 4, false}};
+    for (int i = 0; i < 6; ++i)
+        for (int j = i + 1; j < 6; ++j)
+            if (range[i].written && ranges_meet(range[i].p, range[i].bytes, range[j].p, range[j].bytes))
+                return PSTAT_ERR_PARAM;
     DeviceInfo dev;
     rc = device_info(&dev);
     if (rc != PSTAT_OK) return rc;

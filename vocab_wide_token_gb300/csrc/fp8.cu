@@ -15,6 +15,7 @@ namespace pstat {
 namespace {
 
 constexpr int kF8Block = 128;
+constexpr int64_t kF8MaxStride = (int64_t)1 << 31;  // of scales: products with counts fit
 
 // ---------------------------------------------------------------------------
 // Quantising.  A scale is the least power of two with max|x| <= 448 s: dividing by it is
@@ -713,7 +714,17 @@ int pstat_fp8_quantize(const void* x, pstat_dtype dt, int64_t T, int64_t K, int6
     if (!aligned_to(x, dt == PSTAT_BF16 ? 2 : 4) || !aligned_to(out_scale, 4)) return PSTAT_ERR_ALIGN;
     const int64_t cols = (K + kF8Block - 1) / kF8Block;
     const int64_t row_blocks = rows == 1 ? (T + kQuRows - 1) / kQuRows : (T + kF8Block - 1) / kF8Block;
-    if (scale_row < 1 || scale_col < 1 || cols * row_blocks > INT32_MAX) return PSTAT_ERR_SHAPE;
+    if (scale_row < 1 || scale_col < 1 || scale_row > kF8MaxStride || scale_col > kF8MaxStride ||
+        cols * row_blocks > INT32_MAX)
+        return PSTAT_ERR_SHAPE;
+    const int64_t scale_rows = (T + rows - 1) / rows;  // two scales in one place?
+    if (scale_row <= (cols - 1) * scale_col && scale_col <= (scale_rows - 1) * scale_row)
+        return PSTAT_ERR_SHAPE;
+    const int64_t x_bytes = extent_bytes(T, ld, K, dt == PSTAT_BF16 ? 2 : 4);
+    const int64_t scale_bytes = extent_bytes(scale_rows, scale_row, (cols - 1) * scale_col + 1, 4);
+    if (ranges_meet(out_q, T * K, x, x_bytes) || ranges_meet(out_scale, scale_bytes, x, x_bytes) ||
+        ranges_meet(out_q, T * K, out_scale, scale_bytes))
+        return PSTAT_ERR_PARAM;
     DeviceInfo dev;
     const int rc = device_info(&dev);
     if (rc != PSTAT_OK) return rc;
@@ -734,13 +745,19 @@ int pstat_fp8_logits(const void* q, const float* q_scale, int64_t scale_row, int
                      int64_t ld_out, int* dev_error, pstat_stream_t stream) {
     if (out_dt != PSTAT_F32 && out_dt != PSTAT_BF16) return PSTAT_ERR_DTYPE;
     if (T < 0 || V < 1 || K < 16 || K % 16 || K > (1 << 24) || ld_out < V || T > INT32_MAX / 2 || V > INT32_MAX / 2 ||
-        scale_row < 0 || scale_col < 0)
+        scale_row < 0 || scale_col < 0 || scale_row > kF8MaxStride || scale_col > kF8MaxStride)
         return PSTAT_ERR_SHAPE;
     if (T == 0) return PSTAT_OK;
     if (!q || !q_scale || !W || !W_scale || !out) return PSTAT_ERR_NULLPTR;
     if (!aligned_to(q, 16) || !aligned_to(W, 16) || !aligned_to(q_scale, 4) || !aligned_to(W_scale, 4) ||
         !aligned_to(out, out_dt == PSTAT_BF16 ? 2 : 4))
         return PSTAT_ERR_ALIGN;
+    const int64_t cols = (K + kF8Block - 1) / kF8Block;
+    const int64_t out_bytes = extent_bytes(T, ld_out, V, out_dt == PSTAT_BF16 ? 2 : 4);
+    if (ranges_meet(out, out_bytes, q, T * K) || ranges_meet(out, out_bytes, W, V * K) ||
+        ranges_meet(out, out_bytes, q_scale, extent_bytes(T, scale_row, (cols - 1) * scale_col + 1, 4)) ||
+        ranges_meet(out, out_bytes, W_scale, (V + kF8Block - 1) / kF8Block * cols * 4))
+        return PSTAT_ERR_PARAM;
     DeviceInfo dev;
     const int rc = device_info(&dev);
     if (rc != PSTAT_OK) return rc;

@@ -28,6 +28,17 @@ constexpr size_t kChunkRecordBytes = 16;  // (m, s, u, unused) fp32
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// Bytes that `rows` runs of `width` elements, `stride` apart, reach over (2^62 at most).
+inline int64_t extent_bytes(int64_t rows, int64_t stride, int64_t width, int64_t size) {
+    const __int128 n = ((__int128)(rows - 1) * stride + width) * size;
+    return n < ((__int128)1 << 62) ? (int64_t)n : (int64_t)1 << 62;
+}
+// Whether two ranges of bytes have one in common.
+inline bool ranges_meet(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a_bytes > 0 && b_bytes > 0 && x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
 // Workspace layout of pstat_forward / pstat_backward.
 struct StatsWorkspace {
     size_t chunk_stats_off;  // [T, n_chunks] float4

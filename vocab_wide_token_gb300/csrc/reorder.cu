@@ -147,16 +147,20 @@ bool overlap(const Extent& a, const Extent& b) {
 
 constexpr int64_t kMaxStride = (int64_t)1 << 46;
 
-int check_states(const pstat_beam_state* states, int64_t n, int64_t B, int64_t beams, int64_t out_beams,
-                 bool* in_place) {
+int check_states(const pstat_beam_state* states, int64_t n, const int64_t* parents, int64_t B, int64_t beams,
+                 int64_t out_beams, bool* in_place) {
     if (n < 0 || n > (1 << 20) || B < 0 || B > PSTAT_FILTER_MAX_T || beams < 1 || beams > PSTAT_BEAM_MAX ||
         out_beams < 1 || out_beams > PSTAT_BEAM_MAX_N)
         return PSTAT_ERR_SHAPE;
     if (n > 0 && !states) return PSTAT_ERR_NULLPTR;
     if (n == 0 || B == 0) return PSTAT_OK;
-    std::unique_ptr<Extent[]> v(new (std::nothrow) Extent[2 * n]);
+    if (!parents) return PSTAT_ERR_NULLPTR;
+    if (reinterpret_cast<uintptr_t>(parents) & 7u) return PSTAT_ERR_ALIGN;
+    std::unique_ptr<Extent[]> v(new (std::nothrow) Extent[2 * n + 1]);
     if (!v) return PSTAT_ERR_WORKSPACE;
-    int64_t m = 0;
+    const int64_t parent_bytes = 8 * B * out_beams;
+    v[0] = {reinterpret_cast<uintptr_t>(parents), 1, parent_bytes, 1, parent_bytes, parent_bytes, false};
+    int64_t m = 1;
     bool first = true;
     for (int64_t i = 0; i < n; ++i) {
         const pstat_beam_state& s = states[i];
@@ -168,6 +172,11 @@ int check_states(const pstat_beam_state* states, int64_t n, int64_t B, int64_t b
         for (int64_t stride : {s.row_stride, s.out_row_stride, s.seg_stride, s.out_seg_stride})
             if (stride < 0 || stride > kMaxStride) return PSTAT_ERR_SHAPE;
         // runs of a row, and rows, must not overlap among themselves where they are written
+        for (int64_t stride : {s.seg_stride, s.out_seg_stride})
+            if (stride > 0 && s.segments - 1 > kMaxStride / stride) return PSTAT_ERR_SHAPE;
+        if ((s.row_stride > 0 && B * beams - 1 > kMaxStride / s.row_stride) ||
+            (s.out_row_stride > 0 && B * out_beams - 1 > kMaxStride / s.out_row_stride))
+            return PSTAT_ERR_SHAPE;
         const int64_t out_extent = (s.segments - 1) * s.out_seg_stride + s.seg_bytes;
         const bool nested = (s.segments == 1 || s.out_seg_stride >= s.seg_bytes) && s.out_row_stride >= out_extent;
         const bool across = s.segments > 1 && s.out_row_stride >= s.seg_bytes &&
@@ -252,11 +261,9 @@ extern "C" int pstat_beam_reorder(const pstat_beam_state* states, int64_t n_stat
                                   int64_t B, int64_t beams, int64_t out_beams, int* dev_error,
                                   pstat_stream_t stream) {
     bool in_place = false;
-    int rc = check_states(states, n_states, B, beams, out_beams, &in_place);
+    int rc = check_states(states, n_states, parents, B, beams, out_beams, &in_place);
     if (rc != PSTAT_OK) return rc;
     if (n_states == 0 || B == 0) return PSTAT_OK;
-    if (!parents) return PSTAT_ERR_NULLPTR;
-    if (reinterpret_cast<uintptr_t>(parents) & 7u) return PSTAT_ERR_ALIGN;
     DeviceInfo dev;
     rc = device_info(&dev);
     if (rc != PSTAT_OK) return rc;
