@@ -6,8 +6,11 @@
 //
 // One read and one write of everything, so bound by HBM: 28 bytes an element in fp32,
 // 10 with bf16 parameters and gradients and 8-bit moments.  There the instructions weigh
-// as much as the bytes: 10 bytes at 6.7 TB/s leave an SM about 55 instructions for
-// each element, and decoding, drawing, encoding and the step take most of them.
+// more than the bytes: 10 bytes at 6.7 TB/s leave an SM about 55 instructions for each
+// element, and decoding, drawing (18), encoding and the step are 82, or 60 rounded to nearest.
+// 60 million elements, with bf16 parameters and gradients unless said otherwise:
+//   32-bit moments  202 us, 6.5 TB/s; all in fp32 260 us, 6.5 TB/s
+//   8-bit moments   173 us drawn, 3.5 TB/s; 123 us to nearest, 4.9 TB/s; fp32 drawn 172 us
 //
 // 8-bit moments.  Codes of three bits of mantissa under an exponent that reaches a fixed
 // number of binary orders below the largest of a block of 128: 4 bits and a sign for m
@@ -39,7 +42,8 @@ namespace {
 constexpr int kAdThreads = 256;
 constexpr int kAdBlock = 128;                   // elements that share an exponent: a warp's
 constexpr int kAdUnit = 4096;                   // elements of one tensor, a CTA's turn
-constexpr int kAdCtas = 2, kAdCtasDrawn = 4;                      // per SM
+constexpr int kAdUnitSmall = 512;               // of one with 8-bit moments, a warp's
+constexpr int kAdCtas = 2;                      // per SM
 constexpr int kAdBatch = 600;                   // tensors of one launch (they travel as its arguments)
 constexpr int kDepthM = 14, kDepthV = 30;       // binary orders below a block's largest
 
@@ -217,6 +221,10 @@ struct AdView {
     int64_t n;
     uint32_t key, key_p;
 };
+__device__ __forceinline__ AdView view_of(const AdTensor& at, const AdScalars& s) {
+    const uint32_t key = mix32(s.seed_key ^ at.place, 0xDAA66D2Bu);
+    return {at.p, after_wait(at.g), at.m, at.v, at.n, key, key ^ 0xA54FF53Au};
+}
 __device__ __forceinline__ uint32_t draw_of(const AdView& t, int64_t k) {
     return mix32((uint32_t)k, t.key + (uint32_t)(k >> 32) * 0x9E3779B9u);
 }
@@ -294,200 +302,333 @@ __device__ __forceinline__ float updated_fast(float p, float m, float v, const A
     return fmaf(-s.size, step * m, p * s.decay);
 }
 
-// kRows whole blocks whose tensors start on the vectors' sizes: element 128 b + 4 lane + e is a
-// lane's e-th.  All loads come before the first use.  What is rare in a block takes a branch
-// of its own that the warp goes through together: codes of zero or NaN, values below the
-// least code; and infinities and NaN among the results leave the block to step_block.
+// Copies 16 bytes to shared memory in the background, or none.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// A byte as a word that nothing has to be done with when it comes.
+__device__ __forceinline__ uint32_t load_byte(const uint8_t* at) {
+    uint32_t x;
+    asm volatile("ld.global.u8 %0, [%1];" : "=r"(x) : "l"(at) : "memory");
+    return x;
+}
+constexpr uint32_t kTopsSet = 1u << 16;  // beside a block's new exponents
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// A warp's ring in shared memory, for 8-bit moments: stages of two neighbouring blocks each,
+// their parameters, gradients, codes of m and codes of v.  What a lane holds for blocks on their
+// way is then no register.
+template <bool kBf16P, bool kBf16G>
+struct AdRing {
+    static constexpr int kBlocks = 2;
+    static constexpr int kP = kAdBlock * (kBf16P ? 2 : 4), kG = kAdBlock * (kBf16G ? 2 : 4);  // bytes of a block
+    static constexpr int kAtG = kBlocks * kP, kAtM = kAtG + kBlocks * kG, kAtV = kAtM + kBlocks * kAdBlock;
+    static constexpr int kBytes = kAtV + kBlocks * kAdBlock;
+    static constexpr int kStages = kBytes * 3 * (kAdThreads / 32) < 48 * 1024 ? 3 : 2;
+
+    template <int kBytes>
+    static __device__ __forceinline__ void copy(uint32_t dst, const char* src) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int at = 0; at < kBytes; at += 512)
+            if (kBytes - at >= 512 || 16 * lane < kBytes - at) copy16(dst + at + 16 * lane, src + at + 16 * lane);
+    }
+    // The blocks from b on.
+    static __device__ __forceinline__ void load(uint32_t stage, const AdView& t, int64_t b) {
+        copy<kBlocks * kP>(stage, static_cast<const char*>(t.p) + b * kP);
+        copy<kBlocks * kG>(stage + kAtG, static_cast<const char*>(t.g) + b * kG);
+        copy<kBlocks * kAdBlock>(stage + kAtM, static_cast<const char*>(t.m) + b * kAdBlock);
+        copy<kBlocks * kAdBlock>(stage + kAtV, static_cast<const char*>(t.v) + b * kAdBlock);
+    }
+};
+
+// Blocks b and b + 1 with 8-bit moments, from a stage: element 128 b + 4 lane + e is a lane's
+// e-th of block b.  Both go through each phase together, whose reductions and votes then
+// overlap.  What is rare takes a branch of its own that the warp goes through together: codes
+// of zero, values below the least code.  Where a code or a result is an infinity or NaN
+// nothing is stored, for step_block: false.  `exponents` has lane b % 32's in its lower byte (m)
+// and the next (v), and the new ones come out in the same way.
 //   decoding   bits = (code << 20) + (base << 20)
 //   encoding   the code is bits 20.. of bits + draw - (base << 20), which 16 times as large
 //              is the upper byte
-// 93 instructions an element with drawn roundings (18 for two hashes), 58 without; 96 and 75
-// with a select for every such case.
-template <bool kBf16P, bool kBf16G, bool kSmall, int kRows>
-struct AdRaw {
+template <bool kBf16P, bool kBf16G, bool kRandom>
+__device__ __forceinline__ bool step_small(const uint8_t* stage, uint32_t exponents, const AdView& t,
+                                           const AdScalars& s, int64_t b, uint32_t& tops) {
+    using Ring = AdRing<kBf16P, kBf16G>;
     using P = typename std::conditional<kBf16P, uint2, uint4>::type;
     using G = typename std::conditional<kBf16G, uint2, uint4>::type;
-    P rp[kRows];
-    G rg[kRows];
-    uint4 rm[kSmall ? 1 : kRows], rv[kSmall ? 1 : kRows];
-    uint32_t cm[kRows], cv[kRows], em[kRows], ev[kRows];
-
-    __device__ __forceinline__ void load(const AdView& t, int64_t b) {
-        const int lane = threadIdx.x & 31;
-        const uint8_t *m8 = static_cast<const uint8_t*>(t.m), *v8 = static_cast<const uint8_t*>(t.v);
+    constexpr int kN = Ring::kBlocks;
+    const int lane = threadIdx.x & 31;
+    const int64_t i = b * kAdBlock + 4 * lane;
+    float xm[kN][4], xv[kN][4];
+    uint32_t zeros = 0, nans = 0;
+    uint32_t cm[kN], cv[kN];
 #pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-            const int64_t i = (b + j) * kAdBlock + 4 * lane;
-            rp[j] = *reinterpret_cast<const P*>(static_cast<const char*>(t.p) + i * (kBf16P ? 2 : 4));
-            rg[j] = *reinterpret_cast<const G*>(static_cast<const char*>(t.g) + i * (kBf16G ? 2 : 4));
-            if (kSmall) {
-                cm[j] = *reinterpret_cast<const uint32_t*>(m8 + i);
-                cv[j] = *reinterpret_cast<const uint32_t*>(v8 + i);
-                em[j] = m8[t.n + b + j];
-                ev[j] = v8[t.n + b + j];
-            } else {
-                rm[j] = *reinterpret_cast<const uint4*>(static_cast<const float*>(t.m) + i);
-                rv[j] = *reinterpret_cast<const uint4*>(static_cast<const float*>(t.v) + i);
+    for (int j = 0; j < kN; ++j) {
+        cm[j] = *reinterpret_cast<const uint32_t*>(stage + Ring::kAtM + j * kAdBlock + 4 * lane);
+        cv[j] = *reinterpret_cast<const uint32_t*>(stage + Ring::kAtV + j * kAdBlock + 4 * lane);
+        const uint32_t top = __shfl_sync(0xFFFFFFFFu, exponents, ((int)b + j) & 31);
+        const uint32_t Bm = (uint32_t)code_base(top & 255u, kDepthM) << 20;
+        const uint32_t Bv = (uint32_t)code_base(top >> 8, kDepthV) << 20;
+        const uint32_t w = cm[j] & 0x7F7F7F7Fu;
+        // a byte of 127 (m) or 255 (v), and a byte of 0
+        nans |= (w + 0x01010101u) | ((~cv[j] - 0x01010101u) & cv[j]);
+        zeros |= (w - 0x01010101u) | ((cv[j] - 0x01010101u) & ~cv[j]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t a = __byte_perm(w, 0, 0x4440 + e), c = __byte_perm(cv[j], 0, 0x4440 + e);
+            const uint32_t sign = (cm[j] << (24 - 8 * e)) & 0x80000000u;
+            xm[j][e] = __uint_as_float(a * 0x100000u + Bm | sign);
+            xv[j][e] = __uint_as_float(c * 0x100000u + Bv);
+        }
+    }
+    if (__any_sync(0xFFFFFFFFu, zeros & 0x80808080u)) {
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (!(cm[j] & 0x7Fu << (8 * e))) xm[j][e] = __uint_as_float(__float_as_uint(xm[j][e]) & 0x80000000u);
+                if (!(cv[j] & 0xFFu << (8 * e))) xv[j][e] = 0.f;
+            }
+    }
+    const uint32_t key = t.key + (uint32_t)(i >> 32) * 0x9E3779B9u;  // of both: b is even
+    uint32_t h[kN][4], top_m[kN], top_v[kN];
+    uint2 out_p[kN];
+    float4 out_f[kN];
+    float lost = 0.f;  // a NaN where a parameter is not finite
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        float xp[4], xg[4];
+        uint32_t d[4] = {};
+        unpack4(*reinterpret_cast<const P*>(stage + j * Ring::kP + (int)sizeof(P) * lane), xp);
+        unpack4(*reinterpret_cast<const G*>(stage + Ring::kAtG + j * Ring::kG + (int)sizeof(G) * lane), xg);
+        top_m[j] = top_v[j] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            moments(xg[e], s, xm[j][e], xv[j][e]);
+            top_m[j] = max(top_m[j], __float_as_uint(xm[j][e]) & 0x7FFFFFFFu);
+            top_v[j] = max(top_v[j], __float_as_uint(xv[j][e]));  // no less than +0, or a NaN, which may have a sign
+            xp[e] = updated_fast(xp[e], xm[j][e], xv[j][e], s);
+            if (kBf16P && kRandom) lost = fmaf(xp[e], 0.f, lost);
+            h[j][e] = kRandom ? mix32((uint32_t)i + j * kAdBlock + e, key) : 0u;
+            if (kBf16P && kRandom) d[e] = mix32(h[j][e], t.key_p);
+        }
+        if (kBf16P)
+            out_p[j] = make_uint2(to_bf16<kRandom, false>(xp[0], xp[1], d[0], d[1]),
+                                  to_bf16<kRandom, false>(xp[2], xp[3], d[2], d[3]));
+        else
+            out_f[j] = make_float4(xp[0], xp[1], xp[2], xp[3]);
+    }
+    bool whole = true;
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        top_m[j] = __reduce_max_sync(0xFFFFFFFFu, top_m[j]);
+        top_v[j] = __reduce_max_sync(0xFFFFFFFFu, top_v[j]);
+        whole = whole && top_m[j] < 0x7F800000u && top_v[j] < 0x7F800000u;
+    }
+    if (__any_sync(0xFFFFFFFFu, !whole || (nans & 0x80808080u) || lost != lost)) return false;
+    uint32_t ym[kN][4], yv[kN][4];
+    bool low = false;
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        top_m[j] >>= 23;
+        top_v[j] >>= 23;
+        const uint32_t Bm = (uint32_t)code_base(top_m[j], kDepthM) << 20;
+        const uint32_t Bv = (uint32_t)code_base(top_v[j], kDepthV) << 20;
+        const uint32_t half = kRandom ? 8u : 0x80000u;
+        uint32_t least_m = 0xFFFFFFFFu, least_v = 0xFFFFFFFFu;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // a draw is 16 bits, times 16, and a half of that
+            const uint32_t m = __float_as_uint(xm[j][e]), a = m & 0x7FFFFFFFu, v = __float_as_uint(xv[j][e]);
+            least_m = min(least_m, a);
+            least_v = min(least_v, v);
+            ym[j][e] = a * 16u + (half - Bm) * 16u + (kRandom ? __byte_perm(h[j][e], 0, 0x4324) : 0u);
+            yv[j][e] = v * 16u + (half - Bv) * 16u + (kRandom ? __byte_perm(h[j][e], 0, 0x4104) : 0u);
+            ym[j][e] |= m & 0x80000000u;
+        }
+        low = low || least_m < Bm + (1u << 20) || least_v < Bv + (1u << 20);
+    }
+    if (__any_sync(0xFFFFFFFFu, low)) {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            const uint32_t least_m = ((uint32_t)code_base(top_m[j], kDepthM) << 20) + (1u << 20);
+            const uint32_t least_v = ((uint32_t)code_base(top_v[j], kDepthV) << 20) + (1u << 20);
+            const float unit = __uint_as_float(least_m) * 0x1p-20f;  // as encode_m has it: a power of two
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t draw = kRandom ? (h[j][e] >> 12 & 0xFFFF0u) | 8u : 0x80000u;
+                if ((__float_as_uint(xm[j][e]) & 0x7FFFFFFFu) < least_m)
+                    ym[j][e] = (__float_as_uint(xm[j][e]) & 0x80000000u) |
+                               (fabsf(xm[j][e]) > unit * (float)draw ? 1u << 24 : 0u);
+                if (__float_as_uint(xv[j][e]) < least_v) yv[j][e] = xv[j][e] != 0.f ? 1u << 24 : 0u;
             }
         }
     }
-};
-template <bool kBf16P, bool kBf16G, bool kSmall, bool kRandom, int kRows>
-__device__ __forceinline__ void step_blocks(const AdRaw<kBf16P, kBf16G, kSmall, kRows>& raw, const AdView& t,
-                                            const AdScalars& s, const AdScalars* shared, int64_t b) {
-    const int lane = threadIdx.x & 31;
     uint8_t *m8 = static_cast<uint8_t*>(t.m), *v8 = static_cast<uint8_t*>(t.v);
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        const int64_t at = i + j * kAdBlock;
+        if (kBf16P)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(t.p) + at) = out_p[j];
+        else
+            *reinterpret_cast<float4*>(static_cast<float*>(t.p) + at) = out_f[j];
+        *reinterpret_cast<uint32_t*>(m8 + at) = __byte_perm(__byte_perm(ym[j][0], ym[j][1], 0x0073),
+                                                            __byte_perm(ym[j][2], ym[j][3], 0x0073), 0x5410);
+        *reinterpret_cast<uint32_t*>(v8 + at) = __byte_perm(__byte_perm(yv[j][0], yv[j][1], 0x0073),
+                                                            __byte_perm(yv[j][2], yv[j][3], 0x0073), 0x5410);
+    }
+#pragma unroll
+    for (int j = 0; j < kN; ++j)
+        if (lane == (((int)b + j) & 31)) tops = top_m[j] | top_v[j] << 8 | kTopsSet;
+    return true;
+}
+
+// Two whole blocks with 32-bit moments from b on, as above; all loads come before the first use.
+template <bool kBf16P, bool kBf16G, bool kRandom>
+__device__ __forceinline__ void step_wide(const AdView& t, const AdScalars& s, int64_t b) {
+    using P = typename std::conditional<kBf16P, uint2, uint4>::type;
+    using G = typename std::conditional<kBf16G, uint2, uint4>::type;
     float *m32 = static_cast<float*>(t.m), *v32 = static_cast<float*>(t.v);
+    P rp[2];
+    G rg[2];
+    uint4 rm[2], rv[2];
+    const int64_t i0 = b * kAdBlock + 4 * (threadIdx.x & 31);
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-        const int64_t i = (b + j) * kAdBlock + 4 * lane;
+    for (int j = 0; j < 2; ++j) {
+        const int64_t i = i0 + j * kAdBlock;
+        rp[j] = *reinterpret_cast<const P*>(static_cast<const char*>(t.p) + i * (kBf16P ? 2 : 4));
+        rg[j] = *reinterpret_cast<const G*>(static_cast<const char*>(t.g) + i * (kBf16G ? 2 : 4));
+        rm[j] = *reinterpret_cast<const uint4*>(m32 + i);
+        rv[j] = *reinterpret_cast<const uint4*>(v32 + i);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int64_t i = i0 + j * kAdBlock;
         float xp[4], xg[4], xm[4], xv[4];
-        unpack4(raw.rp[j], xp);
-        unpack4(raw.rg[j], xg);
-        if (kSmall) {
-            const int bm = code_base(raw.em[j], kDepthM), bv = code_base(raw.ev[j], kDepthV);
-            const uint32_t w = raw.cm[j] & 0x7F7F7F7Fu;
-            // a byte of 127 (m) or 255 (v), and a byte of 0
-            const bool nan = ((w + 0x01010101u) | ((~raw.cv[j] - 0x01010101u) & raw.cv[j])) & 0x80808080u;
-            const bool zero = ((w - 0x01010101u) | ((raw.cv[j] - 0x01010101u) & ~raw.cv[j])) & 0x80808080u;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t a = __byte_perm(w, 0, 0x4440 + e), c = __byte_perm(raw.cv[j], 0, 0x4440 + e);
-                const uint32_t sign = (raw.cm[j] << (24 - 8 * e)) & 0x80000000u;
-                xm[e] = __uint_as_float(a * 0x100000u + ((uint32_t)bm << 20) | sign);
-                xv[e] = __uint_as_float(c * 0x100000u + ((uint32_t)bv << 20));
-            }
-            if (__any_sync(0xFFFFFFFFu, nan)) {
-                step_block<kBf16P, kBf16G, true, kRandom>(t, shared, b + j);
-                continue;
-            }
-            if (__any_sync(0xFFFFFFFFu, zero)) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (!(w & 0xFFu << (8 * e))) xm[e] = __uint_as_float(__float_as_uint(xm[e]) & 0x80000000u);
-                    if (!(raw.cv[j] & 0xFFu << (8 * e))) xv[e] = 0.f;
-                }
-            }
-        } else {
-            unpack4(raw.rm[kSmall ? 0 : j], xm);
-            unpack4(raw.rv[kSmall ? 0 : j], xv);
-        }
+        uint32_t d[4] = {};
+        unpack4(rp[j], xp);
+        unpack4(rg[j], xg);
+        unpack4(rm[j], xm);
+        unpack4(rv[j], xv);
         const uint32_t key = t.key + (uint32_t)(i >> 32) * 0x9E3779B9u;
-        uint32_t am[4], av[4], h[4];
-        float lost = 0.f;  // a NaN where a parameter is not finite
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             moments(xg[e], s, xm[e], xv[e]);
-            am[e] = __float_as_uint(xm[e]) & 0x7FFFFFFFu;
-            av[e] = __float_as_uint(xv[e]);  // no less than +0, or a NaN, which may have a sign
-            xp[e] = kSmall ? updated_fast(xp[e], xm[e], xv[e], s) : updated(xp[e], xm[e], xv[e], s);
-            if (kSmall && kBf16P && kRandom) lost = fmaf(xp[e], 0.f, lost);
-            h[e] = kRandom && (kSmall || kBf16P) ? mix32((uint32_t)i + e, key) : 0u;
+            xp[e] = updated(xp[e], xm[e], xv[e], s);
+            if (kBf16P && kRandom) d[e] = mix32(mix32((uint32_t)i + e, key), t.key_p);
         }
-        uint32_t out_m = 0, out_v = 0, top_m = 0, top_v = 0;
-        if (kSmall) {
-            top_m = __reduce_max_sync(0xFFFFFFFFu, max(max(am[0], am[1]), max(am[2], am[3])));
-            top_v = __reduce_max_sync(0xFFFFFFFFu, max(max(av[0], av[1]), max(av[2], av[3])));
-            if (top_m >= 0x7F800000u || top_v >= 0x7F800000u || __any_sync(0xFFFFFFFFu, lost != lost)) {
-                step_block<kBf16P, kBf16G, true, kRandom>(t, shared, b + j);
-                continue;
-            }
-            top_m >>= 23;
-            top_v >>= 23;
-            const uint32_t Bm = (uint32_t)code_base(top_m, kDepthM) << 20;
-            const uint32_t Bv = (uint32_t)code_base(top_v, kDepthV) << 20;
-            const uint32_t half = kRandom ? 8u : 0x80000u;
-            uint32_t ym[4], yv[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {  // a draw is 16 bits, times 16, and a half of that
-                ym[e] = am[e] * 16u + (half - Bm) * 16u + (kRandom ? __byte_perm(h[e], 0, 0x4324) : 0u);
-                yv[e] = av[e] * 16u + (half - Bv) * 16u + (kRandom ? __byte_perm(h[e], 0, 0x4104) : 0u);
-                ym[e] |= __float_as_uint(xm[e]) & 0x80000000u;
-            }
-            const uint32_t least_m = Bm + (1u << 20), least_v = Bv + (1u << 20);
-            if (__any_sync(0xFFFFFFFFu, min(min(am[0], am[1]), min(am[2], am[3])) < least_m ||
-                                            min(min(av[0], av[1]), min(av[2], av[3])) < least_v)) {
-                const float unit = __uint_as_float(least_m) * 0x1p-20f;  // as encode_m has it: a power of two
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t draw = kRandom ? (h[e] >> 12 & 0xFFFF0u) | 8u : 0x80000u;
-                    if (am[e] < least_m)
-                        ym[e] = (__float_as_uint(xm[e]) & 0x80000000u) |
-                                (fabsf(xm[e]) > unit * (float)draw ? 1u << 24 : 0u);
-                    if (av[e] < least_v) yv[e] = av[e] ? 1u << 24 : 0u;
-                }
-            }
-            out_m = __byte_perm(__byte_perm(ym[0], ym[1], 0x0073), __byte_perm(ym[2], ym[3], 0x0073), 0x5410);
-            out_v = __byte_perm(__byte_perm(yv[0], yv[1], 0x0073), __byte_perm(yv[2], yv[3], 0x0073), 0x5410);
-        }
-        if (kBf16P) {
-            uint32_t d[4] = {};
-            if (kRandom) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) d[e] = mix32(h[e], t.key_p);
-            }
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(t.p) + i) =
-                make_uint2(to_bf16<kRandom, !kSmall>(xp[0], xp[1], d[0], d[1]),
-                           to_bf16<kRandom, !kSmall>(xp[2], xp[3], d[2], d[3]));
-        } else {
+        if (kBf16P)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(t.p) + i) = make_uint2(
+                to_bf16<kRandom, true>(xp[0], xp[1], d[0], d[1]), to_bf16<kRandom, true>(xp[2], xp[3], d[2], d[3]));
+        else
             *reinterpret_cast<float4*>(static_cast<float*>(t.p) + i) = make_float4(xp[0], xp[1], xp[2], xp[3]);
-        }
-        if (kSmall) {
-            *reinterpret_cast<uint32_t*>(m8 + i) = out_m;
-            *reinterpret_cast<uint32_t*>(v8 + i) = out_v;
-            if (lane == 0) {
-                m8[t.n + b + j] = (uint8_t)top_m;
-                v8[t.n + b + j] = (uint8_t)top_v;
-            }
-        } else {
-            *reinterpret_cast<float4*>(m32 + i) = make_float4(xm[0], xm[1], xm[2], xm[3]);
-            *reinterpret_cast<float4*>(v32 + i) = make_float4(xv[0], xv[1], xv[2], xv[3]);
-        }
+        *reinterpret_cast<float4*>(m32 + i) = make_float4(xm[0], xm[1], xm[2], xm[3]);
+        *reinterpret_cast<float4*>(v32 + i) = make_float4(xv[0], xv[1], xv[2], xv[3]);
     }
 }
 
-// One warp's blocks of units [u0, u1) of a tensor.  Rounded to nearest, the 8-bit forms load the
-// next blocks before they work on these: 60 million bf16 elements in 172 us, 207 without.  With
-// draws the code is as long again, and twice in a loop it no longer fits the instruction
-// cache: 237 us, and 222 with four CTAs on an SM that load what they work on.
-template <bool kBf16P, bool kBf16G, bool kSmall, bool kRandom>
-__device__ __forceinline__ void step_units(const AdTensor& at, uint32_t u0, uint32_t u1, const AdScalars& s,
-                                           const AdScalars* shared) {
-    constexpr int kRows = kSmall ? 4 : 2, kPerUnit = kAdUnit / kAdBlock;
-    constexpr bool kAhead = kSmall && !kRandom;
-    AdView t = {at.p, after_wait(at.g), at.m, at.v, at.n, mix32(s.seed_key ^ at.place, 0xDAA66D2Bu), 0};
-    t.key_p = t.key ^ 0xA54FF53Au;
-    const bool quick = ((reinterpret_cast<uintptr_t>(t.p) & (kBf16P ? 7u : 15u)) |
-                        (reinterpret_cast<uintptr_t>(t.g) & (kBf16G ? 7u : 15u)) |
-                        ((reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v)) &
-                         (kSmall ? 3u : 15u))) == 0 &&
-                       !(kSmall && s.tiny_eps);
-    // A warp's turns: kRows neighbouring blocks every kAdThreads / 32 * kRows of them.
-    constexpr int kTurn = kAdThreads / 32 * kRows;
-    static_assert(kPerUnit % kTurn == 0, "");
-    const int64_t first = (int64_t)(u0 - at.first_unit) * kPerUnit + (threadIdx.x >> 5) * kRows;
+// A warp's units [u0, u1) of a tensor with 8-bit moments: neighbouring blocks, so that the warp
+// reads and writes the exponents of 32 blocks at once.  (Written a byte at a time by all warps
+// of a CTA, which read others of the same 32 bytes meanwhile, they held it up: 60 million
+// bf16 elements in 218 us, 173 so.)
+template <bool kBf16P, bool kBf16G, bool kRandom>
+__device__ __forceinline__ void step_small_units(const AdTensor& at, uint32_t u0, uint32_t u1, const AdScalars& s,
+                                                 const AdScalars* shared, uint8_t* ring) {
+    using Ring = AdRing<kBf16P, kBf16G>;
+    constexpr int kPerUnit = kAdUnitSmall / kAdBlock, kAhead = Ring::kStages - 1;
+    static_assert(kPerUnit % Ring::kBlocks == 0 && Ring::kBlocks == 2, "");
+    const int lane = threadIdx.x & 31;
+    const AdView t = view_of(at, s);
+    const bool quick = ((reinterpret_cast<uintptr_t>(t.p) | reinterpret_cast<uintptr_t>(t.g) |
+                         reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v)) &
+                        15u) == 0 &&
+                       !s.tiny_eps;
+    int64_t b = (int64_t)(u0 - at.first_unit) * kPerUnit;
     const int64_t blocks = min((t.n + kAdBlock - 1) / kAdBlock, (int64_t)(u1 - at.first_unit) * kPerUnit);
-    const int64_t whole = quick ? t.n / kAdBlock - kRows : -1;  // last start of kRows whole blocks
-    AdRaw<kBf16P, kBf16G, kSmall, kRows> raw[kAhead ? 2 : 1];
-    if (kAhead && first < blocks && first <= whole) raw[0].load(t, first);
-#pragma unroll 1
-    for (int64_t b = first; b < blocks; b += (kAhead ? 2 : 1) * kTurn) {
-#pragma unroll
-        for (int half = 0; half < (kAhead ? 2 : 1); ++half) {
-            const int64_t c = b + half * kTurn, next = c + kTurn;
-            if (c >= blocks) break;
-            if (c > whole) {
-                for (int64_t k = c; k < min(c + kRows, blocks); ++k)
-                    step_block<kBf16P, kBf16G, kSmall, kRandom>(t, shared, k);
-                continue;
-            }
-            if (!kAhead)
-                raw[0].load(t, c);
-            else if (next < blocks && next <= whole)
-                raw[half ^ 1].load(t, next);
-            step_blocks<kBf16P, kBf16G, kSmall, kRandom, kRows>(raw[half], t, s, shared, c);
-        }
+    const int64_t end = quick ? min(blocks, t.n / kAdBlock - 1) : b;  // up to here there are two whole blocks
+    uint8_t *em = static_cast<uint8_t*>(t.m) + t.n, *ev = static_cast<uint8_t*>(t.v) + t.n;
+    const int64_t last = t.n / kAdBlock - 1;
+    const uint32_t ring_at = smem_u32(ring);
+    int64_t chunk = b >> 5;
+    uint32_t tops = 0, exponents = 0, next_m = 0, next_v = 0;
+    if (b < end) {
+        const int64_t k = min(chunk * 32 + lane, last), l = min(k + 32, last);
+        exponents = load_byte(em + k) | load_byte(ev + k) << 8;
+        next_m = load_byte(em + l);
+        next_v = load_byte(ev + l);
     }
+    while (true) {
+        __syncwarp();  // the ring has been read
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (b + 2 * k < end) Ring::load(ring_at + k * Ring::kBytes, t, b + 2 * k);
+            copies_commit();
+        }
+        int stage = 0, fill = kAhead;
+        bool done = true;
+#pragma unroll 1
+        for (; b < end; b += 2) {
+            if (b >> 5 != chunk) {
+                chunk = b >> 5;
+                exponents = next_m | next_v << 8;
+                const int64_t l = min(chunk * 32 + 32 + lane, last);
+                next_m = load_byte(em + l);
+                next_v = load_byte(ev + l);
+            }
+            copies_wait<kAhead - 1>();
+            __syncwarp();  // all lanes' copies are there, and all have read the stage before
+            if (b + 2 * kAhead < end) Ring::load(ring_at + fill * Ring::kBytes, t, b + 2 * kAhead);
+            copies_commit();
+            done = step_small<kBf16P, kBf16G, kRandom>(ring + stage * Ring::kBytes, exponents, t, s, b, tops);
+            if (!done) break;
+            stage = stage + 1 == Ring::kStages ? 0 : stage + 1;
+            fill = fill + 1 == Ring::kStages ? 0 : fill + 1;
+            if ((b & 31) == 30 || b + 2 >= end) {
+                if (tops & kTopsSet) {
+                    em[chunk * 32 + lane] = (uint8_t)tops;
+                    ev[chunk * 32 + lane] = (uint8_t)(tops >> 8);
+                }
+                tops = 0;
+            }
+        }
+        copies_wait<0>();
+        if (done) break;
+        // Blocks that step_block does; what it writes of the exponents stays.
+        step_block<kBf16P, kBf16G, true, kRandom>(t, shared, b);
+        step_block<kBf16P, kBf16G, true, kRandom>(t, shared, b + 1);
+        if (((b & 31) == 30 || b + 2 >= end) && (tops & kTopsSet)) {
+            em[chunk * 32 + lane] = (uint8_t)tops;
+            ev[chunk * 32 + lane] = (uint8_t)(tops >> 8);
+        }
+        if ((b & 31) == 30) tops = 0;
+        b += 2;
+    }
+    for (; b < blocks; ++b) step_block<kBf16P, kBf16G, true, kRandom>(t, shared, b);
+}
+
+// A CTA's units [u0, u1) of a tensor with 32-bit moments: a warp takes two neighbouring blocks
+// every 16.
+template <bool kBf16P, bool kBf16G, bool kRandom>
+__device__ __forceinline__ void step_wide_units(const AdTensor& at, uint32_t u0, uint32_t u1, const AdScalars& s,
+                                                const AdScalars* shared) {
+    constexpr int kPerUnit = kAdUnit / kAdBlock, kTurn = kAdThreads / 32 * 2;
+    static_assert(kPerUnit % kTurn == 0, "");
+    const AdView t = view_of(at, s);
+    const bool quick =
+        ((reinterpret_cast<uintptr_t>(t.p) & (kBf16P ? 7u : 15u)) |
+         (reinterpret_cast<uintptr_t>(t.g) & (kBf16G ? 7u : 15u)) |
+         ((reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v)) & 15u)) == 0;
+    int64_t b = (int64_t)(u0 - at.first_unit) * kPerUnit + (threadIdx.x >> 5) * 2;
+    const int64_t blocks = min((t.n + kAdBlock - 1) / kAdBlock, (int64_t)(u1 - at.first_unit) * kPerUnit);
+    const int64_t end = quick ? min(blocks, t.n / kAdBlock - 1) : 0;  // up to here there are two whole blocks
+#pragma unroll 1
+    for (; b < end; b += kTurn) step_wide<kBf16P, kBf16G, kRandom>(t, s, b);
+    for (; b < blocks; b += kTurn)
+        for (int64_t k = b; k < min(b + 2, blocks); ++k) step_block<kBf16P, kBf16G, false, kRandom>(t, shared, k);
 }
 
 template <int N>
@@ -505,12 +646,17 @@ __device__ __forceinline__ int ad_tensor_of(const AdBatch<N>& g, uint32_t u) {
 
 // One kind of tensors to a launch, so that each has the registers that it needs.
 template <int N, bool kBf16P, bool kBf16G, bool kSmall, bool kRandom>
-__global__ void __launch_bounds__(kAdThreads, kSmall && kRandom ? kAdCtasDrawn : kAdCtas)
+__global__ void __launch_bounds__(kAdThreads, kAdCtas)
     adamw_kernel(const __grid_constant__ AdBatch<N> b, const __grid_constant__ AdOptions o) {
+    using Ring = AdRing<kBf16P, kBf16G>;
     __shared__ AdScalars shared;
-    const uint32_t u0 = (uint32_t)((uint64_t)b.units * blockIdx.x / gridDim.x);
-    const uint32_t u1 = (uint32_t)((uint64_t)b.units * (blockIdx.x + 1) / gridDim.x);
-    int i = ad_tensor_of(b, u0);
+    __shared__ __align__(16) uint8_t rings[kSmall ? kAdThreads / 32 * Ring::kStages * Ring::kBytes : 16];
+    uint8_t* ring = kSmall ? rings + (threadIdx.x >> 5) * Ring::kStages * Ring::kBytes : nullptr;
+    // units go to CTAs in turn, those of 8-bit moments to warps
+    const uint32_t parts = kSmall ? gridDim.x * (kAdThreads / 32) : gridDim.x;
+    const uint32_t part = kSmall ? blockIdx.x * (kAdThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
+    const uint32_t u0 = (uint32_t)((uint64_t)b.units * part / parts);
+    const uint32_t u1 = (uint32_t)((uint64_t)b.units * (part + 1) / parts);
     grid_wait();
     if (threadIdx.x == 0) {
         shared = scalars_of(o);
@@ -518,10 +664,14 @@ __global__ void __launch_bounds__(kAdThreads, kSmall && kRandom ? kAdCtasDrawn :
     }
     __syncthreads();
     const AdScalars s = shared;
-    if (s.skip) return;
+    if (s.skip || u0 == u1) return;
+    int i = ad_tensor_of(b, u0);
     for (uint32_t u = u0; u < u1; ++i) {
         const uint32_t end = i + 1 < b.count ? min(u1, b.t[i + 1].first_unit) : u1;
-        step_units<kBf16P, kBf16G, kSmall, kRandom>(b.t[i], u, end, s, &shared);
+        if (kSmall)
+            step_small_units<kBf16P, kBf16G, kRandom>(b.t[i], u, end, s, &shared, ring);
+        else
+            step_wide_units<kBf16P, kBf16G, kRandom>(b.t[i], u, end, s, &shared);
         u = end;
     }
 }
@@ -650,8 +800,8 @@ int check_options(const pstat_adamw_options* o) {
 
 // Appends a tensor to a batch; false when it is full or its units pass 32 bits.
 template <int N>
-bool add_tensor(AdBatch<N>& b, uint64_t& units, const AdTensor& t) {
-    const uint64_t add = (uint64_t)((t.n + kAdUnit - 1) / kAdUnit);
+bool add_tensor(AdBatch<N>& b, uint64_t& units, const AdTensor& t, int unit) {
+    const uint64_t add = (uint64_t)((t.n + unit - 1) / unit);
     if (b.count == N || units + add > 0xFFFFFFFFull) return false;
     b.t[b.count] = t;
     b.t[b.count++].first_unit = (uint32_t)units;
@@ -682,11 +832,13 @@ int run_kind(const pstat_adamw_tensor* tensors, int64_t n, const AdOptions& o, c
         for (; i < n; ++i) {
             const pstat_adamw_tensor& t = tensors[i];
             if (t.n == 0 || kind_of(t) != kKind) continue;
-            if (!add_tensor(b, units, {t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.n, 0u, (uint32_t)i})) break;
+            if (!add_tensor(b, units, {t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.n, 0u, (uint32_t)i},
+                            kSmall ? kAdUnitSmall : kAdUnit))
+                break;
         }
+        const uint32_t ctas = kSmall ? (b.units - 1) / (kAdThreads / 32) + 1 : b.units;
         if (b.count && launch_behind(adamw_kernel<N, (kKind & 1u) != 0, (kKind & 2u) != 0, kSmall, kRandom>,
-                                     grid_of(b.units, kSmall && kRandom ? kAdCtasDrawn : kAdCtas, dev), kAdThreads, 0, st, 1, b,
-                                     o) != cudaSuccess)
+                                     grid_of(ctas, kAdCtas, dev), kAdThreads, 0, st, 1, b, o) != cudaSuccess)
             return PSTAT_ERR_CUDA;
     }
     return PSTAT_OK;
@@ -734,7 +886,8 @@ int run_moments(const pstat_adamw_moment* list, int64_t n, const DeviceInfo& dev
             const pstat_adamw_moment& t = list[i];
             if (t.n == 0) continue;
             if (!add_tensor(b, units, {t.out_avg, t.out_avg_sq, const_cast<void*>(t.exp_avg),
-                                       const_cast<void*>(t.exp_avg_sq), t.n, 0u, (uint32_t)i}))
+                                       const_cast<void*>(t.exp_avg_sq), t.n, 0u, (uint32_t)i},
+                            kAdUnit))
                 break;
         }
         if (b.count &&
