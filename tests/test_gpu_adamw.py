@@ -270,3 +270,33 @@ def test_refusals(cuda_lib):
     with pytest.raises(ValueError):
         cuda_lib.adamw_state(p, 4)
     assert not bool(p.any())
+
+
+@pytest.mark.parametrize("p_type,g_type,seed", [(BF16, BF16, 7), (BF16, BF16, None), (F32, F32, 7), (BF16, F32, 7),
+                                                (F32, BF16, None)])
+def test_large_8_bit_tensors_in_any_place(cuda_lib, p_type, g_type, seed):
+    """Tensors on 16 bytes take another way than those that are not: the same bits, also
+    where blocks hold zeros, NaN, infinities and values far below their largest, and
+    past 32 blocks for each warp of the GPU."""
+    n = 13_000_077
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    start = [torch.randn(n, generator=gen, device="cuda").to(p_type),
+             (torch.randn(n, generator=gen, device="cuda") *
+              torch.exp2(torch.randint(-40, 3, (n,), generator=gen, device="cuda").float())).to(g_type)]
+    start[1][torch.randint(0, n, (20000,), generator=gen, device="cuda")] = 0
+    start[1][100 * 128:110 * 128] = 0
+    for value, count in ((math.nan, 30), (math.inf, 30)):
+        start[1][torch.randint(0, n, (count,), generator=gen, device="cuda")] = value
+        start[0][torch.randint(0, n, (count,), generator=gen, device="cuda")] = value
+    results = []
+    for off in (0, 1):
+        p, g = (torch.empty(n + off, dtype=x.dtype, device="cuda")[off:].copy_(x) for x in start)
+        m, v = (torch.zeros(n + -(-n // 128) + off, dtype=torch.uint8, device="cuda")[off:] for _ in range(2))
+        for step in (1, 2, 3):
+            cuda_lib.adamw_step(p, g, m, v, step, 1e-2, **HYPER, seed=None if seed is None else seed + step)
+        results.append((p, m, v))
+    (p, m, v), (q, mq, vq) = results
+    assert torch.equal(m, mq) and torch.equal(v, vq)
+    assert torch.equal(torch.isnan(p), torch.isnan(q))
+    assert torch.equal(torch.nan_to_num(p, nan=0.5), torch.nan_to_num(q, nan=0.5))
+    assert 50 < int(torch.isnan(p).sum()) < 1000
