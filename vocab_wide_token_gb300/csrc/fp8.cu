@@ -74,14 +74,28 @@ __device__ __forceinline__ void store8(uint8_t* q, int64_t col, int64_t K, bool 
     }
 }
 
+struct QuArgs {
+    const void* x;
+    int64_t T, K, ld;
+    void* q;
+    float* scale;
+    int64_t scale_row, scale_col;
+    uint32_t col_blocks;
+    int* dev_error;
+};
+
 template <typename E, bool kTall>
 __global__ void __launch_bounds__(kQuThreads)
-    quantize_kernel(const void* x_at, int64_t T, int64_t K, int64_t ld, uint8_t* q, float* scale, int64_t scale_row,
-                    int64_t scale_col, uint32_t col_blocks, int* dev_error) {
+    quantize_kernel(const __grid_constant__ QuArgs a) {
     constexpr int kIter = (kTall ? kF8Block : kQuRows) / 16;
     __shared__ uint32_t warp_top[kQuThreads / 32];
     grid_wait();
-    const E* x = static_cast<const E*>(after_wait(x_at));
+    const E* x = static_cast<const E*>(after_wait(a.x));
+    uint8_t* q = static_cast<uint8_t*>(a.q);
+    float* scale = a.scale;
+    const int64_t T = a.T, K = a.K, ld = a.ld, scale_row = a.scale_row, scale_col = a.scale_col;
+    const uint32_t col_blocks = a.col_blocks;
+    int* dev_error = a.dev_error;
     const uint32_t cb = blockIdx.x % col_blocks;
     const int64_t rb = blockIdx.x / col_blocks;
     const int64_t r0 = rb * (kIter * 16) + threadIdx.x / 16;
@@ -142,6 +156,11 @@ __global__ void __launch_bounds__(kQuThreads)
         }
     }
     if (lost && dev_error && threadIdx.x % 16 == 0) atomicOr(dev_error, PSTAT_DEV_NONFINITE);
+}
+
+template <typename E, bool kTall>
+cudaError_t launch_quantize(const QuArgs& a, unsigned grid, cudaStream_t st) {
+    return launch_behind(quantize_kernel<E, kTall>, grid, kQuThreads, 0, st, 1, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -729,14 +748,13 @@ int pstat_fp8_quantize(const void* x, pstat_dtype dt, int64_t T, int64_t K, int6
     const int rc = device_info(&dev);
     if (rc != PSTAT_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const QuArgs a = {x, T, K, ld, out_q, out_scale, scale_row, scale_col, (uint32_t)cols, dev_error};
     const unsigned grid = (unsigned)(cols * row_blocks);
-    auto launch = [&](auto kernel) {
-        return launch_behind(kernel, grid, kQuThreads, 0, st, 1, x, T, K, ld, static_cast<uint8_t*>(out_q), out_scale,
-                             scale_row, scale_col, (uint32_t)cols, dev_error);
-    };
-    const cudaError_t e =
-        rows == 1 ? (dt == PSTAT_BF16 ? launch(quantize_kernel<uint16_t, false>) : launch(quantize_kernel<float, false>))
-                  : (dt == PSTAT_BF16 ? launch(quantize_kernel<uint16_t, true>) : launch(quantize_kernel<float, true>));
+    cudaError_t e;
+    if (rows == 1)
+        e = dt == PSTAT_BF16 ? launch_quantize<uint16_t, false>(a, grid, st) : launch_quantize<float, false>(a, grid, st);
+    else
+        e = dt == PSTAT_BF16 ? launch_quantize<uint16_t, true>(a, grid, st) : launch_quantize<float, true>(a, grid, st);
     return e == cudaSuccess ? PSTAT_OK : PSTAT_ERR_CUDA;
 }
 
