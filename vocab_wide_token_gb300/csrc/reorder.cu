@@ -6,6 +6,11 @@
 // that a permutation in place needs neither a second buffer nor an order, and a parent
 // of several rows comes from HBM once.  In place a row that is its own parent is
 // neither read nor written.
+//
+// A warp's parents are one load, a lane each: loaded row by row they kept each row's load
+// waiting for the last one's.  Many short CTAs, as what they read and write comes in turns:
+// four caches of 128 rows x 8 x 1501 x 128 bf16, beams 8, in place: 373 us, 6.0 TB/s (430 by
+// row, 8 CTAs to an SM); 4 beams 380 (540), 16 beams 465 (545), 64 beams 560 (1,265).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -20,6 +25,7 @@ namespace pstat {
 namespace {
 
 constexpr int kReThreads = 256;
+constexpr int kReTurns = 256;  // most CTAs for each SM
 constexpr int kReBatch = 300;  // states of one launch (they travel as its arguments)
 
 struct ReState {
@@ -48,34 +54,44 @@ struct ReArgs {
     int* dev_error;
 };
 
+// One column of search b, of every lane that `has` one.  All lanes are here: lane l reads the
+// l-th parent, and the others ask it for that.
 template <typename V, int kRows>
 __device__ __forceinline__ void move_column(const ReState& s, const ReArgs& a, const int64_t* parents,
-                                            int64_t b, uint32_t col) {
+                                            int64_t b, uint32_t col, bool has) {
+    const int lane = threadIdx.x & 31;
     const uint32_t seg = col / s.per_seg, at = col - seg * s.per_seg;
     const char* in = after_wait(s.in) + b * a.beams * s.in_row + seg * s.in_seg + (int64_t)at * sizeof(V);
     char* out = s.out + b * a.out_beams * s.out_row + seg * s.out_seg + (int64_t)at * sizeof(V);
     for (int i0 = 0; i0 < a.out_beams; i0 += kRows) {  // once in place: kRows >= out_beams there
+        constexpr int kWords = (kRows + 31) / 32;
+        int from[kWords];  // -1: the row stays
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            const int i = i0 + 32 * w + lane;
+            const int64_t p = i < a.out_beams ? parents[i] : -1;
+            from[w] = p >= 0 && p < a.beams && !(a.in_place && p == i) ? (int)p : -1;
+        }
         V x[kRows];
-        uint64_t moved = 0;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            if (i0 + i >= a.out_beams) break;
-            const int64_t p = parents[i0 + i];
-            if (p < 0 || p >= a.beams || (a.in_place && p == i)) continue;
-            moved |= 1ull << i;
-            x[i] = *reinterpret_cast<const V*>(in + p * s.in_row);
+            const int p = __shfl_sync(0xFFFFFFFFu, from[i / 32], i % 32);
+            if (has && p >= 0) x[i] = *reinterpret_cast<const V*>(in + p * s.in_row);
         }
 #pragma unroll
-        for (int i = 0; i < kRows; ++i)
-            if (moved >> i & 1) *reinterpret_cast<V*>(out + (int64_t)(i0 + i) * s.out_row) = x[i];
+        for (int i = 0; i < kRows; ++i) {
+            if (__shfl_sync(0xFFFFFFFFu, from[i / 32], i % 32) >= 0 && has) *reinterpret_cast<V*>(out) = x[i];
+            out = after_wait(out + s.out_row);  // opaque: no address is formed, and held, before its turn
+        }
     }
 }
 
-// kRows: rows whose columns a thread holds at a time.  64 of 16 bytes would be all its
-// registers, so such searches move 4 bytes at a time.
+// kRows: rows whose columns a thread holds at a time, as few as the search allows.  64 of 16
+// bytes would be all its registers, so such searches move 8 bytes at a time (64 beams: 560
+// us, 4 bytes 713).
 template <int N, int kRows>
-__global__ void __launch_bounds__(kReThreads) reorder_kernel(const __grid_constant__ ReBatch<N> g,
-                                                            const __grid_constant__ ReArgs a) {
+__global__ void __launch_bounds__(kReThreads, kRows <= 8 ? 4 : kRows <= 16 ? 2 : 1)
+    reorder_kernel(const __grid_constant__ ReBatch<N> g, const __grid_constant__ ReArgs a) {
     grid_wait();
     const int64_t* parents = after_wait(a.parents);
     if (blockIdx.x == 0 && a.dev_error) {
@@ -97,18 +113,18 @@ __global__ void __launch_bounds__(kReThreads) reorder_kernel(const __grid_consta
         const uint32_t r = u - s.first_unit;
         const int64_t b = r / s.units;
         const uint32_t col = (r - (uint32_t)b * s.units) * kReThreads + threadIdx.x;
-        if (col >= s.columns) continue;
+        const bool has = col < s.columns;
         const int64_t* p = parents + b * a.out_beams;
         switch (s.vec) {
             case 16:
-                if constexpr (kRows <= 32) move_column<uint4, kRows>(s, a, p, b, col);
+                if constexpr (kRows <= 32) move_column<uint4, kRows>(s, a, p, b, has ? col : 0u, has);
                 break;
             case 8:
-                if constexpr (kRows <= 32) move_column<uint2, kRows>(s, a, p, b, col);
+                move_column<uint2, kRows>(s, a, p, b, has ? col : 0u, has);
                 break;
-            case 4: move_column<uint32_t, kRows>(s, a, p, b, col); break;
-            case 2: move_column<uint16_t, kRows>(s, a, p, b, col); break;
-            default: move_column<uint8_t, kRows>(s, a, p, b, col); break;
+            case 4: move_column<uint32_t, kRows>(s, a, p, b, has ? col : 0u, has); break;
+            case 2: move_column<uint16_t, kRows>(s, a, p, b, has ? col : 0u, has); break;
+            default: move_column<uint8_t, kRows>(s, a, p, b, has ? col : 0u, has); break;
         }
     }
 }
@@ -237,7 +253,7 @@ int run_rows(const pstat_beam_state* states, int64_t n, const ReArgs& a, uint32_
         }
         g.units = (uint32_t)units;
         if (!g.count) continue;
-        const uint32_t most = (uint32_t)dev.sm_count * 8;
+        const uint32_t most = (uint32_t)dev.sm_count * kReTurns;
         if (launch_behind(reorder_kernel<N, kRows>, g.units < most ? g.units : most, kReThreads, 0, st, 1, g, a) !=
             cudaSuccess)
             return PSTAT_ERR_CUDA;
@@ -272,5 +288,5 @@ extern "C" int pstat_beam_reorder(const pstat_beam_state* states, int64_t n_stat
     if (!in_place || out_beams <= 8) return run_states<8>(states, n_states, a, 16, dev, st);
     if (out_beams <= 16) return run_states<16>(states, n_states, a, 16, dev, st);
     if (out_beams <= 32) return run_states<32>(states, n_states, a, 16, dev, st);
-    return run_states<64>(states, n_states, a, 4, dev, st);
+    return run_states<64>(states, n_states, a, 8, dev, st);
 }
