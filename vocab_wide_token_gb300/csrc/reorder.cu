@@ -7,10 +7,11 @@
 // of several rows comes from HBM once.  In place a row that is its own parent is
 // neither read nor written.
 //
-// A warp's parents are one load, a lane each: loaded row by row they kept each row's load
-// waiting for the last one's.  Many short CTAs, as what they read and write comes in turns:
-// four caches of 128 rows x 8 x 1501 x 128 bf16, beams 8, in place: 373 us, 6.0 TB/s (430 by
-// row, 8 CTAs to an SM); 4 beams 380 (540), 16 beams 465 (545), 64 beams 560 (1,265).
+// A warp's parents are one load, a lane each, and known before the first row is loaded: one by
+// one they kept each row waiting for the last one's.  Many short CTAs, as what they read
+// and write comes in turns.  Four caches of 128 rows x 8 x 1501 x 128 bf16 in place: 8 beams
+// 325 us, 6.9 TB/s (430 row by row with 8 CTAs to an SM); 4 beams 350 (540), 16 beams 360
+// (545), 32 beams 394 (490), 64 beams 505 (1,265).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -72,23 +73,25 @@ __device__ __forceinline__ void move_column(const ReState& s, const ReArgs& a, c
             const int64_t p = i < a.out_beams ? parents[i] : -1;
             from[w] = p >= 0 && p < a.beams && !(a.in_place && p == i) ? (int)p : -1;
         }
+        int p[kRows];  // all before the first row's load
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) p[i] = __shfl_sync(0xFFFFFFFFu, from[i / 32], i % 32) | (has ? 0 : -1);
         V x[kRows];
+        uint64_t moved = 0;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int p = __shfl_sync(0xFFFFFFFFu, from[i / 32], i % 32);
-            if (has && p >= 0) x[i] = *reinterpret_cast<const V*>(in + p * s.in_row);
-        }
+        for (int i = 0; i < kRows; ++i)
+            if (p[i] >= 0) {
+                moved |= 1ull << i;
+                x[i] = *reinterpret_cast<const V*>(in + p[i] * s.in_row);
+            }
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            if (__shfl_sync(0xFFFFFFFFu, from[i / 32], i % 32) >= 0 && has) *reinterpret_cast<V*>(out) = x[i];
-            out = after_wait(out + s.out_row);  // opaque: no address is formed, and held, before its turn
-        }
+        for (int i = 0; i < kRows; ++i)
+            if (moved >> i & 1) *reinterpret_cast<V*>(out + (int64_t)(i0 + i) * s.out_row) = x[i];
     }
 }
 
 // kRows: rows whose columns a thread holds at a time, as few as the search allows.  64 of 16
-// bytes would be all its registers, so such searches move 8 bytes at a time (64 beams: 560
-// us, 4 bytes 713).
+// bytes would be all its registers, so such searches move 8 bytes at a time.
 template <int N, int kRows>
 __global__ void __launch_bounds__(kReThreads, kRows <= 8 ? 4 : kRows <= 16 ? 2 : 1)
     reorder_kernel(const __grid_constant__ ReBatch<N> g, const __grid_constant__ ReArgs a) {
