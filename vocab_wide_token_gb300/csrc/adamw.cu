@@ -9,7 +9,7 @@
 // more than the bytes: 10 bytes at 6.7 TB/s leave an SM about 55 instructions for each
 // element, and decoding, drawing (18), encoding and the step are 82, or 60 rounded to nearest.
 // 60 million elements, with bf16 parameters and gradients unless said otherwise:
-//   32-bit moments  202 us, 6.5 TB/s; all in fp32 260 us, 6.5 TB/s
+//   32-bit moments  202 us drawn, 6.5 TB/s; all in fp32 242 us, 6.9 TB/s
 //   8-bit moments   173 us drawn, 3.5 TB/s; 123 us to nearest, 4.9 TB/s; fp32 drawn 172 us
 //
 // 8-bit moments.  Codes of three bits of mantissa under an exponent that reaches a fixed
@@ -44,6 +44,10 @@ constexpr int kAdBlock = 128;                   // elements that share an expone
 constexpr int kAdUnit = 4096;                   // elements of one tensor, a CTA's turn
 constexpr int kAdUnitSmall = 512;               // of one with 8-bit moments, a warp's
 constexpr int kAdCtas = 2;                      // per SM
+// Most CTAs for each SM of the forms that HBM alone bounds, whose reads and writes then come
+// in turns: 60 million fp32 elements 242 us (260 with kAdCtas), the 8-bit moments' values 91 us
+// (105 with 8).  A drawn step takes longer with more CTAs: 214 us, 202 with kAdCtas.
+constexpr int kAdTurns = 64;
 constexpr int kAdBatch = 600;                   // tensors of one launch (they travel as its arguments)
 constexpr int kDepthM = 14, kDepthV = 30;       // binary orders below a block's largest
 
@@ -836,9 +840,11 @@ int run_kind(const pstat_adamw_tensor* tensors, int64_t n, const AdOptions& o, c
                             kSmall ? kAdUnitSmall : kAdUnit))
                 break;
         }
+        // Many short CTAs where starting one costs little: no draws' keys, and no powers of the betas.
+        const int turns = kSmall || kRandom || o.lr_at || o.step_at ? kAdCtas : kAdTurns;
         const uint32_t ctas = kSmall ? (b.units - 1) / (kAdThreads / 32) + 1 : b.units;
         if (b.count && launch_behind(adamw_kernel<N, (kKind & 1u) != 0, (kKind & 2u) != 0, kSmall, kRandom>,
-                                     grid_of(ctas, kAdCtas, dev), kAdThreads, 0, st, 1, b, o) != cudaSuccess)
+                                     grid_of(ctas, turns, dev), kAdThreads, 0, st, 1, b, o) != cudaSuccess)
             return PSTAT_ERR_CUDA;
     }
     return PSTAT_OK;
@@ -891,7 +897,7 @@ int run_moments(const pstat_adamw_moment* list, int64_t n, const DeviceInfo& dev
                 break;
         }
         if (b.count &&
-            launch_behind(adamw_moments_kernel<N>, grid_of(b.units, 8, dev), kAdThreads, 0, st, 1, b) != cudaSuccess)
+            launch_behind(adamw_moments_kernel<N>, grid_of(b.units, kAdTurns, dev), kAdThreads, 0, st, 1, b) != cudaSuccess)
             return PSTAT_ERR_CUDA;
     }
     return PSTAT_OK;
