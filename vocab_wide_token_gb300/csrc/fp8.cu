@@ -23,7 +23,8 @@ constexpr int64_t kF8MaxStride = (int64_t)1 << 31;  // of scales: products with 
 // the order of operations.  (max|x| / 448 itself would use the last bit of range, but
 // e4m3 is a floating-point type, whose relative step does not depend on it.)
 // A thread takes 8 neighbouring columns of every 16th row of a CTA's rows; all its loads
-// are in flight before the first is used.  Bound by HBM.
+// are in flight before the first is used.  Bound by HBM: 60,000 x 4096 bf16 by 128 x 128 in 114
+// us, 6.4 TB/s, by rows 127 us, 5.8 (with 32 or 128 rows to a CTA 142); 151,936 x 4096 274 us.
 // ---------------------------------------------------------------------------
 constexpr int kQuThreads = 256;
 constexpr int kQuRows = 64;  // rows of a CTA where each has its own scale
@@ -703,6 +704,8 @@ cudaError_t launch_wide(F8Args a, const void* q, const void* W, int64_t K, const
     return launch_behind(fp8_wide_kernel<O>, (unsigned)(2 * pairs), C::kThreads, C::kBytes, st, 2, a);
 }
 
+// The narrowest tile that holds the tokens.  151,936 x 4096, us: up to 32 tokens 94 (tiles for 128
+// take 108 to 152, wide ones 116 to 172), 64 tokens 96 (108, 117), 128 tokens 110 (wide 121).
 template <typename O>
 cudaError_t launch_logits_of(const F8Args& a, const void* q, const void* W, int64_t K, const DeviceInfo& dev,
                              cudaStream_t st) {
