@@ -347,7 +347,9 @@ __global__ void __launch_bounds__(F8Narrow<kN>::kThreads, 1)
             // After a timeout no wait is made and nothing is written, but the sums run to
             // their end: a way out of their loop would cost every sum a register of its own.
             for (int j = 0; j < a.blocks; ++j, ++it) {
-                float* fs = scales + (j & 1) * kCols;
+                // The halves take turns over all tiles: a lane that is ahead writes one only after
+                // the next block's __syncwarp, when every lane has read what it held.
+                float* fs = scales + (it & 1) * kCols;
                 if (lane < kCols) fs[lane] = __fmul_rn(next, next_w);
                 if (j + 1 < a.blocks) {
                     qs += a.scale_col;
