@@ -86,7 +86,8 @@ struct AdScalars {
     float b1, c1, b2, c2, eps, factor, decay, size, root;
     uint32_t seed_key;
     bool skip;
-    bool tiny_eps;  // the root's small values weigh against eps
+    bool small_eps;  // the roots of subnormal numbers weigh against eps (see updated)
+    bool tiny_eps;   // eps itself is no divisor for reciprocals that flush small ones
 };
 
 // 32 bits that are as good as random, from a counter under a key: two rounds of
@@ -126,6 +127,7 @@ __device__ AdScalars scalars_of(const AdOptions& o) {
         const double t = (double)(o.step_at ? *after_wait(o.step_at) : o.step);
         corrections(lr, o.weight_decay, o.beta1, o.beta2, t, s.decay, s.size, s.root);
     }
+    s.small_eps = !(s.eps >= 0x1p-41f * s.root);
     s.tiny_eps = !(s.eps >= 0x1p-60f);
     s.factor = 1.f;
     s.skip = false;
@@ -192,19 +194,26 @@ __device__ __forceinline__ void moments(float g, const AdScalars& s, float& m, f
     v = __fadd_rn(__fmul_rn(v, s.b2), __fmul_rn(__fmul_rn(x, x), s.c2));
 }
 // The root and the quotient are approximations of 2^-22: the step they give is a small
-// part of the parameter, or all of one that was zero.  Where eps is at least 2^-60, a root below
-// 2^-63 does not count beside it, and the divisor is a normal number.
-__device__ __forceinline__ float updated(float p, float m, float v, const AdScalars& s) {
+// part of the parameter, or all of one that was zero.  A root that flushes subnormal numbers drops
+// up to 2^-63, which s.root multiplies: where eps is at least 2^22 times that, it is 2^-22 of the
+// divisor.  Of a smaller eps (1e-15 at the first step with beta2 = 0.999: 0.3%) those numbers
+// are scaled to normal ones first, and divisors as small likewise; others have the same bits
+// either way.
+__device__ __forceinline__ float updated_fast(float p, float m, float v, const AdScalars& s) {
     float root, step;
-    if (s.tiny_eps) {
-        asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v));
-        step = __fdividef(m, fmaf(root, s.root, s.eps));
-    } else {
-        asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(v));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(step) : "f"(fmaf(root, s.root, s.eps)));
-        step *= m;
-    }
-    return fmaf(-s.size, step, p * s.decay);
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(v));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(step) : "f"(fmaf(root, s.root, s.eps)));
+    return fmaf(-s.size, step * m, p * s.decay);
+}
+__device__ __forceinline__ float updated(float p, float m, float v, const AdScalars& s) {
+    if (!s.small_eps) return updated_fast(p, m, v, s);
+    const bool low = v < 0x1p-126f;
+    float root, step;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(low ? v * 0x1p64f : v));
+    if (low) root *= 0x1p-32f;
+    const float divisor = fmaf(root, s.root, s.eps), scale = divisor < 0x1p-100f ? 0x1p100f : 1.f;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(step) : "f"(divisor * scale));
+    return fmaf(-s.size, step * m * scale, p * s.decay);
 }
 // Two parameters to bf16; the draws' upper 16 bits are used.  kAny: they may be NaN.
 template <bool kRandom, bool kAny>
@@ -298,14 +307,6 @@ __device__ __noinline__ void step_block(const AdView t, const AdScalars* shared,
     }
 }
 
-// The step of a normal eps (see updated): a divisor of a normal number.
-__device__ __forceinline__ float updated_fast(float p, float m, float v, const AdScalars& s) {
-    float root, step;
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(v));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(step) : "f"(fmaf(root, s.root, s.eps)));
-    return fmaf(-s.size, step * m, p * s.decay);
-}
-
 // Copies 16 bytes to shared memory in the background, or none.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -353,9 +354,10 @@ struct AdRing {
 // Blocks b and b + 1 with 8-bit moments, from a stage: element 128 b + 4 lane + e is a lane's
 // e-th of block b.  Both go through each phase together, whose reductions and votes then
 // overlap.  What is rare takes a branch of its own that the warp goes through together: codes
-// of zero, values below the least code.  Where a code or a result is an infinity or NaN
-// nothing is stored, for step_block: false.  `exponents` has lane b % 32's in its lower byte (m)
-// and the next (v), and the new ones come out in the same way.
+// of zero, values below the least code.  Where a code or a result is an infinity or NaN, or
+// a root needs more care (small_eps), nothing is stored, for step_block: false.  `exponents`
+// has lane b % 32's in its lower byte (m) and the next (v), and the new ones come out in the
+// same way.
 //   decoding   bits = (code << 20) + (base << 20)
 //   encoding   the code is bits 20.. of bits + draw - (base << 20), which 16 times as large
 //              is the upper byte
@@ -434,6 +436,12 @@ __device__ __forceinline__ bool step_small(const uint8_t* stage, uint32_t expone
         top_v[j] = __reduce_max_sync(0xFFFFFFFFu, top_v[j]);
         whole = whole && top_m[j] < 0x7F800000u && top_v[j] < 0x7F800000u;
     }
+    if (s.small_eps)
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)  // above zero, below 2^-126
+                whole = whole && __float_as_uint(xv[j][e]) - 1u >= 0x7FFFFFu;
     if (__any_sync(0xFFFFFFFFu, !whole || (nans & 0x80808080u) || lost != lost)) return false;
     uint32_t ym[kN][4], yv[kN][4];
     bool low = false;
@@ -650,7 +658,7 @@ __device__ __forceinline__ int ad_tensor_of(const AdBatch<N>& g, uint32_t u) {
 
 // One kind of tensors to a launch, so that each has the registers that it needs.
 template <int N, bool kBf16P, bool kBf16G, bool kSmall, bool kRandom>
-__global__ void __launch_bounds__(kAdThreads, kAdCtas)
+__global__ void __launch_bounds__(kAdThreads, kBf16P && !kSmall && !kRandom ? 3 : kAdCtas)
     adamw_kernel(const __grid_constant__ AdBatch<N> b, const __grid_constant__ AdOptions o) {
     using Ring = AdRing<kBf16P, kBf16G>;
     __shared__ AdScalars shared;
