@@ -1,11 +1,11 @@
 // beams.cu -- the next beams of a search over beams and vocabulary.
 //
-// Continuation (k, v) scores c_k + z_kv, c_k = score_k - M_k - ln S_k.  The records
+// Continuation (k, v) scores (z_kv - M_k) + d_k, d_k = score_k - ln S_k.  The records
 // kernel of the sampler reads the logits once and leaves, per chunk, maximum and sum, and
 // per 256 bytes of columns (a group) their maximum.  beam_finish_kernel, a CTA for a
 // search, does the rest on those:
 //
-//   1. c_k from the records, a warp for each beam;
+//   1. M_k and d_k from the records, a warp for each beam;
 //   2. every thread takes a run of neighbouring groups (of all beams, in order) and its
 //      best score.  The n best continuations lie in the n runs that are best by (score,
 //      place): a run with n better ones before it has n continuations before its own;
@@ -15,11 +15,13 @@
 // So at most n runs, groups and n x 128 columns are ever sorted, whatever the logits are
 // (all equal, say), and ties go by place throughout.
 //
-// Scores are compared as pairs of floats, c_k + z by an exact sum, in 64-bit keys.  c_k
-// carries the error of the fp32 sum S.  Where two continuations of different beams lie
-// closer than that, in or at the end of the list, the S of both beams is summed anew from
-// exact weights (2^-40, filter_math.cuh), and the choice is made again; scores of one beam
-// differ by its logits alone and need none.
+// Scores are compared as pairs of floats, in 64-bit keys.  z - M is exact as a pair, so a
+// row's offset, which its softmax does not depend on, costs no digits; the roundings of low
+// words, in d and in adding it, are 2^-46 (|score| + 2 |score_k| + 28) at most (28 for ln S of
+// 2^20 columns).  d_k also carries the error of the fp32 sum S.  Where two continuations of
+// different beams lie closer than that, in or at the end of the list, the S of both beams is
+// summed anew from exact weights (ln S to 2^-40, filter_math.cuh), and the choice is made
+// again; scores of one beam differ by its logits alone and need none.
 // Bound by the records, hence by HBM, for a batch of searches (64 of 16 beams over 151,936
 // bf16 columns: 65 us, 311 MB at 4.8 TB/s, of which the records are 48 us); by latency for
 // one (4 beams: 15 us, the records 5).
@@ -34,7 +36,7 @@ namespace pstat {
 namespace {
 
 constexpr int kBmKeep = PSTAT_BEAM_MAX_N;  // places of the list that is carried along
-// Error of c_k: kSumError of S, and logf's of 1 ulp of at most ln 2^20 (2^-20).
+// Error of d_k: kSumError of S, and logf's of 1 ulp of at most ln 2^20 (2^-20).
 constexpr float kBmError = 0x1.8p-18f;
 static_assert(kBmError >= kSumError + 0x1p-20f, "");
 static_assert(PSTAT_BEAM_MAX <= 64, "rows of a search in a 64-bit mask");
@@ -60,14 +62,24 @@ __device__ __forceinline__ bool before(const Entry& a, const Entry& b) {
 struct Pair {
     float hi, lo;
 };
-__device__ __forceinline__ Pair pair_sum(const Pair& c, float z) {
-    const float s = __fadd_rn(c.hi, z);
-    const float b = __fsub_rn(s, c.hi);
-    const float e = __fadd_rn(__fsub_rn(c.hi, __fsub_rn(s, b)), __fsub_rn(z, b));
-    const float l = __fadd_rn(e, c.lo);
-    const float hi = __fadd_rn(s, l);
-    return {hi, __fsub_rn(l, __fsub_rn(hi, s))};
+// a + b, exactly.
+__device__ __forceinline__ Pair exact_sum(float a, float b) {
+    const float s = __fadd_rn(a, b);
+    const float t = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
+// a + b to about 2^-47 (|a| + |b|).
+__device__ __forceinline__ Pair pair_sum(const Pair& a, const Pair& b) {
+    const Pair s = exact_sum(a.hi, b.hi);
+    const float l = __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo));
+    const float hi = __fadd_rn(s.hi, l);
+    return {hi, __fsub_rn(l, __fsub_rn(hi, s.hi))};
+}
+// What the scores of a beam's continuations are formed from.
+struct Base {
+    Pair d;  // score - ln S
+    float M;
+};
 __device__ __forceinline__ uint32_t ordered(float x) {  // ascending; +-0 alike
     const uint32_t b = __float_as_uint(x + 0.f);
     return b ^ (uint32_t)(((int32_t)b >> 31) | (int32_t)0x80000000);
@@ -75,9 +87,9 @@ __device__ __forceinline__ uint32_t ordered(float x) {  // ascending; +-0 alike
 __device__ __forceinline__ float unordered(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
-__device__ __forceinline__ uint64_t score_key(const Pair& c, float z) {
-    if (c.hi == -INFINITY || z == -INFINITY) return 0;
-    const Pair s = pair_sum(c, z);
+__device__ __forceinline__ uint64_t score_key(const Base& b, float z) {
+    if (b.d.hi == -INFINITY || z == -INFINITY) return 0;
+    const Pair s = pair_sum(exact_sum(z, -b.M), b.d);
     return (uint64_t)ordered(s.hi) << 32 | ordered(s.lo);
 }
 __device__ __forceinline__ Pair key_score(uint64_t key) {
@@ -92,8 +104,8 @@ __device__ __forceinline__ float pair_gap(uint64_t a, uint64_t b) {
 template <int kThreads>
 struct BeamShared {
     static constexpr int kNew = kThreads - kBmKeep;  // candidates of one round of sorting
-    Pair c[PSTAT_BEAM_MAX];
-    float M[PSTAT_BEAM_MAX], S[PSTAT_BEAM_MAX];
+    Base base[PSTAT_BEAM_MAX];
+    float S[PSTAT_BEAM_MAX];
     uint64_t key[kThreads];
     uint32_t at[kThreads];
     Entry list[kBmKeep];       // what the last selection kept, best first
@@ -241,7 +253,7 @@ __device__ __forceinline__ void select_best(BeamShared<kThreads>& sm, int n, int
 template <typename E, int kThreads>
 __device__ __noinline__ void sum_anew(BeamShared<kThreads>& sm, const BeamArgs& a, int64_t t, int k, float score) {
     const E* row = static_cast<const E*>(a.f.logits) + t * a.f.ld;
-    const float M = sm.M[k];
+    const float M = sm.base[k].M;
     const int scale = fixed_scale(sm.S[k] * (1.f + 2.f * kSumError));
     const TempScale one = temp_scale(1.f);
     constexpr int kVec = Elem<E>::kVec;
@@ -265,9 +277,7 @@ __device__ __noinline__ void sum_anew(BeamShared<kThreads>& sm, const BeamArgs& 
         for (int w = 0; w < kThreads / 32; ++w) sum += sm.sum[w];
         const double lnS = log((double)sum) - scale * 0.69314718055994530942;
         const float hi = (float)lnS;
-        Pair c = pair_sum(pair_sum({score, 0.f}, -M), -hi);
-        c.lo = __fsub_rn(c.lo, (float)(lnS - (double)hi));
-        sm.c[k] = pair_sum(c, 0.f);
+        sm.base[k].d = pair_sum({score, 0.f}, {-hi, -(float)(lnS - (double)hi)});
     }
     __syncthreads();
 }
@@ -295,19 +305,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) beam_finish_kernel(
         const float s = scores[k];
         const float3 r = fold_records(records + (int64_t)k * chunks, chunks, kLog2e, lane);
         if (lane == 0) {
-            Pair c = {-INFINITY, 0.f};
+            Pair d = {-INFINITY, 0.f};
             if (!(s < INFINITY))
                 sm.bad = 1;
             else if (s > -INFINITY) {
                 if (!(r.x < INFINITY))
                     sm.bad = 1;
-                else if (r.x > -INFINITY) {
-                    const Pair p = pair_sum({s, 0.f}, -r.x);
-                    c = pair_sum(p, -logf(r.y));
-                }
+                else if (r.x > -INFINITY)
+                    d = exact_sum(s, -logf(r.y));
             }
-            sm.c[k] = c;
-            sm.M[k] = r.x;
+            sm.base[k] = {d, r.x};
             sm.S[k] = r.y;
         }
     }
@@ -373,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) beam_finish_kernel(
         each_of_run([&](const float(&x)[8], int, int k) {
             const float m = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
                                   fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-            const uint64_t key = score_key(sm.c[k], m);
+            const uint64_t key = score_key(sm.base[k], m);
             if (key > mine.key) mine = {key, threadIdx.x};
         });
         keep_best(sm, mine, n, kThreads);
@@ -386,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) beam_finish_kernel(
                 if (g >= total) continue;
                 float x[8];
                 load8(g, x);
-                const Pair c = sm.c[g / groups];
+                const Base c = sm.base[g / groups];
 #pragma unroll
                 for (int q = 0; q < 8; ++q) emit(Entry{score_key(c, x[q]), (uint32_t)(g + q)}, 8 * i + q);
             }
@@ -397,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) beam_finish_kernel(
             each_of_groups([&](const float(&x)[kVec], int col, int k, int i) {
 #pragma unroll
                 for (int q = 0; q < kVec; ++q)
-                    emit(Entry{score_key(sm.c[k], x[q]), (uint32_t)(k * V + col + q)}, i + q);
+                    emit(Entry{score_key(sm.base[k], x[q]), (uint32_t)(k * V + col + q)}, i + q);
             });
         });
         if (beams == 1) break;
@@ -426,11 +433,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) beam_finish_kernel(
             if (mine.key && (mine.key >= last || pair_gap(last, mine.key) <= kTol))
                 each_of_run([&](const float(&x)[8], int, int k) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) outside(score_key(sm.c[k], x[q]), k);
+                    for (int q = 0; q < 8; ++q) outside(score_key(sm.base[k], x[q]), k);
                 });
             each_of_groups([&](const float(&x)[kVec], int, int k, int) {
 #pragma unroll
-                for (int q = 0; q < kVec; ++q) outside(score_key(sm.c[k], x[q]), k);
+                for (int q = 0; q < kVec; ++q) outside(score_key(sm.base[k], x[q]), k);
             });
         }
         __syncthreads();
