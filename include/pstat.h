@@ -616,10 +616,11 @@ PSTAT_API int pstat_fp8_logits(const void* q, const float* q_scale, int64_t scal
  * continuations the n best, in descending order; equal ones by the lowest (k, v).
  * Scores are compared as they are in exact arithmetic, to 2^-38 of the largest of
  * |s|, |score| and 1; what comes out is within 6e-6 + 2^-24 |score| of the score.  A score of
- * -inf, and a row whose logits are all -inf, is a beam without continuations; places
- * that none is left for get score -inf, parent and token -1.  A score of NaN or +inf, or a row with a NaN or +inf logit (of a
- * beam with a finite score), leaves its search undefined: PSTAT_DEV_EMPTY_ROW, scores
- * NaN, parents and tokens -1.
+ * -inf, and a row whose logits are all -inf, is a beam without continuations; a token
+ * whose z_v - M or score lies below the range of fp32 is none either.  Places that
+ * none is left for get score -inf, parent and token -1.  A score of NaN or +inf, or
+ * a row with a NaN or +inf logit (of a beam with a finite score), leaves its search
+ * undefined: PSTAT_DEV_EMPTY_ROW, scores NaN, parents and tokens -1.
  *   logits      [B beams, ld] of dtype `dt`, V <= PSTAT_FILTER_MAX_V; ld 0: one row for
  *               all beams.
  *   scores      [B, beams] float.

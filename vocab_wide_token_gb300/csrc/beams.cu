@@ -87,9 +87,12 @@ __device__ __forceinline__ uint32_t ordered(float x) {  // ascending; +-0 alike
 __device__ __forceinline__ float unordered(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
+// 0 (no continuation) for what is masked, and for what lies below fp32's range: z - M of a mask
+// of the type's lowest value can, and its sum with such a score.  The low words are NaN then,
+// and so is the sum.
 __device__ __forceinline__ uint64_t score_key(const Base& b, float z) {
-    if (b.d.hi == -INFINITY || z == -INFINITY) return 0;
     const Pair s = pair_sum(exact_sum(z, -b.M), b.d);
+    if (!(s.hi > -INFINITY)) return 0;
     return (uint64_t)ordered(s.hi) << 32 | ordered(s.lo);
 }
 __device__ __forceinline__ Pair key_score(uint64_t key) {

@@ -1297,8 +1297,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int, *, out=None,
     `logits` holds the beams' rows, [B * beams, V].  Continuation (k, v) scores
     scores[b, k] + log softmax(row)[v].  Returns (score [B, n] f32, parent [B, n] int64:
     k, token [B, n] int64: v), best first, equal ones by the lowest (k, v), and
-    (-inf, -1, -1) where no continuation is left.  Which ones they are is decided as in
-    exact arithmetic.  With n twice the beams, as many go on as there were beams even
+    (-inf, -1, -1) where no continuation is left: one whose score lies below float32's range
+    is none.  Which ones they are is decided as in exact arithmetic.  With n twice the beams, as many go on as there were beams even
     when all others end.  `out` may supply the three tensors, `workspace` a uint8
     CUDA tensor of at least ``beam_workspace_size`` bytes, which calls that overlap
     on the GPU may not share.
