@@ -658,6 +658,11 @@ typedef struct {
 PSTAT_API int pstat_beam_reorder(const pstat_beam_state* states, int64_t n_states,
                                  const int64_t* parents, int64_t B, int64_t beams,
                                  int64_t out_beams, int* dev_error, pstat_stream_t stream);
+/* The same into outputs that hold nothing yet: rows without a parent, -1 or outside
+ * [0, beams), become zeros.  Not in place (PSTAT_ERR_PARAM). */
+PSTAT_API int pstat_beam_gather(const pstat_beam_state* states, int64_t n_states,
+                                const int64_t* parents, int64_t B, int64_t beams,
+                                int64_t out_beams, int* dev_error, pstat_stream_t stream);
 
 /*
  * Self-test of the bounded waits.  Every kernel of this library waits on its

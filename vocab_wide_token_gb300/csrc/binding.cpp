@@ -44,6 +44,7 @@ struct Library {
     decltype(&pstat_beam_workspace_size) beam_workspace_size;
     decltype(&pstat_beam_select) beam_select;
     decltype(&pstat_beam_reorder) beam_reorder;
+    decltype(&pstat_beam_gather) beam_gather;
 } lib = {};
 
 const at::Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
@@ -601,8 +602,8 @@ PyObject* beam_reorder(PyObject* const* a, Py_ssize_t argc) {
             taken = taken && take_runs(*xs[i], *os[i], &v[i]);
         }
         if (!taken) return (int)PSTAT_OK;
-        return lib.beam_reorder(v.data(), (int64_t)n, parents->const_data_ptr<int64_t>(), B, rows / B, out_beams, err,
-                                stream_of(device));
+        return (given ? lib.beam_reorder : lib.beam_gather)(v.data(), (int64_t)n, parents->const_data_ptr<int64_t>(),
+                                                            B, rows / B, out_beams, err, stream_of(device));
     });
     if (rc != PSTAT_OK) return refuse(rc);
     if (!taken) Py_RETURN_NONE;
@@ -635,7 +636,18 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
-// bind_more(addresses): those from adamw_step on.
+// bind_gather(address): the last one.
+PyObject* bind_gather(PyObject* const* a, Py_ssize_t n) {
+    void* p = n == 1 ? PyLong_AsVoidPtr(a[0]) : nullptr;
+    if (!p) {
+        if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "one address expected, not null");
+        return nullptr;
+    }
+    lib.beam_gather = reinterpret_cast<decltype(lib.beam_gather)>(p);
+    Py_RETURN_NONE;
+}
+
+// bind_more(addresses): those from adamw_step to beam_reorder.
 PyObject* bind_more(PyObject* const* a, Py_ssize_t n) {
     void* p[7];
     if (n != 7) {
@@ -661,9 +673,9 @@ PyObject* bind_more(PyObject* const* a, Py_ssize_t n) {
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<name>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(bind),      FAST(sample),         FAST(filtered_forward), FAST(filtered_backward),
-                         FAST(grad_norm), FAST(clip_grad_norm), FAST(bind_more),    FAST(adamw_step),
-                         FAST(adamw_moments), FAST(fp8_quantize), FAST(fp8_logits), FAST(beam_select),
-                         FAST(beam_reorder), {nullptr, nullptr, 0, nullptr}};
+                         FAST(grad_norm), FAST(clip_grad_norm), FAST(bind_more),    FAST(bind_gather),
+                         FAST(adamw_step), FAST(adamw_moments), FAST(fp8_quantize), FAST(fp8_logits),
+                         FAST(beam_select), FAST(beam_reorder), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -55,9 +55,11 @@ struct ReArgs {
     int* dev_error;
 };
 
+constexpr int kStays = -1, kZeros = -2;
+
 // One column of search b, of every lane that `has` one.  All lanes are here: lane l reads the
 // l-th parent, and the others ask it for that.
-template <typename V, int kRows>
+template <typename V, int kRows, bool kClear>
 __device__ __forceinline__ void move_column(const ReState& s, const ReArgs& a, const int64_t* parents,
                                             int64_t b, uint32_t col, bool has) {
     const int lane = threadIdx.x & 31;
@@ -66,12 +68,13 @@ __device__ __forceinline__ void move_column(const ReState& s, const ReArgs& a, c
     char* out = s.out + b * a.out_beams * s.out_row + seg * s.out_seg + (int64_t)at * sizeof(V);
     for (int i0 = 0; i0 < a.out_beams; i0 += kRows) {  // once in place: kRows >= out_beams there
         constexpr int kWords = (kRows + 31) / 32;
-        int from[kWords];  // -1: the row stays
+        int from[kWords];  // kStays, kZeros or a parent
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
             const int i = i0 + 32 * w + lane;
             const int64_t p = i < a.out_beams ? parents[i] : -1;
-            from[w] = p >= 0 && p < a.beams && !(a.in_place && p == i) ? (int)p : -1;
+            const bool moves = p >= 0 && p < a.beams && !(a.in_place && p == i);
+            from[w] = moves ? (int)p : kClear && i < a.out_beams ? kZeros : kStays;
         }
         int p[kRows];  // all before the first row's load
 #pragma unroll
@@ -83,6 +86,9 @@ __device__ __forceinline__ void move_column(const ReState& s, const ReArgs& a, c
             if (p[i] >= 0) {
                 moved |= 1ull << i;
                 x[i] = *reinterpret_cast<const V*>(in + p[i] * s.in_row);
+            } else if (kClear && p[i] == kZeros) {
+                moved |= 1ull << i;
+                x[i] = V();
             }
 #pragma unroll
         for (int i = 0; i < kRows; ++i)
@@ -91,8 +97,9 @@ __device__ __forceinline__ void move_column(const ReState& s, const ReArgs& a, c
 }
 
 // kRows: rows whose columns a thread holds at a time, as few as the search allows.  64 of 16
-// bytes would be all its registers, so such searches move 8 bytes at a time.
-template <int N, int kRows>
+// bytes would be all its registers, so such searches move 8 bytes at a time.  kClear: rows
+// without a parent become zeros, and are left as they are otherwise.
+template <int N, int kRows, bool kClear>
 __global__ void __launch_bounds__(kReThreads, kRows <= 8 ? 4 : kRows <= 16 ? 2 : 1)
     reorder_kernel(const __grid_constant__ ReBatch<N> g, const __grid_constant__ ReArgs a) {
     grid_wait();
@@ -120,14 +127,14 @@ __global__ void __launch_bounds__(kReThreads, kRows <= 8 ? 4 : kRows <= 16 ? 2 :
         const int64_t* p = parents + b * a.out_beams;
         switch (s.vec) {
             case 16:
-                if constexpr (kRows <= 32) move_column<uint4, kRows>(s, a, p, b, has ? col : 0u, has);
+                if constexpr (kRows <= 32) move_column<uint4, kRows, kClear>(s, a, p, b, has ? col : 0u, has);
                 break;
             case 8:
-                move_column<uint2, kRows>(s, a, p, b, has ? col : 0u, has);
+                move_column<uint2, kRows, kClear>(s, a, p, b, has ? col : 0u, has);
                 break;
-            case 4: move_column<uint32_t, kRows>(s, a, p, b, has ? col : 0u, has); break;
-            case 2: move_column<uint16_t, kRows>(s, a, p, b, has ? col : 0u, has); break;
-            default: move_column<uint8_t, kRows>(s, a, p, b, has ? col : 0u, has); break;
+            case 4: move_column<uint32_t, kRows, kClear>(s, a, p, b, has ? col : 0u, has); break;
+            case 2: move_column<uint16_t, kRows, kClear>(s, a, p, b, has ? col : 0u, has); break;
+            default: move_column<uint8_t, kRows, kClear>(s, a, p, b, has ? col : 0u, has); break;
         }
     }
 }
@@ -223,7 +230,7 @@ int check_states(const pstat_beam_state* states, int64_t n, const int64_t* paren
     return PSTAT_OK;
 }
 
-template <int N, int kRows>
+template <int N, int kRows, bool kClear>
 int run_rows(const pstat_beam_state* states, int64_t n, const ReArgs& a, uint32_t widest, const DeviceInfo& dev,
              cudaStream_t st) {
     ReBatch<N> g;
@@ -257,18 +264,18 @@ int run_rows(const pstat_beam_state* states, int64_t n, const ReArgs& a, uint32_
         g.units = (uint32_t)units;
         if (!g.count) continue;
         const uint32_t most = (uint32_t)dev.sm_count * kReTurns;
-        if (launch_behind(reorder_kernel<N, kRows>, g.units < most ? g.units : most, kReThreads, 0, st, 1, g, a) !=
-            cudaSuccess)
+        if (launch_behind(reorder_kernel<N, kRows, kClear>, g.units < most ? g.units : most, kReThreads, 0, st, 1, g,
+                          a) != cudaSuccess)
             return PSTAT_ERR_CUDA;
     }
     return PSTAT_OK;
 }
 
-template <int kRows>
+template <int kRows, bool kClear = false>
 int run_states(const pstat_beam_state* states, int64_t n, const ReArgs& a, uint32_t widest, const DeviceInfo& dev,
                cudaStream_t st) {
-    return n <= 16 ? run_rows<16, kRows>(states, n, a, widest, dev, st)
-                   : run_rows<kReBatch, kRows>(states, n, a, widest, dev, st);
+    return n <= 16 ? run_rows<16, kRows, kClear>(states, n, a, widest, dev, st)
+                   : run_rows<kReBatch, kRows, kClear>(states, n, a, widest, dev, st);
 }
 
 }  // namespace
@@ -276,20 +283,35 @@ int run_states(const pstat_beam_state* states, int64_t n, const ReArgs& a, uint3
 
 using namespace pstat;
 
-extern "C" int pstat_beam_reorder(const pstat_beam_state* states, int64_t n_states, const int64_t* parents,
-                                  int64_t B, int64_t beams, int64_t out_beams, int* dev_error,
-                                  pstat_stream_t stream) {
+static int reorder(const pstat_beam_state* states, int64_t n_states, const int64_t* parents, int64_t B,
+                   int64_t beams, int64_t out_beams, bool clear, int* dev_error, pstat_stream_t stream) {
     bool in_place = false;
     int rc = check_states(states, n_states, parents, B, beams, out_beams, &in_place);
     if (rc != PSTAT_OK) return rc;
+    if (clear && in_place) return PSTAT_ERR_PARAM;
     if (n_states == 0 || B == 0) return PSTAT_OK;
     DeviceInfo dev;
     rc = device_info(&dev);
     if (rc != PSTAT_OK) return rc;
     const ReArgs a = {parents, B, (int)beams, (int)out_beams, in_place, dev_error};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (clear) return run_states<8, true>(states, n_states, a, 16, dev, st);
     if (!in_place || out_beams <= 8) return run_states<8>(states, n_states, a, 16, dev, st);
     if (out_beams <= 16) return run_states<16>(states, n_states, a, 16, dev, st);
     if (out_beams <= 32) return run_states<32>(states, n_states, a, 16, dev, st);
     return run_states<64>(states, n_states, a, 8, dev, st);
 }
+
+extern "C" {
+
+int pstat_beam_reorder(const pstat_beam_state* states, int64_t n_states, const int64_t* parents, int64_t B,
+                       int64_t beams, int64_t out_beams, int* dev_error, pstat_stream_t stream) {
+    return reorder(states, n_states, parents, B, beams, out_beams, false, dev_error, stream);
+}
+
+int pstat_beam_gather(const pstat_beam_state* states, int64_t n_states, const int64_t* parents, int64_t B,
+                      int64_t beams, int64_t out_beams, int* dev_error, pstat_stream_t stream) {
+    return reorder(states, n_states, parents, B, beams, out_beams, true, dev_error, stream);
+}
+
+}  // extern "C"

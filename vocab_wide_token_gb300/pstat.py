@@ -124,6 +124,8 @@ def declare_prototypes(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.pstat_beam_select.restype = _i32
     lib.pstat_beam_reorder.argtypes = [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp]
     lib.pstat_beam_reorder.restype = _i32
+    lib.pstat_beam_gather.argtypes = [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp]
+    lib.pstat_beam_gather.restype = _i32
     lib.pstat_noalloc_scratch_bytes.argtypes = []
     lib.pstat_noalloc_scratch_bytes.restype = _sz
     lib.pstat_selftest_wait_timeout.argtypes = [ctypes.c_uint64, _vp, _vp]
@@ -147,6 +149,7 @@ try:
         _lib.pstat_adamw_step, _lib.pstat_adamw_moments, _lib.pstat_fp8_quantize,
         _lib.pstat_fp8_logits, _lib.pstat_beam_workspace_size, _lib.pstat_beam_select,
         _lib.pstat_beam_reorder)))
+    _native.bind_gather(ctypes.cast(_lib.pstat_beam_gather, _vp).value)
 except ImportError:  # not built: every call takes the path below
     _native = None
 
@@ -1367,7 +1370,8 @@ def beam_reorder(states, parents: torch.Tensor, *, out=None, dev_error=None):
     of a cache (``cache[:, :, :length]``).  `out`
     may supply the results; the states themselves, for as many beams as before,
     are reordered in place, and rows of beams that stay are not touched.  A parent of
-    -1 leaves its row as it was.  Returns the list of the results.
+    -1 leaves its row as it was; where there was none, in results of this call's own, the row
+    is zeros.  Returns the list of the results.
     """
     states = _tensor_list(states)
     if _native is not None:
@@ -1387,7 +1391,7 @@ def beam_reorder(states, parents: torch.Tensor, *, out=None, dev_error=None):
     B, out_beams = parents.shape
     parents = _tensor(parents, torch.int64, (B, out_beams), dev, "parents")
     rows = {x.shape[0] if x.dim() else -1 for x in states}
-    if len(rows) != 1 or B == 0 or min(rows) < 0 or min(rows) % B:
+    if len(rows) != 1 or B == 0 or min(rows) < 1 or min(rows) % B:
         raise ValueError("states must have B * beams rows each")
     beams = min(rows) // B
     given = out is not None
@@ -1410,7 +1414,8 @@ def beam_reorder(states, parents: torch.Tensor, *, out=None, dev_error=None):
                       segments, a, b, seg_bytes]
     words = array.array("q", words)
     if len(words):
-        _call(dev, "pstat_beam_reorder", _lib.pstat_beam_reorder,
+        name = "pstat_beam_reorder" if given else "pstat_beam_gather"
+        _call(dev, name, getattr(_lib, name),
               words.buffer_info()[0], len(words) // 8, _ptr(parents), B, beams, out_beams,
               _ptr(_error_flag(dev_error, dev)), _stream(dev))
     if given:
