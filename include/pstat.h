@@ -646,8 +646,10 @@ PSTAT_API int pstat_beam_select(const void* logits, pstat_dtype dt, int64_t B, i
  * seg_bytes bytes; all strides are in bytes.  In place (out == data for all states,
  * equal strides, beams == out_beams) rows of beams that are their own parent are not
  * touched.  An output may overlap nothing else of the call but, in place, its own
- * input (PSTAT_ERR_PARAM).  A parent of -1 leaves its row as it was, and so does one
- * outside [0, beams), which sets PSTAT_DEV_BAD_PARAM.
+ * input (PSTAT_ERR_PARAM).  A row moves by vectors of 16, 8, 4, 2 or 1 bytes, as its
+ * addresses, strides and runs allow, of which it may have 2^32 - 257 (PSTAT_ERR_SHAPE).
+ * A parent of -1 leaves its row as it was, and so does one outside [0, beams), which sets
+ * PSTAT_DEV_BAD_PARAM.
  */
 typedef struct {
     const void* data;

@@ -172,6 +172,31 @@ bool overlap(const Extent& a, const Extent& b) {
 }
 
 constexpr int64_t kMaxStride = (int64_t)1 << 46;
+constexpr uint64_t kMaxUnits = 0xF0000000ull;  // of a launch
+
+// Bytes of the widest vector.  (64 rows of 16 bytes would be all of a thread's registers.)
+uint32_t widest_of(bool in_place, int64_t out_beams) { return in_place && out_beams > 32 ? 8 : 16; }
+
+// A state that is not empty as the kernel takes it, first_unit apart; false where its vectors do
+// not count in 32 bits.
+bool state_of(const pstat_beam_state& p, int64_t B, uint32_t widest, ReState* out) {
+    ReState s = {static_cast<const char*>(p.data), static_cast<char*>(p.out), p.row_stride, p.out_row_stride,
+                 p.seg_stride, p.out_seg_stride, 0, 0, 0, 0, 0, 0};
+    int64_t segments = p.segments, bytes = p.seg_bytes;
+    if (segments > 1 && p.seg_stride == bytes && p.out_seg_stride == bytes) bytes *= segments, segments = 1;
+    if (segments == 1) s.in_seg = s.out_seg = 0;
+    const uint64_t all = reinterpret_cast<uintptr_t>(p.data) | reinterpret_cast<uintptr_t>(p.out) |
+                         (uint64_t)(s.in_row | s.out_row | s.in_seg | s.out_seg | bytes);
+    s.vec = widest;
+    while (all & (s.vec - 1)) s.vec /= 2;
+    const int64_t per_seg = bytes / s.vec;
+    if (per_seg > 0xFFFFFFFFll || segments * per_seg > 0xFFFFFFFFll - kReThreads) return false;
+    s.per_seg = (uint32_t)per_seg;
+    s.columns = (uint32_t)(segments * per_seg);
+    s.units = (s.columns + kReThreads - 1) / kReThreads;
+    *out = s;
+    return (uint64_t)s.units * (uint64_t)B <= kMaxUnits;
+}
 
 int check_states(const pstat_beam_state* states, int64_t n, const int64_t* parents, int64_t B, int64_t beams,
                  int64_t out_beams, bool* in_place) {
@@ -216,6 +241,8 @@ int check_states(const pstat_beam_state* states, int64_t n, const int64_t* paren
         if (same && (beams != out_beams || s.row_stride != s.out_row_stride ||
                      (s.segments > 1 && s.seg_stride != s.out_seg_stride)))
             return PSTAT_ERR_PARAM;
+        ReState taken;  // refused before any state is touched
+        if (!state_of(s, B, widest_of(same, out_beams), &taken)) return PSTAT_ERR_SHAPE;
         const uintptr_t out = reinterpret_cast<uintptr_t>(s.out), in = reinterpret_cast<uintptr_t>(s.data);
         v[m++] = {out, B * out_beams, s.out_row_stride, s.segments, s.segments > 1 ? s.out_seg_stride : s.seg_bytes,
                   s.seg_bytes, true};
@@ -231,8 +258,8 @@ int check_states(const pstat_beam_state* states, int64_t n, const int64_t* paren
 }
 
 template <int N, int kRows, bool kClear>
-int run_rows(const pstat_beam_state* states, int64_t n, const ReArgs& a, uint32_t widest, const DeviceInfo& dev,
-             cudaStream_t st) {
+int run_rows(const pstat_beam_state* states, int64_t n, const ReArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+    const uint32_t widest = widest_of(a.in_place, a.out_beams);
     ReBatch<N> g;
     for (int64_t i = 0; i < n;) {
         g.count = 0;
@@ -240,23 +267,10 @@ int run_rows(const pstat_beam_state* states, int64_t n, const ReArgs& a, uint32_
         for (; i < n && g.count < N; ++i) {
             const pstat_beam_state& p = states[i];
             if (p.segments == 0 || p.seg_bytes == 0) continue;
-            ReState s = {static_cast<const char*>(p.data), static_cast<char*>(p.out), p.row_stride, p.out_row_stride,
-                         p.seg_stride, p.out_seg_stride, 0, 0, 0, 0, 0, 0};
-            int64_t segments = p.segments, bytes = p.seg_bytes;
-            if (segments > 1 && p.seg_stride == bytes && p.out_seg_stride == bytes) bytes *= segments, segments = 1;
-            if (segments == 1) s.in_seg = s.out_seg = 0;
-            const uint64_t all = reinterpret_cast<uintptr_t>(p.data) | reinterpret_cast<uintptr_t>(p.out) |
-                                 (uint64_t)(s.in_row | s.out_row | s.in_seg | s.out_seg | bytes);
-            s.vec = widest;
-            while (all & (s.vec - 1)) s.vec /= 2;
-            const int64_t per_seg = bytes / s.vec;
-            if (per_seg > 0xFFFFFFFFll || segments * per_seg > 0xFFFFFFFFll - kReThreads) return PSTAT_ERR_SHAPE;
-            s.per_seg = (uint32_t)per_seg;
-            s.columns = (uint32_t)(segments * per_seg);
-            s.units = (s.columns + kReThreads - 1) / kReThreads;
+            ReState s;
+            if (!state_of(p, a.B, widest, &s)) return PSTAT_ERR_SHAPE;  // not after check_states
             const uint64_t add = (uint64_t)s.units * (uint64_t)a.B;
-            if (add > 0xF0000000ull) return PSTAT_ERR_SHAPE;
-            if (units + add > 0xF0000000ull) break;
+            if (units + add > kMaxUnits) break;
             s.first_unit = (uint32_t)units;
             units += add;
             g.s[g.count++] = s;
@@ -272,10 +286,9 @@ int run_rows(const pstat_beam_state* states, int64_t n, const ReArgs& a, uint32_
 }
 
 template <int kRows, bool kClear = false>
-int run_states(const pstat_beam_state* states, int64_t n, const ReArgs& a, uint32_t widest, const DeviceInfo& dev,
-               cudaStream_t st) {
-    return n <= 16 ? run_rows<16, kRows, kClear>(states, n, a, widest, dev, st)
-                   : run_rows<kReBatch, kRows, kClear>(states, n, a, widest, dev, st);
+int run_states(const pstat_beam_state* states, int64_t n, const ReArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+    return n <= 16 ? run_rows<16, kRows, kClear>(states, n, a, dev, st)
+                   : run_rows<kReBatch, kRows, kClear>(states, n, a, dev, st);
 }
 
 }  // namespace
@@ -295,11 +308,11 @@ static int reorder(const pstat_beam_state* states, int64_t n_states, const int64
     if (rc != PSTAT_OK) return rc;
     const ReArgs a = {parents, B, (int)beams, (int)out_beams, in_place, dev_error};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (clear) return run_states<8, true>(states, n_states, a, 16, dev, st);
-    if (!in_place || out_beams <= 8) return run_states<8>(states, n_states, a, 16, dev, st);
-    if (out_beams <= 16) return run_states<16>(states, n_states, a, 16, dev, st);
-    if (out_beams <= 32) return run_states<32>(states, n_states, a, 16, dev, st);
-    return run_states<64>(states, n_states, a, 8, dev, st);
+    if (clear) return run_states<8, true>(states, n_states, a, dev, st);
+    if (!in_place || out_beams <= 8) return run_states<8>(states, n_states, a, dev, st);
+    if (out_beams <= 16) return run_states<16>(states, n_states, a, dev, st);
+    if (out_beams <= 32) return run_states<32>(states, n_states, a, dev, st);
+    return run_states<64>(states, n_states, a, dev, st);
 }
 
 extern "C" {
