@@ -55,8 +55,6 @@ struct ReArgs {
     int* dev_error;
 };
 
-constexpr int kStays = -1, kZeros = -2;
-
 // One column of search b, of every lane that `has` one.  All lanes are here: lane l reads the
 // l-th parent, and the others ask it for that.
 template <typename V, int kRows, bool kClear>
@@ -68,13 +66,12 @@ __device__ __forceinline__ void move_column(const ReState& s, const ReArgs& a, c
     char* out = s.out + b * a.out_beams * s.out_row + seg * s.out_seg + (int64_t)at * sizeof(V);
     for (int i0 = 0; i0 < a.out_beams; i0 += kRows) {  // once in place: kRows >= out_beams there
         constexpr int kWords = (kRows + 31) / 32;
-        int from[kWords];  // kStays, kZeros or a parent
+        int from[kWords];  // -1: the row stays
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
             const int i = i0 + 32 * w + lane;
             const int64_t p = i < a.out_beams ? parents[i] : -1;
-            const bool moves = p >= 0 && p < a.beams && !(a.in_place && p == i);
-            from[w] = moves ? (int)p : kClear && i < a.out_beams ? kZeros : kStays;
+            from[w] = p >= 0 && p < a.beams && !(a.in_place && p == i) ? (int)p : -1;
         }
         int p[kRows];  // all before the first row's load
 #pragma unroll
@@ -86,13 +83,16 @@ __device__ __forceinline__ void move_column(const ReState& s, const ReArgs& a, c
             if (p[i] >= 0) {
                 moved |= 1ull << i;
                 x[i] = *reinterpret_cast<const V*>(in + p[i] * s.in_row);
-            } else if (kClear && p[i] == kZeros) {
-                moved |= 1ull << i;
-                x[i] = V();
             }
 #pragma unroll
         for (int i = 0; i < kRows; ++i)
             if (moved >> i & 1) *reinterpret_cast<V*>(out + (int64_t)(i0 + i) * s.out_row) = x[i];
+        if constexpr (kClear) {  // rare, and the same rows for all lanes
+            static_assert(kRows <= 32, "");
+            uint32_t none = __ballot_sync(0xFFFFFFFFu, from[0] < 0 && lane < kRows && i0 + lane < a.out_beams);
+            for (; none; none &= none - 1)
+                if (has) *reinterpret_cast<V*>(out + (int64_t)(i0 + __ffs(none) - 1) * s.out_row) = V();
+        }
     }
 }
 
@@ -187,9 +187,9 @@ bool state_of(const pstat_beam_state& p, int64_t B, uint32_t widest, ReState* ou
     if (segments == 1) s.in_seg = s.out_seg = 0;
     const uint64_t all = reinterpret_cast<uintptr_t>(p.data) | reinterpret_cast<uintptr_t>(p.out) |
                          (uint64_t)(s.in_row | s.out_row | s.in_seg | s.out_seg | bytes);
-    s.vec = widest;
-    while (all & (s.vec - 1)) s.vec /= 2;
-    const int64_t per_seg = bytes / s.vec;
+    const int shift = __builtin_ctzll(all | widest);
+    s.vec = 1u << shift;
+    const int64_t per_seg = bytes >> shift;
     if (per_seg > 0xFFFFFFFFll || segments * per_seg > 0xFFFFFFFFll - kReThreads) return false;
     s.per_seg = (uint32_t)per_seg;
     s.columns = (uint32_t)(segments * per_seg);
