@@ -84,6 +84,7 @@ struct AdOptions {
 // What the elements need of the options.
 struct AdScalars {
     float b1, c1, b2, c2, eps, factor, decay, size, root;
+    float rest;  // of the gradients' factor: 1, or a power of two (see scalars_of)
     uint32_t seed_key;
     bool skip;
     bool small_eps;  // the roots of subnormal numbers weigh against eps (see updated)
@@ -129,12 +130,18 @@ __device__ AdScalars scalars_of(const AdOptions& o) {
     }
     s.small_eps = !(s.eps >= 0x1p-41f * s.root);
     s.tiny_eps = !(s.eps >= 0x1p-60f);
-    s.factor = 1.f;
+    s.factor = s.rest = 1.f;
     s.skip = false;
     if (o.norm) {
         const float norm = *after_wait(o.norm);
         if (!(norm < INFINITY)) s.skip = true;
         if (norm > o.max_norm) s.factor = __fdiv_rn(o.max_norm, norm);
+        // A factor below the normal numbers (max_norm < 4) has lost bits, while what it scales, up to
+        // 2^128, comes out as a normal number: 2^125 times as large it keeps them.
+        if (s.factor < 0x1p-126f) {
+            s.factor = __fdiv_rn(__fmul_rn(o.max_norm, 0x1p125f), norm);
+            s.rest = 0x1p-125f;
+        }
     }
     const uint64_t seed = o.seed_at ? (uint64_t)*after_wait(o.seed_at) : o.seed;
     s.seed_key = mix32((uint32_t)(seed >> 32) ^ mix32((uint32_t)seed, 0x9E3779B9u), 0x3C6EF372u);
@@ -188,8 +195,10 @@ __device__ __forceinline__ uint32_t finite_bits(float x) {
     return a < 0x7F800000u ? a : 0u;
 }
 
+// kAny: the factor may have a rest.
+template <bool kAny>
 __device__ __forceinline__ void moments(float g, const AdScalars& s, float& m, float& v) {
-    const float x = __fmul_rn(g, s.factor);
+    const float x = kAny ? __fmul_rn(__fmul_rn(g, s.factor), s.rest) : __fmul_rn(g, s.factor);
     m = __fadd_rn(__fmul_rn(m, s.b1), __fmul_rn(x, s.c1));
     v = __fadd_rn(__fmul_rn(v, s.b2), __fmul_rn(__fmul_rn(x, x), s.c2));
 }
@@ -270,7 +279,7 @@ __device__ __noinline__ void step_block(const AdView t, const AdScalars* shared,
             xm[e] = in ? m32[k] : 0.f;
             xv[e] = in ? v32[k] : 0.f;
         }
-        moments(xg, s, xm[e], xv[e]);
+        moments<true>(xg, s, xm[e], xv[e]);
         xp[e] = updated(xp[e], xm[e], xv[e], s);
         top_m = max(top_m, finite_bits(xm[e]));
         top_v = max(top_v, finite_bits(xv[e]));
@@ -415,7 +424,7 @@ __device__ __forceinline__ bool step_small(const uint8_t* stage, uint32_t expone
         top_m[j] = top_v[j] = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            moments(xg[e], s, xm[j][e], xv[j][e]);
+            moments<false>(xg[e], s, xm[j][e], xv[j][e]);
             top_m[j] = max(top_m[j], __float_as_uint(xm[j][e]) & 0x7FFFFFFFu);
             top_v[j] = max(top_v[j], __float_as_uint(xv[j][e]));  // no less than +0, or a NaN, which may have a sign
             xp[e] = updated_fast(xp[e], xm[j][e], xv[j][e], s);
@@ -529,7 +538,7 @@ __device__ __forceinline__ void step_wide(const AdView& t, const AdScalars& s, i
         const uint32_t key = t.key + (uint32_t)(i >> 32) * 0x9E3779B9u;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            moments(xg[e], s, xm[e], xv[e]);
+            moments<false>(xg[e], s, xm[e], xv[e]);
             xp[e] = updated(xp[e], xm[e], xv[e], s);
             if (kBf16P && kRandom) d[e] = mix32(mix32((uint32_t)i + e, key), t.key_p);
         }
@@ -558,7 +567,7 @@ __device__ __forceinline__ void step_small_units(const AdTensor& at, uint32_t u0
     const bool quick = ((reinterpret_cast<uintptr_t>(t.p) | reinterpret_cast<uintptr_t>(t.g) |
                          reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v)) &
                         15u) == 0 &&
-                       !s.tiny_eps;
+                       !s.tiny_eps && s.rest == 1.f;
     int64_t b = (int64_t)(u0 - at.first_unit) * kPerUnit;
     const int64_t blocks = min((t.n + kAdBlock - 1) / kAdBlock, (int64_t)(u1 - at.first_unit) * kPerUnit);
     const int64_t end = quick ? min(blocks, t.n / kAdBlock - 1) : b;  // up to here there are two whole blocks
@@ -633,7 +642,8 @@ __device__ __forceinline__ void step_wide_units(const AdTensor& at, uint32_t u0,
     const bool quick =
         ((reinterpret_cast<uintptr_t>(t.p) & (kBf16P ? 7u : 15u)) |
          (reinterpret_cast<uintptr_t>(t.g) & (kBf16G ? 7u : 15u)) |
-         ((reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v)) & 15u)) == 0;
+         ((reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v)) & 15u)) == 0 &&
+        s.rest == 1.f;
     int64_t b = (int64_t)(u0 - at.first_unit) * kPerUnit + (threadIdx.x >> 5) * 2;
     const int64_t blocks = min((t.n + kAdBlock - 1) / kAdBlock, (int64_t)(u1 - at.first_unit) * kPerUnit);
     const int64_t end = quick ? min(blocks, t.n / kAdBlock - 1) : 0;  // up to here there are two whole blocks
