@@ -93,7 +93,7 @@ enum {
 #define PSTAT_DEV_EMPTY_ROW 0x2 /* every logit of a row is -inf: softmax undefined */
 #define PSTAT_DEV_TIMEOUT 0x4   /* a bounded wait on an asynchronous copy gave up */
 #define PSTAT_DEV_RANGE 0x8     /* lm_head backward: a value exceeds the fp16 range (65504) */
-#define PSTAT_DEV_BAD_PARAM 0x10 /* a row's temperature, top_p, min_p, uniform or parent is out of range */
+#define PSTAT_DEV_BAD_PARAM 0x10 /* a row's temperature, top_p, min_p, uniform or parent, or a rate or step, is out of range */
 #define PSTAT_DEV_NONFINITE 0x20 /* the gradient norm, or an element to be quantised, is infinite or NaN */
 
 #define PSTAT_MAX_SHARDS 64
@@ -532,7 +532,9 @@ PSTAT_API int pstat_clip_grad_norm(const pstat_tensor* tensors, int64_t n_tensor
  *                   the call (PSTAT_ERR_PARAM).
  *   lr_at, step_at, seed_at     device values that take the place of lr, step and
  *                   seed where not NULL, so that a captured step can be replayed.
- *                   step >= 1 (t above); one on the device is not checked.
+ *                   step >= 1 (t above).  A rate on the device that is negative, infinite
+ *                   or NaN, and a step below 1, set PSTAT_DEV_BAD_PARAM, and nothing is
+ *                   changed.
  */
 #define PSTAT_ADAMW_MAX_TENSORS ((int64_t)1 << 28)
 typedef struct {

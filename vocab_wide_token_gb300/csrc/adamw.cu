@@ -86,7 +86,7 @@ struct AdScalars {
     float b1, c1, b2, c2, eps, factor, decay, size, root;
     float rest;  // of the gradients' factor: 1, or a power of two (see scalars_of)
     uint32_t seed_key;
-    bool skip;
+    int skip;        // bits of PSTAT_DEV_* for which nothing is done
     bool small_eps;  // the roots of subnormal numbers weigh against eps (see updated)
     bool tiny_eps;   // eps itself is no divisor for reciprocals that flush small ones
 };
@@ -123,18 +123,19 @@ __device__ AdScalars scalars_of(const AdOptions& o) {
     s.decay = o.decay;
     s.size = o.size;
     s.root = o.root;
+    s.skip = 0;
     if (o.lr_at || o.step_at) {
         const double lr = o.lr_at ? (double)*after_wait(o.lr_at) : o.lr;
         const double t = (double)(o.step_at ? *after_wait(o.step_at) : o.step);
+        if (!(lr >= 0.0 && lr < INFINITY) || t < 1.0) s.skip |= PSTAT_DEV_BAD_PARAM;  // as the host's
         corrections(lr, o.weight_decay, o.beta1, o.beta2, t, s.decay, s.size, s.root);
     }
     s.small_eps = !(s.eps >= 0x1p-41f * s.root);
     s.tiny_eps = !(s.eps >= 0x1p-60f);
     s.factor = s.rest = 1.f;
-    s.skip = false;
     if (o.norm) {
         const float norm = *after_wait(o.norm);
-        if (!(norm < INFINITY)) s.skip = true;
+        if (!(norm < INFINITY)) s.skip |= PSTAT_DEV_NONFINITE;
         if (norm > o.max_norm) s.factor = __fdiv_rn(o.max_norm, norm);
         // A factor below the normal numbers (max_norm < 4) has lost bits, while what it scales, up to
         // 2^128, comes out as a normal number: 2^125 times as large it keeps them.
@@ -682,7 +683,7 @@ __global__ void __launch_bounds__(kAdThreads, kBf16P && !kSmall && !kRandom ? 3 
     grid_wait();
     if (threadIdx.x == 0) {
         shared = scalars_of(o);
-        if (shared.skip && blockIdx.x == 0 && o.dev_error) atomicOr(o.dev_error, PSTAT_DEV_NONFINITE);
+        if (shared.skip && blockIdx.x == 0 && o.dev_error) atomicOr(o.dev_error, shared.skip);
     }
     __syncthreads();
     const AdScalars s = shared;

@@ -1095,7 +1095,8 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999
     ``grad_norm``'s scalar tensor: with it the gradients are clipped on the way, and
     one that is not finite sets DEV_NONFINITE and changes nothing.  `step`, `lr` and
     `seed` may be one-element tensors (int64, float32, int64) that a captured step
-    reads at each replay.
+    reads at each replay; a step or rate there that a number would be refused for
+    sets DEV_BAD_PARAM and changes nothing.
 
     What is held in fewer than 32 bits is rounded to nearest; with a `seed`, up or
     down with the probability of the distance, by a hash of seed, tensor and
