@@ -254,8 +254,8 @@ __device__ __forceinline__ void select_best(BeamShared<kThreads>& sm, int n, int
 
 // ln S of a beam's row from exact weights: every thread of the CTA.
 template <typename E, int kThreads>
-__device__ __noinline__ void sum_anew(BeamShared<kThreads>& sm, const BeamArgs& a, int64_t t, int k, float score) {
-    const E* row = static_cast<const E*>(a.f.logits) + t * a.f.ld;
+__device__ __noinline__ void sum_anew(BeamShared<kThreads>& sm, const BeamArgs& a, const E* row, int k,
+                                      float score) {
     const float M = sm.base[k].M;
     const int scale = fixed_scale(sm.S[k] * (1.f + 2.f * kSumError));
     const TempScale one = temp_scale(1.f);
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) beam_finish_kernel(
     const float* scores = after_wait(a.scores) + t0;
     const float4* records = after_wait(a.f.records) + t0 * chunks;
     const E* maxima = static_cast<const E*>(after_wait(a.f.group_max)) + t0 * chunks * 32;
-    const E* logits = static_cast<const E*>(a.f.logits) + t0 * a.f.ld;
+    const E* logits = static_cast<const E*>(after_wait(a.f.logits)) + t0 * a.f.ld;
 
     for (int k = warp; k < beams; k += kThreads / 32) {
         const float s = scores[k];
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) beam_finish_kernel(
         __syncthreads();
         if (!rows) break;
         for (int k = 0; k < beams; ++k)
-            if (rows >> k & 1) sum_anew<E>(sm, a, t0 + k, k, scores[k]);
+            if (rows >> k & 1) sum_anew<E>(sm, a, logits + (int64_t)k * a.f.ld, k, scores[k]);
         exact |= rows;
     }
     if ((int)threadIdx.x < n) {
