@@ -93,7 +93,7 @@ enum {
 #define PSTAT_DEV_EMPTY_ROW 0x2 /* every logit of a row is -inf: softmax undefined */
 #define PSTAT_DEV_TIMEOUT 0x4   /* a bounded wait on an asynchronous copy gave up */
 #define PSTAT_DEV_RANGE 0x8     /* lm_head backward: a value exceeds the fp16 range (65504) */
-#define PSTAT_DEV_BAD_PARAM 0x10 /* a row's temperature, top_p, min_p, uniform or parent, or a rate or step, is out of range */
+#define PSTAT_DEV_BAD_PARAM 0x10 /* a temperature, top_p, min_p, uniform, parent, rate or step is out of range */
 #define PSTAT_DEV_NONFINITE 0x20 /* the gradient norm, or an element to be quantised, is infinite or NaN */
 
 #define PSTAT_MAX_SHARDS 64

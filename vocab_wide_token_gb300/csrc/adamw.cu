@@ -7,10 +7,14 @@
 // One read and one write of everything, so bound by HBM: 28 bytes an element in fp32,
 // 10 with bf16 parameters and gradients and 8-bit moments.  There the instructions weigh
 // more than the bytes: 10 bytes at 6.7 TB/s leave an SM about 55 instructions for each
-// element, and decoding, drawing (18), encoding and the step are 82, or 60 rounded to nearest.
+// element, and decoding, drawing (18), encoding and the step are 85, or 64 rounded to nearest.
 // 60 million elements, with bf16 parameters and gradients unless said otherwise:
-//   32-bit moments  202 us drawn, 6.5 TB/s; all in fp32 242 us, 6.9 TB/s
-//   8-bit moments   173 us drawn, 3.5 TB/s; 123 us to nearest, 4.9 TB/s; fp32 drawn 172 us
+//   32-bit moments  203 us drawn, 6.5 TB/s; 191 to nearest; all in fp32 241 us, 7.0 TB/s
+//   8-bit moments   171 us drawn, 3.5 TB/s; 124 us to nearest, 4.9 TB/s; fp32 drawn 153 us
+// Codes of zero and values below the least code cost more, up to 30 us where nearly every
+// block has some.
+// A tensor with an address off 16 bytes goes element by element (step_block): 353 us to nearest
+// and 488 drawn with 32-bit moments, 501 and 546 with 8-bit ones.
 //
 // 8-bit moments.  Codes of three bits of mantissa under an exponent that reaches a fixed
 // number of binary orders below the largest of a block of 128: 4 bits and a sign for m
@@ -479,7 +483,9 @@ __device__ __forceinline__ bool step_small(const uint8_t* stage, uint32_t expone
         for (int j = 0; j < kN; ++j) {
             const uint32_t least_m = ((uint32_t)code_base(top_m[j], kDepthM) << 20) + (1u << 20);
             const uint32_t least_v = ((uint32_t)code_base(top_v[j], kDepthV) << 20) + (1u << 20);
-            const float unit = __uint_as_float(least_m) * 0x1p-20f;  // as encode_m has it: a power of two
+            // Nine eighths of a power of two, or 2^-129: this product and that with a draw are
+            // exact, as encode_m's are.
+            const float unit = __uint_as_float(least_m) * 0x1p-20f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const uint32_t draw = kRandom ? (h[j][e] >> 12 & 0xFFFF0u) | 8u : 0x80000u;
@@ -556,7 +562,7 @@ __device__ __forceinline__ void step_wide(const AdView& t, const AdScalars& s, i
 // A warp's units [u0, u1) of a tensor with 8-bit moments: neighbouring blocks, so that the warp
 // reads and writes the exponents of 32 blocks at once.  (Written a byte at a time by all warps
 // of a CTA, which read others of the same 32 bytes meanwhile, they held it up: 60 million
-// bf16 elements in 218 us, 173 so.)
+// bf16 elements in 218 us, 171 so.)
 template <bool kBf16P, bool kBf16G, bool kRandom>
 __device__ __forceinline__ void step_small_units(const AdTensor& at, uint32_t u0, uint32_t u1, const AdScalars& s,
                                                  const AdScalars* shared, uint8_t* ring) {

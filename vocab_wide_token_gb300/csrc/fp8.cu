@@ -172,7 +172,8 @@ cudaError_t launch_quantize(const QuArgs& a, unsigned grid, cudaStream_t st) {
 // on the tile that it falls in.
 //   warp 0    copies tiles of W and q into a ring of stages (TMA, 128-byte swizzle)
 //   warp 1    issues tcgen05.mma (K 32), four to a block
-//   the others  a thread adds up one lane of the accumulator for up to 64 columns
+//   the others  a thread adds up one lane of the accumulator for up to 32 columns (narrow tiles)
+//               or 128 (wide ones)
 // Up to 128 tokens (narrow tiles) 128 rows of W are M and the tokens N (16, 32, 64 or 128): few
 // tokens cost few columns.  Bound by the one pass over W.
 // Beyond (wide tiles) 256 tokens are M, 256 rows of W N, by a pair of CTAs (cta_group::2) that
@@ -181,7 +182,8 @@ cudaError_t launch_quantize(const QuArgs& a, unsigned grid, cudaStream_t st) {
 // for the operands' way from L2: an SM takes in 32 KB for every 128 x 256 x 128 products,
 // alone 48 KB.  8 epilogue warps with 128 columns each: with 16 of 64 the instructions of
 // waiting and handing on, four warps' on each scheduler, bound it (2048 x 60,000 x 4096 in
-// 454 us; 373 so).  4096 x 151,936 x 4096 takes 1.82 ms, 2.8 PFLOP/s: two accumulators of 256
+// 454 us; 373 so).  4096 x 151,936 x 4096 takes 1.84 to 1.90 ms, 2.7 to 2.8 PFLOP/s (one call
+// after another, which the power limit slows, 2.0 ms with the quantising): two accumulators of 256
 // columns fill tensor memory, and a block's products (512 cycles), their way to the epilogue,
 // its loads and its word back to the issuing CTA take 1,500 to 1,600 for two blocks.
 // All waits are bounded; on a timeout a CTA drains what is in flight and ends.

@@ -2,16 +2,19 @@
 //
 // Row b K + i of every output becomes row b K' + parents[b, i] of its input.  Bound by
 // HBM.  A thread owns a column of 16 bytes (or what alignment leaves of them) through all
-// rows of a search: it loads the column of every row's parent before it stores any, so
-// that a permutation in place needs neither a second buffer nor an order, and a parent
-// of several rows comes from HBM once.  In place a row that is its own parent is
-// neither read nor written.
+// rows of a search.  In place it loads the column of every row's parent before it stores any,
+// so that a permutation needs neither a second buffer nor an order; a row that is its own
+// parent is neither read nor written.  Into other buffers it goes by rounds of 8 rows, and a
+// parent of rows in several rounds is asked for in each.
 //
 // A warp's parents are one load, a lane each, and known before the first row is loaded: one by
 // one they kept each row waiting for the last one's.  Many short CTAs, as what they read
 // and write comes in turns.  Four caches of 128 rows x 8 x 1501 x 128 bf16 in place: 8 beams
 // 325 us, 6.9 TB/s (430 row by row with 8 CTAs to an SM); 4 beams 350 (540), 16 beams 360
-// (545), 32 beams 394 (490), 64 beams 505 (1,265).
+// (545), 32 beams 394 (490), 64 beams 505 (1,265).  Views whose rows or runs start off 16
+// bytes move by what they start on: 8 x 1501 (of 1600) x 102 bf16, 4 bytes at a time, 734 us in
+// place and 773 into other buffers, x 101, 2 bytes, 1,281 and 1,338, where HBM would do with 275
+// and 307.
 #include <cuda_runtime.h>
 
 #include <algorithm>
